@@ -521,6 +521,164 @@ vrcclResult_t vrcclShardRange(size_t count, vrcclDataType_t dtype, int nshards, 
 vrcclResult_t vrcclAllReduceNoAlloc(const void* const* sendbufs, void* const* recvbufs, size_t count, int nranks,
                                     vrcclDataType_t dtype, vrcclRedOp_t op, vrcclStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Operators of a replica: what a data-parallel rank computes between two
+ * AllReduces of its gradients -- layer norm, the linear layer and a
+ * distillation loss, forward and backward. They need no communicator: a call
+ * runs on the current CUDA device, is asynchronous on `stream` like every
+ * call here, allocates nothing (what scratch it needs the caller passes as
+ * `workspace`) and may be captured in a CUDA graph.
+ *
+ * Matrices are row-major with a row stride in elements (ldx, ...), which may
+ * exceed the row's length; only the elements of the rows are read or
+ * written. Pointers must be aligned to their element's size; rows that all
+ * start on 16-byte boundaries are faster. The operators take vrcclFloat32,
+ * vrcclBfloat16 and vrcclFloat16 (the linear layer only the latter two).
+ * Sums and statistics are held in binary32 and each result is rounded once
+ * (to nearest even); there are no atomic sums, so the same call gives the
+ * same bits.
+ *
+ * Errors of all of them: vrcclInvalidArgument (a null or misaligned pointer,
+ * a row stride below the row's length, an enum or a size out of range, a
+ * workspace that is too small, an output that overlaps an input other than
+ * as the call allows); vrcclCudaError (launch failure).
+ */
+
+/*
+ * vrcclLayerNormForward -- y = (x - mean) * rstd * gamma + beta over the
+ * columns of each row, rstd = 1 / sqrt(mean((x - mean)^2) + eps).
+ *   x, y         [rows, cols] of dtype; y may be x (same stride).
+ *   gamma, beta  [cols] of paramType, or NULL (1 and 0).
+ *   mean, rstd   out, [rows] binary32: what the backward pass takes; either
+ *                may be NULL.
+ *   rows, cols   0 of either -> success, nothing launched.
+ *   eps          >= 0.
+ */
+vrcclResult_t vrcclLayerNormForward(const void* x, size_t ldx, const void* gamma, const void* beta, void* y,
+                                    size_t ldy, float* mean, float* rstd, size_t rows, size_t cols,
+                                    vrcclDataType_t dtype, vrcclDataType_t paramType, float eps,
+                                    vrcclStream_t stream);
+
+/* vrcclLayerNormWorkspace -- bytes of workspace the backward pass of this
+ * size needs (the partial sums of the weights' gradients). */
+vrcclResult_t vrcclLayerNormWorkspace(size_t rows, size_t cols, size_t* bytes);
+
+/*
+ * vrcclLayerNormBackward -- with xh = (x - mean) * rstd and g = dy * gamma:
+ *   dx = rstd * (g - mean(g) - xh * mean(g * xh))      per row
+ *   dgamma = sum over rows of dy * xh,  dbeta = sum over rows of dy
+ *   dy, x, dx      [rows, cols] of dtype; dx may be dy or x (same stride).
+ *   gamma          [cols] of paramType, or NULL (1).
+ *   mean, rstd     [rows], as the forward pass wrote them.
+ *   dgamma, dbeta  out, [cols] of paramType; either may be NULL. With
+ *                  rows == 0 they are set to zero.
+ *   workspace      16-byte aligned, vrcclLayerNormWorkspace bytes; NULL where
+ *                  neither gradient is asked for.
+ */
+vrcclResult_t vrcclLayerNormBackward(const void* dy, size_t lddy, const void* x, size_t ldx, const void* gamma,
+                                     const float* mean, const float* rstd, void* dx, size_t lddx, void* dgamma,
+                                     void* dbeta, size_t rows, size_t cols, vrcclDataType_t dtype,
+                                     vrcclDataType_t paramType, void* workspace, size_t workspaceBytes,
+                                     vrcclStream_t stream);
+
+/* Activations of the linear layer: gelu is z * Phi(z) with the normal
+ * distribution Phi, gelu-tanh its approximation
+ * z/2 * (1 + tanh(sqrt(2/pi) * (z + 0.044715 z^3))), silu z / (1 + exp(-z)). */
+typedef enum {
+  vrcclActNone = 0,
+  vrcclActRelu = 1,
+  vrcclActGelu = 2,
+  vrcclActGeluTanh = 3,
+  vrcclActSilu = 4,
+  vrcclNumActs = 5
+} vrcclActivation_t;
+
+/* vrcclLinearWorkspace -- bytes of workspace a call of this size may need
+ * (backward: 0 or 1), whatever its strides. A forward call whose x and w
+ * have all their rows on 16-byte boundaries needs none. */
+vrcclResult_t vrcclLinearWorkspace(int backward, size_t rows, size_t outs, size_t ins, vrcclDataType_t dtype,
+                                   vrcclActivation_t act, size_t* bytes);
+
+/*
+ * vrcclLinearForward -- z = x w^T + bias, y = act(z) + residual.
+ *   x         [rows, ins];  w [outs, ins];  y [rows, outs].
+ *   bias      [outs], or NULL.
+ *   residual  [rows, outs], or NULL; y may be residual (same stride).
+ *   z         out, [rows, outs]: what the backward pass of an activation
+ *             takes, or NULL.
+ *   dtype     vrcclBfloat16 or vrcclFloat16, of every operand. Products and
+ *             sums are binary32. vrcclFloat32 -> vrcclInvalidUsage: the
+ *             tensor cores would round its operands to 10 fraction bits.
+ *   workspace 256-byte aligned; may be NULL where none is needed.
+ */
+vrcclResult_t vrcclLinearForward(const void* x, size_t ldx, const void* w, size_t ldw, const void* bias,
+                                 const void* residual, size_t ldr, void* y, size_t ldy, void* z, size_t ldz,
+                                 size_t rows, size_t outs, size_t ins, vrcclDataType_t dtype, vrcclActivation_t act,
+                                 void* workspace, size_t workspaceBytes, vrcclStream_t stream);
+
+/*
+ * vrcclLinearBackward -- with dz = dy * act'(z):
+ *   dx = dz w,  dw = dz^T x,  dbias = sum over rows of dz
+ * (the residual's gradient is dy itself).
+ *   dy, z     [rows, outs]; z as the forward pass wrote it, not read for
+ *             vrcclActNone.
+ *   x, w      [rows, ins], [outs, ins].
+ *   dx, dw, dbias  out, [rows, ins], [outs, ins], [outs]; each may be NULL.
+ *             A sum over no rows is zero.
+ * With an activation dz is rounded to dtype before the two products, which
+ * take their operands in it; dbias sums the unrounded values.
+ */
+vrcclResult_t vrcclLinearBackward(const void* dy, size_t lddy, const void* z, size_t ldz, const void* x, size_t ldx,
+                                  const void* w, size_t ldw, void* dx, size_t lddx, void* dw, size_t lddw, void* dbias,
+                                  size_t rows, size_t outs, size_t ins, vrcclDataType_t dtype, vrcclActivation_t act,
+                                  void* workspace, size_t workspaceBytes, vrcclStream_t stream);
+
+/* vrcclLinearGetAsyncError -- vrcclSuccess, or vrcclTimeout after a linear
+ * call on the current device whose kernel gave up a wait (its outputs are
+ * then undefined). Waits for the device's work. */
+vrcclResult_t vrcclLinearGetAsyncError(vrcclResult_t* asyncErr);
+
+/* Most teacher entries a row of the distillation loss may have. */
+#define VRCCL_DISTILL_MAX_K 1024
+
+/*
+ * vrcclDistillForward -- the loss of a student against a teacher known by
+ * its top logits: with temperature T, p = softmax(teacher / T) over a row's
+ * kept entries and q = softmax(logits / T) over the vocabulary,
+ *   loss = T^2 * sum over entries of p * (log p - log q[index]).
+ * An entry is kept if its index lies in [0, vocab) and its logit is above
+ * -inf; entries that share an index add up. A row without kept entries has
+ * loss 0 (a padding position; its logits are not read). Masked student
+ * logits may be -inf or the type's lowest value.
+ *   logits   [rows, vocab] of dtype.
+ *   teacher  [rows, k] of teacherType;  index [rows, k] of indexType
+ *            (vrcclInt32 or vrcclInt64), k <= VRCCL_DISTILL_MAX_K.
+ *   loss     out, [rows] binary32.
+ *   stats    out, [rows, 2] binary32, 8-byte aligned, or NULL: the row's
+ *            largest logit and the logarithm of the sum of
+ *            exp((logits - largest) / T); 0, 0 for a row without entries.
+ *   temperature  > 0, and its reciprocal finite.
+ */
+vrcclResult_t vrcclDistillForward(const void* logits, size_t ldl, const void* teacher, size_t ldt, const void* index,
+                                  size_t ldi, float* loss, float* stats, size_t rows, size_t vocab, size_t k,
+                                  vrcclDataType_t dtype, vrcclDataType_t teacherType, vrcclDataType_t indexType,
+                                  float temperature, vrcclStream_t stream);
+
+/*
+ * vrcclDistillBackward -- the gradient of those losses,
+ *   dlogits[v] = dloss * T * (q[v] - sum of p over the entries with index v),
+ * zero in rows without kept entries.
+ *   stats    as the forward pass wrote them.
+ *   dloss    binary32, row r's at dloss[r * dlossStride] (stride 0: one
+ *            value for all rows).
+ *   dlogits  out, [rows, vocab] of dtype; may be logits (same stride).
+ */
+vrcclResult_t vrcclDistillBackward(const void* logits, size_t ldl, const void* teacher, size_t ldt, const void* index,
+                                   size_t ldi, const float* stats, const float* dloss, size_t dlossStride,
+                                   void* dlogits, size_t ldd, size_t rows, size_t vocab, size_t k,
+                                   vrcclDataType_t dtype, vrcclDataType_t teacherType, vrcclDataType_t indexType,
+                                   float temperature, vrcclStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,151 @@
+// Building blocks of the operators a replica runs between two AllReduces
+// (layer norm, linear layer, distillation loss): element access, reductions
+// over a warp or a block, and the host checks they share.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstddef>
+#include <cstdint>
+
+#include "device_common.cuh"
+
+namespace vrccl {
+
+// Largest row count, row length and row stride an operator takes: products
+// of two of them and an element size stay far inside 64 bits.
+constexpr size_t kMaxExtent = size_t(1) << 40;
+
+__host__ __device__ constexpr int floatTypeSize(int dt) { return dt == vrcclFloat32 ? 4 : 2; }
+inline bool isOperatorType(int dt) { return dt == vrcclFloat32 || dt == vrcclBfloat16 || dt == vrcclFloat16; }
+
+// A [rows, cols] operand: present, its address a multiple of its elements'
+// size, its row stride no shorter than a row.
+inline bool goodMatrix(const void* p, size_t ld, size_t cols, int elemSize) {
+  return p && (uintptr_t)p % elemSize == 0 && ld >= cols && ld < kMaxExtent;
+}
+inline bool goodVector(const void* p, int elemSize) { return p && (uintptr_t)p % elemSize == 0; }
+// Every row of a matrix starts on a 16-byte boundary.
+inline bool rowsAligned(const void* p, size_t ld, int elemSize) {
+  return ((uintptr_t)p | (uintptr_t)(ld * elemSize)) % 16 == 0;
+}
+// Bytes of the matrix from its first element to its last.
+inline size_t spanBytes(size_t ld, size_t rows, size_t cols, int elemSize) {
+  return rows == 0 ? 0 : ((rows - 1) * ld + cols) * elemSize;
+}
+inline bool overlap(const void* a, size_t an, const void* b, size_t bn) {
+  return a && b && an && bn && (uintptr_t)a < (uintptr_t)b + bn && (uintptr_t)b < (uintptr_t)a + an;
+}
+
+inline vrcclResult_t launchResult() {
+  return cudaGetLastError() == cudaSuccess ? vrcclSuccess : vrcclCudaError;
+}
+// Multiprocessors of the current device (asked for once a device).
+int smCount();
+
+// ------------------------------------------------------------ element access
+// N consecutive elements of type DT as binary32. With N elements in 16 (or
+// 8, 4) bytes one wide load; the caller guarantees the alignment.
+
+template <int DT>
+__device__ __forceinline__ float loadOne(const void* p, size_t i) {
+  using S = typename Ty<DT>::S;
+  return Ty<DT>::toF(reinterpret_cast<const S*>(p)[i]);
+}
+__device__ __forceinline__ float loadParam(const void* p, int dt, size_t i) {
+  return dt == vrcclFloat32    ? reinterpret_cast<const float*>(p)[i]
+         : dt == vrcclBfloat16 ? loadOne<vrcclBfloat16>(p, i)
+                               : loadOne<vrcclFloat16>(p, i);
+}
+__device__ __forceinline__ void storeParam(void* p, int dt, size_t i, float x) {
+  if (dt == vrcclFloat32)
+    reinterpret_cast<float*>(p)[i] = x;
+  else
+    reinterpret_cast<unsigned short*>(p)[i] =
+        dt == vrcclBfloat16 ? Ty<vrcclBfloat16>::fromF(x) : Ty<vrcclFloat16>::fromF(x);
+}
+
+// The two elements of a packed word (2-byte types).
+template <int DT>
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+  if constexpr (DT == vrcclBfloat16) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  } else {
+    return make_float2(Ty<DT>::toF((unsigned short)(w & 0xffffu)), Ty<DT>::toF((unsigned short)(w >> 16)));
+  }
+}
+template <int DT>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t d;
+  if constexpr (DT == vrcclBfloat16)
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
+// A 16-byte vector of elements <-> binary32.
+template <int DT>
+struct Vec16 {
+  static constexpr int N = 16 / floatTypeSize(DT);
+  static __device__ __forceinline__ void expand(const uint4& v, float (&f)[N]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (N == 4) {
+        f[i] = __uint_as_float(w[i]);
+      } else {
+        const float2 p = unpack2<DT>(w[i]);
+        f[2 * i] = p.x;
+        f[2 * i + 1] = p.y;
+      }
+    }
+  }
+  static __device__ __forceinline__ uint4 pack(const float (&f)[N]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (N == 4)
+        w[i] = __float_as_uint(f[i]);
+      else
+        w[i] = pack2<DT>(f[2 * i], f[2 * i + 1]);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+
+// ------------------------------------------------------------ reductions
+
+__device__ __forceinline__ float warpSum(float x) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+__device__ __forceinline__ float2 warpSum2(float2 x) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    x.x += __shfl_xor_sync(0xffffffffu, x.x, o);
+    x.y += __shfl_xor_sync(0xffffffffu, x.y, o);
+  }
+  return x;
+}
+// Sums over a block of up to 32 warps, the result in every thread. `s` holds
+// 32 entries; calls that follow one another take turns between two arrays, so
+// that one barrier a call is enough.
+__device__ __forceinline__ float2 blockSum2(float2 x, float2* s) {
+  x = warpSum2(x);
+  const int lane = threadIdx.x & 31, warps = (blockDim.x + 31) >> 5;
+  if (lane == 0) s[threadIdx.x >> 5] = x;
+  __syncthreads();
+  return warpSum2(lane < warps ? s[lane] : make_float2(0.f, 0.f));
+}
+__device__ __forceinline__ float blockSum(float x, float* s) {
+  x = warpSum(x);
+  const int lane = threadIdx.x & 31, warps = (blockDim.x + 31) >> 5;
+  if (lane == 0) s[threadIdx.x >> 5] = x;
+  __syncthreads();
+  return warpSum(lane < warps ? s[lane] : 0.f);
+}
+
+}  // namespace vrccl

@@ -1,0 +1,907 @@
+// Linear layer: a matrix product with bias, activation and residual in its
+// epilogue, and its gradients.
+//
+//   z = x W^T + b,  y = act(z) + r                   x [rows, ins], W [outs, ins]
+//   dz = dy act'(z),  dx = dz W,  dW = dz^T x,  db = sum over rows of dz
+//
+// All three products are D[M, N] = A B^T with a contraction of length K, run by
+// one persistent tcgen05 kernel. An operand is "K-major" where the contraction
+// runs along its rows in memory (x and W forward, dz in dx) and "MN-major"
+// where it runs down its columns (W in dx, both operands of dW); the tensor
+// cores read either from the same 128-byte-swizzled tiles, so no operand is
+// ever transposed in memory.
+//
+// Warp roles of a block: one thread issues the TMA copies of 64-deep slices
+// of A and B into a ring of shared-memory stages, one issues the MMAs, four
+// warps read finished accumulators out of TMEM, apply the epilogue and store.
+// TMEM holds two accumulators, so a tile's epilogue runs under the next one's
+// products.
+//
+// A call with few rows (one token and its like) is bound by reading W once:
+// linearFew streams W with wide loads over all multiprocessors instead.
+#include <cuda.h>
+
+#include "ops_common.cuh"
+
+namespace vrccl {
+namespace {
+
+// ------------------------------------------------------------ activations
+
+template <int ACT>
+__device__ __forceinline__ float activate(float z) {
+  if constexpr (ACT == vrcclActRelu) return z > 0.f ? z : (z != z ? z : 0.f);
+  if constexpr (ACT == vrcclActGelu) return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
+  if constexpr (ACT == vrcclActGeluTanh)
+    return 0.5f * z * (1.f + tanhf(0.79788456080286536f * (z + 0.044715f * z * z * z)));
+  if constexpr (ACT == vrcclActSilu) return z / (1.f + __expf(-z));
+  return z;
+}
+template <int ACT>
+__device__ __forceinline__ float slope(float z) {
+  if constexpr (ACT == vrcclActRelu) return z > 0.f ? 1.f : 0.f;
+  if constexpr (ACT == vrcclActGelu)
+    return 0.5f * (1.f + erff(z * 0.70710678118654752f)) + z * __expf(-0.5f * z * z) * 0.39894228040143268f;
+  if constexpr (ACT == vrcclActGeluTanh) {
+    const float t = tanhf(0.79788456080286536f * (z + 0.044715f * z * z * z));
+    return 0.5f * (1.f + t) + 0.5f * z * (1.f - t * t) * 0.79788456080286536f * (1.f + 0.134145f * z * z);
+  }
+  if constexpr (ACT == vrcclActSilu) {
+    const float s = 1.f / (1.f + __expf(-z));
+    return s * (1.f + z * (1.f - s));
+  }
+  return 1.f;
+}
+
+// ------------------------------------------------------------ tcgen05, TMA
+
+// A wait that has not come true after this long never will: the kernel then
+// records a timeout, drains what it has in flight and ends.
+constexpr unsigned long long kWaitNs = 2000000000ull;
+
+__device__ int gLinearStatus;  // vrcclResult_t of the first device-side failure
+
+// false = gave up (this wait, or another one of the block)
+__device__ __forceinline__ bool waitBar(unsigned long long* bar, unsigned parity, volatile int* dead,
+                                        unsigned long long limit = kWaitNs) {
+  if (mbarTryWait(bar, parity)) return true;
+  const unsigned long long t0 = globalTimer();
+  while (!mbarTryWait(bar, parity)) {
+    if (*dead) return false;
+    if (globalTimer() - t0 > limit) {
+      *dead = 1;
+      atomicCAS(&gLinearStatus, 0, (int)vrcclTimeout);
+      return false;
+    }
+  }
+  return true;
+}
+__device__ __forceinline__ void mbarArriveExpect(unsigned long long* bar, unsigned bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smemAddr(bar)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void tmaLoad2d(const CUtensorMap* map, void* dst, unsigned long long* bar, int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
+          smemAddr(dst)),
+      "l"(map), "r"(smemAddr(bar)), "r"(x), "r"(y)
+      : "memory");
+}
+__device__ __forceinline__ void tcFenceBefore() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tcFenceAfter() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tcCommit(unsigned long long* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smemAddr(bar))
+               : "memory");
+}
+__device__ __forceinline__ void tcMma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n"
+      ".reg .pred p;\n"
+      "setp.ne.b32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n"
+      "}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tcLoad32(uint32_t addr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n"
+      "tcgen05.wait::ld.sync.aligned;\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr)
+      : "memory");
+}
+
+// Shared-memory operand descriptor of a tile with 128-byte swizzle. K-major:
+// rows of 64 contraction elements (128 bytes), eight rows to a swizzle block,
+// blocks 1024 bytes apart. MN-major: rows of 64 M (or N) elements, one row a
+// contraction index; eight of them make a swizzle block (1024 bytes apart),
+// and the next 64 M elements start 8192 bytes on (one 64 x 64 box).
+__device__ __forceinline__ uint64_t operandDesc(uint32_t addr, bool mn) {
+  uint64_t d = (addr >> 4) & 0x3fff;
+  d |= (uint64_t)(mn ? 8192 >> 4 : 1) << 16;  // leading dimension
+  d |= (uint64_t)(1024 >> 4) << 32;           // stride dimension
+  d |= (uint64_t)1 << 46;                     // descriptor version
+  d |= (uint64_t)2 << 61;                     // 128-byte swizzle
+  return d;
+}
+
+// ------------------------------------------------------------ the product
+
+constexpr int kBM = 128, kBK = 64;
+constexpr int kProductThreads = 192;  // TMA warp, MMA warp, four epilogue warps
+
+struct ProductArgs {
+  CUtensorMap a, b;
+  void* d;               // [M, N]
+  void* z;               // the sums before activation, or NULL
+  const void* bias;      // [N] or NULL
+  const void* residual;  // [M, N] or NULL
+  size_t ldd, ldz, ldr;
+  int M, N, K;
+  bool aMN, bMN;         // operand majors
+  bool wideD, wideZ, wideR;  // rows of d / z / residual start on 16-byte boundaries
+  int act;
+};
+
+template <int BN>
+struct ProductShape {
+  static constexpr int kStageBytes = (kBM + BN) * kBK * 2;
+  static constexpr int kStages = BN == 256 ? 4 : BN == 128 ? 6 : 8;
+  static constexpr int kSmem = kStages * kStageBytes + 1024;
+  static constexpr int kTmemCols = 2 * BN < 32 ? 32 : 2 * BN;
+};
+
+template <int DT, int ACT>
+__device__ __forceinline__ void finish(const ProductArgs& a, float (&f)[32], size_t m, int n) {
+  using S = typename Ty<DT>::S;
+  const int left = a.N - n;  // columns that exist, of 32
+  if (a.z) {
+    S* z = static_cast<S*>(a.z) + m * a.ldz + n;
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      float g[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) g[e] = f[v * 8 + e];
+      if (a.wideZ && v * 8 + 8 <= left) {
+        reinterpret_cast<uint4*>(z)[v] = Vec16<DT>::pack(g);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (v * 8 + e < left) z[v * 8 + e] = Ty<DT>::fromF(g[e]);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 32; ++i) f[i] = activate<ACT>(f[i]);
+  if (a.residual) {
+    const S* r = static_cast<const S*>(a.residual) + m * a.ldr + n;
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      if (a.wideR && v * 8 + 8 <= left) {
+        float g[8];
+        Vec16<DT>::expand(reinterpret_cast<const uint4*>(r)[v], g);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[v * 8 + e] += g[e];
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (v * 8 + e < left) f[v * 8 + e] += Ty<DT>::toF(r[v * 8 + e]);
+      }
+    }
+  }
+  S* d = static_cast<S*>(a.d) + m * a.ldd + n;
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    float g[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) g[e] = f[v * 8 + e];
+    if (a.wideD && v * 8 + 8 <= left) {
+      reinterpret_cast<uint4*>(d)[v] = Vec16<DT>::pack(g);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (v * 8 + e < left) d[v * 8 + e] = Ty<DT>::fromF(g[e]);
+    }
+  }
+}
+
+template <int DT, int BN>
+__global__ void __launch_bounds__(kProductThreads) productKernel(const __grid_constant__ ProductArgs a) {
+  using Sh = ProductShape<BN>;
+  constexpr int kStages = Sh::kStages;
+  extern __shared__ unsigned char dyn[];
+  __shared__ unsigned long long full[kStages], empty[kStages], accFull[2], accEmpty[2], drained;
+  __shared__ uint32_t tmemSlot;
+  __shared__ int deadWord;
+  volatile int* dead = &deadWord;
+  unsigned char* smem = dyn + ((1024 - (smemAddr(dyn) & 1023)) & 1023);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbarInit(&full[s], 1);
+      mbarInit(&empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbarInit(&accFull[s], 1);
+      mbarInit(&accEmpty[s], 4);
+    }
+    mbarInit(&drained, 1);
+    deadWord = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smemAddr(&tmemSlot)),
+                 "r"(Sh::kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tcFenceBefore();
+  __syncthreads();
+  tcFenceAfter();
+  const uint32_t tmem = tmemSlot;
+
+  const int tilesM = (a.M + kBM - 1) / kBM, tilesN = (a.N + BN - 1) / BN, tiles = tilesM * tilesN;
+  const int steps = (a.K + kBK - 1) / kBK;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int stage = 0, round = 0;
+      bool ok = true;
+      for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+        const int m = tile % tilesM * kBM, n = tile / tilesM * BN;
+        for (int k = 0; k < steps; ++k) {
+          if (round > 0 && !(ok = waitBar(&empty[stage], (round - 1) & 1, dead))) break;
+          unsigned char* sa = smem + stage * Sh::kStageBytes;
+          unsigned char* sb = sa + kBM * kBK * 2;
+          mbarArriveExpect(&full[stage], Sh::kStageBytes);
+          if (!a.aMN) {
+            tmaLoad2d(&a.a, sa, &full[stage], k * kBK, m);
+          } else {
+            for (int i = 0; i < kBM / 64; ++i) tmaLoad2d(&a.a, sa + i * 8192, &full[stage], m + i * 64, k * kBK);
+          }
+          if (!a.bMN) {
+            tmaLoad2d(&a.b, sb, &full[stage], k * kBK, n);
+          } else {
+            for (int i = 0; i < BN / 64; ++i) tmaLoad2d(&a.b, sb + i * 8192, &full[stage], n + i * 64, k * kBK);
+          }
+          if (++stage == kStages) {
+            stage = 0;
+            ++round;
+          }
+        }
+      }
+      // given up: no copy may land after the block has gone
+      if (!ok) {
+        int quiet = 0;
+        for (int s = 0; s < kStages; ++s) {
+          const int issued = round + (s < stage ? 1 : 0);
+          if (issued > 0) waitBar(&full[s], (issued - 1) & 1, &quiet, 100000000ull);
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      // f32 accumulators; A and B of the element type; majors; N / 8, M / 16
+      const uint32_t idesc = 1u << 4 | (DT == vrcclBfloat16 ? 1u : 0u) << 7 | (DT == vrcclBfloat16 ? 1u : 0u) << 10 |
+                             (a.aMN ? 1u : 0u) << 15 | (a.bMN ? 1u : 0u) << 16 | (uint32_t)(BN / 8) << 17 |
+                             (uint32_t)(kBM / 16) << 24;
+      // 16 contraction elements on: 32 bytes along a K-major row, 16 rows of an MN-major tile
+      const uint32_t aStep = a.aMN ? 2048 >> 4 : 32 >> 4, bStep = a.bMN ? 2048 >> 4 : 32 >> 4;
+      int stage = 0, round = 0, turn = 0;
+      bool ok = true;
+      for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x, ++turn) {
+        const int acc = turn & 1, use = turn >> 1;
+        if (use > 0 && !(ok = waitBar(&accEmpty[acc], (use - 1) & 1, dead))) break;
+        tcFenceAfter();
+        const uint32_t d = tmem + acc * BN;
+        for (int k = 0; k < steps; ++k) {
+          if (!(ok = waitBar(&full[stage], round & 1, dead))) break;
+          tcFenceAfter();
+          const uint32_t sa = smemAddr(smem + stage * Sh::kStageBytes);
+          const uint64_t da = operandDesc(sa, a.aMN), db = operandDesc(sa + kBM * kBK * 2, a.bMN);
+#pragma unroll
+          for (int i = 0; i < kBK / 16; ++i) tcMma(d, da + i * aStep, db + i * bStep, idesc, k > 0 || i > 0);
+          tcCommit(&empty[stage]);
+          if (++stage == kStages) {
+            stage = 0;
+            ++round;
+          }
+        }
+        if (ok) tcCommit(&accFull[acc]);
+      }
+      if (!ok) {  // given up: the products in flight end before TMEM is freed
+        int quiet = 0;
+        tcCommit(&drained);
+        waitBar(&drained, 0, &quiet, 100000000ull);
+      }
+    }
+    __syncwarp();
+  } else {
+    const int quarter = warp & 3;  // the TMEM lanes this warp may read
+    int turn = 0;
+    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, ++turn) {
+      const int m0 = tile % tilesM * kBM, n0 = tile / tilesM * BN;
+      const int acc = turn & 1, use = turn >> 1;
+      bool ok = lane != 0 || waitBar(&accFull[acc], use & 1, dead);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tcFenceAfter();
+      const int m = m0 + quarter * 32 + lane;
+      for (int c = 0; c < BN; c += 32) {
+        if (n0 + c >= a.N) break;
+        uint32_t raw[32];
+        tcLoad32(tmem + ((uint32_t)(quarter * 32) << 16) + acc * BN + c, raw);
+        float f[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(raw[i]);
+        if (m < a.M) {
+          if (a.bias) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (n0 + c + i < a.N) f[i] += loadOne<DT>(a.bias, n0 + c + i);
+          }
+          switch (a.act) {
+            case vrcclActRelu: finish<DT, vrcclActRelu>(a, f, m, n0 + c); break;
+            case vrcclActGelu: finish<DT, vrcclActGelu>(a, f, m, n0 + c); break;
+            case vrcclActGeluTanh: finish<DT, vrcclActGeluTanh>(a, f, m, n0 + c); break;
+            case vrcclActSilu: finish<DT, vrcclActSilu>(a, f, m, n0 + c); break;
+            default: finish<DT, vrcclActNone>(a, f, m, n0 + c); break;
+          }
+        }
+      }
+      tcFenceBefore();
+      __syncwarp();
+      if (lane == 0) mbarArrive(&accEmpty[acc]);
+    }
+  }
+  tcFenceBefore();
+  __syncthreads();
+  tcFenceAfter();
+  if (warp == 1)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(Sh::kTmemCols));
+}
+
+// ------------------------------------------------------------ few rows
+
+constexpr int kFewRows = 8;
+constexpr int kFewOuts = 4;  // outputs a block: x is read once for four rows of W
+constexpr int kFewThreads = 256;
+
+struct FewArgs {
+  const void* x;
+  const void* w;
+  const void* bias;
+  const void* residual;
+  void* y;
+  void* z;
+  size_t ldx, ldw, ldr, ldy, ldz;
+  int rows, outs, ins, act;
+};
+
+__device__ __forceinline__ float activateBy(int act, float z) {
+  switch (act) {
+    case vrcclActRelu: return activate<vrcclActRelu>(z);
+    case vrcclActGelu: return activate<vrcclActGelu>(z);
+    case vrcclActGeluTanh: return activate<vrcclActGeluTanh>(z);
+    case vrcclActSilu: return activate<vrcclActSilu>(z);
+  }
+  return z;
+}
+
+// MR rows of x against four rows of W a block, the contraction dealt to the
+// threads in 16-byte vectors (WIDE) or single elements, joined at the end.
+template <int DT, int MR, bool WIDE>
+__global__ void __launch_bounds__(kFewThreads) linearFew(const __grid_constant__ FewArgs a) {
+  using S = typename Ty<DT>::S;
+  constexpr int V = WIDE ? 8 : 1;
+  __shared__ float part[kFewThreads / 32][kFewOuts * MR];
+  const S* x = static_cast<const S*>(a.x);
+  const S* w = static_cast<const S*>(a.w);
+  const int n0 = blockIdx.x * kFewOuts;
+  float acc[kFewOuts][MR] = {};
+  const int nvec = a.ins / V;
+  for (int i = threadIdx.x; i < nvec; i += kFewThreads) {
+    float wf[kFewOuts][V];
+#pragma unroll
+    for (int o = 0; o < kFewOuts; ++o) {
+      const S* row = w + (size_t)min(n0 + o, a.outs - 1) * a.ldw + (size_t)i * V;
+      if constexpr (WIDE)
+        Vec16<DT>::expand(__ldcs(reinterpret_cast<const uint4*>(row)), wf[o]);
+      else
+        wf[o][0] = Ty<DT>::toF(*row);
+    }
+#pragma unroll
+    for (int m = 0; m < MR; ++m) {
+      float xf[V];
+      const S* row = x + (size_t)min(m, a.rows - 1) * a.ldx + (size_t)i * V;
+      if constexpr (WIDE)
+        Vec16<DT>::expand(__ldg(reinterpret_cast<const uint4*>(row)), xf);
+      else
+        xf[0] = Ty<DT>::toF(*row);
+#pragma unroll
+      for (int o = 0; o < kFewOuts; ++o)
+#pragma unroll
+        for (int e = 0; e < V; ++e) acc[o][m] += wf[o][e] * xf[e];
+    }
+  }
+#pragma unroll
+  for (int o = 0; o < kFewOuts; ++o)
+#pragma unroll
+    for (int m = 0; m < MR; ++m) {
+      const float s = warpSum(acc[o][m]);
+      if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5][o * MR + m] = s;
+    }
+  __syncthreads();
+  if (threadIdx.x < kFewOuts * MR) {
+    const int n = n0 + threadIdx.x / MR, m = threadIdx.x % MR;
+    if (n >= a.outs || m >= a.rows) return;
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < kFewThreads / 32; ++i) s += part[i][threadIdx.x];
+    if (a.bias) s += loadOne<DT>(a.bias, n);
+    if (a.z) static_cast<S*>(a.z)[(size_t)m * a.ldz + n] = Ty<DT>::fromF(s);
+    s = activateBy(a.act, s);
+    if (a.residual) s += loadOne<DT>(a.residual, (size_t)m * a.ldr + n);
+    static_cast<S*>(a.y)[(size_t)m * a.ldy + n] = Ty<DT>::fromF(s);
+  }
+}
+
+// ------------------------------------------------------------ operands and the bias gradient
+
+// A copy whose rows start on 16-byte boundaries, which TMA needs. The ragged
+// end of a row is left as it is: no copy reads past the row's last element.
+__global__ void __launch_bounds__(256) packRows(const unsigned short* src, size_t lds, unsigned short* dst, size_t ldd,
+                                                size_t rows, size_t cols) {
+  for (size_t r = blockIdx.y; r < rows; r += gridDim.y)
+    for (size_t c = (size_t)blockIdx.x * 256 + threadIdx.x; c < cols; c += (size_t)gridDim.x * 256)
+      dst[r * ldd + c] = src[r * lds + c];
+}
+
+struct SlopeArgs {
+  const void* dy;
+  const void* z;
+  void* dz;        // NULL: only the sums
+  float* partial;  // [blocks][cols] or NULL
+  size_t lddy, ldz, lddz, rows;
+  int cols;
+};
+constexpr int kSlopeRows = 8;  // row groups of a block; 32 lanes of V columns across
+
+// dz = dy act'(z), rounded to the element type: the tensor cores take their
+// operands in it. The bias gradient sums the unrounded values.
+template <int DT, int ACT, bool WIDE>
+__global__ void __launch_bounds__(256) linearSlope(const __grid_constant__ SlopeArgs a) {
+  using S = typename Ty<DT>::S;
+  constexpr int V = WIDE ? 8 : 1;
+  __shared__ float part[kSlopeRows][32 * V];
+  const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
+  const int c = (blockIdx.x * 32 + lane) * V;
+  float sum[V] = {};
+  if (c < a.cols) {
+    for (size_t r = (size_t)blockIdx.y * kSlopeRows + g; r < a.rows; r += (size_t)gridDim.y * kSlopeRows) {
+      float d[V], z[V];
+      const S* dy = static_cast<const S*>(a.dy) + r * a.lddy + c;
+      const S* zp = ACT == vrcclActNone ? nullptr : static_cast<const S*>(a.z) + r * a.ldz + c;
+      if constexpr (WIDE)
+        Vec16<DT>::expand(__ldg(reinterpret_cast<const uint4*>(dy)), d);
+      else
+        d[0] = Ty<DT>::toF(*dy);
+      if constexpr (ACT != vrcclActNone) {
+        if constexpr (WIDE)
+          Vec16<DT>::expand(__ldcs(reinterpret_cast<const uint4*>(zp)), z);
+        else
+          z[0] = Ty<DT>::toF(*zp);
+#pragma unroll
+        for (int e = 0; e < V; ++e) d[e] *= slope<ACT>(z[e]);
+      }
+#pragma unroll
+      for (int e = 0; e < V; ++e) sum[e] += d[e];
+      if (a.dz) {
+        S* dz = static_cast<S*>(a.dz) + r * a.lddz + c;
+        if constexpr (WIDE)
+          *reinterpret_cast<uint4*>(dz) = Vec16<DT>::pack(d);
+        else
+          dz[0] = Ty<DT>::fromF(d[0]);
+      }
+    }
+  }
+  if (!a.partial) return;
+#pragma unroll
+  for (int e = 0; e < V; ++e) part[g][lane * V + e] = sum[e];
+  __syncthreads();
+  for (int i = threadIdx.x; i < 32 * V; i += 256) {
+    const int col = blockIdx.x * 32 * V + i;
+    if (col >= a.cols) continue;
+    float s = 0.f;
+#pragma unroll
+    for (int k = 0; k < kSlopeRows; ++k) s += part[k][i];
+    a.partial[(size_t)blockIdx.y * a.cols + col] = s;
+  }
+}
+
+template <int DT>
+__global__ void __launch_bounds__(256) linearBiasJoin(const float* partial, int blocks, int cols, void* db) {
+  __shared__ float part[8][32];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
+  float s = 0.f;
+  if (c < cols)
+    for (int b = w; b < blocks; b += 8) s += partial[(size_t)b * cols + c];
+  part[w][lane] = s;
+  __syncthreads();
+  if (w == 0 && c < cols) {
+#pragma unroll
+    for (int i = 1; i < 8; ++i) s += part[i][lane];
+    static_cast<typename Ty<DT>::S*>(db)[c] = Ty<DT>::fromF(s);
+  }
+}
+
+// ------------------------------------------------------------ host
+
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeFn encodeFn() {
+  static const EncodeFn fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess) {
+      cudaGetLastError();
+      p = nullptr;
+    }
+    return (EncodeFn)p;
+  }();
+  return fn;
+}
+
+// Tiles of 64 x boxRows out of a [rows, cols] matrix of 2-byte elements whose
+// rows start on 16-byte boundaries; what lies outside reads as zero.
+bool makeMap(CUtensorMap* map, int dtype, const void* p, size_t ld, size_t rows, size_t cols, int boxRows) {
+  const EncodeFn fn = encodeFn();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {cols, rows}, strides[1] = {ld * 2};
+  const cuuint32_t box[2] = {64, (cuuint32_t)boxRows}, step[2] = {1, 1};
+  return fn(map, dtype == vrcclBfloat16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+            const_cast<void*>(p), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct Operand {
+  const void* p;
+  size_t ld, rows, cols;  // as it lies in memory
+  bool mn;                // the contraction runs over its rows
+};
+
+size_t packedLd(size_t cols) { return (cols + 7) / 8 * 8; }
+size_t packedBytes(size_t rows, size_t cols) { return (rows * packedLd(cols) * 2 + 255) / 256 * 256; }
+
+// Hands out the workspace in order.
+struct Scratch {
+  unsigned char* p;
+  size_t left;
+  void* take(size_t bytes) {
+    if (!p || bytes > left) return nullptr;
+    void* r = p;
+    p += bytes;
+    left -= bytes;
+    return r;
+  }
+};
+
+// Workspace that aligned() takes for an operand.
+size_t packNeed(const void* p, size_t ld, size_t rows, size_t cols) {
+  return rowsAligned(p, ld, 2) ? 0 : packedBytes(rows, cols);
+}
+// The operand with its rows on 16-byte boundaries, copied where they are not.
+bool aligned(Operand& o, Scratch& ws, cudaStream_t st) {
+  if (rowsAligned(o.p, o.ld, 2)) return true;
+  unsigned short* q = static_cast<unsigned short*>(ws.take(packedBytes(o.rows, o.cols)));
+  if (!q) return false;
+  const size_t ld = packedLd(o.cols);
+  const dim3 grid((unsigned)std::min<size_t>((o.cols + 255) / 256, 64), (unsigned)std::min<size_t>(o.rows, 4096));
+  packRows<<<grid, 256, 0, st>>>(static_cast<const unsigned short*>(o.p), o.ld, q, ld, o.rows, o.cols);
+  o.p = q;
+  o.ld = ld;
+  return true;
+}
+
+template <int DT, int BN>
+vrcclResult_t launchProduct(ProductArgs& a, const Operand& A, const Operand& B, cudaStream_t st) {
+  using Sh = ProductShape<BN>;
+  if (!makeMap(&a.a, DT, A.p, A.ld, A.rows, A.cols, A.mn ? kBK : kBM) ||
+      !makeMap(&a.b, DT, B.p, B.ld, B.rows, B.cols, B.mn ? kBK : BN))
+    return vrcclInternalError;
+  static bool raised[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return vrcclCudaError;
+  if (!raised[dev]) {
+    if (cudaFuncSetAttribute(productKernel<DT, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem) !=
+        cudaSuccess) {
+      cudaGetLastError();
+      return vrcclCudaError;
+    }
+    raised[dev] = true;
+  }
+  const long long tiles = (long long)((a.M + kBM - 1) / kBM) * ((a.N + BN - 1) / BN);
+  const int grid = (int)std::min<long long>(tiles, smCount());
+  productKernel<DT, BN><<<grid, kProductThreads, Sh::kSmem, st>>>(a);
+  return launchResult();
+}
+
+// D = A B^T with the epilogue of `a`.
+template <int DT>
+vrcclResult_t product(ProductArgs& a, const Operand& A, const Operand& B, cudaStream_t st) {
+  a.aMN = A.mn;
+  a.bMN = B.mn;
+  a.wideD = rowsAligned(a.d, a.ldd, 2);
+  a.wideZ = a.z && rowsAligned(a.z, a.ldz, 2);
+  a.wideR = a.residual && rowsAligned(a.residual, a.ldr, 2);
+  const long long tm = (a.M + kBM - 1) / kBM;
+  auto tiles = [&](int bn) { return tm * ((a.N + bn - 1) / bn); };
+  if (tiles(256) >= smCount()) return launchProduct<DT, 256>(a, A, B, st);
+  if (tiles(128) >= smCount()) return launchProduct<DT, 128>(a, A, B, st);
+  return launchProduct<DT, 64>(a, A, B, st);
+}
+
+template <int DT, int MR>
+void launchFew(const FewArgs& a, bool wide, cudaStream_t st) {
+  const unsigned grid = (unsigned)((a.outs + kFewOuts - 1) / kFewOuts);
+  if (wide)
+    linearFew<DT, MR, true><<<grid, kFewThreads, 0, st>>>(a);
+  else
+    linearFew<DT, MR, false><<<grid, kFewThreads, 0, st>>>(a);
+}
+template <int DT>
+vrcclResult_t few(const FewArgs& a, bool wide, cudaStream_t st) {
+  if (a.rows == 1)
+    launchFew<DT, 1>(a, wide, st);
+  else if (a.rows == 2)
+    launchFew<DT, 2>(a, wide, st);
+  else if (a.rows <= 4)
+    launchFew<DT, 4>(a, wide, st);
+  else
+    launchFew<DT, 8>(a, wide, st);
+  return launchResult();
+}
+
+// Row blocks of linearSlope: enough for two waves of blocks.
+int slopeBlocks(size_t rows, size_t cols) {
+  const size_t across = (cols + 255) / 256;
+  const size_t want = std::max<size_t>(1, (size_t)smCount() * 8 / across);
+  return (int)std::min<size_t>(want, (rows + kSlopeRows - 1) / kSlopeRows);
+}
+
+// Workspace of the bias gradient's partial sums.
+size_t biasBytes(size_t rows, size_t outs) { return (size_t(slopeBlocks(rows, outs)) * outs * 4 + 255) / 256 * 256; }
+
+template <int DT, bool WIDE>
+void launchSlope(int act, dim3 grid, const SlopeArgs& a, cudaStream_t st) {
+  switch (act) {
+    case vrcclActRelu: linearSlope<DT, vrcclActRelu, WIDE><<<grid, 256, 0, st>>>(a); break;
+    case vrcclActGelu: linearSlope<DT, vrcclActGelu, WIDE><<<grid, 256, 0, st>>>(a); break;
+    case vrcclActGeluTanh: linearSlope<DT, vrcclActGeluTanh, WIDE><<<grid, 256, 0, st>>>(a); break;
+    case vrcclActSilu: linearSlope<DT, vrcclActSilu, WIDE><<<grid, 256, 0, st>>>(a); break;
+    default: linearSlope<DT, vrcclActNone, WIDE><<<grid, 256, 0, st>>>(a); break;
+  }
+}
+
+bool goodLinear(size_t rows, size_t outs, size_t ins, int dtype, int act) {
+  const size_t most = (size_t(1) << 31) - 65536;
+  return rows < most && outs < most && ins < most && isOperatorType(dtype) && (unsigned)act < (unsigned)vrcclNumActs;
+}
+
+template <int DT>
+vrcclResult_t backward(const void* dy, size_t lddy, const void* z, size_t ldz, const void* x, size_t ldx, const void* w,
+                       size_t ldw, void* dx, size_t lddx, void* dw, size_t lddw, void* dbias, size_t rows, size_t outs,
+                       size_t ins, int act, Scratch ws, cudaStream_t st) {
+  Operand g = {dy, lddy, rows, outs, false};
+  const bool rewrite = act != vrcclActNone && (dx || dw);
+  if (rewrite || dbias) {
+    SlopeArgs s = {};
+    s.dy = dy;
+    s.z = z;
+    s.lddy = lddy;
+    s.ldz = ldz;
+    s.rows = rows;
+    s.cols = (int)outs;
+    if (rewrite) {
+      s.lddz = packedLd(outs);
+      if (!(s.dz = ws.take(packedBytes(rows, outs)))) return vrcclInvalidArgument;
+      g.p = s.dz;
+      g.ld = s.lddz;
+    }
+    const int blocks = slopeBlocks(rows, outs);
+    if (dbias && !(s.partial = static_cast<float*>(ws.take(biasBytes(rows, outs)))))
+      return vrcclInvalidArgument;
+    const bool wide = outs % 8 == 0 && rowsAligned(dy, lddy, 2) && (act == vrcclActNone || rowsAligned(z, ldz, 2));
+    const int across = wide ? 256 : 32;
+    const dim3 grid((unsigned)((outs + across - 1) / across), (unsigned)blocks);
+    if (wide)
+      launchSlope<DT, true>(act, grid, s, st);
+    else
+      launchSlope<DT, false>(act, grid, s, st);
+    if (dbias)
+      linearBiasJoin<DT><<<(unsigned)((outs + 31) / 32), 256, 0, st>>>(s.partial, blocks, (int)outs, dbias);
+  }
+  if ((dx || dw) && !aligned(g, ws, st)) return vrcclInvalidArgument;
+  if (dx) {
+    Operand b = {w, ldw, outs, ins, true};
+    if (!aligned(b, ws, st)) return vrcclInvalidArgument;
+    ProductArgs a = {};
+    a.d = dx;
+    a.ldd = lddx;
+    a.M = (int)rows;
+    a.N = (int)ins;
+    a.K = (int)outs;
+    const vrcclResult_t r = product<DT>(a, g, b, st);
+    if (r != vrcclSuccess) return r;
+  }
+  if (dw) {
+    Operand b = {x, ldx, rows, ins, true};
+    if (!aligned(b, ws, st)) return vrcclInvalidArgument;
+    g.mn = true;
+    ProductArgs a = {};
+    a.d = dw;
+    a.ldd = lddw;
+    a.M = (int)outs;
+    a.N = (int)ins;
+    a.K = (int)rows;
+    const vrcclResult_t r = product<DT>(a, g, b, st);
+    if (r != vrcclSuccess) return r;
+  }
+  return launchResult();
+}
+
+vrcclResult_t zeroRows(void* p, size_t ld, size_t rows, size_t cols, cudaStream_t st) {
+  if (cudaMemset2DAsync(p, ld * 2, 0, cols * 2, rows, st) != cudaSuccess) {
+    cudaGetLastError();
+    return vrcclCudaError;
+  }
+  return vrcclSuccess;
+}
+
+}  // namespace
+}  // namespace vrccl
+
+using namespace vrccl;
+
+extern "C" vrcclResult_t vrcclLinearWorkspace(int backward, size_t rows, size_t outs, size_t ins, vrcclDataType_t dtype,
+                                              vrcclActivation_t act, size_t* bytes) {
+  if (!bytes || !goodLinear(rows, outs, ins, dtype, act)) return vrcclInvalidArgument;
+  if (dtype == vrcclFloat32) return vrcclInvalidUsage;
+  *bytes = packedBytes(rows, ins) + packedBytes(outs, ins);
+  if (backward) *bytes += packedBytes(rows, outs) + biasBytes(rows, outs);
+  return vrcclSuccess;
+}
+
+extern "C" vrcclResult_t vrcclLinearForward(const void* x, size_t ldx, const void* w, size_t ldw, const void* bias,
+                                            const void* residual, size_t ldr, void* y, size_t ldy, void* z, size_t ldz,
+                                            size_t rows, size_t outs, size_t ins, vrcclDataType_t dtype,
+                                            vrcclActivation_t act, void* workspace, size_t workspaceBytes,
+                                            vrcclStream_t stream) {
+  if (!goodLinear(rows, outs, ins, dtype, act)) return vrcclInvalidArgument;
+  if (dtype == vrcclFloat32) return vrcclInvalidUsage;
+  if (rows == 0 || outs == 0) return vrcclSuccess;
+  if ((ins && (!goodMatrix(x, ldx, ins, 2) || !goodMatrix(w, ldw, ins, 2))) || !goodMatrix(y, ldy, outs, 2) ||
+      (bias && !goodVector(bias, 2)) || (residual && !goodMatrix(residual, ldr, outs, 2)) ||
+      (z && !goodMatrix(z, ldz, outs, 2)) || (workspace && !goodVector(workspace, 256)))
+    return vrcclInvalidArgument;
+  const size_t ySpan = spanBytes(ldy, rows, outs, 2), zSpan = spanBytes(ldz, rows, outs, 2);
+  const size_t xSpan = spanBytes(ldx, rows, ins, 2), wSpan = spanBytes(ldw, outs, ins, 2);
+  if (overlap(y, ySpan, x, xSpan) || overlap(y, ySpan, w, wSpan) || overlap(z, zSpan, x, xSpan) ||
+      overlap(z, zSpan, w, wSpan) || overlap(z, zSpan, y, ySpan) || overlap(z, zSpan, residual, spanBytes(ldr, rows, outs, 2)) ||
+      overlap(y, ySpan, bias, outs * 2) || overlap(z, zSpan, bias, outs * 2) ||
+      (!(residual == y && ldr == ldy) && overlap(y, ySpan, residual, spanBytes(ldr, rows, outs, 2))))
+    return vrcclInvalidArgument;
+  cudaStream_t st = (cudaStream_t)stream;
+  if (rows <= kFewRows || ins == 0) {
+    // ins == 0 is a sum over nothing: the epilogue of zeros, eight rows a call
+    const bool wide = ins % 8 == 0 && rowsAligned(x, ldx, 2) && rowsAligned(w, ldw, 2);
+    for (size_t r = 0; r < rows; r += kFewRows) {
+      FewArgs a = {};
+      a.x = static_cast<const char*>(x) + r * ldx * 2 * (ins != 0);
+      a.w = w;
+      a.bias = bias;
+      a.residual = residual ? static_cast<const char*>(residual) + r * ldr * 2 : nullptr;
+      a.y = static_cast<char*>(y) + r * ldy * 2;
+      a.z = z ? static_cast<char*>(z) + r * ldz * 2 : nullptr;
+      a.ldx = ldx;
+      a.ldw = ldw;
+      a.ldr = ldr;
+      a.ldy = ldy;
+      a.ldz = ldz;
+      a.rows = (int)std::min<size_t>(kFewRows, rows - r);
+      a.outs = (int)outs;
+      a.ins = (int)ins;
+      a.act = act;
+      const vrcclResult_t res =
+          dtype == vrcclBfloat16 ? few<vrcclBfloat16>(a, wide, st) : few<vrcclFloat16>(a, wide, st);
+      if (res != vrcclSuccess) return res;
+    }
+    return vrcclSuccess;
+  }
+  const size_t need = packNeed(x, ldx, rows, ins) + packNeed(w, ldw, outs, ins);
+  if (need && (!workspace || workspaceBytes < need)) return vrcclInvalidArgument;
+  Scratch ws = {static_cast<unsigned char*>(workspace), workspaceBytes};
+  Operand A = {x, ldx, rows, ins, false}, B = {w, ldw, outs, ins, false};
+  if (!aligned(A, ws, st) || !aligned(B, ws, st)) return vrcclInvalidArgument;
+  ProductArgs a = {};
+  a.d = y;
+  a.z = z;
+  a.bias = bias;
+  a.residual = residual;
+  a.ldd = ldy;
+  a.ldz = ldz;
+  a.ldr = ldr;
+  a.M = (int)rows;
+  a.N = (int)outs;
+  a.K = (int)ins;
+  a.act = act;
+  return dtype == vrcclBfloat16 ? product<vrcclBfloat16>(a, A, B, st) : product<vrcclFloat16>(a, A, B, st);
+}
+
+extern "C" vrcclResult_t vrcclLinearBackward(const void* dy, size_t lddy, const void* z, size_t ldz, const void* x,
+                                             size_t ldx, const void* w, size_t ldw, void* dx, size_t lddx, void* dw,
+                                             size_t lddw, void* dbias, size_t rows, size_t outs, size_t ins,
+                                             vrcclDataType_t dtype, vrcclActivation_t act, void* workspace,
+                                             size_t workspaceBytes, vrcclStream_t stream) {
+  if (!goodLinear(rows, outs, ins, dtype, act)) return vrcclInvalidArgument;
+  if (dtype == vrcclFloat32) return vrcclInvalidUsage;
+  const bool acts = act != vrcclActNone;
+  if ((dx && !goodMatrix(dx, lddx, ins, 2)) || (dw && !goodMatrix(dw, lddw, ins, 2)) || (dbias && !goodVector(dbias, 2)) ||
+      (workspace && !goodVector(workspace, 256)))
+    return vrcclInvalidArgument;
+  cudaStream_t st = (cudaStream_t)stream;
+  // a sum over no rows, or over no outputs, is zero
+  if (rows == 0 || outs == 0 || ins == 0) {
+    vrcclResult_t r = vrcclSuccess;
+    if (dx && rows && ins) r = zeroRows(dx, lddx, rows, ins, st);
+    if (r == vrcclSuccess && dw && outs && ins) r = zeroRows(dw, lddw, outs, ins, st);
+    if (r != vrcclSuccess || !dbias || !outs) return r;
+    if (rows == 0) return zeroRows(dbias, outs, 1, outs, st);
+    dx = dw = nullptr;  // ins == 0: the bias gradient is all there is
+  }
+  const size_t gSpan = spanBytes(lddy, rows, outs, 2), zSpan = spanBytes(ldz, rows, outs, 2);
+  const size_t xSpan = spanBytes(ldx, rows, ins, 2), wSpan = spanBytes(ldw, outs, ins, 2);
+  if (!goodMatrix(dy, lddy, outs, 2) || (acts && !goodMatrix(z, ldz, outs, 2)) || (dw && !goodMatrix(x, ldx, ins, 2)) ||
+      (dx && !goodMatrix(w, ldw, ins, 2)))
+    return vrcclInvalidArgument;
+  struct {
+    void* p;
+    size_t n;
+  } out[3] = {{dx, spanBytes(lddx, rows, ins, 2)}, {dw, spanBytes(lddw, outs, ins, 2)}, {dbias, outs * 2}};
+  for (int i = 0; i < 3; ++i) {
+    if (overlap(out[i].p, out[i].n, dy, gSpan) || (acts && overlap(out[i].p, out[i].n, z, zSpan)) ||
+        overlap(out[i].p, out[i].n, x, xSpan) || overlap(out[i].p, out[i].n, w, wSpan))
+      return vrcclInvalidArgument;
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i].p, out[i].n, out[j].p, out[j].n)) return vrcclInvalidArgument;
+  }
+  size_t need = dbias ? biasBytes(rows, outs) : 0;
+  if (dx || dw) need += acts ? packedBytes(rows, outs) : packNeed(dy, lddy, rows, outs);
+  if (dx) need += packNeed(w, ldw, outs, ins);
+  if (dw) need += packNeed(x, ldx, rows, ins);
+  if (need && (!workspace || workspaceBytes < need)) return vrcclInvalidArgument;
+  Scratch ws = {static_cast<unsigned char*>(workspace), workspaceBytes};
+  return dtype == vrcclBfloat16 ? backward<vrcclBfloat16>(dy, lddy, z, ldz, x, ldx, w, ldw, dx, lddx, dw, lddw, dbias,
+                                                          rows, outs, ins, act, ws, st)
+                                : backward<vrcclFloat16>(dy, lddy, z, ldz, x, ldx, w, ldw, dx, lddx, dw, lddw, dbias,
+                                                         rows, outs, ins, act, ws, st);
+}
+
+extern "C" vrcclResult_t vrcclLinearGetAsyncError(vrcclResult_t* asyncErr) {
+  if (!asyncErr) return vrcclInvalidArgument;
+  int code = 0;
+  if (cudaMemcpyFromSymbol(&code, gLinearStatus, sizeof(code)) != cudaSuccess) {
+    cudaGetLastError();
+    return vrcclCudaError;
+  }
+  *asyncErr = (vrcclResult_t)code;
+  return vrcclSuccess;
+}

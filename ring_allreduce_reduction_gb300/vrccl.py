@@ -31,15 +31,18 @@ PROTOS = {"simple": 0, "ll": 1, "ll128": 2, "auto": 3}
 ALGO_NAMES = {v: k for k, v in ALGOS.items()}
 PROTO_NAMES = {v: k for k, v in PROTOS.items()}
 ELEM_SIZE = {"int32": 4, "float32": 4, "bfloat16": 2, "float16": 2, "int8": 1, "uint8": 1, "int64": 8, "float64": 8}
+ACTS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 MAX_RANKS = 128
 MAX_CHANNELS = 64
 STEPS = 16
+DISTILL_MAX_K = 1024
 
 _TORCH_DTYPES = {torch.int32: "int32", torch.float32: "float32", torch.bfloat16: "bfloat16",
                  torch.float16: "float16", torch.int8: "int8", torch.uint8: "uint8", torch.int64: "int64",
                  torch.float64: "float64"}
 
 _c_int_p = ctypes.POINTER(ctypes.c_int)
+_p, _z, _i, _f = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.c_float
 _sig = {
     "vrcclCommInit": [ctypes.POINTER(ctypes.c_void_p), ctypes.c_int, ctypes.c_int],
     "vrcclAllReduce": [ctypes.POINTER(ctypes.c_void_p), ctypes.POINTER(ctypes.c_void_p), ctypes.c_size_t,
@@ -72,11 +75,20 @@ _sig = {
                         ctypes.POINTER(ctypes.c_size_t)],
     "vrcclAllReduceNoAlloc": [ctypes.POINTER(ctypes.c_void_p), ctypes.POINTER(ctypes.c_void_p), ctypes.c_size_t,
                               ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_void_p],
+    "vrcclLayerNormForward": [_p, _z, _p, _p, _p, _z, _p, _p, _z, _z, _i, _i, _f, _p],
+    "vrcclLayerNormWorkspace": [_z, _z, ctypes.POINTER(_z)],
+    "vrcclLayerNormBackward": [_p, _z, _p, _z, _p, _p, _p, _p, _z, _p, _p, _z, _z, _i, _i, _p, _z, _p],
+    "vrcclLinearWorkspace": [_i, _z, _z, _z, _i, _i, ctypes.POINTER(_z)],
+    "vrcclLinearForward": [_p, _z, _p, _z, _p, _p, _z, _p, _z, _p, _z, _z, _z, _z, _i, _i, _p, _z, _p],
+    "vrcclLinearBackward": [_p, _z, _p, _z, _p, _z, _p, _z, _p, _z, _p, _z, _p, _z, _z, _z, _i, _i, _p, _z, _p],
+    "vrcclLinearGetAsyncError": [_c_int_p],
+    "vrcclDistillForward": [_p, _z, _p, _z, _p, _z, _p, _p, _z, _z, _z, _i, _i, _i, _f, _p],
+    "vrcclDistillBackward": [_p, _z, _p, _z, _p, _z, _p, _p, _z, _p, _z, _z, _z, _z, _i, _i, _i, _f, _p],
 }
 for _name, _args in _sig.items():
-    _f = getattr(_lib, _name)
-    _f.argtypes = _args
-    _f.restype = ctypes.c_int
+    _fn = getattr(_lib, _name)
+    _fn.argtypes = _args
+    _fn.restype = ctypes.c_int
 _lib.vrcclGetErrorString.argtypes = [ctypes.c_int]
 _lib.vrcclGetErrorString.restype = ctypes.c_char_p
 
@@ -282,6 +294,97 @@ def vrcclCommLoadTuning(comm, path: str) -> int:
     k = ctypes.c_int()
     _check(_lib.vrcclCommLoadTuning(comm, path.encode(), ctypes.byref(k)), "vrcclCommLoadTuning")
     return k.value
+
+
+# ------------------------------------------------------------ operators of a replica
+# Matrices default to rows without gaps (ld = the row's length); a buffer may
+# be None where include/vrccl.h allows NULL.
+
+def _opt(x) -> int | None:
+    return None if x is None else x.data_ptr() if isinstance(x, torch.Tensor) else int(x)
+
+
+def vrcclLayerNormForward(x, gamma, beta, y, mean, rstd, rows: int, cols: int, dtype, ptype, eps: float = 1e-5,
+                          ldx: int | None = None, ldy: int | None = None, stream=None) -> None:
+    _check(_lib.vrcclLayerNormForward(_opt(x), cols if ldx is None else ldx, _opt(gamma), _opt(beta), _opt(y),
+                                      cols if ldy is None else ldy, _opt(mean), _opt(rstd), rows, cols,
+                                      _enum(DTYPES, dtype, "dtype"), _enum(DTYPES, ptype, "dtype"), eps,
+                                      _stream(stream)), "vrcclLayerNormForward")
+
+
+def vrcclLayerNormWorkspace(rows: int, cols: int) -> int:
+    n = ctypes.c_size_t()
+    _check(_lib.vrcclLayerNormWorkspace(rows, cols, ctypes.byref(n)), "vrcclLayerNormWorkspace")
+    return n.value
+
+
+def vrcclLayerNormBackward(dy, x, gamma, mean, rstd, dx, dgamma, dbeta, rows: int, cols: int, dtype, ptype,
+                           workspace=None, workspace_bytes: int = 0, lddy: int | None = None, ldx: int | None = None,
+                           lddx: int | None = None, stream=None) -> None:
+    _check(_lib.vrcclLayerNormBackward(_opt(dy), cols if lddy is None else lddy, _opt(x),
+                                       cols if ldx is None else ldx, _opt(gamma), _opt(mean), _opt(rstd), _opt(dx),
+                                       cols if lddx is None else lddx, _opt(dgamma), _opt(dbeta), rows, cols,
+                                       _enum(DTYPES, dtype, "dtype"), _enum(DTYPES, ptype, "dtype"), _opt(workspace),
+                                       workspace_bytes, _stream(stream)), "vrcclLayerNormBackward")
+
+
+def vrcclLinearWorkspace(direction: str, rows: int, outs: int, ins: int, dtype, act="none") -> int:
+    """Bytes for direction "forward" or "backward" (see include/vrccl.h)."""
+    n = ctypes.c_size_t()
+    _check(_lib.vrcclLinearWorkspace({"forward": 0, "backward": 1}[direction], rows, outs, ins,
+                                     _enum(DTYPES, dtype, "dtype"), _enum(ACTS, act, "activation"),
+                                     ctypes.byref(n)), "vrcclLinearWorkspace")
+    return n.value
+
+
+def vrcclLinearForward(x, w, bias, residual, y, z, rows: int, outs: int, ins: int, dtype, act="none", workspace=None,
+                       workspace_bytes: int = 0, ldx: int | None = None, ldw: int | None = None,
+                       ldr: int | None = None, ldy: int | None = None, ldz: int | None = None, stream=None) -> None:
+    _check(_lib.vrcclLinearForward(_opt(x), ins if ldx is None else ldx, _opt(w), ins if ldw is None else ldw,
+                                   _opt(bias), _opt(residual), outs if ldr is None else ldr, _opt(y),
+                                   outs if ldy is None else ldy, _opt(z), outs if ldz is None else ldz, rows, outs,
+                                   ins, _enum(DTYPES, dtype, "dtype"), _enum(ACTS, act, "activation"),
+                                   _opt(workspace), workspace_bytes, _stream(stream)), "vrcclLinearForward")
+
+
+def vrcclLinearBackward(dy, z, x, w, dx, dw, dbias, rows: int, outs: int, ins: int, dtype, act="none",
+                        workspace=None, workspace_bytes: int = 0, lddy: int | None = None, ldz: int | None = None,
+                        ldx: int | None = None, ldw: int | None = None, lddx: int | None = None,
+                        lddw: int | None = None, stream=None) -> None:
+    _check(_lib.vrcclLinearBackward(_opt(dy), outs if lddy is None else lddy, _opt(z), outs if ldz is None else ldz,
+                                    _opt(x), ins if ldx is None else ldx, _opt(w), ins if ldw is None else ldw,
+                                    _opt(dx), ins if lddx is None else lddx, _opt(dw), ins if lddw is None else lddw,
+                                    _opt(dbias), rows, outs, ins, _enum(DTYPES, dtype, "dtype"),
+                                    _enum(ACTS, act, "activation"), _opt(workspace), workspace_bytes,
+                                    _stream(stream)), "vrcclLinearBackward")
+
+
+def vrcclLinearGetAsyncError() -> int:
+    e = ctypes.c_int()
+    _check(_lib.vrcclLinearGetAsyncError(ctypes.byref(e)), "vrcclLinearGetAsyncError")
+    return e.value
+
+
+def vrcclDistillForward(logits, teacher, index, loss, stats, rows: int, vocab: int, k: int, dtype, teacher_dtype,
+                        index_dtype, temperature: float = 1.0, ldl: int | None = None, ldt: int | None = None,
+                        ldi: int | None = None, stream=None) -> None:
+    _check(_lib.vrcclDistillForward(_opt(logits), vocab if ldl is None else ldl, _opt(teacher),
+                                    k if ldt is None else ldt, _opt(index), k if ldi is None else ldi, _opt(loss),
+                                    _opt(stats), rows, vocab, k, _enum(DTYPES, dtype, "dtype"),
+                                    _enum(DTYPES, teacher_dtype, "dtype"), _enum(DTYPES, index_dtype, "dtype"),
+                                    temperature, _stream(stream)), "vrcclDistillForward")
+
+
+def vrcclDistillBackward(logits, teacher, index, stats, dloss, dlogits, rows: int, vocab: int, k: int, dtype,
+                         teacher_dtype, index_dtype, temperature: float = 1.0, dloss_stride: int = 1,
+                         ldl: int | None = None, ldt: int | None = None, ldi: int | None = None,
+                         ldd: int | None = None, stream=None) -> None:
+    _check(_lib.vrcclDistillBackward(_opt(logits), vocab if ldl is None else ldl, _opt(teacher),
+                                     k if ldt is None else ldt, _opt(index), k if ldi is None else ldi, _opt(stats),
+                                     _opt(dloss), dloss_stride, _opt(dlogits), vocab if ldd is None else ldd, rows,
+                                     vocab, k, _enum(DTYPES, dtype, "dtype"), _enum(DTYPES, teacher_dtype, "dtype"),
+                                     _enum(DTYPES, index_dtype, "dtype"), temperature, _stream(stream)),
+           "vrcclDistillBackward")
 
 
 def raw_call(name: str, *args) -> int:
