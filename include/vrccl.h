@@ -633,10 +633,10 @@ vrcclResult_t vrcclLinearBackward(const void* dy, size_t lddy, const void* z, si
                                   size_t rows, size_t outs, size_t ins, vrcclDataType_t dtype, vrcclActivation_t act,
                                   void* workspace, size_t workspaceBytes, vrcclStream_t stream);
 
-/* vrcclLinearGetAsyncError -- vrcclSuccess, or vrcclTimeout after a linear
- * call on the current device whose kernel gave up a wait (its outputs are
+/* vrcclReplicaGetAsyncError -- vrcclSuccess, or vrcclTimeout after an
+ * operator's kernel on the current device gave up a wait (its outputs are
  * then undefined). Waits for the device's work. */
-vrcclResult_t vrcclLinearGetAsyncError(vrcclResult_t* asyncErr);
+vrcclResult_t vrcclReplicaGetAsyncError(vrcclResult_t* asyncErr);
 
 /* Most teacher entries a row of the distillation loss may have. */
 #define VRCCL_DISTILL_MAX_K 1024

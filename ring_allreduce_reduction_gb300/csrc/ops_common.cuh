@@ -41,6 +41,8 @@ inline bool overlap(const void* a, size_t an, const void* b, size_t bn) {
 inline vrcclResult_t launchResult() {
   return cudaGetLastError() == cudaSuccess ? vrcclSuccess : vrcclCudaError;
 }
+// A failed wait of the layer norm's kernels (each translation unit holds its own device-side word).
+int normStatus(int* code);
 // Multiprocessors of the current device (asked for once a device).
 int smCount();
 

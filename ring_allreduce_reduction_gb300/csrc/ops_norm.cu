@@ -34,6 +34,8 @@ struct NormArgs {
   size_t ldx, lddy, ldy, rows;
   int cols;
   int ptype;
+  bool wideParams;  // gamma and beta start on 16-byte boundaries
+  int stages, teams, teamThreads;
   float eps;
 };
 
@@ -76,22 +78,507 @@ struct Held {
   }
 };
 
+// V parameters from column c on; `wide`: one 16- or 8-byte load a group, which
+// the caller allows where the parameters start on a 16-byte boundary.
 template <int V>
-__device__ __forceinline__ void loadParams(const void* p, int ptype, int c, float dflt, float (&f)[V]) {
+__device__ __forceinline__ void loadParams(const void* p, int ptype, bool wide, int c, float dflt, float (&f)[V]) {
+  if (!p) {
 #pragma unroll
-  for (int e = 0; e < V; ++e) f[e] = p ? loadParam(p, ptype, c + e) : dflt;
+    for (int e = 0; e < V; ++e) f[e] = dflt;
+    return;
+  }
+  if constexpr (V >= 4) {
+    if (wide && ptype == vrcclFloat32) {
+#pragma unroll
+      for (int e = 0; e < V; e += 4) {
+        const float4 q = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + c + e));
+        f[e] = q.x, f[e + 1] = q.y, f[e + 2] = q.z, f[e + 3] = q.w;
+      }
+      return;
+    }
+    if (wide) {
+#pragma unroll
+      for (int e = 0; e < V; e += 4) {
+        const uint2 q = __ldg(reinterpret_cast<const uint2*>(static_cast<const unsigned short*>(p) + c + e));
+        const float2 lo = ptype == vrcclBfloat16 ? unpack2<vrcclBfloat16>(q.x) : unpack2<vrcclFloat16>(q.x);
+        const float2 hi = ptype == vrcclBfloat16 ? unpack2<vrcclBfloat16>(q.y) : unpack2<vrcclFloat16>(q.y);
+        f[e] = lo.x, f[e + 1] = lo.y, f[e + 2] = hi.x, f[e + 3] = hi.y;
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < V; ++e) f[e] = loadParam(p, ptype, c + e);
 }
 
-// One row a block, or one row a warp (WARP) where 32 lanes hold it.
-template <int DT, bool VEC, int EPT, bool WARP>
+// ------------------------------------------------------------ teams
+// Rows of up to 8192 elements. A block of up to 512 threads is cut into teams
+// of a few warps, 16 elements of a row a thread; every team walks rows of its
+// own with the grid's stride and keeps its columns' parameters in registers.
+// Rows arrive in shared memory by bulk copies, several rows ahead, so the
+// copies run under the sums and the stores; the barrier inside a row's
+// reduction is also the point where every thread has taken its elements out of
+// the stage, and the team's first thread refills it.
+constexpr int kTeamElems = 16;
+constexpr int kTeamCols = 512 * kTeamElems;
+constexpr int kMaxStages = 8;
+constexpr int kTeamSmem = 192 * 1024;  // of the 227 KB a block may have
+constexpr unsigned long long kRowWaitNs = 2000000000ull;
+
+__device__ int gNormStatus;  // vrcclResult_t of the first device-side failure
+
+// Two binary32 values in one register pair: Blackwell adds and multiplies both
+// in one instruction. Forward is bound by issue slots nearly as much as by
+// memory, and this halves its arithmetic.
+using F2 = unsigned long long;
+__device__ __forceinline__ F2 pair(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 split(F2 a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// Where a row's bytes lie and which of them a bulk copy may take: 16-byte
+// blocks that lie inside the matrix's own bytes, first row's start to last
+// row's end. A row on no 16-byte boundary shares its first and last block with
+// the gap before and after it, which is copied and ignored; the few elements in
+// blocks that the matrix's ends cut are read straight from memory.
+struct Window {
+  uintptr_t row, lo, hi;
+  bool cut;
+};
+__device__ __forceinline__ Window window(const void* p, size_t ld, size_t row, size_t rows, int cols, int E) {
+  Window w;
+  const uintptr_t base = (uintptr_t)p;
+  w.row = base + row * ld * E;
+  const uintptr_t end = w.row + (uintptr_t)cols * E;
+  w.lo = w.row & ~(uintptr_t)15;
+  w.hi = (end + 15) & ~(uintptr_t)15;
+  w.cut = false;
+  if (row == 0 && w.lo < base) {
+    w.lo += 16;
+    w.cut = true;
+  }
+  if (row == rows - 1 && w.hi > end) {
+    w.hi -= 16;
+    w.cut = true;
+  }
+  if (w.hi < w.lo) w.hi = w.lo;
+  return w;
+}
+__host__ __device__ constexpr int slotBytes(int cols, int E) { return ((cols * E + 15) / 16 + 1) * 16; }
+
+// The 16 elements of thread t of a team of T: element q is column
+// ((q / V) T + t) V + q % V, V a whole 16-byte vector (VEC) or 1.
+template <int DT, bool VEC>
+struct Team {
+  static constexpr int E = floatTypeSize(DT), V = VEC ? 16 / E : 1, NV = kTeamElems / V;
+  using S = typename Ty<DT>::S;
+
+  static __device__ __forceinline__ void fetch(unsigned char* slot, const void* p, size_t ld, size_t row, size_t rows,
+                                               int cols, unsigned long long* bar, unsigned long long policy) {
+    if constexpr (VEC) {
+      bulkLoadOnce(slot, static_cast<const char*>(p) + row * ld * E, cols * E, bar, policy);
+      return;
+    }
+    const Window w = window(p, ld, row, rows, cols, E);
+    if (w.hi > w.lo) bulkLoadOnce(slot + (w.lo - (w.row & ~(uintptr_t)15)), (const void*)w.lo, w.hi - w.lo, bar, policy);
+  }
+  static __device__ __forceinline__ unsigned fetchBytes(const void* p, size_t ld, size_t row, size_t rows, int cols) {
+    if constexpr (VEC) return cols * E;
+    const Window w = window(p, ld, row, rows, cols, E);
+    return w.hi - w.lo;
+  }
+  static __device__ __forceinline__ void take(const unsigned char* slot, const void* p, size_t ld, size_t row,
+                                              size_t rows, int cols, int t, int T, float (&f)[kTeamElems]) {
+    if constexpr (VEC) {
+      const uint4* v = reinterpret_cast<const uint4*>(slot);
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int i = j * T + t;
+        float g[V];
+        Vec16<DT>::expand(i * V < cols ? v[i] : make_uint4(0, 0, 0, 0), g);
+#pragma unroll
+        for (int e = 0; e < V; ++e) f[j * V + e] = g[e];
+      }
+    } else {
+      const Window w = window(p, ld, row, rows, cols, E);
+      const S* v = reinterpret_cast<const S*>(slot + (w.row & 15));
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int c = j * T + t;
+        f[j] = 0.f;
+        if (c < cols) {
+          const uintptr_t at = w.row + (uintptr_t)c * E;
+          f[j] = Ty<DT>::toF(w.cut && (at < w.lo || at >= w.hi) ? *(const S*)at : v[c]);
+        }
+      }
+    }
+  }
+  static __device__ __forceinline__ void store(void* row, int cols, int t, int T, const float (&f)[kTeamElems]) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int i = j * T + t;
+      if (i * V >= cols) continue;
+      if constexpr (VEC) {
+        float g[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e) g[e] = f[j * V + e];
+        __stcs(reinterpret_cast<uint4*>(row) + i, Vec16<DT>::pack(g));
+      } else {
+        reinterpret_cast<S*>(row)[i] = Ty<DT>::fromF(f[j]);
+      }
+    }
+  }
+  static __device__ __forceinline__ void params(const void* p, int ptype, bool wide, float dflt, int cols, int t, int T,
+                                                float (&f)[kTeamElems]) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * T + t) * V;
+      float g[V];
+#pragma unroll
+      for (int e = 0; e < V; ++e) g[e] = 0.f;
+      if (c < cols) loadParams<V>(p, ptype, wide, c, dflt, g);
+#pragma unroll
+      for (int e = 0; e < V; ++e) f[j * V + e] = g[e];
+    }
+  }
+  static __device__ __forceinline__ bool held(int q, int cols, int t, int T) { return (q / V * T + t) * V < cols; }
+};
+
+__device__ __forceinline__ void teamSync(int team, int T) {
+  if (T == 32)
+    __syncwarp();
+  else
+    asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(T) : "memory");
+}
+// Sets *dead when the copy has not come after a time in which it must have.
+__device__ __forceinline__ void waitRow(unsigned long long* bar, unsigned parity, int* dead,
+                                        unsigned long long limit = kRowWaitNs) {
+  if (mbarTryWait(bar, parity)) return;
+  const unsigned long long t0 = globalTimer();
+  while (!mbarTryWait(bar, parity))
+    if (globalTimer() - t0 > limit) {
+      *reinterpret_cast<volatile int*>(dead) = 1;
+      return;
+    }
+}
+// Given up with the ring at (stage, round): records it, and lets no copy that
+// is in flight land after the block has gone.
+__device__ __noinline__ void abandon(unsigned long long* full, int stages, int stage, int round, bool first, int* dead) {
+  if (!first) return;
+  atomicCAS(&gNormStatus, 0, (int)vrcclTimeout);
+  for (int s = 0; s < stages; ++s) waitRow(&full[s], (round + (s < stage ? 1 : 0)) & 1, dead, 100000000ull);
+}
+__device__ __forceinline__ void expectBytes(unsigned long long* bar, unsigned bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smemAddr(bar)), "r"(bytes) : "memory");
+}
+
+// Two rows a turn, so that one row's reduction hides the other's latency and
+// one shuffle moves both rows' values (lanes 0-15 end up with row 0's sum,
+// lanes 16-31 with row 1's).
+__device__ __forceinline__ float sumTwo(float a, float b, bool high) {
+  float x = (high ? b : a) + __shfl_xor_sync(0xffffffffu, high ? a : b, 16);
+#pragma unroll
+  for (int o = 8; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+__device__ __forceinline__ float sumHalf(float x) {
+#pragma unroll
+  for (int o = 8; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
+template <int DT, bool VEC>
+__global__ void __launch_bounds__(512) normForwardTeams(const __grid_constant__ NormArgs a) {
+  using M = Team<DT, VEC>;
+  constexpr int E = M::E, NP = kTeamElems / 2;
+  extern __shared__ __align__(128) unsigned char ring[];
+  __shared__ unsigned long long full[16 * kMaxStages];
+  __shared__ float2 red[16][2][2][16];  // team, turn, row, warp: (sum, squares about the warp's mean)
+  __shared__ int deadWord[16];
+  const int T = a.teamThreads, team = threadIdx.x / T, t = threadIdx.x - team * T, lane = t & 31;
+  const int cols = a.cols, stages = a.stages, slot = slotBytes(cols, E), warps = T >> 5;
+  unsigned char* mine = ring + (size_t)team * stages * slot;
+  unsigned long long* bar = full + team * kMaxStages;
+  int* dead = &deadWord[team];
+  const size_t stride = (size_t)gridDim.x * a.teams, first = (size_t)blockIdx.x * a.teams + team;
+  unsigned long long policy = 0;
+  if (t == 0) {
+    for (int s = 0; s < stages; ++s) mbarInit(&bar[s], 1);
+    *dead = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    policy = evictFirstPolicy();
+  }
+  auto refill = [&](int s, size_t row) {
+    if (row >= a.rows) return;
+    expectBytes(&bar[s], M::fetchBytes(a.x, a.ldx, row, a.rows, cols));
+    M::fetch(mine + (size_t)s * slot, a.x, a.ldx, row, a.rows, cols, &bar[s], policy);
+  };
+  if (t == 0)
+    for (int s = 0; s < stages; ++s) refill(s, first + s * stride);
+  F2 g[NP], b[NP];
+  {
+    float p[kTeamElems];
+    M::params(a.gamma, a.ptype, a.wideParams, 1.f, cols, t, T, p);
+#pragma unroll
+    for (int i = 0; i < NP; ++i) g[i] = pair(p[2 * i], p[2 * i + 1]);
+    M::params(a.beta, a.ptype, a.wideParams, 0.f, cols, t, T, p);
+#pragma unroll
+    for (int i = 0; i < NP; ++i) b[i] = pair(p[2 * i], p[2 * i + 1]);
+  }
+  const float inv = 1.f / (float)cols;
+  const bool high = lane >= 16;
+  // elements of warp w of the team: of this thread's own, and of the one its lane joins
+  auto warpCount = [&](int w) {
+    int n = 0;
+    for (int j = 0; j < M::NV; ++j) n += min(32, max(0, (cols + M::V - 1) / M::V - j * T - w * 32)) * M::V;
+    return (float)n;
+  };
+  const float ownCount = warpCount(t >> 5), ownInv = ownCount > 0.f ? 1.f / ownCount : 0.f;
+  const float joinCount = (lane & 15) < warps ? warpCount(lane & 15) : 0.f, joinInv = joinCount > 0.f ? 1.f / joinCount : 0.f;
+  teamSync(team, T);
+  int stage = 0, round = 0, turn = 0;
+  for (size_t row = first; row < a.rows; row += 2 * stride) {
+    const bool two = row + stride < a.rows;
+    float f[2][kTeamElems];
+    waitRow(&bar[stage], round & 1, dead);
+    M::take(mine + (size_t)stage * slot, a.x, a.ldx, row, a.rows, cols, t, T, f[0]);
+    if (two) {
+      waitRow(&bar[stage + 1], round & 1, dead);
+      M::take(mine + (size_t)(stage + 1) * slot, a.x, a.ldx, row + stride, a.rows, cols, t, T, f[1]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kTeamElems; ++i) f[1][i] = 0.f;
+    }
+    F2 x[2][NP];
+    float s[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      F2 acc = 0;
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        x[r][i] = pair(f[r][2 * i], f[r][2 * i + 1]);
+        acc = add2(acc, x[r][i]);
+      }
+      const float2 q = split(acc);
+      s[r] = q.x + q.y;
+    }
+    const float both = sumTwo(s[0], s[1], high);
+    const float m0 = __shfl_sync(0xffffffffu, both, 0) * ownInv, m1 = __shfl_sync(0xffffffffu, both, 16) * ownInv;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const F2 minus = pair(r ? -m1 : -m0, r ? -m1 : -m0);
+      F2 acc = 0;
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        const F2 d = add2(x[r][i], minus);
+        if constexpr (VEC) {
+          if (M::held(2 * i, cols, t, T)) acc = fma2(d, d, acc);
+        } else {
+          const float2 q = split(d);
+          acc = fma2(d, pair(M::held(2 * i, cols, t, T) ? q.x : 0.f, M::held(2 * i + 1, cols, t, T) ? q.y : 0.f), acc);
+        }
+      }
+      const float2 q = split(acc);
+      s[r] = q.x + q.y;
+    }
+    const float squares = sumTwo(s[0], s[1], high);
+    turn ^= 1;
+    if ((lane & 15) == 0) red[team][turn][high][t >> 5] = make_float2(both, squares);
+    teamSync(team, T);
+    if (*reinterpret_cast<volatile int*>(dead)) {
+      abandon(bar, stages, stage, round, t == 0, dead);
+      break;
+    }
+    if (t == 0) {
+      refill(stage, row + stages * stride);
+      refill(stage + 1, row + (stages + 1) * stride);
+    }
+    // squares = sum over warps of squares_w + count_w (mean_w - mean)^2
+    const float2 w = (lane & 15) < warps ? red[team][turn][high][lane & 15] : make_float2(0.f, 0.f);
+    const float mean = sumHalf(w.x) * inv, d = w.x * joinInv - mean;
+    const float rstd = rsqrtf(sumHalf(w.y + joinCount * d * d) * inv + a.eps);
+    if (t == 0 || (t == 16 && two)) {
+      const size_t at = t ? row + stride : row;
+      if (a.mean) a.mean[at] = mean;
+      if (a.rstd) a.rstd[at] = rstd;
+    }
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const float rs = __shfl_sync(0xffffffffu, rstd, r * 16), mn = __shfl_sync(0xffffffffu, mean, r * 16);
+      if (r && !two) break;
+      const F2 scale = pair(rs, rs), shift = pair(-mn, -mn);
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        const float2 q = split(fma2(mul2(add2(x[r][i], shift), scale), g[i], b[i]));
+        f[r][2 * i] = q.x;
+        f[r][2 * i + 1] = q.y;
+      }
+      M::store(static_cast<char*>(a.y) + (row + r * stride) * a.ldy * E, cols, t, T, f[r]);
+    }
+    if ((stage += 2) == stages) {
+      stage = 0;
+      ++round;
+    }
+  }
+}
+
+// Backward: x and dy rows arrive together, a row a turn; the columns' two sums
+// stay in registers to the end, where the block's teams add them up.
+template <int DT, bool VEC>
+__global__ void __launch_bounds__(512) normBackwardTeams(const __grid_constant__ NormArgs a) {
+  using M = Team<DT, VEC>;
+  constexpr int E = M::E, NP = kTeamElems / 2;
+  extern __shared__ __align__(128) unsigned char ring[];
+  __shared__ unsigned long long full[16 * kMaxStages];
+  __shared__ float2 red[16][2][16];
+  __shared__ int deadWord[16];
+  const int T = a.teamThreads, team = threadIdx.x / T, t = threadIdx.x - team * T, lane = t & 31;
+  const int cols = a.cols, stages = a.stages, slot = slotBytes(cols, E), warps = T >> 5;
+  unsigned char* mine = ring + (size_t)team * stages * 2 * slot;
+  unsigned long long* bar = full + team * kMaxStages;
+  int* dead = &deadWord[team];
+  const size_t stride = (size_t)gridDim.x * a.teams, first = (size_t)blockIdx.x * a.teams + team;
+  unsigned long long policy = 0;
+  if (t == 0) {
+    for (int s = 0; s < stages; ++s) mbarInit(&bar[s], 1);
+    *dead = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    policy = evictFirstPolicy();
+  }
+  auto refill = [&](int s, size_t row) {
+    if (row >= a.rows) return;
+    unsigned char* q = mine + (size_t)s * 2 * slot;
+    expectBytes(&bar[s], M::fetchBytes(a.x, a.ldx, row, a.rows, cols) + M::fetchBytes(a.dy, a.lddy, row, a.rows, cols));
+    M::fetch(q, a.x, a.ldx, row, a.rows, cols, &bar[s], policy);
+    M::fetch(q + slot, a.dy, a.lddy, row, a.rows, cols, &bar[s], policy);
+  };
+  if (t == 0)
+    for (int s = 0; s < stages; ++s) refill(s, first + s * stride);
+  F2 g[NP], dg[NP], db[NP];
+  {
+    float p[kTeamElems];
+    M::params(a.gamma, a.ptype, a.wideParams, 1.f, cols, t, T, p);
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      g[i] = pair(p[2 * i], p[2 * i + 1]);
+      dg[i] = db[i] = 0;
+    }
+  }
+  const float inv = 1.f / (float)cols;
+  float nextMean = 0.f, nextRstd = 0.f;
+  if (first < a.rows) {
+    nextMean = a.mean[first];
+    nextRstd = a.rstd[first];
+  }
+  teamSync(team, T);
+  int stage = 0, round = 0, turn = 0;
+  for (size_t row = first; row < a.rows; row += stride) {
+    const float mean = nextMean, rstd = nextRstd;
+    waitRow(&bar[stage], round & 1, dead);
+    const unsigned char* q = mine + (size_t)stage * 2 * slot;
+    F2 xh[NP], gd[NP];
+    float2 s;
+    {
+      float f[kTeamElems];
+      const F2 scale = pair(rstd, rstd), shift = pair(-mean, -mean);
+      M::take(q, a.x, a.ldx, row, a.rows, cols, t, T, f);
+#pragma unroll
+      for (int i = 0; i < NP; ++i) xh[i] = mul2(add2(pair(f[2 * i], f[2 * i + 1]), shift), scale);
+      M::take(q + slot, a.dy, a.lddy, row, a.rows, cols, t, T, f);
+      F2 sg = 0, sx = 0;  // dy is zero in columns that do not exist
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        const F2 d = pair(f[2 * i], f[2 * i + 1]);
+        gd[i] = mul2(d, g[i]);
+        sg = add2(sg, gd[i]);
+        sx = fma2(gd[i], xh[i], sx);
+        dg[i] = fma2(d, xh[i], dg[i]);
+        db[i] = add2(db[i], d);
+      }
+      const float2 u = split(sg), w = split(sx);
+      s = make_float2(u.x + u.y, w.x + w.y);
+    }
+    const float part = sumTwo(s.x, s.y, lane >= 16);
+    turn ^= 1;
+    if ((lane & 15) == 0) reinterpret_cast<float*>(&red[team][turn][t >> 5])[lane >> 4] = part;
+    teamSync(team, T);
+    if (*reinterpret_cast<volatile int*>(dead)) {
+      abandon(bar, stages, stage, round, t == 0, dead);
+      break;
+    }
+    if (t == 0) refill(stage, row + stages * stride);
+    if (row + stride < a.rows) {
+      nextMean = a.mean[row + stride];
+      nextRstd = a.rstd[row + stride];
+    }
+    const float joined = sumHalf((lane & 15) < warps ? reinterpret_cast<float*>(&red[team][turn][lane & 15])[lane >> 4] : 0.f);
+    const float m1 = __shfl_sync(0xffffffffu, joined, 0) * inv, m2 = __shfl_sync(0xffffffffu, joined, 16) * inv;
+    const F2 n1 = pair(-m1, -m1), n2 = pair(-m2, -m2), scale = pair(rstd, rstd);
+    float f[kTeamElems];
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const float2 u = split(mul2(scale, fma2(xh[i], n2, add2(gd[i], n1))));
+      f[2 * i] = u.x;
+      f[2 * i + 1] = u.y;
+    }
+    M::store(static_cast<char*>(a.y) + row * a.ldy * E, cols, t, T, f);
+    if (++stage == stages) {
+      stage = 0;
+      ++round;
+    }
+  }
+  if (!a.partial) return;
+  // the teams own the same columns: every team lays its sums out, and the block adds them in the teams' order
+  float* sum = reinterpret_cast<float*>(ring);
+  __syncthreads();  // no team reads its ring any more
+#pragma unroll
+  for (int i = 0; i < kTeamElems; ++i) {
+    if (!M::held(i, cols, t, T)) continue;
+    float* q = sum + (size_t)team * 2 * cols + (i / M::V * T + t) * M::V + i % M::V;
+    const float2 u = split(dg[i / 2]), v = split(db[i / 2]);
+    q[0] = i & 1 ? u.y : u.x;
+    q[cols] = i & 1 ? v.y : v.x;
+  }
+  __syncthreads();
+  float* p = a.partial + (size_t)blockIdx.x * 2 * cols;
+  for (int c = threadIdx.x; c < 2 * cols; c += blockDim.x) {
+    float x = sum[c];
+    for (int w = 1; w < a.teams; ++w) x += sum[(size_t)w * 2 * cols + c];
+    p[c] = x;
+  }
+}
+
+// ------------------------------------------------------------ a row a block
+// Rows of up to 32768 elements, one a block, EPT elements a thread.
+template <int DT, bool VEC, int EPT>
 __global__ void __launch_bounds__(1024) normForward(const __grid_constant__ NormArgs a) {
   using H = Held<DT, VEC, EPT>;
   constexpr int V = H::V, NV = H::NV, E = floatTypeSize(DT);
   __shared__ float red[2][32];
-  const int T = WARP ? 32 : blockDim.x, t = WARP ? threadIdx.x & 31 : threadIdx.x;
-  const size_t per = WARP ? blockDim.x >> 5 : 1;
+  const int T = blockDim.x, t = threadIdx.x;
   const float inv = 1.f / (float)a.cols;
-  for (size_t row = blockIdx.x * per + (WARP ? threadIdx.x >> 5 : 0); row < a.rows; row += gridDim.x * per) {
+  for (size_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
     H h;
     h.load(static_cast<const char*>(a.x) + row * a.ldx * E, t, T, a.cols);
     float f[V], s = 0.f;
@@ -101,8 +588,7 @@ __global__ void __launch_bounds__(1024) normForward(const __grid_constant__ Norm
 #pragma unroll
       for (int e = 0; e < V; ++e) s += f[e];
     }
-    s = WARP ? warpSum(s) : blockSum(s, red[0]);
-    const float mean = s * inv;
+    const float mean = blockSum(s, red[0]) * inv;
     s = 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -112,8 +598,7 @@ __global__ void __launch_bounds__(1024) normForward(const __grid_constant__ Norm
         for (int e = 0; e < V; ++e) s += (f[e] - mean) * (f[e] - mean);
       }
     }
-    s = WARP ? warpSum(s) : blockSum(s, red[1]);
-    const float rstd = 1.f / sqrtf(s * inv + a.eps);
+    const float rstd = 1.f / sqrtf(blockSum(s, red[1]) * inv + a.eps);
     if (t == 0) {
       if (a.mean) a.mean[row] = mean;
       if (a.rstd) a.rstd[row] = rstd;
@@ -124,8 +609,8 @@ __global__ void __launch_bounds__(1024) normForward(const __grid_constant__ Norm
       const int i = j * T + t;
       if (i * V < a.cols) {
         float g[V], b[V];
-        loadParams<V>(a.gamma, a.ptype, i * V, 1.f, g);
-        loadParams<V>(a.beta, a.ptype, i * V, 0.f, b);
+        loadParams<V>(a.gamma, a.ptype, a.wideParams, i * V, 1.f, g);
+        loadParams<V>(a.beta, a.ptype, a.wideParams, i * V, 0.f, b);
         h.get(j, f);
 #pragma unroll
         for (int e = 0; e < V; ++e) f[e] = (f[e] - mean) * rstd * g[e] + b[e];
@@ -166,19 +651,19 @@ __global__ void __launch_bounds__(1024) normForwardLong(const __grid_constant__ 
   }
 }
 
-template <int DT, bool VEC, int EPT, bool WARP>
-__global__ void __launch_bounds__(WARP ? 128 : 1024) normBackward(const __grid_constant__ NormArgs a) {
+// Rows of up to 16384 elements backward, one a block at a time.
+template <int DT, bool VEC, int EPT>
+__global__ void __launch_bounds__(1024) normBackward(const __grid_constant__ NormArgs a) {
   using H = Held<DT, VEC, EPT>;
   constexpr int V = H::V, NV = H::NV, E = floatTypeSize(DT);
   __shared__ float2 red[2][32];
-  const int T = WARP ? 32 : blockDim.x, t = WARP ? threadIdx.x & 31 : threadIdx.x;
-  const size_t per = WARP ? blockDim.x >> 5 : 1;
+  const int T = blockDim.x, t = threadIdx.x;
   const float inv = 1.f / (float)a.cols;
   float dg[EPT], db[EPT];
 #pragma unroll
   for (int i = 0; i < EPT; ++i) dg[i] = db[i] = 0.f;
   int turn = 0;
-  for (size_t row = blockIdx.x * per + (WARP ? threadIdx.x >> 5 : 0); row < a.rows; row += gridDim.x * per) {
+  for (size_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
     H hx, hd;
     hx.load(static_cast<const char*>(a.x) + row * a.ldx * E, t, T, a.cols);
     hd.load(static_cast<const char*>(a.dy) + row * a.lddy * E, t, T, a.cols);
@@ -189,7 +674,7 @@ __global__ void __launch_bounds__(WARP ? 128 : 1024) normBackward(const __grid_c
     for (int j = 0; j < NV; ++j) {
       const int c = (j * T + t) * V;
       if (c < a.cols) {
-        loadParams<V>(a.gamma, a.ptype, c, 1.f, g);
+        loadParams<V>(a.gamma, a.ptype, a.wideParams, c, 1.f, g);
         hx.get(j, fx);
         hd.get(j, fd);
 #pragma unroll
@@ -202,14 +687,14 @@ __global__ void __launch_bounds__(WARP ? 128 : 1024) normBackward(const __grid_c
         }
       }
     }
-    s = WARP ? warpSum2(s) : blockSum2(s, red[turn ^= 1]);
+    s = blockSum2(s, red[turn ^= 1]);
     const float m1 = s.x * inv, m2 = s.y * inv;
     void* out = static_cast<char*>(a.y) + row * a.ldy * E;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int i = j * T + t;
       if (i * V < a.cols) {
-        loadParams<V>(a.gamma, a.ptype, i * V, 1.f, g);
+        loadParams<V>(a.gamma, a.ptype, a.wideParams, i * V, 1.f, g);
         hx.get(j, fx);
         hd.get(j, fd);
 #pragma unroll
@@ -220,38 +705,12 @@ __global__ void __launch_bounds__(WARP ? 128 : 1024) normBackward(const __grid_c
   }
   if (!a.partial) return;
   float* p = a.partial + (size_t)blockIdx.x * 2 * a.cols;
-  if constexpr (WARP) {
-    // the block's warps own the same columns: add them up in warp order
-    __shared__ float sum[2 * 32 * EPT];
-    for (int w = 0; w < (int)per; ++w) {
-      if ((int)(threadIdx.x >> 5) == w) {
 #pragma unroll
-        for (int i = 0; i < EPT; ++i) {
-          float* q = sum + i * 32 + t;
-          q[0] = w ? q[0] + dg[i] : dg[i];
-          q[32 * EPT] = w ? q[32 * EPT] + db[i] : db[i];
-        }
-      }
-      __syncthreads();
-    }
-    if (threadIdx.x < 32) {
-#pragma unroll
-      for (int i = 0; i < EPT; ++i) {
-        const int c = ((i / V) * T + t) * V + i % V;
-        if (c < a.cols) {
-          p[c] = sum[i * 32 + t];
-          p[a.cols + c] = sum[32 * EPT + i * 32 + t];
-        }
-      }
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < EPT; ++i) {
-      const int c = ((i / V) * T + t) * V + i % V;
-      if (c < a.cols) {
-        p[c] = dg[i];
-        p[a.cols + c] = db[i];
-      }
+  for (int i = 0; i < EPT; ++i) {
+    const int c = ((i / V) * T + t) * V + i % V;
+    if (c < a.cols) {
+      p[c] = dg[i];
+      p[a.cols + c] = db[i];
     }
   }
 }
@@ -324,60 +783,86 @@ __global__ void __launch_bounds__(256) normJoin(const float* partial, int blocks
 
 // ------------------------------------------------------------ host
 
-constexpr int kWarpRowCols = 1024;  // a warp holds 32 lanes x 32 elements
-
+enum Walk { kTeams, kBlockRow, kLongRow };
 struct Shape {
-  bool vec, warp, held;
-  int ept, threads, perBlock;
+  Walk walk;
+  bool vec;
+  int per;       // kBlockRow: elements a thread
+  int threads;   // of a block
+  int teams, teamThreads, stages, smem;
+  int resident;  // blocks a multiprocessor
 };
-Shape normShape(int cols, int elem, bool aligned) {
-  Shape s;
-  const int v = 16 / elem;
-  s.vec = aligned && cols % v == 0;
-  s.held = cols <= kMaxHeldCols;
-  s.warp = cols <= kWarpRowCols;
-  if (s.warp) {
-    s.ept = cols <= 256 ? 8 : cols <= 512 ? 16 : 32;
-    s.threads = 128;
-    s.perBlock = 4;
+Shape normShape(size_t rows, int cols, int elem, bool aligned, bool forward) {
+  Shape s = {};
+  s.vec = aligned && cols % (16 / elem) == 0;
+  s.teams = 1;
+  auto up = [](int n, int per) { return std::max(32, (n + per * 32 - 1) / (per * 32) * 32); };
+  if (cols <= kTeamCols) {
+    // one block of up to 512 threads a multiprocessor: 128 registers each. With few rows, fewer teams to a block.
+    s.walk = kTeams;
+    s.teamThreads = up(cols, kTeamElems);
+    s.teams = (int)std::min<size_t>(512 / s.teamThreads, std::max<size_t>(1, (rows + smCount() - 1) / smCount()));
+    s.threads = s.teams * s.teamThreads;
+    const int row = slotBytes(cols, elem) * (forward ? 1 : 2);
+    s.stages = std::min(kMaxStages, kTeamSmem / (s.teams * row)) & (forward ? ~1 : ~0);
+    s.smem = s.teams * s.stages * row;
+    s.resident = 1;
+  } else if (cols <= (forward ? kMaxHeldCols : kMaxHeldCols / 2)) {
+    s.walk = kBlockRow;
+    s.per = cols <= 16384 ? 16 : 32;
+    s.threads = up(cols, s.per);
+    s.resident = forward ? 1 << 20 : 1;
   } else {
-    s.ept = cols <= 8192 ? 8 : cols <= 16384 ? 16 : 32;
-    s.threads = std::max(64, ((cols + s.ept - 1) / s.ept + 31) / 32 * 32);
-    s.perBlock = 1;
+    s.walk = kLongRow;
+    s.threads = 1024;
+    s.resident = forward ? 1 << 20 : 2;
   }
   return s;
 }
-// Blocks that walk the rows of a backward pass, each with one row of partial sums.
-int normBlocks(size_t rows, int cols) {
-  const size_t groups = cols <= kWarpRowCols ? (rows + 3) / 4 : rows;
-  return (int)std::min<size_t>(groups, (size_t)smCount() * 2);
+int normBlocks(size_t rows, const Shape& s) {
+  return (int)std::min<size_t>((rows + s.teams - 1) / s.teams, (size_t)smCount() * s.resident);
+}
+// Row blocks of the partial sums, whatever the strides and the type of a call.
+int mostBlocks(size_t rows, int cols) {
+  int most = 0;
+  for (int elem : {2, 4})
+    for (bool aligned : {false, true}) most = std::max(most, normBlocks(rows, normShape(rows, cols, elem, aligned, false)));
+  return most;
 }
 
 using NormFn = void (*)(NormArgs);
-template <int DT, bool VEC, bool WARP, bool FWD>
-NormFn pickEpt(int ept) {
-  if constexpr (FWD)
-    return ept == 8 ? normForward<DT, VEC, 8, WARP> : ept == 16 ? normForward<DT, VEC, 16, WARP> : normForward<DT, VEC, 32, WARP>;
-  else
-    return ept == 8 ? normBackward<DT, VEC, 8, WARP> : ept == 16 ? normBackward<DT, VEC, 16, WARP> : normBackward<DT, VEC, 32, WARP>;
+template <int DT, bool VEC, bool FWD>
+NormFn pickWalk(const Shape& s) {
+  if constexpr (FWD) {
+    if (s.walk == kTeams) return normForwardTeams<DT, VEC>;
+    return s.per == 16 ? normForward<DT, VEC, 16> : normForward<DT, VEC, 32>;
+  } else {
+    return s.walk == kTeams ? normBackwardTeams<DT, VEC> : normBackward<DT, VEC, 16>;
+  }
 }
 template <int DT, bool FWD>
-NormFn pickShape(const Shape& s) {
-  if (s.vec) return s.warp ? pickEpt<DT, true, true, FWD>(s.ept) : pickEpt<DT, true, false, FWD>(s.ept);
-  return s.warp ? pickEpt<DT, false, true, FWD>(s.ept) : pickEpt<DT, false, false, FWD>(s.ept);
+NormFn pickKernel(const Shape& s) {
+  if (s.walk == kLongRow) {
+    if constexpr (FWD) return normForwardLong<DT>;
+    else return normBackwardLong<DT>;
+  }
+  return s.vec ? pickWalk<DT, true, FWD>(s) : pickWalk<DT, false, FWD>(s);
 }
 template <bool FWD>
-NormFn pickKernel(int dt, const Shape& s) {
-  if (!s.held) {
-    if constexpr (FWD)
-      return dt == vrcclFloat32 ? normForwardLong<vrcclFloat32>
-             : dt == vrcclBfloat16 ? normForwardLong<vrcclBfloat16> : normForwardLong<vrcclFloat16>;
-    else
-      return dt == vrcclFloat32 ? normBackwardLong<vrcclFloat32>
-             : dt == vrcclBfloat16 ? normBackwardLong<vrcclBfloat16> : normBackwardLong<vrcclFloat16>;
+vrcclResult_t launchNorm(int dt, const Shape& s, unsigned blocks, NormArgs& a, cudaStream_t st) {
+  const NormFn fn = dt == vrcclFloat32    ? pickKernel<vrcclFloat32, FWD>(s)
+                    : dt == vrcclBfloat16 ? pickKernel<vrcclBfloat16, FWD>(s)
+                                          : pickKernel<vrcclFloat16, FWD>(s);
+  if (s.smem > 32 * 1024 &&  // (beside static shared memory, 48 KB come without asking)
+      cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, s.smem) != cudaSuccess) {
+    cudaGetLastError();
+    return vrcclCudaError;
   }
-  return dt == vrcclFloat32 ? pickShape<vrcclFloat32, FWD>(s)
-         : dt == vrcclBfloat16 ? pickShape<vrcclBfloat16, FWD>(s) : pickShape<vrcclFloat16, FWD>(s);
+  a.stages = s.stages;
+  a.teams = s.teams;
+  a.teamThreads = s.teamThreads;
+  fn<<<blocks, s.threads, s.smem, st>>>(a);
+  return launchResult();
 }
 
 bool goodSizes(size_t rows, size_t cols, int dtype, int ptype) {
@@ -385,6 +870,8 @@ bool goodSizes(size_t rows, size_t cols, int dtype, int ptype) {
 }
 
 }  // namespace
+
+int normStatus(int* code) { return cudaMemcpyFromSymbol(code, gNormStatus, sizeof(*code)); }
 
 int smCount() {
   static int count[64] = {};
@@ -418,7 +905,7 @@ extern "C" vrcclResult_t vrcclLayerNormForward(const void* x, size_t ldx, const 
     return vrcclInvalidArgument;
   if (!(x == y && ldx == ldy) && overlap(x, spanBytes(ldx, rows, cols, E), y, spanBytes(ldy, rows, cols, E)))
     return vrcclInvalidArgument;
-  const Shape s = normShape((int)cols, E, rowsAligned(x, ldx, E) && rowsAligned(y, ldy, E));
+  const Shape s = normShape(rows, (int)cols, E, rowsAligned(x, ldx, E) && rowsAligned(y, ldy, E), true);
   NormArgs a = {};
   a.x = x;
   a.gamma = gamma;
@@ -432,15 +919,13 @@ extern "C" vrcclResult_t vrcclLayerNormForward(const void* x, size_t ldx, const 
   a.cols = (int)cols;
   a.ptype = paramType;
   a.eps = eps;
-  const size_t blocks = std::min<size_t>((rows + s.perBlock - 1) / s.perBlock, size_t(1) << 30);
-  const int threads = s.held ? s.threads : 1024;
-  pickKernel<true>(dtype, s)<<<(unsigned)blocks, threads, 0, (cudaStream_t)stream>>>(a);
-  return launchResult();
+  a.wideParams = (((uintptr_t)gamma | (uintptr_t)beta) & 15) == 0;
+  return launchNorm<true>(dtype, s, (unsigned)normBlocks(rows, s), a, (cudaStream_t)stream);
 }
 
 extern "C" vrcclResult_t vrcclLayerNormWorkspace(size_t rows, size_t cols, size_t* bytes) {
   if (!bytes || !goodSizes(rows, cols, vrcclFloat32, vrcclFloat32)) return vrcclInvalidArgument;
-  *bytes = size_t(normBlocks(rows, (int)cols)) * 2 * cols * sizeof(float);
+  *bytes = size_t(mostBlocks(rows, (int)cols)) * 2 * cols * sizeof(float);
   return vrcclSuccess;
 }
 
@@ -471,10 +956,11 @@ extern "C" vrcclResult_t vrcclLayerNormBackward(const void* dy, size_t lddy, con
   if ((!(dx == dy && lddx == lddy) && overlap(dx, outSpan, dy, spanBytes(lddy, rows, cols, E))) ||
       (!(dx == x && lddx == ldx) && overlap(dx, outSpan, x, spanBytes(ldx, rows, cols, E))))
     return vrcclInvalidArgument;
-  const int blocks = normBlocks(rows, (int)cols);
+  const Shape s =
+      normShape(rows, (int)cols, E, rowsAligned(dy, lddy, E) && rowsAligned(x, ldx, E) && rowsAligned(dx, lddx, E), false);
+  const int blocks = normBlocks(rows, s);
   if (weights && (!goodVector(workspace, 16) || workspaceBytes < size_t(blocks) * 2 * cols * sizeof(float)))
     return vrcclInvalidArgument;
-  const Shape s = normShape((int)cols, E, rowsAligned(dy, lddy, E) && rowsAligned(x, ldx, E) && rowsAligned(dx, lddx, E));
   NormArgs a = {};
   a.x = x;
   a.dy = dy;
@@ -489,7 +975,8 @@ extern "C" vrcclResult_t vrcclLayerNormBackward(const void* dy, size_t lddy, con
   a.rows = rows;
   a.cols = (int)cols;
   a.ptype = paramType;
-  if (!s.held && weights) {
+  a.wideParams = ((uintptr_t)gamma & 15) == 0;
+  if (s.walk == kLongRow && weights) {
     const dim3 grid((unsigned)((cols + 255) / 256), (unsigned)blocks);
     if (dtype == vrcclFloat32)
       normColumns<vrcclFloat32><<<grid, 256, 0, st>>>(a);
@@ -498,7 +985,8 @@ extern "C" vrcclResult_t vrcclLayerNormBackward(const void* dy, size_t lddy, con
     else
       normColumns<vrcclFloat16><<<grid, 256, 0, st>>>(a);
   }
-  pickKernel<false>(dtype, s)<<<(unsigned)blocks, s.held ? s.threads : 1024, 0, st>>>(a);
+  const vrcclResult_t r = launchNorm<false>(dtype, s, (unsigned)blocks, a, st);
+  if (r != vrcclSuccess) return r;
   if (weights)
     normJoin<<<dim3((unsigned)((cols + 31) / 32), 2), 256, 0, st>>>(static_cast<const float*>(workspace), blocks,
                                                                     (int)cols, dgamma, dbeta, paramType);

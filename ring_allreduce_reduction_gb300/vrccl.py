@@ -81,7 +81,7 @@ _sig = {
     "vrcclLinearWorkspace": [_i, _z, _z, _z, _i, _i, ctypes.POINTER(_z)],
     "vrcclLinearForward": [_p, _z, _p, _z, _p, _p, _z, _p, _z, _p, _z, _z, _z, _z, _i, _i, _p, _z, _p],
     "vrcclLinearBackward": [_p, _z, _p, _z, _p, _z, _p, _z, _p, _z, _p, _z, _p, _z, _z, _z, _i, _i, _p, _z, _p],
-    "vrcclLinearGetAsyncError": [_c_int_p],
+    "vrcclReplicaGetAsyncError": [_c_int_p],
     "vrcclDistillForward": [_p, _z, _p, _z, _p, _z, _p, _p, _z, _z, _z, _i, _i, _i, _f, _p],
     "vrcclDistillBackward": [_p, _z, _p, _z, _p, _z, _p, _p, _z, _p, _z, _z, _z, _z, _i, _i, _i, _f, _p],
 }
@@ -359,9 +359,9 @@ def vrcclLinearBackward(dy, z, x, w, dx, dw, dbias, rows: int, outs: int, ins: i
                                     _stream(stream)), "vrcclLinearBackward")
 
 
-def vrcclLinearGetAsyncError() -> int:
+def vrcclReplicaGetAsyncError() -> int:
     e = ctypes.c_int()
-    _check(_lib.vrcclLinearGetAsyncError(ctypes.byref(e)), "vrcclLinearGetAsyncError")
+    _check(_lib.vrcclReplicaGetAsyncError(ctypes.byref(e)), "vrcclReplicaGetAsyncError")
     return e.value
 
 

@@ -80,7 +80,7 @@ def test_linear_refusals(lib):
     for change in bad:
         assert _call(lib.vrcclLinearBackward, bwd, **change) == 1, change
     assert _call(lib.vrcclLinearBackward, bwd, dtype=F32) == 2
-    assert lib.vrcclLinearGetAsyncError(None) == 1
+    assert lib.vrcclReplicaGetAsyncError(None) == 1
 
 
 def test_distill_refusals(lib):
