@@ -28,13 +28,21 @@ namespace {
 
 // ------------------------------------------------------------ activations
 
+// 1 / (1 + exp(x)); exp may overflow: the reciprocal of infinity is 0
+__device__ __forceinline__ float logistic(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + __expf(x)));
+  return r;
+}
+
 template <int ACT>
 __device__ __forceinline__ float activate(float z) {
   if constexpr (ACT == vrcclActRelu) return z > 0.f ? z : (z != z ? z : 0.f);
   if constexpr (ACT == vrcclActGelu) return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
+  // (1 + tanh u) / 2 = 1 / (1 + exp(-2u)), which loses nothing where tanh u nears -1
   if constexpr (ACT == vrcclActGeluTanh)
-    return 0.5f * z * (1.f + tanhf(0.79788456080286536f * (z + 0.044715f * z * z * z)));
-  if constexpr (ACT == vrcclActSilu) return z / (1.f + __expf(-z));
+    return z * logistic(-1.5957691216057308f * (z + 0.044715f * z * z * z));
+  if constexpr (ACT == vrcclActSilu) return z * logistic(-z);
   return z;
 }
 template <int ACT>
@@ -42,12 +50,13 @@ __device__ __forceinline__ float slope(float z) {
   if constexpr (ACT == vrcclActRelu) return z > 0.f ? 1.f : 0.f;
   if constexpr (ACT == vrcclActGelu)
     return 0.5f * (1.f + erff(z * 0.70710678118654752f)) + z * __expf(-0.5f * z * z) * 0.39894228040143268f;
+  // with y = z s(w), w = 2 sqrt(2/pi) (z + 0.044715 z^3), s(w) = 1 / (1 + exp(-w)):  y' = s + z s (1 - s) w'
   if constexpr (ACT == vrcclActGeluTanh) {
-    const float t = tanhf(0.79788456080286536f * (z + 0.044715f * z * z * z));
-    return 0.5f * (1.f + t) + 0.5f * z * (1.f - t * t) * 0.79788456080286536f * (1.f + 0.134145f * z * z);
+    const float s = logistic(-1.5957691216057308f * (z + 0.044715f * z * z * z));
+    return s + z * s * (1.f - s) * 1.5957691216057308f * (1.f + 0.134145f * z * z);
   }
   if constexpr (ACT == vrcclActSilu) {
-    const float s = 1.f / (1.f + __expf(-z));
+    const float s = logistic(-z);
     return s * (1.f + z * (1.f - s));
   }
   return 1.f;
@@ -79,30 +88,101 @@ __device__ __forceinline__ bool waitBar(unsigned long long* bar, unsigned parity
 __device__ __forceinline__ void mbarArriveExpect(unsigned long long* bar, unsigned bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smemAddr(bar)), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ void tmaLoad2d(const CUtensorMap* map, void* dst, unsigned long long* bar, int x, int y) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
-          smemAddr(dst)),
-      "l"(map), "r"(smemAddr(bar)), "r"(x), "r"(y)
-      : "memory");
+__device__ __forceinline__ uint32_t clusterRank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void clusterSync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The address of this shared variable in block `rank` of the cluster.
+__device__ __forceinline__ uint32_t inBlock(const void* p, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smemAddr(p)), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void mbarArriveAt(uint32_t addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+// `bar`: a shared::cluster address; in a pair of blocks it may be the other block's.
+template <int CG>
+__device__ __forceinline__ void tmaLoad2d(const CUtensorMap* map, void* dst, uint32_t bar, int x, int y) {
+  if constexpr (CG == 2)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, "
+        "%4}], [%2];" ::"r"(smemAddr(dst)),
+        "l"(map), "r"(bar), "r"(x), "r"(y)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
+            smemAddr(dst)),
+        "l"(map), "r"(bar), "r"(x), "r"(y)
+        : "memory");
+}
+__device__ __forceinline__ void tmaStore2d(const CUtensorMap* map, const void* src, int x, int y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(map),
+               "r"(smemAddr(src)), "r"(x), "r"(y)
+               : "memory");
 }
 __device__ __forceinline__ void tcFenceBefore() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tcFenceAfter() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+// Arrives on `bar` (in a pair: on both blocks') once the MMAs issued so far are done.
+template <int CG>
 __device__ __forceinline__ void tcCommit(unsigned long long* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smemAddr(bar))
-               : "memory");
+  if constexpr (CG == 2)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smemAddr(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+  else
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smemAddr(bar))
+                 : "memory");
 }
+template <int CG>
 __device__ __forceinline__ void tcMma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
-  asm volatile(
-      "{\n"
-      ".reg .pred p;\n"
-      "setp.ne.b32 p, %4, 0;\n"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n"
-      "}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
-      : "memory");
+  if constexpr (CG == 2)
+    asm volatile(
+        "{\n"
+        ".reg .pred p;\n"
+        "setp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n"
+        "}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n"
+        ".reg .pred p;\n"
+        "setp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n"
+        "}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+        : "memory");
 }
-__device__ __forceinline__ void tcLoad32(uint32_t addr, uint32_t (&r)[32]) {
+template <int CG>
+__device__ __forceinline__ void tmemAlloc(uint32_t* slot, int cols) {
+  if constexpr (CG == 2) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smemAddr(slot)), "r"(cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  } else {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smemAddr(slot)), "r"(cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+}
+template <int CG>
+__device__ __forceinline__ void tmemFree(uint32_t addr, int cols) {
+  if constexpr (CG == 2)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols));
+  else
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols));
+}
+__device__ __forceinline__ void tcLoad32(uint32_t addr, float (&f)[32]) {
+  uint32_t r[32];
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
       "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
@@ -114,6 +194,8 @@ __device__ __forceinline__ void tcLoad32(uint32_t addr, uint32_t (&r)[32]) {
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(addr)
       : "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(r[i]);
 }
 
 // Shared-memory operand descriptor of a tile with 128-byte swizzle. K-major:
@@ -132,11 +214,13 @@ __device__ __forceinline__ uint64_t operandDesc(uint32_t addr, bool mn) {
 
 // ------------------------------------------------------------ the product
 
-constexpr int kBM = 128, kBK = 64;
-constexpr int kProductThreads = 192;  // TMA warp, MMA warp, four epilogue warps
+constexpr int kBM = 128, kBK = 64;  // rows of A a block, contraction elements a stage
+constexpr int kEpilogueWarps = 8;
+constexpr int kProductThreads = 32 * (2 + kEpilogueWarps);  // TMA warp, MMA warp, epilogue warps
+constexpr int kStoreBytes = 32 * 64 * 2;                    // one warp's 32 rows x 64 columns on the way out
 
 struct ProductArgs {
-  CUtensorMap a, b;
+  CUtensorMap a, b, dMap, zMap;
   void* d;               // [M, N]
   void* z;               // the sums before activation, or NULL
   const void* bias;      // [N] or NULL
@@ -144,75 +228,106 @@ struct ProductArgs {
   size_t ldd, ldz, ldr;
   int M, N, K;
   bool aMN, bMN;         // operand majors
-  bool wideD, wideZ, wideR;  // rows of d / z / residual start on 16-byte boundaries
+  bool wideD, wideZ;     // d / z may be stored by TMA
+  bool wideR;            // the residual's rows start on 16-byte boundaries
+  bool wideBias;
   int act;
 };
 
-template <int BN>
+// A tile is CG x 128 rows of A by BN rows of B. In a pair of blocks (CG = 2)
+// each holds its 128 rows of A and half of B's, and one thread issues MMAs
+// that run on both multiprocessors: B crosses into shared memory once for the
+// two of them, which a single block's 128 x 256 tile cannot afford (its stages
+// would take 1.5 times the L2 bandwidth for the same arithmetic).
+template <int CG, int BN>
 struct ProductShape {
-  static constexpr int kStageBytes = (kBM + BN) * kBK * 2;
-  static constexpr int kStages = BN == 256 ? 4 : BN == 128 ? 6 : 8;
-  static constexpr int kSmem = kStages * kStageBytes + 1024;
-  static constexpr int kTmemCols = 2 * BN < 32 ? 32 : 2 * BN;
+  static constexpr int kBRows = BN / CG;
+  static constexpr int kStageBytes = (kBM + kBRows) * kBK * 2;
+  static constexpr int kStages = BN == 64 ? 6 : 5;
+  static constexpr int kSmem = kStages * kStageBytes + kEpilogueWarps * 2 * kStoreBytes + 1024;
+  static constexpr int kTmemCols = 2 * BN;
 };
 
-template <int DT, int ACT>
-__device__ __forceinline__ void finish(const ProductArgs& a, float (&f)[32], size_t m, int n) {
-  using S = typename Ty<DT>::S;
-  const int left = a.N - n;  // columns that exist, of 32
-  if (a.z) {
-    S* z = static_cast<S*>(a.z) + m * a.ldz + n;
-#pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      float g[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) g[e] = f[v * 8 + e];
-      if (a.wideZ && v * 8 + 8 <= left) {
-        reinterpret_cast<uint4*>(z)[v] = Vec16<DT>::pack(g);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (v * 8 + e < left) z[v * 8 + e] = Ty<DT>::fromF(g[e]);
-      }
+// Writes one warp's finished 32 x 64 elements from its staging buffer (rows of
+// 128 bytes, 16-byte pieces swizzled by the row) to memory.
+template <int DT>
+__device__ __forceinline__ void storeBox(const ProductArgs& a, const CUtensorMap* map, void* out, size_t ld, bool wide,
+                                         const unsigned char* buf, int m, int n, int lane) {
+  if (wide) {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if (lane == 0) {
+      tmaStore2d(map, buf, n, m);  // what lies outside the matrix is not written
+      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
     }
-  }
-#pragma unroll
-  for (int i = 0; i < 32; ++i) f[i] = activate<ACT>(f[i]);
-  if (a.residual) {
-    const S* r = static_cast<const S*>(a.residual) + m * a.ldr + n;
-#pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      if (a.wideR && v * 8 + 8 <= left) {
-        float g[8];
-        Vec16<DT>::expand(reinterpret_cast<const uint4*>(r)[v], g);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[v * 8 + e] += g[e];
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (v * 8 + e < left) f[v * 8 + e] += Ty<DT>::toF(r[v * 8 + e]);
-      }
+  } else {
+    __syncwarp();
+    unsigned short* o = static_cast<unsigned short*>(out) + (size_t)m * ld + n;
+    const int rows = min(32, a.M - m), c = 2 * lane;
+    const bool lo = n + c < a.N, hi = n + c + 1 < a.N;
+    for (int r = 0; r < rows; ++r) {
+      const uint32_t w =
+          *reinterpret_cast<const uint32_t*>(buf + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + ((lane & 3) << 2));
+      if (lo) o[(size_t)r * ld + c] = (unsigned short)(w & 0xffffu);
+      if (hi) o[(size_t)r * ld + c + 1] = (unsigned short)(w >> 16);
     }
+    __syncwarp();
   }
-  S* d = static_cast<S*>(a.d) + m * a.ldd + n;
+}
+template <int DT>
+__device__ __forceinline__ void stage32(unsigned char* buf, int half, int lane, const float (&f)[32]) {
 #pragma unroll
   for (int v = 0; v < 4; ++v) {
     float g[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) g[e] = f[v * 8 + e];
-    if (a.wideD && v * 8 + 8 <= left) {
-      reinterpret_cast<uint4*>(d)[v] = Vec16<DT>::pack(g);
+    *reinterpret_cast<uint4*>(buf + lane * 128 + (((half * 4 + v) ^ (lane & 7)) << 4)) = Vec16<DT>::pack(g);
+  }
+}
+
+template <int DT, int ACT>
+__device__ __forceinline__ void finish(const ProductArgs& a, float (&f)[32], size_t m, int n) {
+  using S = typename Ty<DT>::S;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) f[i] = activate<ACT>(f[i]);
+  if (!a.residual || m >= (size_t)a.M) return;
+  const int left = a.N - n;  // columns that exist, of 32
+  const S* r = static_cast<const S*>(a.residual) + m * a.ldr + n;
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    if (a.wideR && v * 8 + 8 <= left) {
+      float g[8];
+      Vec16<DT>::expand(reinterpret_cast<const uint4*>(r)[v], g);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[v * 8 + e] += g[e];
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        if (v * 8 + e < left) d[v * 8 + e] = Ty<DT>::fromF(g[e]);
+        if (v * 8 + e < left) f[v * 8 + e] += Ty<DT>::toF(r[v * 8 + e]);
+    }
+  }
+}
+template <int DT>
+__device__ __forceinline__ void addBias(const ProductArgs& a, float (&f)[32], int n) {
+  const int left = a.N - n;
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    if (a.wideBias && v * 8 + 8 <= left) {
+      float g[8];
+      Vec16<DT>::expand(__ldg(reinterpret_cast<const uint4*>(static_cast<const char*>(a.bias) + (size_t)n * 2) + v), g);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[v * 8 + e] += g[e];
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (v * 8 + e < left) f[v * 8 + e] += loadOne<DT>(a.bias, n + v * 8 + e);
     }
   }
 }
 
-template <int DT, int BN>
-__global__ void __launch_bounds__(kProductThreads) productKernel(const __grid_constant__ ProductArgs a) {
-  using Sh = ProductShape<BN>;
+template <int DT, int CG, int BN>
+__global__ void __launch_bounds__(kProductThreads, 1) productKernel(const __grid_constant__ ProductArgs a) {
+  using Sh = ProductShape<CG, BN>;
   constexpr int kStages = Sh::kStages;
   extern __shared__ unsigned char dyn[];
   __shared__ unsigned long long full[kStages], empty[kStages], accFull[2], accEmpty[2], drained;
@@ -221,6 +336,8 @@ __global__ void __launch_bounds__(kProductThreads) productKernel(const __grid_co
   volatile int* dead = &deadWord;
   unsigned char* smem = dyn + ((1024 - (smemAddr(dyn) & 1023)) & 1023);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = CG == 2 ? clusterRank() : 0;
+  constexpr int kWorkers = BN >= 128 ? kEpilogueWarps : 4;  // warps that have 64 columns to finish
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -229,46 +346,46 @@ __global__ void __launch_bounds__(kProductThreads) productKernel(const __grid_co
     }
     for (int s = 0; s < 2; ++s) {
       mbarInit(&accFull[s], 1);
-      mbarInit(&accEmpty[s], 4);
+      mbarInit(&accEmpty[s], kWorkers * CG);
     }
     mbarInit(&drained, 1);
     deadWord = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smemAddr(&tmemSlot)),
-                 "r"(Sh::kTmemCols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-  }
+  if (warp == 1) tmemAlloc<CG>(&tmemSlot, Sh::kTmemCols);
   tcFenceBefore();
+  __syncwarp();
+  if constexpr (CG == 2) clusterSync();
   __syncthreads();
   tcFenceAfter();
   const uint32_t tmem = tmemSlot;
 
-  const int tilesM = (a.M + kBM - 1) / kBM, tilesN = (a.N + BN - 1) / BN, tiles = tilesM * tilesN;
+  const int tilesM = (a.M + CG * kBM - 1) / (CG * kBM), tilesN = (a.N + BN - 1) / BN, tiles = tilesM * tilesN;
   const int steps = (a.K + kBK - 1) / kBK;
+  const int first = blockIdx.x / CG, stride = gridDim.x / CG;
 
   if (warp == 0) {
     if (lane == 0) {
       int stage = 0, round = 0;
       bool ok = true;
-      for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
-        const int m = tile % tilesM * kBM, n = tile / tilesM * BN;
+      for (int tile = first; tile < tiles && ok; tile += stride) {
+        const int m = tile % tilesM * (CG * kBM) + (int)rank * kBM, n = tile / tilesM * BN + (int)rank * Sh::kBRows;
         for (int k = 0; k < steps; ++k) {
           if (round > 0 && !(ok = waitBar(&empty[stage], (round - 1) & 1, dead))) break;
           unsigned char* sa = smem + stage * Sh::kStageBytes;
           unsigned char* sb = sa + kBM * kBK * 2;
-          mbarArriveExpect(&full[stage], Sh::kStageBytes);
+          // both blocks' copies count on the first block's barrier, which its MMA thread waits on
+          if (rank == 0) mbarArriveExpect(&full[stage], Sh::kStageBytes * CG);
+          const uint32_t bar = CG == 2 ? inBlock(&full[stage], 0) : smemAddr(&full[stage]);
           if (!a.aMN) {
-            tmaLoad2d(&a.a, sa, &full[stage], k * kBK, m);
+            tmaLoad2d<CG>(&a.a, sa, bar, k * kBK, m);
           } else {
-            for (int i = 0; i < kBM / 64; ++i) tmaLoad2d(&a.a, sa + i * 8192, &full[stage], m + i * 64, k * kBK);
+            for (int i = 0; i < kBM / 64; ++i) tmaLoad2d<CG>(&a.a, sa + i * 8192, bar, m + i * 64, k * kBK);
           }
           if (!a.bMN) {
-            tmaLoad2d(&a.b, sb, &full[stage], k * kBK, n);
+            tmaLoad2d<CG>(&a.b, sb, bar, k * kBK, n);
           } else {
-            for (int i = 0; i < BN / 64; ++i) tmaLoad2d(&a.b, sb + i * 8192, &full[stage], n + i * 64, k * kBK);
+            for (int i = 0; i < Sh::kBRows / 64; ++i) tmaLoad2d<CG>(&a.b, sb + i * 8192, bar, n + i * 64, k * kBK);
           }
           if (++stage == kStages) {
             stage = 0;
@@ -277,7 +394,7 @@ __global__ void __launch_bounds__(kProductThreads) productKernel(const __grid_co
         }
       }
       // given up: no copy may land after the block has gone
-      if (!ok) {
+      if (!ok && rank == 0) {
         int quiet = 0;
         for (int s = 0; s < kStages; ++s) {
           const int issued = round + (s < stage ? 1 : 0);
@@ -287,16 +404,16 @@ __global__ void __launch_bounds__(kProductThreads) productKernel(const __grid_co
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
+    if (lane == 0 && rank == 0) {
       // f32 accumulators; A and B of the element type; majors; N / 8, M / 16
       const uint32_t idesc = 1u << 4 | (DT == vrcclBfloat16 ? 1u : 0u) << 7 | (DT == vrcclBfloat16 ? 1u : 0u) << 10 |
                              (a.aMN ? 1u : 0u) << 15 | (a.bMN ? 1u : 0u) << 16 | (uint32_t)(BN / 8) << 17 |
-                             (uint32_t)(kBM / 16) << 24;
+                             (uint32_t)(CG * kBM / 16) << 24;
       // 16 contraction elements on: 32 bytes along a K-major row, 16 rows of an MN-major tile
       const uint32_t aStep = a.aMN ? 2048 >> 4 : 32 >> 4, bStep = a.bMN ? 2048 >> 4 : 32 >> 4;
       int stage = 0, round = 0, turn = 0;
       bool ok = true;
-      for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x, ++turn) {
+      for (int tile = first; tile < tiles && ok; tile += stride, ++turn) {
         const int acc = turn & 1, use = turn >> 1;
         if (use > 0 && !(ok = waitBar(&accEmpty[acc], (use - 1) & 1, dead))) break;
         tcFenceAfter();
@@ -307,64 +424,87 @@ __global__ void __launch_bounds__(kProductThreads) productKernel(const __grid_co
           const uint32_t sa = smemAddr(smem + stage * Sh::kStageBytes);
           const uint64_t da = operandDesc(sa, a.aMN), db = operandDesc(sa + kBM * kBK * 2, a.bMN);
 #pragma unroll
-          for (int i = 0; i < kBK / 16; ++i) tcMma(d, da + i * aStep, db + i * bStep, idesc, k > 0 || i > 0);
-          tcCommit(&empty[stage]);
+          for (int i = 0; i < kBK / 16; ++i) tcMma<CG>(d, da + i * aStep, db + i * bStep, idesc, k > 0 || i > 0);
+          tcCommit<CG>(&empty[stage]);
           if (++stage == kStages) {
             stage = 0;
             ++round;
           }
         }
-        if (ok) tcCommit(&accFull[acc]);
+        if (ok) tcCommit<CG>(&accFull[acc]);
       }
       if (!ok) {  // given up: the products in flight end before TMEM is freed
         int quiet = 0;
-        tcCommit(&drained);
+        tcCommit<CG>(&drained);
         waitBar(&drained, 0, &quiet, 100000000ull);
       }
     }
     __syncwarp();
-  } else {
+  } else if (warp - 2 < kWorkers) {
     const int quarter = warp & 3;  // the TMEM lanes this warp may read
-    int turn = 0;
-    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, ++turn) {
-      const int m0 = tile % tilesM * kBM, n0 = tile / tilesM * BN;
+    const int part = (warp - 2) >> 2;
+    constexpr int kCols = BN / (kWorkers / 4);  // columns a warp finishes, 64 at a time
+    unsigned char* buf = smem + kStages * Sh::kStageBytes + (warp - 2) * 2 * kStoreBytes;
+    int turn = 0, which = 0;
+    for (int tile = first; tile < tiles; tile += stride, ++turn) {
+      const int m0 = tile % tilesM * (CG * kBM) + (int)rank * kBM + quarter * 32, n0 = tile / tilesM * BN + part * kCols;
       const int acc = turn & 1, use = turn >> 1;
       bool ok = lane != 0 || waitBar(&accFull[acc], use & 1, dead);
       if (!__all_sync(0xffffffffu, ok)) break;
       tcFenceAfter();
-      const int m = m0 + quarter * 32 + lane;
-      for (int c = 0; c < BN; c += 32) {
-        if (n0 + c >= a.N) break;
-        uint32_t raw[32];
-        tcLoad32(tmem + ((uint32_t)(quarter * 32) << 16) + acc * BN + c, raw);
-        float f[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(raw[i]);
-        if (m < a.M) {
-          if (a.bias) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (n0 + c + i < a.N) f[i] += loadOne<DT>(a.bias, n0 + c + i);
+      const uint32_t from = tmem + ((uint32_t)(quarter * 32) << 16) + acc * BN + part * kCols;
+      if (m0 < a.M) {
+        for (int c = 0; c < kCols && n0 + c < a.N; c += 64) {
+          // the buffers take turns; the store that last read one has to be done with it
+          unsigned char* zb = buf + which * kStoreBytes;
+          if (a.z) which ^= 1;
+          unsigned char* yb = buf + which * kStoreBytes;
+          which ^= 1;
+          if (lane == 0) {
+            if (a.z)
+              asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+            else
+              asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
           }
-          switch (a.act) {
-            case vrcclActRelu: finish<DT, vrcclActRelu>(a, f, m, n0 + c); break;
-            case vrcclActGelu: finish<DT, vrcclActGelu>(a, f, m, n0 + c); break;
-            case vrcclActGeluTanh: finish<DT, vrcclActGeluTanh>(a, f, m, n0 + c); break;
-            case vrcclActSilu: finish<DT, vrcclActSilu>(a, f, m, n0 + c); break;
-            default: finish<DT, vrcclActNone>(a, f, m, n0 + c); break;
+          __syncwarp();
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float f[32];
+            tcLoad32(from + c + h * 32, f);
+            const int n = n0 + c + h * 32;
+            if (a.bias) addBias<DT>(a, f, n);
+            if (a.z) stage32<DT>(zb, h, lane, f);
+            const size_t m = m0 + lane;
+            switch (a.act) {
+              case vrcclActRelu: finish<DT, vrcclActRelu>(a, f, m, n); break;
+              case vrcclActGelu: finish<DT, vrcclActGelu>(a, f, m, n); break;
+              case vrcclActGeluTanh: finish<DT, vrcclActGeluTanh>(a, f, m, n); break;
+              case vrcclActSilu: finish<DT, vrcclActSilu>(a, f, m, n); break;
+              default: finish<DT, vrcclActNone>(a, f, m, n); break;
+            }
+            stage32<DT>(yb, h, lane, f);
           }
+          if (a.z) storeBox<DT>(a, &a.zMap, a.z, a.ldz, a.wideZ, zb, m0, n0 + c, lane);
+          storeBox<DT>(a, &a.dMap, a.d, a.ldd, a.wideD, yb, m0, n0 + c, lane);
         }
       }
       tcFenceBefore();
       __syncwarp();
-      if (lane == 0) mbarArrive(&accEmpty[acc]);
+      if (lane == 0) {
+        if constexpr (CG == 2)
+          mbarArriveAt(inBlock(&accEmpty[acc], 0));
+        else
+          mbarArrive(&accEmpty[acc]);
+      }
     }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    __syncwarp();
   }
   tcFenceBefore();
   __syncthreads();
+  if constexpr (CG == 2) clusterSync();  // no block leaves while the other may still signal it or use its operands
   tcFenceAfter();
-  if (warp == 1)
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(Sh::kTmemCols));
+  if (warp == 1) tmemFree<CG>(tmem, Sh::kTmemCols);
 }
 
 // ------------------------------------------------------------ few rows
@@ -611,27 +751,42 @@ bool aligned(Operand& o, Scratch& ws, cudaStream_t st) {
   return true;
 }
 
-template <int DT, int BN>
+template <int DT, int CG, int BN>
 vrcclResult_t launchProduct(ProductArgs& a, const Operand& A, const Operand& B, cudaStream_t st) {
-  using Sh = ProductShape<BN>;
+  using Sh = ProductShape<CG, BN>;
   if (!makeMap(&a.a, DT, A.p, A.ld, A.rows, A.cols, A.mn ? kBK : kBM) ||
-      !makeMap(&a.b, DT, B.p, B.ld, B.rows, B.cols, B.mn ? kBK : BN))
+      !makeMap(&a.b, DT, B.p, B.ld, B.rows, B.cols, B.mn ? kBK : Sh::kBRows) ||
+      (a.wideD && !makeMap(&a.dMap, DT, a.d, a.ldd, a.M, a.N, 32)) ||
+      (a.wideZ && !makeMap(&a.zMap, DT, a.z, a.ldz, a.M, a.N, 32)))
     return vrcclInternalError;
   static bool raised[64] = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return vrcclCudaError;
   if (!raised[dev]) {
-    if (cudaFuncSetAttribute(productKernel<DT, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem) !=
+    if (cudaFuncSetAttribute(productKernel<DT, CG, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem) !=
         cudaSuccess) {
       cudaGetLastError();
       return vrcclCudaError;
     }
     raised[dev] = true;
   }
-  const long long tiles = (long long)((a.M + kBM - 1) / kBM) * ((a.N + BN - 1) / BN);
-  const int grid = (int)std::min<long long>(tiles, smCount());
-  productKernel<DT, BN><<<grid, kProductThreads, Sh::kSmem, st>>>(a);
-  return launchResult();
+  const long long tiles = (long long)((a.M + CG * kBM - 1) / (CG * kBM)) * ((a.N + BN - 1) / BN);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)std::min<long long>(tiles, smCount() / CG) * CG);
+  cfg.blockDim = dim3(kProductThreads);
+  cfg.dynamicSmemBytes = Sh::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = CG;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, productKernel<DT, CG, BN>, a) != cudaSuccess) {
+    cudaGetLastError();
+    return vrcclCudaError;
+  }
+  return vrcclSuccess;
 }
 
 // D = A B^T with the epilogue of `a`.
@@ -639,14 +794,15 @@ template <int DT>
 vrcclResult_t product(ProductArgs& a, const Operand& A, const Operand& B, cudaStream_t st) {
   a.aMN = A.mn;
   a.bMN = B.mn;
-  a.wideD = rowsAligned(a.d, a.ldd, 2);
-  a.wideZ = a.z && rowsAligned(a.z, a.ldz, 2);
+  // a TMA store writes whole 16-byte pieces: rows that end inside one are stored by the warps
+  a.wideD = a.N % 8 == 0 && rowsAligned(a.d, a.ldd, 2);
+  a.wideZ = a.z && a.N % 8 == 0 && rowsAligned(a.z, a.ldz, 2);
   a.wideR = a.residual && rowsAligned(a.residual, a.ldr, 2);
-  const long long tm = (a.M + kBM - 1) / kBM;
-  auto tiles = [&](int bn) { return tm * ((a.N + bn - 1) / bn); };
-  if (tiles(256) >= smCount()) return launchProduct<DT, 256>(a, A, B, st);
-  if (tiles(128) >= smCount()) return launchProduct<DT, 128>(a, A, B, st);
-  return launchProduct<DT, 64>(a, A, B, st);
+  a.wideBias = (uintptr_t)a.bias % 16 == 0;
+  auto tiles = [&](long long bm, long long bn) { return (a.M + bm - 1) / bm * ((a.N + bn - 1) / bn); };
+  if (tiles(256, 256) >= smCount() / 2) return launchProduct<DT, 2, 256>(a, A, B, st);
+  if (tiles(128, 128) >= smCount()) return launchProduct<DT, 1, 128>(a, A, B, st);
+  return launchProduct<DT, 1, 64>(a, A, B, st);
 }
 
 template <int DT, int MR>
@@ -895,13 +1051,13 @@ extern "C" vrcclResult_t vrcclLinearBackward(const void* dy, size_t lddy, const 
                                                          rows, outs, ins, act, ws, st);
 }
 
-extern "C" vrcclResult_t vrcclLinearGetAsyncError(vrcclResult_t* asyncErr) {
+extern "C" vrcclResult_t vrcclReplicaGetAsyncError(vrcclResult_t* asyncErr) {
   if (!asyncErr) return vrcclInvalidArgument;
-  int code = 0;
-  if (cudaMemcpyFromSymbol(&code, gLinearStatus, sizeof(code)) != cudaSuccess) {
+  int code = 0, norm = 0;
+  if (cudaMemcpyFromSymbol(&code, gLinearStatus, sizeof(code)) != cudaSuccess || normStatus(&norm) != cudaSuccess) {
     cudaGetLastError();
     return vrcclCudaError;
   }
-  *asyncErr = (vrcclResult_t)code;
+  *asyncErr = (vrcclResult_t)(code ? code : norm);
   return vrcclSuccess;
 }

@@ -292,7 +292,7 @@ def _linear_check(torch, v, rows, outs, ins, dtype, act, pad=0, offset=0, bias=T
     own = 1.2 * sums + 16 * EPS * (1 + np.abs(wz)) + (0 if Rv is None else 2 * EPS * np.abs(Rv))
     _close(y.get(), wy, u * np.abs(wy) * 1.01 + own + TINY[dtype], "y")
     assert y.intact() and x.intact() and w.intact()
-    assert v.vrcclLinearGetAsyncError() == 0
+    assert v.vrcclReplicaGetAsyncError() == 0
     return x, w, z, dy
 
 
@@ -316,7 +316,7 @@ def _linear_back(torch, v, rows, outs, ins, dtype, act, pad=0, offset=0, seed=2)
     es = 0 if act == "none" else (32 * EPS * np.abs(D) * (1 + np.abs(Z))).sum(0)
     _close(_host(db), wdb, u * np.abs(wdb) * 1.01 + es + (rows + 16) * EPS * dz.sum(0) + TINY[dtype], "dbias")
     assert dx.intact() and dw.intact() and dy.intact() and z.intact()
-    assert v.vrcclLinearGetAsyncError() == 0
+    assert v.vrcclReplicaGetAsyncError() == 0
     return x, w, z, dy, dx, dw, db
 
 
@@ -343,6 +343,14 @@ def test_linear_strides(torch, v, rows, pad, offset):
     _linear_check(torch, v, rows, 88, 104, "bfloat16", "silu", pad, offset)
     _linear_back(torch, v, rows, 88, 104, "bfloat16", "silu", pad, offset)
     _linear_back(torch, v, rows, 88, 104, "float16", "none", pad, offset)
+
+
+@pytest.mark.parametrize("rows,outs,ins,pad", [(129, 257, 65, 7), (300, 1001, 33, 23), (65, 63, 127, 1)])
+def test_linear_ragged_rows_on_vector_boundaries(torch, v, rows, outs, ins, pad):
+    """Rows that end inside a vector but start on one: nothing past a row's end is written."""
+    for act in ("none", "relu"):
+        _linear_check(torch, v, rows, outs, ins, "bfloat16", act, pad)
+        _linear_back(torch, v, rows, outs, ins, "bfloat16", act, pad)
 
 
 @pytest.mark.parametrize("rows,outs,ins", [(2048, 2560, 192), (4100, 1300, 320), (300, 5000, 64), (24, 6000, 2048),
