@@ -64,20 +64,21 @@ __device__ __forceinline__ float slope(float z) {
 
 // ------------------------------------------------------------ tcgen05, TMA
 
-// A wait that has not come true after this long never will: the kernel then
-// records a timeout, drains what it has in flight and ends.
-constexpr unsigned long long kWaitNs = 2000000000ull;
+// A wait that has not come true after so many cycles (a second and more) never
+// will: the kernel then records a timeout, drains what it has in flight and
+// ends. (The cycle counter: reading the global timer costs as much as a copy.)
+constexpr long long kWaitCycles = 3000000000ll, kDrainCycles = 200000000ll;
 
 __device__ int gLinearStatus;  // vrcclResult_t of the first device-side failure
 
 // false = gave up (this wait, or another one of the block)
 __device__ __forceinline__ bool waitBar(unsigned long long* bar, unsigned parity, volatile int* dead,
-                                        unsigned long long limit = kWaitNs) {
+                                        long long limit = kWaitCycles) {
   if (mbarTryWait(bar, parity)) return true;
-  const unsigned long long t0 = globalTimer();
+  const long long t0 = clock64();
   while (!mbarTryWait(bar, parity)) {
     if (*dead) return false;
-    if (globalTimer() - t0 > limit) {
+    if (clock64() - t0 > limit) {
       *dead = 1;
       atomicCAS(&gLinearStatus, 0, (int)vrcclTimeout);
       return false;
@@ -87,6 +88,22 @@ __device__ __forceinline__ bool waitBar(unsigned long long* bar, unsigned parity
 }
 __device__ __forceinline__ void mbarArriveExpect(unsigned long long* bar, unsigned bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smemAddr(bar)), "r"(bytes) : "memory");
+}
+// One lane of a converged warp. The TMA and MMA warps run their loops whole, so
+// that addresses and descriptors stay in uniform registers, and only the
+// copies and MMAs themselves are one lane's: with the loop in a single lane's
+// branch every MMA waited for its operands to be moved there, and a 64-deep
+// step took 650 cycles whatever the tile.
+__device__ __forceinline__ bool electOne() {
+  uint32_t p;
+  asm volatile(
+      "{\n"
+      ".reg .pred p;\n"
+      "elect.sync _|p, 0xffffffff;\n"
+      "selp.u32 %0, 1, 0, p;\n"
+      "}\n"
+      : "=r"(p));
+  return p != 0;
 }
 __device__ __forceinline__ uint32_t clusterRank() {
   uint32_t r;
@@ -335,7 +352,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) productKernel(const __grid
   __shared__ int deadWord;
   volatile int* dead = &deadWord;
   unsigned char* smem = dyn + ((1024 - (smemAddr(dyn) & 1023)) & 1023);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t rank = CG == 2 ? clusterRank() : 0;
   constexpr int kWorkers = BN >= 128 ? kEpilogueWarps : 4;  // warps that have 64 columns to finish
 
@@ -358,85 +375,92 @@ __global__ void __launch_bounds__(kProductThreads, 1) productKernel(const __grid
   if constexpr (CG == 2) clusterSync();
   __syncthreads();
   tcFenceAfter();
-  const uint32_t tmem = tmemSlot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, tmemSlot, 0);
 
   const int tilesM = (a.M + CG * kBM - 1) / (CG * kBM), tilesN = (a.N + BN - 1) / BN, tiles = tilesM * tilesN;
   const int steps = (a.K + kBK - 1) / kBK;
   const int first = blockIdx.x / CG, stride = gridDim.x / CG;
 
   if (warp == 0) {
-    if (lane == 0) {
-      int stage = 0, round = 0;
-      bool ok = true;
-      for (int tile = first; tile < tiles && ok; tile += stride) {
-        const int m = tile % tilesM * (CG * kBM) + (int)rank * kBM, n = tile / tilesM * BN + (int)rank * Sh::kBRows;
-        for (int k = 0; k < steps; ++k) {
-          if (round > 0 && !(ok = waitBar(&empty[stage], (round - 1) & 1, dead))) break;
-          unsigned char* sa = smem + stage * Sh::kStageBytes;
-          unsigned char* sb = sa + kBM * kBK * 2;
-          // both blocks' copies count on the first block's barrier, which its MMA thread waits on
+    const bool one = electOne();
+    const uint32_t firstBar = CG == 2 ? inBlock(&full[0], 0) : smemAddr(&full[0]);
+    int stage = 0, round = 0;
+    bool ok = true;
+    for (int tile = first; tile < tiles && ok; tile += stride) {
+      const int m = tile % tilesM * (CG * kBM) + (int)rank * kBM, n = tile / tilesM * BN + (int)rank * Sh::kBRows;
+      for (int k = 0; k < steps; ++k) {
+        if (round > 0 && !(ok = __all_sync(0xffffffffu, waitBar(&empty[stage], (round - 1) & 1, dead)))) break;
+        unsigned char* sa = smem + stage * Sh::kStageBytes;
+        unsigned char* sb = sa + kBM * kBK * 2;
+        const uint32_t bar = firstBar + stage * 8;
+        if (one) {
+          // both blocks' copies count on the first block's barrier, which its MMA warp waits on
           if (rank == 0) mbarArriveExpect(&full[stage], Sh::kStageBytes * CG);
-          const uint32_t bar = CG == 2 ? inBlock(&full[stage], 0) : smemAddr(&full[stage]);
           if (!a.aMN) {
             tmaLoad2d<CG>(&a.a, sa, bar, k * kBK, m);
           } else {
+#pragma unroll
             for (int i = 0; i < kBM / 64; ++i) tmaLoad2d<CG>(&a.a, sa + i * 8192, bar, m + i * 64, k * kBK);
           }
           if (!a.bMN) {
             tmaLoad2d<CG>(&a.b, sb, bar, k * kBK, n);
           } else {
+#pragma unroll
             for (int i = 0; i < Sh::kBRows / 64; ++i) tmaLoad2d<CG>(&a.b, sb + i * 8192, bar, n + i * 64, k * kBK);
           }
-          if (++stage == kStages) {
-            stage = 0;
-            ++round;
-          }
+        }
+        if (++stage == kStages) {
+          stage = 0;
+          ++round;
         }
       }
-      // given up: no copy may land after the block has gone
-      if (!ok && rank == 0) {
-        int quiet = 0;
-        for (int s = 0; s < kStages; ++s) {
-          const int issued = round + (s < stage ? 1 : 0);
-          if (issued > 0) waitBar(&full[s], (issued - 1) & 1, &quiet, 100000000ull);
-        }
+    }
+    // given up: no copy may land after the block has gone
+    if (!ok && rank == 0 && lane == 0) {
+      int quiet = 0;
+      for (int s = 0; s < kStages; ++s) {
+        const int issued = round + (s < stage ? 1 : 0);
+        if (issued > 0) waitBar(&full[s], (issued - 1) & 1, &quiet, kDrainCycles);
       }
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
+      const bool one = electOne();
       // f32 accumulators; A and B of the element type; majors; N / 8, M / 16
       const uint32_t idesc = 1u << 4 | (DT == vrcclBfloat16 ? 1u : 0u) << 7 | (DT == vrcclBfloat16 ? 1u : 0u) << 10 |
                              (a.aMN ? 1u : 0u) << 15 | (a.bMN ? 1u : 0u) << 16 | (uint32_t)(BN / 8) << 17 |
                              (uint32_t)(CG * kBM / 16) << 24;
       // 16 contraction elements on: 32 bytes along a K-major row, 16 rows of an MN-major tile
       const uint32_t aStep = a.aMN ? 2048 >> 4 : 32 >> 4, bStep = a.bMN ? 2048 >> 4 : 32 >> 4;
+      const uint64_t descA = operandDesc(smemAddr(smem), a.aMN), descB = operandDesc(smemAddr(smem) + kBM * kBK * 2, a.bMN);
       int stage = 0, round = 0, turn = 0;
       bool ok = true;
       for (int tile = first; tile < tiles && ok; tile += stride, ++turn) {
         const int acc = turn & 1, use = turn >> 1;
-        if (use > 0 && !(ok = waitBar(&accEmpty[acc], (use - 1) & 1, dead))) break;
+        if (use > 0 && !(ok = __all_sync(0xffffffffu, waitBar(&accEmpty[acc], (use - 1) & 1, dead)))) break;
         tcFenceAfter();
         const uint32_t d = tmem + acc * BN;
         for (int k = 0; k < steps; ++k) {
-          if (!(ok = waitBar(&full[stage], round & 1, dead))) break;
+          if (!(ok = __all_sync(0xffffffffu, waitBar(&full[stage], round & 1, dead)))) break;
           tcFenceAfter();
-          const uint32_t sa = smemAddr(smem + stage * Sh::kStageBytes);
-          const uint64_t da = operandDesc(sa, a.aMN), db = operandDesc(sa + kBM * kBK * 2, a.bMN);
+          const uint64_t da = descA + stage * (Sh::kStageBytes >> 4), db = descB + stage * (Sh::kStageBytes >> 4);
+          if (one) {
 #pragma unroll
-          for (int i = 0; i < kBK / 16; ++i) tcMma<CG>(d, da + i * aStep, db + i * bStep, idesc, k > 0 || i > 0);
-          tcCommit<CG>(&empty[stage]);
+            for (int i = 0; i < kBK / 16; ++i) tcMma<CG>(d, da + i * aStep, db + i * bStep, idesc, k > 0 || i > 0);
+            tcCommit<CG>(&empty[stage]);
+          }
           if (++stage == kStages) {
             stage = 0;
             ++round;
           }
         }
-        if (ok) tcCommit<CG>(&accFull[acc]);
+        if (ok && one) tcCommit<CG>(&accFull[acc]);
       }
-      if (!ok) {  // given up: the products in flight end before TMEM is freed
+      if (!ok && one) {  // given up: the products in flight end before TMEM is freed
         int quiet = 0;
         tcCommit<CG>(&drained);
-        waitBar(&drained, 0, &quiet, 100000000ull);
+        waitBar(&drained, 0, &quiet, kDrainCycles);
       }
     }
     __syncwarp();

@@ -123,7 +123,7 @@ constexpr int kTeamElems = 16;
 constexpr int kTeamCols = 512 * kTeamElems;
 constexpr int kMaxStages = 8;
 constexpr int kTeamSmem = 192 * 1024;  // of the 227 KB a block may have
-constexpr unsigned long long kRowWaitNs = 2000000000ull;
+constexpr long long kRowWaitCycles = 3000000000ll, kDrainCycles = 200000000ll;  // a second and more
 
 __device__ int gNormStatus;  // vrcclResult_t of the first device-side failure
 
@@ -273,11 +273,11 @@ __device__ __forceinline__ void teamSync(int team, int T) {
 }
 // Sets *dead when the copy has not come after a time in which it must have.
 __device__ __forceinline__ void waitRow(unsigned long long* bar, unsigned parity, int* dead,
-                                        unsigned long long limit = kRowWaitNs) {
+                                        long long limit = kRowWaitCycles) {
   if (mbarTryWait(bar, parity)) return;
-  const unsigned long long t0 = globalTimer();
+  const long long t0 = clock64();
   while (!mbarTryWait(bar, parity))
-    if (globalTimer() - t0 > limit) {
+    if (clock64() - t0 > limit) {
       *reinterpret_cast<volatile int*>(dead) = 1;
       return;
     }
@@ -287,7 +287,7 @@ __device__ __forceinline__ void waitRow(unsigned long long* bar, unsigned parity
 __device__ __noinline__ void abandon(unsigned long long* full, int stages, int stage, int round, bool first, int* dead) {
   if (!first) return;
   atomicCAS(&gNormStatus, 0, (int)vrcclTimeout);
-  for (int s = 0; s < stages; ++s) waitRow(&full[s], (round + (s < stage ? 1 : 0)) & 1, dead, 100000000ull);
+  for (int s = 0; s < stages; ++s) waitRow(&full[s], (round + (s < stage ? 1 : 0)) & 1, dead, kDrainCycles);
 }
 __device__ __forceinline__ void expectBytes(unsigned long long* bar, unsigned bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smemAddr(bar)), "r"(bytes) : "memory");
