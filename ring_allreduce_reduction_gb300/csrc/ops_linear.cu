@@ -21,6 +21,9 @@
 // linearFew streams W with wide loads over all multiprocessors instead.
 #include <cuda.h>
 
+#include <cstring>
+#include <utility>
+
 #include "ops_common.cuh"
 
 namespace vrccl {
@@ -35,10 +38,27 @@ __device__ __forceinline__ float logistic(float x) {
   return r;
 }
 
+// Phi(z), the normal distribution, and exp(-z^2/2), which its slope needs too:
+// Abramowitz and Stegun, Handbook of Mathematical Functions, 7.1.26,
+//   erfc(x) = t (a1 + t (a2 + t (a3 + t (a4 + t a5)))) exp(-x^2), t = 1 / (1 + 0.3275911 x), x = |z| / sqrt(2) >= 0,
+// whose error is below 1.5e-7: half that in Phi, about one unit of binary32 at
+// 1. It costs two special-function instructions and a dozen others where erff
+// costs some forty, which made the gradient's pass over dy and z compute bound.
+__device__ __forceinline__ float normalPhi(float z, float* density = nullptr) {
+  const float x = fabsf(z) * 0.70710678118654752f;
+  float t;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(fmaf(0.3275911f, x, 1.f)));
+  const float e = __expf(-0.5f * z * z);
+  const float p = t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 1.061405429f, -1.453152027f), 1.421413741f), -0.284496736f), 0.254829592f);
+  if (density) *density = e;
+  const float tail = 0.5f * p * e;  // Phi(-|z|)
+  return z > 0.f ? 1.f - tail : tail;
+}
+
 template <int ACT>
 __device__ __forceinline__ float activate(float z) {
   if constexpr (ACT == vrcclActRelu) return z > 0.f ? z : (z != z ? z : 0.f);
-  if constexpr (ACT == vrcclActGelu) return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
+  if constexpr (ACT == vrcclActGelu) return z * normalPhi(z);
   // (1 + tanh u) / 2 = 1 / (1 + exp(-2u)), which loses nothing where tanh u nears -1
   if constexpr (ACT == vrcclActGeluTanh)
     return z * logistic(-1.5957691216057308f * (z + 0.044715f * z * z * z));
@@ -48,8 +68,11 @@ __device__ __forceinline__ float activate(float z) {
 template <int ACT>
 __device__ __forceinline__ float slope(float z) {
   if constexpr (ACT == vrcclActRelu) return z > 0.f ? 1.f : 0.f;
-  if constexpr (ACT == vrcclActGelu)
-    return 0.5f * (1.f + erff(z * 0.70710678118654752f)) + z * __expf(-0.5f * z * z) * 0.39894228040143268f;
+  if constexpr (ACT == vrcclActGelu) {
+    float e;
+    const float phi = normalPhi(z, &e);
+    return phi + z * e * 0.39894228040143268f;
+  }
   // with y = z s(w), w = 2 sqrt(2/pi) (z + 0.044715 z^3), s(w) = 1 / (1 + exp(-w)):  y' = s + z s (1 - s) w'
   if constexpr (ACT == vrcclActGeluTanh) {
     const float s = logistic(-1.5957691216057308f * (z + 0.044715f * z * z * z));
@@ -236,7 +259,7 @@ constexpr int kEpilogueWarps = 8;
 constexpr int kProductThreads = 32 * (2 + kEpilogueWarps);  // TMA warp, MMA warp, epilogue warps
 constexpr int kStoreBytes = 32 * 64 * 2;                    // one warp's 32 rows x 64 columns on the way out
 
-struct ProductArgs {
+struct Problem {
   CUtensorMap a, b, dMap, zMap;
   void* d;               // [M, N]
   void* z;               // the sums before activation, or NULL
@@ -249,6 +272,39 @@ struct ProductArgs {
   bool wideR;            // the residual's rows start on 16-byte boundaries
   bool wideBias;
   int act;
+  int tilesM, tiles, steps;
+};
+
+// A launch computes one product or two (a linear layer's two gradients, which
+// would each leave part of the GPU idle in its last round of tiles). The first
+// one's tiles are dealt out in turn; unit u (a block, or a pair) then takes
+// tiles from[u] to from[u + 1] of the second, so that all end together.
+constexpr int kMaxUnits = 256;
+struct ProductArgs {
+  Problem p[2];
+  unsigned short from[kMaxUnits + 1];
+};
+
+// A unit's tiles in order.
+struct Walk {
+  int which, tile, stride, end;
+  __device__ __forceinline__ Walk(const ProductArgs& a, int unit, int units)
+      : which(0), tile(unit), stride(units), end(a.p[0].tiles) {
+    settle(a, unit);
+  }
+  __device__ __forceinline__ void settle(const ProductArgs& a, int unit) {
+    if (which == 0 && tile >= end) {
+      which = 1;
+      tile = a.from[unit];
+      end = a.from[unit + 1];
+      stride = 1;
+    }
+  }
+  __device__ __forceinline__ bool more() const { return tile < end; }
+  __device__ __forceinline__ void next(const ProductArgs& a, int unit) {
+    tile += stride;
+    settle(a, unit);
+  }
 };
 
 // A tile is CG x 128 rows of A by BN rows of B. In a pair of blocks (CG = 2)
@@ -268,7 +324,7 @@ struct ProductShape {
 // Writes one warp's finished 32 x 64 elements from its staging buffer (rows of
 // 128 bytes, 16-byte pieces swizzled by the row) to memory.
 template <int DT>
-__device__ __forceinline__ void storeBox(const ProductArgs& a, const CUtensorMap* map, void* out, size_t ld, bool wide,
+__device__ __forceinline__ void storeBox(const Problem& a, const CUtensorMap* map, void* out, size_t ld, bool wide,
                                          const unsigned char* buf, int m, int n, int lane) {
   if (wide) {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -303,7 +359,7 @@ __device__ __forceinline__ void stage32(unsigned char* buf, int half, int lane, 
 }
 
 template <int DT, int ACT>
-__device__ __forceinline__ void finish(const ProductArgs& a, float (&f)[32], size_t m, int n) {
+__device__ __forceinline__ void finish(const Problem& a, float (&f)[32], size_t m, int n) {
   using S = typename Ty<DT>::S;
 #pragma unroll
   for (int i = 0; i < 32; ++i) f[i] = activate<ACT>(f[i]);
@@ -325,7 +381,7 @@ __device__ __forceinline__ void finish(const ProductArgs& a, float (&f)[32], siz
   }
 }
 template <int DT>
-__device__ __forceinline__ void addBias(const ProductArgs& a, float (&f)[32], int n) {
+__device__ __forceinline__ void addBias(const Problem& a, float (&f)[32], int n) {
   const int left = a.N - n;
 #pragma unroll
   for (int v = 0; v < 4; ++v) {
@@ -343,7 +399,7 @@ __device__ __forceinline__ void addBias(const ProductArgs& a, float (&f)[32], in
 }
 
 template <int DT, int CG, int BN>
-__global__ void __launch_bounds__(kProductThreads, 1) productKernel(const __grid_constant__ ProductArgs a) {
+__global__ void __launch_bounds__(kProductThreads, 1) productKernel(const __grid_constant__ ProductArgs args) {
   using Sh = ProductShape<CG, BN>;
   constexpr int kStages = Sh::kStages;
   extern __shared__ unsigned char dyn[];
@@ -377,18 +433,17 @@ __global__ void __launch_bounds__(kProductThreads, 1) productKernel(const __grid
   tcFenceAfter();
   const uint32_t tmem = __shfl_sync(0xffffffffu, tmemSlot, 0);
 
-  const int tilesM = (a.M + CG * kBM - 1) / (CG * kBM), tilesN = (a.N + BN - 1) / BN, tiles = tilesM * tilesN;
-  const int steps = (a.K + kBK - 1) / kBK;
-  const int first = blockIdx.x / CG, stride = gridDim.x / CG;
+  const int unit = blockIdx.x / CG;
 
   if (warp == 0) {
     const bool one = electOne();
     const uint32_t firstBar = CG == 2 ? inBlock(&full[0], 0) : smemAddr(&full[0]);
     int stage = 0, round = 0;
     bool ok = true;
-    for (int tile = first; tile < tiles && ok; tile += stride) {
-      const int m = tile % tilesM * (CG * kBM) + (int)rank * kBM, n = tile / tilesM * BN + (int)rank * Sh::kBRows;
-      for (int k = 0; k < steps; ++k) {
+    for (Walk w(args, unit, gridDim.x / CG); w.more() && ok; w.next(args, unit)) {
+      const Problem& a = args.p[w.which];
+      const int m = w.tile % a.tilesM * (CG * kBM) + (int)rank * kBM, n = w.tile / a.tilesM * BN + (int)rank * Sh::kBRows;
+      for (int k = 0; k < a.steps; ++k) {
         if (round > 0 && !(ok = __all_sync(0xffffffffu, waitBar(&empty[stage], (round - 1) & 1, dead)))) break;
         unsigned char* sa = smem + stage * Sh::kStageBytes;
         unsigned char* sb = sa + kBM * kBK * 2;
@@ -427,21 +482,22 @@ __global__ void __launch_bounds__(kProductThreads, 1) productKernel(const __grid
   } else if (warp == 1) {
     if (rank == 0) {
       const bool one = electOne();
-      // f32 accumulators; A and B of the element type; majors; N / 8, M / 16
-      const uint32_t idesc = 1u << 4 | (DT == vrcclBfloat16 ? 1u : 0u) << 7 | (DT == vrcclBfloat16 ? 1u : 0u) << 10 |
-                             (a.aMN ? 1u : 0u) << 15 | (a.bMN ? 1u : 0u) << 16 | (uint32_t)(BN / 8) << 17 |
-                             (uint32_t)(CG * kBM / 16) << 24;
-      // 16 contraction elements on: 32 bytes along a K-major row, 16 rows of an MN-major tile
-      const uint32_t aStep = a.aMN ? 2048 >> 4 : 32 >> 4, bStep = a.bMN ? 2048 >> 4 : 32 >> 4;
-      const uint64_t descA = operandDesc(smemAddr(smem), a.aMN), descB = operandDesc(smemAddr(smem) + kBM * kBK * 2, a.bMN);
       int stage = 0, round = 0, turn = 0;
       bool ok = true;
-      for (int tile = first; tile < tiles && ok; tile += stride, ++turn) {
+      for (Walk w(args, unit, gridDim.x / CG); w.more() && ok; w.next(args, unit), ++turn) {
+        const Problem& a = args.p[w.which];
+        // f32 accumulators; A and B of the element type; majors; N / 8, M / 16
+        const uint32_t idesc = 1u << 4 | (DT == vrcclBfloat16 ? 1u : 0u) << 7 | (DT == vrcclBfloat16 ? 1u : 0u) << 10 |
+                               (a.aMN ? 1u : 0u) << 15 | (a.bMN ? 1u : 0u) << 16 | (uint32_t)(BN / 8) << 17 |
+                               (uint32_t)(CG * kBM / 16) << 24;
+        // 16 contraction elements on: 32 bytes along a K-major row, 16 rows of an MN-major tile
+        const uint32_t aStep = a.aMN ? 2048 >> 4 : 32 >> 4, bStep = a.bMN ? 2048 >> 4 : 32 >> 4;
+        const uint64_t descA = operandDesc(smemAddr(smem), a.aMN), descB = operandDesc(smemAddr(smem) + kBM * kBK * 2, a.bMN);
         const int acc = turn & 1, use = turn >> 1;
         if (use > 0 && !(ok = __all_sync(0xffffffffu, waitBar(&accEmpty[acc], (use - 1) & 1, dead)))) break;
         tcFenceAfter();
         const uint32_t d = tmem + acc * BN;
-        for (int k = 0; k < steps; ++k) {
+        for (int k = 0; k < a.steps; ++k) {
           if (!(ok = __all_sync(0xffffffffu, waitBar(&full[stage], round & 1, dead)))) break;
           tcFenceAfter();
           const uint64_t da = descA + stage * (Sh::kStageBytes >> 4), db = descB + stage * (Sh::kStageBytes >> 4);
@@ -470,8 +526,10 @@ __global__ void __launch_bounds__(kProductThreads, 1) productKernel(const __grid
     constexpr int kCols = BN / (kWorkers / 4);  // columns a warp finishes, 64 at a time
     unsigned char* buf = smem + kStages * Sh::kStageBytes + (warp - 2) * 2 * kStoreBytes;
     int turn = 0, which = 0;
-    for (int tile = first; tile < tiles; tile += stride, ++turn) {
-      const int m0 = tile % tilesM * (CG * kBM) + (int)rank * kBM + quarter * 32, n0 = tile / tilesM * BN + part * kCols;
+    for (Walk w(args, unit, gridDim.x / CG); w.more(); w.next(args, unit), ++turn) {
+      const Problem& a = args.p[w.which];
+      const int m0 = w.tile % a.tilesM * (CG * kBM) + (int)rank * kBM + quarter * 32;
+      const int n0 = w.tile / a.tilesM * BN + part * kCols;
       const int acc = turn & 1, use = turn >> 1;
       bool ok = lane != 0 || waitBar(&accFull[acc], use & 1, dead);
       if (!__all_sync(0xffffffffu, ok)) break;
@@ -636,6 +694,7 @@ struct SlopeArgs {
   int cols;
 };
 constexpr int kSlopeRows = 8;  // row groups of a block; 32 lanes of V columns across
+constexpr int kSlopeTurn = 4;  // rows a thread has in flight
 
 // dz = dy act'(z), rounded to the element type: the tensor cores take their
 // operands in it. The bias gradient sums the unrounded values.
@@ -648,30 +707,45 @@ __global__ void __launch_bounds__(256) linearSlope(const __grid_constant__ Slope
   const int c = (blockIdx.x * 32 + lane) * V;
   float sum[V] = {};
   if (c < a.cols) {
-    for (size_t r = (size_t)blockIdx.y * kSlopeRows + g; r < a.rows; r += (size_t)gridDim.y * kSlopeRows) {
-      float d[V], z[V];
-      const S* dy = static_cast<const S*>(a.dy) + r * a.lddy + c;
-      const S* zp = ACT == vrcclActNone ? nullptr : static_cast<const S*>(a.z) + r * a.ldz + c;
-      if constexpr (WIDE)
-        Vec16<DT>::expand(__ldg(reinterpret_cast<const uint4*>(dy)), d);
-      else
-        d[0] = Ty<DT>::toF(*dy);
-      if constexpr (ACT != vrcclActNone) {
-        if constexpr (WIDE)
-          Vec16<DT>::expand(__ldcs(reinterpret_cast<const uint4*>(zp)), z);
-        else
-          z[0] = Ty<DT>::toF(*zp);
+    const size_t step = (size_t)gridDim.y * kSlopeRows;
+    using Raw = std::conditional_t<WIDE, uint4, S>;
+    for (size_t r0 = (size_t)blockIdx.y * kSlopeRows + g; r0 < a.rows; r0 += kSlopeTurn * step) {
+      Raw d[kSlopeTurn], z[kSlopeTurn];  // the rows of a turn are all asked for before the first is used
 #pragma unroll
-        for (int e = 0; e < V; ++e) d[e] *= slope<ACT>(z[e]);
+      for (int u = 0; u < kSlopeTurn; ++u) {
+        const size_t r = r0 + u * step;
+        if (r < a.rows) {
+          d[u] = __ldg(reinterpret_cast<const Raw*>(static_cast<const S*>(a.dy) + r * a.lddy + c));
+          if constexpr (ACT != vrcclActNone)
+            z[u] = __ldcs(reinterpret_cast<const Raw*>(static_cast<const S*>(a.z) + r * a.ldz + c));
+        }
       }
 #pragma unroll
-      for (int e = 0; e < V; ++e) sum[e] += d[e];
-      if (a.dz) {
-        S* dz = static_cast<S*>(a.dz) + r * a.lddz + c;
+      for (int u = 0; u < kSlopeTurn; ++u) {
+        const size_t r = r0 + u * step;
+        if (r >= a.rows) break;
+        float f[V], h[V];
         if constexpr (WIDE)
-          *reinterpret_cast<uint4*>(dz) = Vec16<DT>::pack(d);
+          Vec16<DT>::expand(d[u], f);
         else
-          dz[0] = Ty<DT>::fromF(d[0]);
+          f[0] = Ty<DT>::toF(d[u]);
+        if constexpr (ACT != vrcclActNone) {
+          if constexpr (WIDE)
+            Vec16<DT>::expand(z[u], h);
+          else
+            h[0] = Ty<DT>::toF(z[u]);
+#pragma unroll
+          for (int e = 0; e < V; ++e) f[e] *= slope<ACT>(h[e]);
+        }
+#pragma unroll
+        for (int e = 0; e < V; ++e) sum[e] += f[e];
+        if (a.dz) {
+          S* dz = static_cast<S*>(a.dz) + r * a.lddz + c;
+          if constexpr (WIDE)
+            *reinterpret_cast<uint4*>(dz) = Vec16<DT>::pack(f);
+          else
+            dz[0] = Ty<DT>::fromF(f[0]);
+        }
       }
     }
   }
@@ -775,14 +849,32 @@ bool aligned(Operand& o, Scratch& ws, cudaStream_t st) {
   return true;
 }
 
+// A product and where its operands lie.
+struct Product {
+  Problem p;
+  Operand A, B;
+};
+Product makeProduct(const Operand& A, const Operand& B, void* d, size_t ldd, size_t M, size_t N, size_t K) {
+  Product q = {};
+  q.A = A;
+  q.B = B;
+  q.p.d = d;
+  q.p.ldd = ldd;
+  q.p.M = (int)M;
+  q.p.N = (int)N;
+  q.p.K = (int)K;
+  q.p.aMN = A.mn;
+  q.p.bMN = B.mn;
+  return q;
+}
+
+long long tileCount(const Problem& p, int bm, int bn) {
+  return (long long)((p.M + bm - 1) / bm) * ((p.N + bn - 1) / bn);
+}
+
 template <int DT, int CG, int BN>
-vrcclResult_t launchProduct(ProductArgs& a, const Operand& A, const Operand& B, cudaStream_t st) {
+vrcclResult_t launchProducts(const Product* q, int n, cudaStream_t st) {
   using Sh = ProductShape<CG, BN>;
-  if (!makeMap(&a.a, DT, A.p, A.ld, A.rows, A.cols, A.mn ? kBK : kBM) ||
-      !makeMap(&a.b, DT, B.p, B.ld, B.rows, B.cols, B.mn ? kBK : Sh::kBRows) ||
-      (a.wideD && !makeMap(&a.dMap, DT, a.d, a.ldd, a.M, a.N, 32)) ||
-      (a.wideZ && !makeMap(&a.zMap, DT, a.z, a.ldz, a.M, a.N, 32)))
-    return vrcclInternalError;
   static bool raised[64] = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return vrcclCudaError;
@@ -794,9 +886,55 @@ vrcclResult_t launchProduct(ProductArgs& a, const Operand& A, const Operand& B, 
     }
     raised[dev] = true;
   }
-  const long long tiles = (long long)((a.M + CG * kBM - 1) / (CG * kBM)) * ((a.N + BN - 1) / BN);
+  ProductArgs args;
+  memset(&args, 0, sizeof(args));
+  long long total = 0;
+  for (int i = 0; i < n; ++i) {
+    Problem& p = args.p[i];
+    const Operand &A = q[i].A, &B = q[i].B;
+    p = q[i].p;
+    p.wideR = p.residual && rowsAligned(p.residual, p.ldr, 2);
+    p.wideBias = (uintptr_t)p.bias % 16 == 0;
+    // a TMA store writes whole 16-byte pieces: rows that end inside one are stored by the warps
+    p.wideD = p.N % 8 == 0 && rowsAligned(p.d, p.ldd, 2);
+    p.wideZ = p.z && p.N % 8 == 0 && rowsAligned(p.z, p.ldz, 2);
+    p.tilesM = (p.M + CG * kBM - 1) / (CG * kBM);
+    p.tiles = (int)tileCount(p, CG * kBM, BN);
+    p.steps = (p.K + kBK - 1) / kBK;
+    total += p.tiles;
+    if (!makeMap(&p.a, DT, A.p, A.ld, A.rows, A.cols, A.mn ? kBK : kBM) ||
+        !makeMap(&p.b, DT, B.p, B.ld, B.rows, B.cols, B.mn ? kBK : Sh::kBRows) ||
+        (p.wideD && !makeMap(&p.dMap, DT, p.d, p.ldd, p.M, p.N, 32)) ||
+        (p.wideZ && !makeMap(&p.zMap, DT, p.z, p.ldz, p.M, p.N, 32)))
+      return vrcclInternalError;
+  }
+  const int units = (int)std::min<long long>(total, std::min(smCount() / CG, kMaxUnits));
+  if (n == 2) {
+    // every unit's share of the second product tops up what it has of the first, to the smallest common level
+    const long long steps0 = args.p[0].steps, steps1 = args.p[1].steps;
+    auto has = [&](int u) { return (args.p[0].tiles - u + units - 1) / units * steps0; };
+    auto holds = [&](long long level) {
+      long long t = 0;
+      for (int u = 0; u < units; ++u) t += std::max(0ll, level - has(u)) / steps1;
+      return t;
+    };
+    long long lo = 0, hi = has(0) + (long long)args.p[1].tiles * steps1;
+    while (lo < hi) {
+      const long long mid = (lo + hi) / 2;
+      if (holds(mid) >= args.p[1].tiles)
+        hi = mid;
+      else
+        lo = mid + 1;
+    }
+    long long given = 0;
+    for (int u = 0; u < units; ++u) {
+      args.from[u] = (unsigned short)given;
+      given = std::min<long long>(args.p[1].tiles, given + std::max(0ll, lo - has(u)) / steps1);
+    }
+    args.from[units] = (unsigned short)given;
+  }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)std::min<long long>(tiles, smCount() / CG) * CG);
+  cfg.gridDim = dim3((unsigned)(units * CG));
   cfg.blockDim = dim3(kProductThreads);
   cfg.dynamicSmemBytes = Sh::kSmem;
   cfg.stream = st;
@@ -806,27 +944,28 @@ vrcclResult_t launchProduct(ProductArgs& a, const Operand& A, const Operand& B, 
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, productKernel<DT, CG, BN>, a) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, productKernel<DT, CG, BN>, args) != cudaSuccess) {
     cudaGetLastError();
     return vrcclCudaError;
   }
   return vrcclSuccess;
 }
 
-// D = A B^T with the epilogue of `a`.
+// The widest tile that still gives every multiprocessor one.
 template <int DT>
-vrcclResult_t product(ProductArgs& a, const Operand& A, const Operand& B, cudaStream_t st) {
-  a.aMN = A.mn;
-  a.bMN = B.mn;
-  // a TMA store writes whole 16-byte pieces: rows that end inside one are stored by the warps
-  a.wideD = a.N % 8 == 0 && rowsAligned(a.d, a.ldd, 2);
-  a.wideZ = a.z && a.N % 8 == 0 && rowsAligned(a.z, a.ldz, 2);
-  a.wideR = a.residual && rowsAligned(a.residual, a.ldr, 2);
-  a.wideBias = (uintptr_t)a.bias % 16 == 0;
-  auto tiles = [&](long long bm, long long bn) { return (a.M + bm - 1) / bm * ((a.N + bn - 1) / bn); };
-  if (tiles(256, 256) >= smCount() / 2) return launchProduct<DT, 2, 256>(a, A, B, st);
-  if (tiles(128, 128) >= smCount()) return launchProduct<DT, 1, 128>(a, A, B, st);
-  return launchProduct<DT, 1, 64>(a, A, B, st);
+vrcclResult_t products(const Product* q, int n, cudaStream_t st) {
+  auto tiles = [&](int bm, int bn) {
+    long long t = 0;
+    for (int i = 0; i < n; ++i) t += tileCount(q[i].p, bm, bn);
+    return t;
+  };
+  if (n == 2 && tiles(256, 256) > 60000) {  // more than a launch counts: they fill the GPU one by one
+    const vrcclResult_t r = products<DT>(q, 1, st);
+    return r == vrcclSuccess ? products<DT>(q + 1, 1, st) : r;
+  }
+  if (tiles(256, 256) >= smCount() / 2) return launchProducts<DT, 2, 256>(q, n, st);
+  if (tiles(128, 128) >= smCount()) return launchProducts<DT, 1, 128>(q, n, st);
+  return launchProducts<DT, 1, 64>(q, n, st);
 }
 
 template <int DT, int MR>
@@ -910,32 +1049,21 @@ vrcclResult_t backward(const void* dy, size_t lddy, const void* z, size_t ldz, c
       linearBiasJoin<DT><<<(unsigned)((outs + 31) / 32), 256, 0, st>>>(s.partial, blocks, (int)outs, dbias);
   }
   if ((dx || dw) && !aligned(g, ws, st)) return vrcclInvalidArgument;
+  Product q[2];
+  int n = 0;
   if (dx) {
     Operand b = {w, ldw, outs, ins, true};
     if (!aligned(b, ws, st)) return vrcclInvalidArgument;
-    ProductArgs a = {};
-    a.d = dx;
-    a.ldd = lddx;
-    a.M = (int)rows;
-    a.N = (int)ins;
-    a.K = (int)outs;
-    const vrcclResult_t r = product<DT>(a, g, b, st);
-    if (r != vrcclSuccess) return r;
+    q[n++] = makeProduct(g, b, dx, lddx, rows, ins, outs);
   }
   if (dw) {
     Operand b = {x, ldx, rows, ins, true};
     if (!aligned(b, ws, st)) return vrcclInvalidArgument;
     g.mn = true;
-    ProductArgs a = {};
-    a.d = dw;
-    a.ldd = lddw;
-    a.M = (int)outs;
-    a.N = (int)ins;
-    a.K = (int)rows;
-    const vrcclResult_t r = product<DT>(a, g, b, st);
-    if (r != vrcclSuccess) return r;
+    q[n++] = makeProduct(g, b, dw, lddw, outs, ins, rows);
   }
-  return launchResult();
+  if (n == 2 && q[0].p.K < q[1].p.K) std::swap(q[0], q[1]);  // the longer tiles first: the shorter ones even out the end
+  return n ? products<DT>(q, n, st) : launchResult();
 }
 
 vrcclResult_t zeroRows(void* p, size_t ld, size_t rows, size_t cols, cudaStream_t st) {
@@ -1011,19 +1139,14 @@ extern "C" vrcclResult_t vrcclLinearForward(const void* x, size_t ldx, const voi
   Scratch ws = {static_cast<unsigned char*>(workspace), workspaceBytes};
   Operand A = {x, ldx, rows, ins, false}, B = {w, ldw, outs, ins, false};
   if (!aligned(A, ws, st) || !aligned(B, ws, st)) return vrcclInvalidArgument;
-  ProductArgs a = {};
-  a.d = y;
-  a.z = z;
-  a.bias = bias;
-  a.residual = residual;
-  a.ldd = ldy;
-  a.ldz = ldz;
-  a.ldr = ldr;
-  a.M = (int)rows;
-  a.N = (int)outs;
-  a.K = (int)ins;
-  a.act = act;
-  return dtype == vrcclBfloat16 ? product<vrcclBfloat16>(a, A, B, st) : product<vrcclFloat16>(a, A, B, st);
+  Product q = makeProduct(A, B, y, ldy, rows, outs, ins);
+  q.p.z = z;
+  q.p.bias = bias;
+  q.p.residual = residual;
+  q.p.ldz = ldz;
+  q.p.ldr = ldr;
+  q.p.act = act;
+  return dtype == vrcclBfloat16 ? products<vrcclBfloat16>(&q, 1, st) : products<vrcclFloat16>(&q, 1, st);
 }
 
 extern "C" vrcclResult_t vrcclLinearBackward(const void* dy, size_t lddy, const void* z, size_t ldz, const void* x,
