@@ -85,6 +85,16 @@ __device__ __forceinline__ float slope(float z) {
   return 1.f;
 }
 
+__device__ __forceinline__ float activateBy(int act, float z) {
+  switch (act) {
+    case vrcclActRelu: return activate<vrcclActRelu>(z);
+    case vrcclActGelu: return activate<vrcclActGelu>(z);
+    case vrcclActGeluTanh: return activate<vrcclActGeluTanh>(z);
+    case vrcclActSilu: return activate<vrcclActSilu>(z);
+  }
+  return z;
+}
+
 // ------------------------------------------------------------ tcgen05, TMA
 
 // A wait that has not come true after so many cycles (a second and more) never
@@ -242,10 +252,10 @@ __device__ __forceinline__ void tcLoad32(uint32_t addr, float (&f)[32]) {
 // rows of 64 contraction elements (128 bytes), eight rows to a swizzle block,
 // blocks 1024 bytes apart. MN-major: rows of 64 M (or N) elements, one row a
 // contraction index; eight of them make a swizzle block (1024 bytes apart),
-// and the next 64 M elements start 8192 bytes on (one 64 x 64 box).
-__device__ __forceinline__ uint64_t operandDesc(uint32_t addr, bool mn) {
+// and the next 64 M elements start a box of 64 x depth elements on.
+__device__ __forceinline__ uint64_t operandDesc(uint32_t addr, bool mn, int depth) {
   uint64_t d = (addr >> 4) & 0x3fff;
-  d |= (uint64_t)(mn ? 8192 >> 4 : 1) << 16;  // leading dimension
+  d |= (uint64_t)(mn ? depth * 128 >> 4 : 1) << 16;  // leading dimension
   d |= (uint64_t)(1024 >> 4) << 32;           // stride dimension
   d |= (uint64_t)1 << 46;                     // descriptor version
   d |= (uint64_t)2 << 61;                     // 128-byte swizzle
@@ -254,7 +264,7 @@ __device__ __forceinline__ uint64_t operandDesc(uint32_t addr, bool mn) {
 
 // ------------------------------------------------------------ the product
 
-constexpr int kBM = 128, kBK = 64;  // rows of A a block, contraction elements a stage
+constexpr int kBM = 128;  // rows of A a block
 constexpr int kEpilogueWarps = 8;
 constexpr int kProductThreads = 32 * (2 + kEpilogueWarps);  // TMA warp, MMA warp, epilogue warps
 constexpr int kStoreBytes = 32 * 64 * 2;                    // one warp's 32 rows x 64 columns on the way out
@@ -270,7 +280,6 @@ struct Problem {
   bool aMN, bMN;         // operand majors
   bool wideD, wideZ;     // d / z may be stored by TMA
   bool wideR;            // the residual's rows start on 16-byte boundaries
-  bool wideBias;
   int act;
   int tilesM, tiles, steps;
 };
@@ -315,8 +324,12 @@ struct Walk {
 template <int CG, int BN>
 struct ProductShape {
   static constexpr int kBRows = BN / CG;
+  // Contraction elements a stage. Waiting for a stage and signalling it free costs its MMA warp some 150 cycles: nothing
+  // under the MMAs of the wider tiles (which gain more from five shallow stages than from two deep ones: 4096 cubed on
+  // 128 x 128 tiles 107 us against 147), but as much again under a narrow one's.
+  static constexpr int kBK = BN <= 64 ? 128 : 64;
   static constexpr int kStageBytes = (kBM + kBRows) * kBK * 2;
-  static constexpr int kStages = BN == 64 ? 6 : 5;
+  static constexpr int kStages = BN == 64 ? 3 : 5;
   static constexpr int kSmem = kStages * kStageBytes + kEpilogueWarps * 2 * kStoreBytes + 1024;
   static constexpr int kTmemCols = 2 * BN;
 };
@@ -380,22 +393,77 @@ __device__ __forceinline__ void finish(const Problem& a, float (&f)[32], size_t 
     }
   }
 }
+// The bias of 64 columns from n on, a pair a lane, asked for before a tile's products are waited for; a column's value
+// then comes from its lane. (Loaded where it is used, each 32 columns waited 1200 cycles for it.)
 template <int DT>
-__device__ __forceinline__ void addBias(const Problem& a, float (&f)[32], int n) {
-  const int left = a.N - n;
+__device__ __forceinline__ uint32_t biasPair(const Problem& a, int n, int lane) {
+  const unsigned short* p = static_cast<const unsigned short*>(a.bias) + n + 2 * lane;
+  const uint32_t lo = n + 2 * lane < a.N ? p[0] : 0u, hi = n + 2 * lane + 1 < a.N ? p[1] : 0u;
+  return lo | hi << 16;
+}
+template <int DT>
+__device__ __forceinline__ void addBias(float (&f)[32], uint32_t pair, int half) {
 #pragma unroll
-  for (int v = 0; v < 4; ++v) {
-    if (a.wideBias && v * 8 + 8 <= left) {
-      float g[8];
-      Vec16<DT>::expand(__ldg(reinterpret_cast<const uint4*>(static_cast<const char*>(a.bias) + (size_t)n * 2) + v), g);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) f[v * 8 + e] += g[e];
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (v * 8 + e < left) f[v * 8 + e] += loadOne<DT>(a.bias, n + v * 8 + e);
-    }
+  for (int j = 0; j < 16; ++j) {
+    const float2 v = unpack2<DT>(__shfl_sync(0xffffffffu, pair, half * 16 + j));
+    f[2 * j] += v.x;
+    f[2 * j + 1] += v.y;
   }
+}
+
+// One stage of a block's operands: rows m.. of A and n.. of B, contraction elements k..k + BK. A K-major operand comes as
+// boxes of 64 contraction elements (one swizzled row each), an MN-major one as boxes of 64 rows.
+template <int CG, int BN>
+__device__ __forceinline__ void loadStage(const Problem& a, unsigned char* sa, uint32_t bar, int m, int n, int k) {
+  using Sh = ProductShape<CG, BN>;
+  constexpr int BK = Sh::kBK;
+  unsigned char* sb = sa + kBM * BK * 2;
+  if (!a.aMN) {
+#pragma unroll
+    for (int i = 0; i < BK / 64; ++i) tmaLoad2d<CG>(&a.a, sa + i * kBM * 128, bar, k + i * 64, m);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kBM / 64; ++i) tmaLoad2d<CG>(&a.a, sa + i * BK * 128, bar, m + i * 64, k);
+  }
+  if (!a.bMN) {
+#pragma unroll
+    for (int i = 0; i < BK / 64; ++i) tmaLoad2d<CG>(&a.b, sb + i * Sh::kBRows * 128, bar, k + i * 64, n);
+  } else {
+#pragma unroll
+    for (int i = 0; i < Sh::kBRows / 64; ++i) tmaLoad2d<CG>(&a.b, sb + i * BK * 128, bar, n + i * 64, k);
+  }
+}
+// How the MMAs of a problem address a stage: 16 contraction elements on are 32 bytes along a K-major row (and the next box
+// after four of them), 16 rows of an MN-major tile.
+struct Issue {
+  uint64_t descA, descB;
+  uint32_t idesc;
+  uint32_t aStep, bStep, aBox, bBox;
+};
+template <int DT, int CG, int BN>
+__device__ __forceinline__ Issue makeIssue(const Problem& a, uint32_t smem) {
+  using Sh = ProductShape<CG, BN>;
+  constexpr uint32_t kType = DT == vrcclBfloat16 ? 1u : 0u;
+  Issue q;
+  // f32 accumulators; A and B of the element type; majors; N / 8, M / 16
+  q.idesc = 1u << 4 | kType << 7 | kType << 10 | (a.aMN ? 1u : 0u) << 15 | (a.bMN ? 1u : 0u) << 16 |
+            (uint32_t)(BN / 8) << 17 | (uint32_t)(CG * kBM / 16) << 24;
+  q.descA = operandDesc(smem, a.aMN, Sh::kBK);
+  q.descB = operandDesc(smem + kBM * Sh::kBK * 2, a.bMN, Sh::kBK);
+  q.aStep = a.aMN ? 2048 >> 4 : 32 >> 4;
+  q.bStep = a.bMN ? 2048 >> 4 : 32 >> 4;
+  q.aBox = a.aMN ? 4 * 2048 >> 4 : kBM * 128 >> 4;
+  q.bBox = a.bMN ? 4 * 2048 >> 4 : Sh::kBRows * 128 >> 4;
+  return q;
+}
+template <int CG, int BN>
+__device__ __forceinline__ void issueStage(const Issue& q, uint32_t d, int stage, bool fresh) {
+  using Sh = ProductShape<CG, BN>;
+  const uint64_t da = q.descA + stage * (Sh::kStageBytes >> 4), db = q.descB + stage * (Sh::kStageBytes >> 4);
+#pragma unroll
+  for (int i = 0; i < Sh::kBK / 16; ++i)
+    tcMma<CG>(d, da + (i >> 2) * q.aBox + (i & 3) * q.aStep, db + (i >> 2) * q.bBox + (i & 3) * q.bStep, q.idesc,
+              !fresh || i > 0);
 }
 
 template <int DT, int CG, int BN>
@@ -445,24 +513,10 @@ __global__ void __launch_bounds__(kProductThreads, 1) productKernel(const __grid
       const int m = w.tile % a.tilesM * (CG * kBM) + (int)rank * kBM, n = w.tile / a.tilesM * BN + (int)rank * Sh::kBRows;
       for (int k = 0; k < a.steps; ++k) {
         if (round > 0 && !(ok = __all_sync(0xffffffffu, waitBar(&empty[stage], (round - 1) & 1, dead)))) break;
-        unsigned char* sa = smem + stage * Sh::kStageBytes;
-        unsigned char* sb = sa + kBM * kBK * 2;
-        const uint32_t bar = firstBar + stage * 8;
         if (one) {
           // both blocks' copies count on the first block's barrier, which its MMA warp waits on
           if (rank == 0) mbarArriveExpect(&full[stage], Sh::kStageBytes * CG);
-          if (!a.aMN) {
-            tmaLoad2d<CG>(&a.a, sa, bar, k * kBK, m);
-          } else {
-#pragma unroll
-            for (int i = 0; i < kBM / 64; ++i) tmaLoad2d<CG>(&a.a, sa + i * 8192, bar, m + i * 64, k * kBK);
-          }
-          if (!a.bMN) {
-            tmaLoad2d<CG>(&a.b, sb, bar, k * kBK, n);
-          } else {
-#pragma unroll
-            for (int i = 0; i < Sh::kBRows / 64; ++i) tmaLoad2d<CG>(&a.b, sb + i * 8192, bar, n + i * 64, k * kBK);
-          }
+          loadStage<CG, BN>(a, smem + stage * Sh::kStageBytes, firstBar + stage * 8, m, n, k * Sh::kBK);
         }
         if (++stage == kStages) {
           stage = 0;
@@ -486,13 +540,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) productKernel(const __grid
       bool ok = true;
       for (Walk w(args, unit, gridDim.x / CG); w.more() && ok; w.next(args, unit), ++turn) {
         const Problem& a = args.p[w.which];
-        // f32 accumulators; A and B of the element type; majors; N / 8, M / 16
-        const uint32_t idesc = 1u << 4 | (DT == vrcclBfloat16 ? 1u : 0u) << 7 | (DT == vrcclBfloat16 ? 1u : 0u) << 10 |
-                               (a.aMN ? 1u : 0u) << 15 | (a.bMN ? 1u : 0u) << 16 | (uint32_t)(BN / 8) << 17 |
-                               (uint32_t)(CG * kBM / 16) << 24;
-        // 16 contraction elements on: 32 bytes along a K-major row, 16 rows of an MN-major tile
-        const uint32_t aStep = a.aMN ? 2048 >> 4 : 32 >> 4, bStep = a.bMN ? 2048 >> 4 : 32 >> 4;
-        const uint64_t descA = operandDesc(smemAddr(smem), a.aMN), descB = operandDesc(smemAddr(smem) + kBM * kBK * 2, a.bMN);
+        const Issue q = makeIssue<DT, CG, BN>(a, smemAddr(smem));
         const int acc = turn & 1, use = turn >> 1;
         if (use > 0 && !(ok = __all_sync(0xffffffffu, waitBar(&accEmpty[acc], (use - 1) & 1, dead)))) break;
         tcFenceAfter();
@@ -500,10 +548,8 @@ __global__ void __launch_bounds__(kProductThreads, 1) productKernel(const __grid
         for (int k = 0; k < a.steps; ++k) {
           if (!(ok = __all_sync(0xffffffffu, waitBar(&full[stage], round & 1, dead)))) break;
           tcFenceAfter();
-          const uint64_t da = descA + stage * (Sh::kStageBytes >> 4), db = descB + stage * (Sh::kStageBytes >> 4);
           if (one) {
-#pragma unroll
-            for (int i = 0; i < kBK / 16; ++i) tcMma<CG>(d, da + i * aStep, db + i * bStep, idesc, k > 0 || i > 0);
+            issueStage<CG, BN>(q, d, stage, k == 0);
             tcCommit<CG>(&empty[stage]);
           }
           if (++stage == kStages) {
@@ -531,12 +577,18 @@ __global__ void __launch_bounds__(kProductThreads, 1) productKernel(const __grid
       const int m0 = w.tile % a.tilesM * (CG * kBM) + (int)rank * kBM + quarter * 32;
       const int n0 = w.tile / a.tilesM * BN + part * kCols;
       const int acc = turn & 1, use = turn >> 1;
+      uint32_t bias[kCols / 64];
+      if (a.bias)
+#pragma unroll
+        for (int i = 0; i < kCols / 64; ++i) bias[i] = biasPair<DT>(a, n0 + i * 64, lane);
       bool ok = lane != 0 || waitBar(&accFull[acc], use & 1, dead);
       if (!__all_sync(0xffffffffu, ok)) break;
       tcFenceAfter();
       const uint32_t from = tmem + ((uint32_t)(quarter * 32) << 16) + acc * BN + part * kCols;
       if (m0 < a.M) {
-        for (int c = 0; c < kCols && n0 + c < a.N; c += 64) {
+#pragma unroll
+        for (int c = 0; c < kCols; c += 64) {
+          if (n0 + c >= a.N) break;
           // the buffers take turns; the store that last read one has to be done with it
           unsigned char* zb = buf + which * kStoreBytes;
           if (a.z) which ^= 1;
@@ -554,7 +606,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) productKernel(const __grid
             float f[32];
             tcLoad32(from + c + h * 32, f);
             const int n = n0 + c + h * 32;
-            if (a.bias) addBias<DT>(a, f, n);
+            if (a.bias) addBias<DT>(f, bias[c / 64], h);
             if (a.z) stage32<DT>(zb, h, lane, f);
             const size_t m = m0 + lane;
             switch (a.act) {
@@ -589,9 +641,201 @@ __global__ void __launch_bounds__(kProductThreads, 1) productKernel(const __grid
   if (warp == 1) tmemFree<CG>(tmem, Sh::kTmemCols);
 }
 
+// ------------------------------------------------------------ split contraction
+
+// Few tiles and a long contraction: the blocks of a cluster take a part of it
+// each for one tile of 128 x BN, lay their sums out in shared memory, and each
+// finishes its share of the tile from everyone's, added in the blocks' order,
+// through distributed shared memory. One launch, no workspace, the same bits
+// every time.
+//
+// With few rows of x a tile of 128 of them would be mostly padding, and the
+// stages that hold it are missing for W, which is all such a call has to read.
+// Then the operands change places (SWAP): W gives the tile's 128 rows, x its
+// columns, and the result is turned back on the way out.
+constexpr int kMaxSplit = 8;
+template <int BN, bool SWAP>
+struct SplitShape {
+  static constexpr int kStages = BN == 32 ? 5 : 4;
+  static constexpr int kSmem = kStages * ProductShape<1, BN>::kStageBytes + 1024;
+  // floats from one row of the sums to the next (SWAP: from one column): 16-byte accesses fall on different banks
+  static constexpr int kRow = SWAP ? kBM + 4 : BN + 4;
+};
+
+template <int DT>
+__device__ __forceinline__ void finish4(const Problem& a, float (&f)[4], size_t m, int n, int cols) {
+  using S = typename Ty<DT>::S;
+  const int left = min(4, cols - n);
+  auto put = [&](void* out, size_t ld) {
+    S* o = static_cast<S*>(out) + m * ld + n;
+    if (left == 4 && ((uintptr_t)o & 7) == 0) {
+      *reinterpret_cast<uint2*>(o) = make_uint2(pack2<DT>(f[0], f[1]), pack2<DT>(f[2], f[3]));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < left) o[i] = Ty<DT>::fromF(f[i]);
+    }
+  };
+  if (a.bias) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < left) f[i] += loadOne<DT>(a.bias, n + i);
+  }
+  if (a.z) put(a.z, a.ldz);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = activateBy(a.act, f[i]);
+  if (a.residual) {
+    const S* r = static_cast<const S*>(a.residual) + m * a.ldr + n;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < left) f[i] += Ty<DT>::toF(r[i]);
+  }
+  put(a.d, a.ldd);
+}
+
+template <int DT, int BN, bool SWAP>
+__global__ void __launch_bounds__(kProductThreads, 1) productSplit(const __grid_constant__ Problem a, int parts) {
+  using Sh = ProductShape<1, BN>;
+  using Sp = SplitShape<BN, SWAP>;
+  constexpr int kStages = Sp::kStages;
+  extern __shared__ unsigned char dyn[];
+  __shared__ unsigned long long full[kStages], empty[kStages], accFull, drained;
+  __shared__ uint32_t tmemSlot;
+  __shared__ int deadWord;
+  volatile int* dead = &deadWord;
+  unsigned char* smem = dyn + ((1024 - (smemAddr(dyn) & 1023)) & 1023);
+  float* part = reinterpret_cast<float*>(smem);  // over the stages, once they have all been used
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const int rank = clusterRank(), tile = blockIdx.x / parts;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbarInit(&full[s], 1);
+      mbarInit(&empty[s], 1);
+    }
+    mbarInit(&accFull, 1);
+    mbarInit(&drained, 1);
+    deadWord = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) tmemAlloc<1>(&tmemSlot, BN);
+  tcFenceBefore();
+  __syncthreads();
+  tcFenceAfter();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, tmemSlot, 0);
+  const int m0 = tile % a.tilesM * kBM, n0 = tile / a.tilesM * BN;
+  const int rows = SWAP ? a.N : a.M, cols = SWAP ? a.M : a.N;  // of the result
+  const int per = (a.steps + parts - 1) / parts, lo = min(a.steps, rank * per), hi = min(a.steps, lo + per);
+  if (warp == 0) {
+    const bool one = electOne();
+    int stage = 0, round = 0;
+    bool ok = true;
+    for (int k = lo; k < hi; ++k) {
+      if (round > 0 && !(ok = __all_sync(0xffffffffu, waitBar(&empty[stage], (round - 1) & 1, dead)))) break;
+      if (one) {
+        mbarArriveExpect(&full[stage], Sh::kStageBytes);
+        loadStage<1, BN>(a, smem + stage * Sh::kStageBytes, smemAddr(&full[stage]), m0, n0, k * Sh::kBK);
+      }
+      if (++stage == kStages) {
+        stage = 0;
+        ++round;
+      }
+    }
+    if (!ok && lane == 0) {  // given up: no copy may land after the block has gone
+      int quiet = 0;
+      for (int s = 0; s < kStages; ++s) {
+        const int issued = round + (s < stage ? 1 : 0);
+        if (issued > 0) waitBar(&full[s], (issued - 1) & 1, &quiet, kDrainCycles);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    const bool one = electOne();
+    const Issue q = makeIssue<DT, 1, BN>(a, smemAddr(smem));
+    int stage = 0, round = 0;
+    bool ok = true;
+    for (int k = lo; k < hi; ++k) {
+      if (!(ok = __all_sync(0xffffffffu, waitBar(&full[stage], round & 1, dead)))) break;
+      tcFenceAfter();
+      if (one) {
+        issueStage<1, BN>(q, tmem, stage, k == lo);
+        tcCommit<1>(&empty[stage]);
+      }
+      if (++stage == kStages) {
+        stage = 0;
+        ++round;
+      }
+    }
+    if (one) {
+      if (ok) {
+        tcCommit<1>(&accFull);
+      } else {  // given up: the products in flight end before TMEM is freed
+        int quiet = 0;
+        tcCommit<1>(&drained);
+        waitBar(&drained, 0, &quiet, kDrainCycles);
+      }
+    }
+    __syncwarp();
+  } else if (warp < 6) {
+    const int quarter = warp & 3;  // the TMEM lanes this warp may read
+    const bool ok = __all_sync(0xffffffffu, waitBar(&accFull, 0, dead));
+    tcFenceAfter();
+    const int r = quarter * 32 + lane;
+#pragma unroll
+    for (int h = 0; h < BN / 32 && ok; ++h) {
+      float f[32];
+      if (lo < hi) {
+        tcLoad32(tmem + ((uint32_t)(quarter * 32) << 16) + h * 32, f);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) f[i] = 0.f;
+      }
+      if constexpr (SWAP) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) part[(h * 32 + i) * Sp::kRow + r] = f[i];
+      } else {
+#pragma unroll
+        for (int i = 0; i < 32; i += 4)
+          *reinterpret_cast<float4*>(part + r * Sp::kRow + h * 32 + i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
+      }
+    }
+    tcFenceBefore();
+  }
+  __syncthreads();
+  clusterSync();
+  if (warp >= 2) {
+    // groups of four outputs along a row of the result, dealt to the blocks in runs
+    constexpr int kAcross = SWAP ? kBM / 4 : BN / 4, kDown = SWAP ? BN : kBM;
+    const int share = kAcross * kDown / parts;
+    for (int g = rank * share + threadIdx.x - 64; g < (rank + 1) * share; g += kProductThreads - 64) {
+      const int r = g / kAcross, c = g % kAcross * 4;
+      const int m = (SWAP ? n0 : m0) + r, n = (SWAP ? m0 : n0) + c;
+      if (m >= rows || n >= cols) continue;
+      float f[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int s = 0; s < parts; ++s) {
+        float4 v;
+        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                     : "r"(inBlock(part + r * Sp::kRow + c, s))
+                     : "memory");
+        f[0] += v.x;
+        f[1] += v.y;
+        f[2] += v.z;
+        f[3] += v.w;
+      }
+      finish4<DT>(a, f, m, n, cols);
+    }
+  }
+  __syncwarp();
+  clusterSync();  // no block leaves while another reads its sums
+  tcFenceAfter();
+  if (warp == 1) tmemFree<1>(tmem, BN);
+}
+
 // ------------------------------------------------------------ few rows
 
-constexpr int kFewRows = 8;
+// One or two rows: 4096 x 4096 in 7.6 us where the split product takes 10.4. Up to eight where W would first have to be
+// copied for TMA, which alone reads and writes it once more.
+constexpr int kFewRows = 2, kFewRowsUnaligned = 8;
 constexpr int kFewOuts = 4;  // outputs a block: x is read once for four rows of W
 constexpr int kFewThreads = 256;
 
@@ -606,14 +850,22 @@ struct FewArgs {
   int rows, outs, ins, act;
 };
 
-__device__ __forceinline__ float activateBy(int act, float z) {
-  switch (act) {
-    case vrcclActRelu: return activate<vrcclActRelu>(z);
-    case vrcclActGelu: return activate<vrcclActGelu>(z);
-    case vrcclActGeluTanh: return activate<vrcclActGeluTanh>(z);
-    case vrcclActSilu: return activate<vrcclActSilu>(z);
+// The warp's sums of N values a lane, value i in the lanes i (32 / N) and on: at every step a lane gives half of its values
+// to its partner and keeps the other half, N - 1 shuffles and a few where N separate sums would take 5 N.
+template <int N>
+__device__ __forceinline__ float laneSums(float (&v)[N], int lane) {
+  int o = 16;
+#pragma unroll
+  for (int half = N / 2; half > 0; half /= 2, o /= 2) {
+    const bool upper = lane & o;
+#pragma unroll
+    for (int i = 0; i < half; ++i) {
+      const float give = upper ? v[i] : v[i + half], keep = upper ? v[i + half] : v[i];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+    }
   }
-  return z;
+  for (; o > 0; o /= 2) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+  return v[0];
 }
 
 // MR rows of x against four rows of W a block, the contraction dealt to the
@@ -652,13 +904,9 @@ __global__ void __launch_bounds__(kFewThreads) linearFew(const __grid_constant__
         for (int e = 0; e < V; ++e) acc[o][m] += wf[o][e] * xf[e];
     }
   }
-#pragma unroll
-  for (int o = 0; o < kFewOuts; ++o)
-#pragma unroll
-    for (int m = 0; m < MR; ++m) {
-      const float s = warpSum(acc[o][m]);
-      if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5][o * MR + m] = s;
-    }
+  const float s = laneSums(reinterpret_cast<float(&)[kFewOuts * MR]>(acc), threadIdx.x & 31);
+  constexpr int kLanes = 32 / (kFewOuts * MR);  // lanes that hold the same sum
+  if (threadIdx.x % kLanes == 0) part[threadIdx.x >> 5][(threadIdx.x & 31) / kLanes] = s;
   __syncthreads();
   if (threadIdx.x < kFewOuts * MR) {
     const int n = n0 + threadIdx.x / MR, m = threadIdx.x % MR;
@@ -676,13 +924,22 @@ __global__ void __launch_bounds__(kFewThreads) linearFew(const __grid_constant__
 
 // ------------------------------------------------------------ operands and the bias gradient
 
-// A copy whose rows start on 16-byte boundaries, which TMA needs. The ragged
-// end of a row is left as it is: no copy reads past the row's last element.
-__global__ void __launch_bounds__(256) packRows(const unsigned short* src, size_t lds, unsigned short* dst, size_t ldd,
-                                                size_t rows, size_t cols) {
-  for (size_t r = blockIdx.y; r < rows; r += gridDim.y)
-    for (size_t c = (size_t)blockIdx.x * 256 + threadIdx.x; c < cols; c += (size_t)gridDim.x * 256)
-      dst[r * ldd + c] = src[r * lds + c];
+// Copies whose rows start on 16-byte boundaries, which TMA needs; one launch
+// for all operands of a call. What is left of a row's last 16 bytes stays as it
+// is: no copy reads past the row's last element.
+struct PackJob {
+  const unsigned short* src;
+  unsigned short* dst;
+  size_t lds, ldd, rows, cols;
+};
+struct PackArgs {
+  PackJob job[3];
+};
+__global__ void __launch_bounds__(256) packRows(const __grid_constant__ PackArgs a) {
+  const PackJob& j = a.job[blockIdx.z];
+  for (size_t r = blockIdx.y; r < j.rows; r += gridDim.y)
+    for (size_t c = (size_t)blockIdx.x * 256 + threadIdx.x; c < j.cols; c += (size_t)gridDim.x * 256)
+      j.dst[r * j.ldd + c] = j.src[r * j.lds + c];
 }
 
 struct SlopeArgs {
@@ -832,22 +1089,35 @@ struct Scratch {
   }
 };
 
-// Workspace that aligned() takes for an operand.
+// Workspace that a copy of an operand takes.
 size_t packNeed(const void* p, size_t ld, size_t rows, size_t cols) {
   return rowsAligned(p, ld, 2) ? 0 : packedBytes(rows, cols);
 }
-// The operand with its rows on 16-byte boundaries, copied where they are not.
-bool aligned(Operand& o, Scratch& ws, cudaStream_t st) {
-  if (rowsAligned(o.p, o.ld, 2)) return true;
-  unsigned short* q = static_cast<unsigned short*>(ws.take(packedBytes(o.rows, o.cols)));
-  if (!q) return false;
-  const size_t ld = packedLd(o.cols);
-  const dim3 grid((unsigned)std::min<size_t>((o.cols + 255) / 256, 64), (unsigned)std::min<size_t>(o.rows, 4096));
-  packRows<<<grid, 256, 0, st>>>(static_cast<const unsigned short*>(o.p), o.ld, q, ld, o.rows, o.cols);
-  o.p = q;
-  o.ld = ld;
-  return true;
-}
+// Operands to be copied before a call's products.
+struct Packing {
+  PackArgs args = {};
+  int jobs = 0;
+  // The operand as the products will find it; false: the workspace is too small.
+  bool add(Operand& o, Scratch& ws) {
+    if (rowsAligned(o.p, o.ld, 2)) return true;
+    unsigned short* q = static_cast<unsigned short*>(ws.take(packedBytes(o.rows, o.cols)));
+    if (!q) return false;
+    args.job[jobs++] = {static_cast<const unsigned short*>(o.p), q, o.ld, packedLd(o.cols), o.rows, o.cols};
+    o.p = q;
+    o.ld = packedLd(o.cols);
+    return true;
+  }
+  void launch(cudaStream_t st) const {
+    if (!jobs) return;
+    size_t rows = 0, cols = 0;
+    for (int i = 0; i < jobs; ++i) {
+      rows = std::max(rows, args.job[i].rows);
+      cols = std::max(cols, args.job[i].cols);
+    }
+    const dim3 grid((unsigned)std::min<size_t>((cols + 255) / 256, 64), (unsigned)std::min<size_t>(rows, 4096), (unsigned)jobs);
+    packRows<<<grid, 256, 0, st>>>(args);
+  }
+};
 
 // A product and where its operands lie.
 struct Product {
@@ -894,16 +1164,15 @@ vrcclResult_t launchProducts(const Product* q, int n, cudaStream_t st) {
     const Operand &A = q[i].A, &B = q[i].B;
     p = q[i].p;
     p.wideR = p.residual && rowsAligned(p.residual, p.ldr, 2);
-    p.wideBias = (uintptr_t)p.bias % 16 == 0;
     // a TMA store writes whole 16-byte pieces: rows that end inside one are stored by the warps
     p.wideD = p.N % 8 == 0 && rowsAligned(p.d, p.ldd, 2);
     p.wideZ = p.z && p.N % 8 == 0 && rowsAligned(p.z, p.ldz, 2);
     p.tilesM = (p.M + CG * kBM - 1) / (CG * kBM);
     p.tiles = (int)tileCount(p, CG * kBM, BN);
-    p.steps = (p.K + kBK - 1) / kBK;
+    p.steps = (p.K + Sh::kBK - 1) / Sh::kBK;
     total += p.tiles;
-    if (!makeMap(&p.a, DT, A.p, A.ld, A.rows, A.cols, A.mn ? kBK : kBM) ||
-        !makeMap(&p.b, DT, B.p, B.ld, B.rows, B.cols, B.mn ? kBK : Sh::kBRows) ||
+    if (!makeMap(&p.a, DT, A.p, A.ld, A.rows, A.cols, A.mn ? Sh::kBK : kBM) ||
+        !makeMap(&p.b, DT, B.p, B.ld, B.rows, B.cols, B.mn ? Sh::kBK : Sh::kBRows) ||
         (p.wideD && !makeMap(&p.dMap, DT, p.d, p.ldd, p.M, p.N, 32)) ||
         (p.wideZ && !makeMap(&p.zMap, DT, p.z, p.ldz, p.M, p.N, 32)))
       return vrcclInternalError;
@@ -951,41 +1220,137 @@ vrcclResult_t launchProducts(const Product* q, int n, cudaStream_t st) {
   return vrcclSuccess;
 }
 
-// The widest tile that still gives every multiprocessor one.
+template <int DT, int BN, bool SWAP>
+vrcclResult_t launchSplit(const Product& q, int parts, cudaStream_t st) {
+  using Sh = ProductShape<1, BN>;
+  using Sp = SplitShape<BN, SWAP>;
+  static bool raised[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return vrcclCudaError;
+  if (!raised[dev]) {
+    if (cudaFuncSetAttribute(productSplit<DT, BN, SWAP>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sp::kSmem) !=
+        cudaSuccess) {
+      cudaGetLastError();
+      return vrcclCudaError;
+    }
+    raised[dev] = true;
+  }
+  Problem p = q.p;
+  const Operand &A = SWAP ? q.B : q.A, &B = SWAP ? q.A : q.B;
+  if (SWAP) {
+    std::swap(p.M, p.N);
+    std::swap(p.aMN, p.bMN);
+  }
+  p.tilesM = (p.M + kBM - 1) / kBM;
+  p.tiles = (int)tileCount(p, kBM, BN);
+  p.steps = (p.K + Sh::kBK - 1) / Sh::kBK;
+  if (!makeMap(&p.a, DT, A.p, A.ld, A.rows, A.cols, A.mn ? Sh::kBK : kBM) ||
+      !makeMap(&p.b, DT, B.p, B.ld, B.rows, B.cols, B.mn ? Sh::kBK : Sh::kBRows))
+    return vrcclInternalError;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(p.tiles * parts));
+  cfg.blockDim = dim3(kProductThreads);
+  cfg.dynamicSmemBytes = Sp::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = parts;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, productSplit<DT, BN, SWAP>, p, parts) != cudaSuccess) {
+    cudaGetLastError();
+    return vrcclCudaError;
+  }
+  return vrcclSuccess;
+}
+
+// Blocks to a cluster for `tiles` tiles of `steps` stages: as many as find a multiprocessor each and two stages of work.
+// (Eight blocks that fill a multiprocessor each are hard to place: 16 clusters of them took 15 us where 16 of four took 11,
+// so they are left to calls with few tiles.)
+int splitParts(long long tiles, long long steps) {
+  int parts = 1;
+  while (parts < kMaxSplit && tiles * parts * 2 <= smCount() && parts * 4 <= steps && (parts < 4 || tiles <= 8)) parts *= 2;
+  return parts;
+}
+
+// Which tile: the one whose last unit ends first, by measured cycles: a step
+// of 64 contraction elements and a tile's epilogue (which runs under the next
+// tile's steps where they take longer). At 4096 cubed: pairs 83 us, 128 x 128
+// tiles 107, 128 x 64 tiles 171; at 1024 cubed 12.4, 8.8 and 8.3.
+enum Tile { kPair256, kBlock128, kBlock64, kSplit64, kSwap32, kSwap64 };
+struct Choice {
+  Tile tile;
+  int parts;
+};
+Choice chooseTile(const Product* q, int n) {
+  if (n == 1 && q->p.M <= 64 && !q->p.aMN && !q->p.bMN) {
+    const bool narrow = q->p.M <= 32;
+    return {narrow ? kSwap32 : kSwap64, splitParts((q->p.N + kBM - 1) / kBM, (q->p.K + 127) / 128)};
+  }
+  struct {
+    Tile tile;
+    int bm, bn, blocks, step, end;
+  } static const kinds[3] = {{kPair256, 256, 256, 2, 520, 6000}, {kBlock128, 128, 128, 1, 420, 3000}, {kBlock64, 128, 64, 1, 341, 2200}};
+  Choice best = {kPair256, 1};
+  double least = 1e300;
+  for (const auto& k : kinds) {
+    const int units = smCount() / k.blocks;
+    double cycles = 0, longest = 0;
+    long long tiles = 0;
+    for (int i = 0; i < n; ++i) {
+      const double tile = std::max<double>((q[i].p.K + 63) / 64 * k.step, k.end);
+      const long long t = tileCount(q[i].p, k.bm, k.bn);
+      // one product: whole rounds of tiles; two: the second evens out the end
+      cycles += tile * (n == 1 ? (double)((t + units - 1) / units) : (double)t / units);
+      longest = std::max(longest, tile);
+      tiles += t;
+    }
+    cycles = std::max(n == 1 ? cycles : cycles + longest / 4, longest) + k.end;
+    if (cycles < least) {
+      least = cycles;
+      best = {k.tile, 1};
+    }
+    if (k.tile == kBlock64 && n == 1) {
+      const int parts = splitParts(tiles, (q->p.K + 127) / 128);
+      const double split = longest / parts + k.end + 3000;
+      if (parts > 1 && split < least) best = {kSplit64, parts};
+    }
+  }
+  return best;
+}
+
 template <int DT>
 vrcclResult_t products(const Product* q, int n, cudaStream_t st) {
-  auto tiles = [&](int bm, int bn) {
-    long long t = 0;
-    for (int i = 0; i < n; ++i) t += tileCount(q[i].p, bm, bn);
-    return t;
-  };
-  if (n == 2 && tiles(256, 256) > 60000) {  // more than a launch counts: they fill the GPU one by one
+  if (n == 2 && tileCount(q[0].p, 256, 256) + tileCount(q[1].p, 256, 256) > 60000) {
+    // more than a launch counts: they fill the GPU one by one
     const vrcclResult_t r = products<DT>(q, 1, st);
     return r == vrcclSuccess ? products<DT>(q + 1, 1, st) : r;
   }
-  if (tiles(256, 256) >= smCount() / 2) return launchProducts<DT, 2, 256>(q, n, st);
-  if (tiles(128, 128) >= smCount()) return launchProducts<DT, 1, 128>(q, n, st);
-  return launchProducts<DT, 1, 64>(q, n, st);
+  const Choice c = chooseTile(q, n);
+  switch (c.tile) {
+    case kPair256: return launchProducts<DT, 2, 256>(q, n, st);
+    case kBlock128: return launchProducts<DT, 1, 128>(q, n, st);
+    case kBlock64: return launchProducts<DT, 1, 64>(q, n, st);
+    case kSplit64: return launchSplit<DT, 64, false>(q[0], c.parts, st);
+    case kSwap32: return launchSplit<DT, 32, true>(q[0], c.parts, st);
+    case kSwap64: return launchSplit<DT, 64, true>(q[0], c.parts, st);
+  }
+  return vrcclInternalError;
 }
 
-template <int DT, int MR>
-void launchFew(const FewArgs& a, bool wide, cudaStream_t st) {
-  const unsigned grid = (unsigned)((a.outs + kFewOuts - 1) / kFewOuts);
-  if (wide)
-    linearFew<DT, MR, true><<<grid, kFewThreads, 0, st>>>(a);
-  else
-    linearFew<DT, MR, false><<<grid, kFewThreads, 0, st>>>(a);
+template <int DT, int MR, bool WIDE>
+void launchFew(const FewArgs& a, cudaStream_t st) {
+  linearFew<DT, MR, WIDE><<<(unsigned)((a.outs + kFewOuts - 1) / kFewOuts), kFewThreads, 0, st>>>(a);
 }
 template <int DT>
 vrcclResult_t few(const FewArgs& a, bool wide, cudaStream_t st) {
-  if (a.rows == 1)
-    launchFew<DT, 1>(a, wide, st);
-  else if (a.rows == 2)
-    launchFew<DT, 2>(a, wide, st);
-  else if (a.rows <= 4)
-    launchFew<DT, 4>(a, wide, st);
+  if (wide && a.rows <= 2)
+    a.rows == 1 ? launchFew<DT, 1, true>(a, st) : launchFew<DT, 2, true>(a, st);
+  else if (a.rows <= 2)
+    a.rows == 1 ? launchFew<DT, 1, false>(a, st) : launchFew<DT, 2, false>(a, st);
   else
-    launchFew<DT, 8>(a, wide, st);
+    a.rows <= 4 ? launchFew<DT, 4, false>(a, st) : launchFew<DT, 8, false>(a, st);
   return launchResult();
 }
 
@@ -1048,19 +1413,16 @@ vrcclResult_t backward(const void* dy, size_t lddy, const void* z, size_t ldz, c
     if (dbias)
       linearBiasJoin<DT><<<(unsigned)((outs + 31) / 32), 256, 0, st>>>(s.partial, blocks, (int)outs, dbias);
   }
-  if ((dx || dw) && !aligned(g, ws, st)) return vrcclInvalidArgument;
+  Packing pack;
+  Operand wt = {w, ldw, outs, ins, true}, xt = {x, ldx, rows, ins, true};
+  if (((dx || dw) && !pack.add(g, ws)) || (dx && !pack.add(wt, ws)) || (dw && !pack.add(xt, ws))) return vrcclInvalidArgument;
+  pack.launch(st);
   Product q[2];
   int n = 0;
-  if (dx) {
-    Operand b = {w, ldw, outs, ins, true};
-    if (!aligned(b, ws, st)) return vrcclInvalidArgument;
-    q[n++] = makeProduct(g, b, dx, lddx, rows, ins, outs);
-  }
+  if (dx) q[n++] = makeProduct(g, wt, dx, lddx, rows, ins, outs);
   if (dw) {
-    Operand b = {x, ldx, rows, ins, true};
-    if (!aligned(b, ws, st)) return vrcclInvalidArgument;
     g.mn = true;
-    q[n++] = makeProduct(g, b, dw, lddw, outs, ins, rows);
+    q[n++] = makeProduct(g, xt, dw, lddw, outs, ins, rows);
   }
   if (n == 2 && q[0].p.K < q[1].p.K) std::swap(q[0], q[1]);  // the longer tiles first: the shorter ones even out the end
   return n ? products<DT>(q, n, st) : launchResult();
@@ -1108,10 +1470,11 @@ extern "C" vrcclResult_t vrcclLinearForward(const void* x, size_t ldx, const voi
       (!(residual == y && ldr == ldy) && overlap(y, ySpan, residual, spanBytes(ldr, rows, outs, 2))))
     return vrcclInvalidArgument;
   cudaStream_t st = (cudaStream_t)stream;
-  if (rows <= kFewRows || ins == 0) {
-    // ins == 0 is a sum over nothing: the epilogue of zeros, eight rows a call
-    const bool wide = ins % 8 == 0 && rowsAligned(x, ldx, 2) && rowsAligned(w, ldw, 2);
-    for (size_t r = 0; r < rows; r += kFewRows) {
+  const bool apart = rowsAligned(x, ldx, 2) && rowsAligned(w, ldw, 2);
+  if (rows <= (size_t)(apart ? kFewRows : kFewRowsUnaligned) || ins == 0) {
+    // ins == 0 is a sum over nothing: the epilogue of zeros, a few rows a launch
+    const bool wide = ins % 8 == 0 && apart && rows <= (size_t)kFewRows;
+    for (size_t r = 0; r < rows; r += kFewRowsUnaligned) {
       FewArgs a = {};
       a.x = static_cast<const char*>(x) + r * ldx * 2 * (ins != 0);
       a.w = w;
@@ -1124,7 +1487,7 @@ extern "C" vrcclResult_t vrcclLinearForward(const void* x, size_t ldx, const voi
       a.ldr = ldr;
       a.ldy = ldy;
       a.ldz = ldz;
-      a.rows = (int)std::min<size_t>(kFewRows, rows - r);
+      a.rows = (int)std::min<size_t>(kFewRowsUnaligned, rows - r);
       a.outs = (int)outs;
       a.ins = (int)ins;
       a.act = act;
@@ -1138,7 +1501,9 @@ extern "C" vrcclResult_t vrcclLinearForward(const void* x, size_t ldx, const voi
   if (need && (!workspace || workspaceBytes < need)) return vrcclInvalidArgument;
   Scratch ws = {static_cast<unsigned char*>(workspace), workspaceBytes};
   Operand A = {x, ldx, rows, ins, false}, B = {w, ldw, outs, ins, false};
-  if (!aligned(A, ws, st) || !aligned(B, ws, st)) return vrcclInvalidArgument;
+  Packing pack;
+  if (!pack.add(A, ws) || !pack.add(B, ws)) return vrcclInvalidArgument;
+  pack.launch(st);
   Product q = makeProduct(A, B, y, ldy, rows, outs, ins);
   q.p.z = z;
   q.p.bias = bias;

@@ -361,6 +361,17 @@ def test_linear_many_tiles(torch, v, rows, outs, ins):
     _linear_back(torch, v, rows, outs, ins, "bfloat16", "none")
 
 
+@pytest.mark.parametrize("rows,outs,ins", [(3, 4096, 512), (5, 1000, 1000), (16, 1024, 4096), (20, 130, 2056), (32, 136, 136),
+                                           (33, 1000, 2048), (64, 64, 4096), (65, 520, 1536), (128, 1024, 2048),
+                                           (250, 300, 1100), (512, 512, 4096), (130, 72, 4104)])
+def test_linear_split_contractions(torch, v, rows, outs, ins):
+    """Few rows or few tiles against a long contraction: every way a call is cut."""
+    for act in ("silu", "none"):
+        _linear_check(torch, v, rows, outs, ins, "bfloat16", act)
+    _linear_check(torch, v, rows, outs, ins, "float16", "gelu", 8, 8)
+    _linear_back(torch, v, rows, outs, ins, "bfloat16", "none")
+
+
 def test_linear_residual_in_place(torch, v):
     for rows in (3, 150):
         x, w, b, r, _ = _linear_mats(torch, rows, 136, 64, "bfloat16", 0, 0, 4)
