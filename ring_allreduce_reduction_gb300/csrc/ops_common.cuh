@@ -46,6 +46,45 @@ int normStatus(int* code);
 // Multiprocessors of the current device (asked for once a device).
 int smCount();
 
+// A kernel that may be launched while the one before it on its stream still
+// runs (LaunchShape::after): waits for that one's results. And in the one before: the
+// rest of this block's work needs no multiprocessor's worth of room, so the
+// next kernel's blocks may come in and wait.
+__device__ __forceinline__ void waitForPrevious() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void letNextIn() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+// Launch with a block's dynamic shared memory and cluster; `after`: without waiting for the stream's previous kernel to end
+// (`fn` calls waitForPrevious() before it touches memory), so that the launch runs under that kernel.
+struct LaunchShape {
+  dim3 grid;
+  int threads, smem, cluster;  // cluster: blocks, or 0
+  bool after;
+};
+template <typename... Params, typename... Args>
+vrcclResult_t launchShaped(void (*fn)(Params...), const LaunchShape& s, cudaStream_t st, const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = s.grid;
+  cfg.blockDim = dim3((unsigned)s.threads);
+  cfg.dynamicSmemBytes = (size_t)s.smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  cfg.attrs = attr;
+  if (s.after) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (s.cluster) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+    attr[cfg.numAttrs].val.clusterDim.x = (unsigned)s.cluster;
+    attr[cfg.numAttrs].val.clusterDim.y = attr[cfg.numAttrs].val.clusterDim.z = 1;
+    ++cfg.numAttrs;
+  }
+  if (cudaLaunchKernelEx(&cfg, fn, Params(args)...) != cudaSuccess) {
+    cudaGetLastError();
+    return vrcclCudaError;
+  }
+  return vrcclSuccess;
+}
+
 // ------------------------------------------------------------ element access
 // N consecutive elements of type DT as binary32. With N elements in 16 (or
 // 8, 4) bytes one wide load; the caller guarantees the alignment.
@@ -148,6 +187,24 @@ __device__ __forceinline__ float blockSum(float x, float* s) {
   if (lane == 0) s[threadIdx.x >> 5] = x;
   __syncthreads();
   return warpSum(lane < warps ? s[lane] : 0.f);
+}
+
+// The sum of `rows` values `stride` apart, one column a lane, the rows dealt to
+// a block's 32 warps and joined in warp order; the result in warp 0.
+__device__ __forceinline__ float columnSum(const float* p, int rows, size_t stride, bool exists) {
+  __shared__ float part[32][32];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  float s = 0.f;
+  if (exists)
+#pragma unroll 8
+    for (int r = w; r < rows; r += 32) s += p[r * stride];
+  part[w][lane] = s;
+  __syncthreads();
+  if (w == 0) {
+#pragma unroll
+    for (int i = 1; i < 32; ++i) s += part[i][lane];
+  }
+  return s;
 }
 
 }  // namespace vrccl

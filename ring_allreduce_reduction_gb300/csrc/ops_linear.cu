@@ -500,6 +500,8 @@ __global__ void __launch_bounds__(kProductThreads, 1) productKernel(const __grid
   __syncthreads();
   tcFenceAfter();
   const uint32_t tmem = __shfl_sync(0xffffffffu, tmemSlot, 0);
+  letNextIn();
+  waitForPrevious();
 
   const int unit = blockIdx.x / CG;
 
@@ -722,6 +724,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) productSplit(const __grid_
   __syncthreads();
   tcFenceAfter();
   const uint32_t tmem = __shfl_sync(0xffffffffu, tmemSlot, 0);
+  waitForPrevious();
   const int m0 = tile % a.tilesM * kBM, n0 = tile / a.tilesM * BN;
   const int rows = SWAP ? a.N : a.M, cols = SWAP ? a.M : a.N;  // of the result
   const int per = (a.steps + parts - 1) / parts, lo = min(a.steps, rank * per), hi = min(a.steps, lo + per);
@@ -937,6 +940,8 @@ struct PackArgs {
 };
 __global__ void __launch_bounds__(256) packRows(const __grid_constant__ PackArgs a) {
   const PackJob& j = a.job[blockIdx.z];
+  letNextIn();
+  waitForPrevious();
   for (size_t r = blockIdx.y; r < j.rows; r += gridDim.y)
     for (size_t c = (size_t)blockIdx.x * 256 + threadIdx.x; c < j.cols; c += (size_t)gridDim.x * 256)
       j.dst[r * j.ldd + c] = j.src[r * j.lds + c];
@@ -963,6 +968,7 @@ __global__ void __launch_bounds__(256) linearSlope(const __grid_constant__ Slope
   const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
   const int c = (blockIdx.x * 32 + lane) * V;
   float sum[V] = {};
+  letNextIn();
   if (c < a.cols) {
     const size_t step = (size_t)gridDim.y * kSlopeRows;
     using Raw = std::conditional_t<WIDE, uint4, S>;
@@ -1021,19 +1027,11 @@ __global__ void __launch_bounds__(256) linearSlope(const __grid_constant__ Slope
 }
 
 template <int DT>
-__global__ void __launch_bounds__(256) linearBiasJoin(const float* partial, int blocks, int cols, void* db) {
-  __shared__ float part[8][32];
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
-  float s = 0.f;
-  if (c < cols)
-    for (int b = w; b < blocks; b += 8) s += partial[(size_t)b * cols + c];
-  part[w][lane] = s;
-  __syncthreads();
-  if (w == 0 && c < cols) {
-#pragma unroll
-    for (int i = 1; i < 8; ++i) s += part[i][lane];
-    static_cast<typename Ty<DT>::S*>(db)[c] = Ty<DT>::fromF(s);
-  }
+__global__ void __launch_bounds__(1024) linearBiasJoin(const float* partial, int blocks, int cols, void* db) {
+  const int c = blockIdx.x * 32 + (threadIdx.x & 31);
+  waitForPrevious();
+  const float s = columnSum(partial + c, blocks, cols, c < cols);
+  if (threadIdx.x < 32 && c < cols) static_cast<typename Ty<DT>::S*>(db)[c] = Ty<DT>::fromF(s);
 }
 
 // ------------------------------------------------------------ host
@@ -1107,15 +1105,15 @@ struct Packing {
     o.ld = packedLd(o.cols);
     return true;
   }
-  void launch(cudaStream_t st) const {
-    if (!jobs) return;
+  vrcclResult_t launch(bool after, cudaStream_t st) const {
+    if (!jobs) return vrcclSuccess;
     size_t rows = 0, cols = 0;
     for (int i = 0; i < jobs; ++i) {
       rows = std::max(rows, args.job[i].rows);
       cols = std::max(cols, args.job[i].cols);
     }
     const dim3 grid((unsigned)std::min<size_t>((cols + 255) / 256, 64), (unsigned)std::min<size_t>(rows, 4096), (unsigned)jobs);
-    packRows<<<grid, 256, 0, st>>>(args);
+    return launchShaped(packRows, {grid, 256, 0, 0, after}, st, args);
   }
 };
 
@@ -1143,7 +1141,7 @@ long long tileCount(const Problem& p, int bm, int bn) {
 }
 
 template <int DT, int CG, int BN>
-vrcclResult_t launchProducts(const Product* q, int n, cudaStream_t st) {
+vrcclResult_t launchProducts(const Product* q, int n, bool after, cudaStream_t st) {
   using Sh = ProductShape<CG, BN>;
   static bool raised[64] = {};
   int dev = 0;
@@ -1202,26 +1200,12 @@ vrcclResult_t launchProducts(const Product* q, int n, cudaStream_t st) {
     }
     args.from[units] = (unsigned short)given;
   }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(units * CG));
-  cfg.blockDim = dim3(kProductThreads);
-  cfg.dynamicSmemBytes = Sh::kSmem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = CG;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, productKernel<DT, CG, BN>, args) != cudaSuccess) {
-    cudaGetLastError();
-    return vrcclCudaError;
-  }
-  return vrcclSuccess;
+  return launchShaped(productKernel<DT, CG, BN>, {dim3((unsigned)(units * CG)), kProductThreads, Sh::kSmem, CG, after}, st,
+                      args);
 }
 
 template <int DT, int BN, bool SWAP>
-vrcclResult_t launchSplit(const Product& q, int parts, cudaStream_t st) {
+vrcclResult_t launchSplit(const Product& q, int parts, bool after, cudaStream_t st) {
   using Sh = ProductShape<1, BN>;
   using Sp = SplitShape<BN, SWAP>;
   static bool raised[64] = {};
@@ -1247,22 +1231,8 @@ vrcclResult_t launchSplit(const Product& q, int parts, cudaStream_t st) {
   if (!makeMap(&p.a, DT, A.p, A.ld, A.rows, A.cols, A.mn ? Sh::kBK : kBM) ||
       !makeMap(&p.b, DT, B.p, B.ld, B.rows, B.cols, B.mn ? Sh::kBK : Sh::kBRows))
     return vrcclInternalError;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(p.tiles * parts));
-  cfg.blockDim = dim3(kProductThreads);
-  cfg.dynamicSmemBytes = Sp::kSmem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = parts;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, productSplit<DT, BN, SWAP>, p, parts) != cudaSuccess) {
-    cudaGetLastError();
-    return vrcclCudaError;
-  }
-  return vrcclSuccess;
+  return launchShaped(productSplit<DT, BN, SWAP>,
+                      {dim3((unsigned)(p.tiles * parts)), kProductThreads, Sp::kSmem, parts, after}, st, p, parts);
 }
 
 // Blocks to a cluster for `tiles` tiles of `steps` stages: as many as find a multiprocessor each and two stages of work.
@@ -1320,21 +1290,22 @@ Choice chooseTile(const Product* q, int n) {
   return best;
 }
 
+// `after`: the stream's last kernel is this call's own and lets the next one in.
 template <int DT>
-vrcclResult_t products(const Product* q, int n, cudaStream_t st) {
+vrcclResult_t products(const Product* q, int n, bool after, cudaStream_t st) {
   if (n == 2 && tileCount(q[0].p, 256, 256) + tileCount(q[1].p, 256, 256) > 60000) {
     // more than a launch counts: they fill the GPU one by one
-    const vrcclResult_t r = products<DT>(q, 1, st);
-    return r == vrcclSuccess ? products<DT>(q + 1, 1, st) : r;
+    const vrcclResult_t r = products<DT>(q, 1, after, st);
+    return r == vrcclSuccess ? products<DT>(q + 1, 1, false, st) : r;
   }
   const Choice c = chooseTile(q, n);
   switch (c.tile) {
-    case kPair256: return launchProducts<DT, 2, 256>(q, n, st);
-    case kBlock128: return launchProducts<DT, 1, 128>(q, n, st);
-    case kBlock64: return launchProducts<DT, 1, 64>(q, n, st);
-    case kSplit64: return launchSplit<DT, 64, false>(q[0], c.parts, st);
-    case kSwap32: return launchSplit<DT, 32, true>(q[0], c.parts, st);
-    case kSwap64: return launchSplit<DT, 64, true>(q[0], c.parts, st);
+    case kPair256: return launchProducts<DT, 2, 256>(q, n, after, st);
+    case kBlock128: return launchProducts<DT, 1, 128>(q, n, after, st);
+    case kBlock64: return launchProducts<DT, 1, 64>(q, n, after, st);
+    case kSplit64: return launchSplit<DT, 64, false>(q[0], c.parts, after, st);
+    case kSwap32: return launchSplit<DT, 32, true>(q[0], c.parts, after, st);
+    case kSwap64: return launchSplit<DT, 64, true>(q[0], c.parts, after, st);
   }
   return vrcclInternalError;
 }
@@ -1385,6 +1356,9 @@ vrcclResult_t backward(const void* dy, size_t lddy, const void* z, size_t ldz, c
                        size_t ldw, void* dx, size_t lddx, void* dw, size_t lddw, void* dbias, size_t rows, size_t outs,
                        size_t ins, int act, Scratch ws, cudaStream_t st) {
   Operand g = {dy, lddy, rows, outs, false};
+  const float* partial = nullptr;
+  int blocks = 0;
+  bool after = false;
   const bool rewrite = act != vrcclActNone && (dx || dw);
   if (rewrite || dbias) {
     SlopeArgs s = {};
@@ -1400,23 +1374,24 @@ vrcclResult_t backward(const void* dy, size_t lddy, const void* z, size_t ldz, c
       g.p = s.dz;
       g.ld = s.lddz;
     }
-    const int blocks = slopeBlocks(rows, outs);
     if (dbias && !(s.partial = static_cast<float*>(ws.take(biasBytes(rows, outs)))))
       return vrcclInvalidArgument;
     const bool wide = outs % 8 == 0 && rowsAligned(dy, lddy, 2) && (act == vrcclActNone || rowsAligned(z, ldz, 2));
     const int across = wide ? 256 : 32;
-    const dim3 grid((unsigned)((outs + across - 1) / across), (unsigned)blocks);
+    const dim3 grid((unsigned)((outs + across - 1) / across), (unsigned)slopeBlocks(rows, outs));
     if (wide)
       launchSlope<DT, true>(act, grid, s, st);
     else
       launchSlope<DT, false>(act, grid, s, st);
-    if (dbias)
-      linearBiasJoin<DT><<<(unsigned)((outs + 31) / 32), 256, 0, st>>>(s.partial, blocks, (int)outs, dbias);
+    partial = s.partial;
+    blocks = (int)grid.y;
+    after = true;
   }
   Packing pack;
   Operand wt = {w, ldw, outs, ins, true}, xt = {x, ldx, rows, ins, true};
   if (((dx || dw) && !pack.add(g, ws)) || (dx && !pack.add(wt, ws)) || (dw && !pack.add(xt, ws))) return vrcclInvalidArgument;
-  pack.launch(st);
+  if (pack.launch(after, st) != vrcclSuccess) return vrcclCudaError;
+  after |= pack.jobs > 0;
   Product q[2];
   int n = 0;
   if (dx) q[n++] = makeProduct(g, wt, dx, lddx, rows, ins, outs);
@@ -1425,7 +1400,15 @@ vrcclResult_t backward(const void* dy, size_t lddy, const void* z, size_t ldz, c
     q[n++] = makeProduct(g, xt, dw, lddw, outs, ins, rows);
   }
   if (n == 2 && q[0].p.K < q[1].p.K) std::swap(q[0], q[1]);  // the longer tiles first: the shorter ones even out the end
-  return n ? products<DT>(q, n, st) : launchResult();
+  if (n) {
+    const vrcclResult_t r = products<DT>(q, n, after, st);
+    if (r != vrcclSuccess) return r;
+  }
+  // last: nothing waits for it, and its launch runs under the products
+  if (dbias)
+    return launchShaped(linearBiasJoin<DT>, {dim3((unsigned)((outs + 31) / 32)), 1024, 0, 0, true}, st, partial, blocks,
+                        (int)outs, dbias);
+  return launchResult();
 }
 
 vrcclResult_t zeroRows(void* p, size_t ld, size_t rows, size_t cols, cudaStream_t st) {
@@ -1503,7 +1486,7 @@ extern "C" vrcclResult_t vrcclLinearForward(const void* x, size_t ldx, const voi
   Operand A = {x, ldx, rows, ins, false}, B = {w, ldw, outs, ins, false};
   Packing pack;
   if (!pack.add(A, ws) || !pack.add(B, ws)) return vrcclInvalidArgument;
-  pack.launch(st);
+  if (pack.launch(false, st) != vrcclSuccess) return vrcclCudaError;
   Product q = makeProduct(A, B, y, ldy, rows, outs, ins);
   q.p.z = z;
   q.p.bias = bias;
@@ -1511,7 +1494,8 @@ extern "C" vrcclResult_t vrcclLinearForward(const void* x, size_t ldx, const voi
   q.p.ldz = ldz;
   q.p.ldr = ldr;
   q.p.act = act;
-  return dtype == vrcclBfloat16 ? products<vrcclBfloat16>(&q, 1, st) : products<vrcclFloat16>(&q, 1, st);
+  return dtype == vrcclBfloat16 ? products<vrcclBfloat16>(&q, 1, pack.jobs > 0, st)
+                                : products<vrcclFloat16>(&q, 1, pack.jobs > 0, st);
 }
 
 extern "C" vrcclResult_t vrcclLinearBackward(const void* dy, size_t lddy, const void* z, size_t ldz, const void* x,

@@ -164,7 +164,6 @@ __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
 // blocks that the matrix's ends cut are read straight from memory.
 struct Window {
   uintptr_t row, lo, hi;
-  bool cut;
 };
 __device__ __forceinline__ Window window(const void* p, size_t ld, size_t row, size_t rows, int cols, int E) {
   Window w;
@@ -173,15 +172,8 @@ __device__ __forceinline__ Window window(const void* p, size_t ld, size_t row, s
   const uintptr_t end = w.row + (uintptr_t)cols * E;
   w.lo = w.row & ~(uintptr_t)15;
   w.hi = (end + 15) & ~(uintptr_t)15;
-  w.cut = false;
-  if (row == 0 && w.lo < base) {
-    w.lo += 16;
-    w.cut = true;
-  }
-  if (row == rows - 1 && w.hi > end) {
-    w.hi -= 16;
-    w.cut = true;
-  }
+  if (row == 0 && w.lo < base) w.lo += 16;
+  if (row == rows - 1 && w.hi > end) w.hi -= 16;
   if (w.hi < w.lo) w.hi = w.lo;
   return w;
 }
@@ -221,15 +213,22 @@ struct Team {
         for (int e = 0; e < V; ++e) f[j * V + e] = g[e];
       }
     } else {
-      const Window w = window(p, ld, row, rows, cols, E);
-      const S* v = reinterpret_cast<const S*>(slot + (w.row & 15));
+      const unsigned skew = ((unsigned)(uintptr_t)p + (unsigned)row * (unsigned)ld * E) & 15;
+      const S* v = reinterpret_cast<const S*>(slot + skew);
+      const bool cut = (row == 0 && skew != 0) || (row == rows - 1 && ((skew + (unsigned)cols * E) & 15) != 0);
+      if (!cut) {
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const int c = j * T + t;
-        f[j] = 0.f;
-        if (c < cols) {
+        for (int j = 0; j < NV; ++j) {
+          const int c = j * T + t;
+          f[j] = c < cols ? Ty<DT>::toF(v[c]) : 0.f;
+        }
+      } else {
+        const Window w = window(p, ld, row, rows, cols, E);
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+          const int c = j * T + t;
           const uintptr_t at = w.row + (uintptr_t)c * E;
-          f[j] = Ty<DT>::toF(w.cut && (at < w.lo || at >= w.hi) ? *(const S*)at : v[c]);
+          f[j] = c < cols ? Ty<DT>::toF(at < w.lo || at >= w.hi ? *(const S*)at : v[c]) : 0.f;
         }
       }
     }
@@ -486,6 +485,7 @@ __global__ void __launch_bounds__(512) normBackwardTeams(const __grid_constant__
     }
   }
   const float inv = 1.f / (float)cols;
+  letNextIn();
   float nextMean = 0.f, nextRstd = 0.f;
   if (first < a.rows) {
     nextMean = a.mean[first];
@@ -761,24 +761,15 @@ __global__ void __launch_bounds__(256) normColumns(const __grid_constant__ NormA
 }
 
 // dgamma and dbeta from the blocks' partial sums: 32 columns a block, the
-// partial rows split over its 8 warps and joined in warp order.
-__global__ void __launch_bounds__(256) normJoin(const float* partial, int blocks, int cols, void* dgamma, void* dbeta,
-                                                int ptype) {
-  __shared__ float part[8][32];
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + lane;
-  const int which = blockIdx.y;
-  float s = 0.f;
-  if (c < cols)
-    for (int b = w; b < blocks; b += 8) s += partial[(size_t)b * 2 * cols + (size_t)which * cols + c];
-  part[w][lane] = s;
-  __syncthreads();
-  if (w == 0 && c < cols) {
-#pragma unroll
-    for (int i = 1; i < 8; ++i) s += part[i][lane];
-    void* out = which ? dbeta : dgamma;
-    if (out) storeParam(out, ptype, c, s);
-  }
+// partial rows split over its 32 warps (a handful each, all asked for at once)
+// and joined in warp order.
+__global__ void __launch_bounds__(1024) normJoin(const float* partial, int blocks, int cols, void* dgamma, void* dbeta,
+                                                 int ptype) {
+  const int c = blockIdx.x * 32 + (threadIdx.x & 31), which = blockIdx.y;
+  waitForPrevious();
+  const float s = columnSum(partial + (size_t)which * cols + c, blocks, (size_t)2 * cols, c < cols);
+  void* out = which ? dbeta : dgamma;
+  if (threadIdx.x < 32 && c < cols && out) storeParam(out, ptype, c, s);
 }
 
 // ------------------------------------------------------------ host
@@ -988,7 +979,7 @@ extern "C" vrcclResult_t vrcclLayerNormBackward(const void* dy, size_t lddy, con
   const vrcclResult_t r = launchNorm<false>(dtype, s, (unsigned)blocks, a, st);
   if (r != vrcclSuccess) return r;
   if (weights)
-    normJoin<<<dim3((unsigned)((cols + 31) / 32), 2), 256, 0, st>>>(static_cast<const float*>(workspace), blocks,
-                                                                    (int)cols, dgamma, dbeta, paramType);
-  return launchResult();
+    return launchShaped(normJoin, {dim3((unsigned)((cols + 31) / 32), 2), 1024, 0, 0, true}, st,
+                        static_cast<const float*>(workspace), blocks, (int)cols, dgamma, dbeta, (int)paramType);
+  return vrcclSuccess;
 }

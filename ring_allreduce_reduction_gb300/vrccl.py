@@ -111,9 +111,14 @@ def _ptr(x) -> int:
     return int(x)
 
 
+# The current stream's handle without a Stream object, which takes 3 us to
+# make: as long as a launch.
+_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch.cuda.current_device
+
+
 def _stream(s) -> int | None:
     if s is None:
-        return torch.cuda.current_stream().cuda_stream
+        return _raw_stream(_current_device())
     if isinstance(s, torch.cuda.Stream):
         return s.cuda_stream
     return int(s)
