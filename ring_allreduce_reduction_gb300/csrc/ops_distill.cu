@@ -33,7 +33,9 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 512;  // of a block, at most
+constexpr int kUnroll = 4;     // vectors a thread asks for at once
+constexpr int kSeen = 2 * VRCCL_DISTILL_MAX_K;  // hash table slots; 2^11, which the hash is shifted to
 
 struct DistillArgs {
   const void* logits;
@@ -50,73 +52,51 @@ struct DistillArgs {
   float temperature, invT;
 };
 
-// The row's kept teacher entries in shared memory.
-struct Entries {
-  float p[VRCCL_DISTILL_MAX_K];     // p_j, 0 where not kept
-  float logp[VRCCL_DISTILL_MAX_K];
-  float s[VRCCL_DISTILL_MAX_K];     // the student's logit there
-  int at[VRCCL_DISTILL_MAX_K];      // the entry's index, -1 where not kept
-};
-
 __device__ __forceinline__ float warpMax(float x) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
   return x;
 }
-__device__ __forceinline__ float blockMax(float x, float* s) {
-  x = warpMax(x);
-  const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-  if (lane == 0) s[threadIdx.x >> 5] = x;
-  __syncthreads();
-  return warpMax(lane < warps ? s[lane] : -INFINITY);
-}
 
-// Loads the entries and forms the teacher's distribution; false (in every
-// thread) where none is kept. Entry j belongs to thread j mod blockDim.
+// A thread's entries: number j of the row is thread j mod blockDim's. They are
+// asked for before the row's logits and used after them.
+constexpr int kOwnEntries = 2;  // blocks have at least k / 2 threads
+struct Entries {
+  int at[kOwnEntries];   // the index, -1 where the entry is not kept
+  float t[kOwnEntries];  // the teacher's logit
+  float s[kOwnEntries];  // the student's logit there
+};
+// true: this thread has a kept one
 template <int DT>
-__device__ __forceinline__ bool loadEntries(const DistillArgs& a, size_t row, Entries& en, float* r0, float* r1) {
-  constexpr int E = floatTypeSize(DT);
-  const char* logits = static_cast<const char*>(a.logits) + row * a.ldl * E;
-  const int te = a.ttype == vrcclFloat32 ? 4 : 2;
-  const char* teacher = static_cast<const char*>(a.teacher) + row * a.ldt * te;
+__device__ __forceinline__ bool loadEntries(const DistillArgs& a, size_t row, Entries& en) {
+  const char* logits = static_cast<const char*>(a.logits) + row * a.ldl * floatTypeSize(DT);
+  const char* teacher = static_cast<const char*>(a.teacher) + row * a.ldt * (a.ttype == vrcclFloat32 ? 4 : 2);
+  bool any = false;
+#pragma unroll
+  for (int i = 0; i < kOwnEntries; ++i) {
+    const int j = threadIdx.x + i * blockDim.x;
+    en.at[i] = -1;
+    en.t[i] = en.s[i] = 0.f;
+    if (j < a.k) {
+      const long long at = a.wide ? static_cast<const long long*>(a.index)[row * a.ldi + j]
+                                  : static_cast<const int*>(a.index)[row * a.ldi + j];
+      en.t[i] = loadParam(teacher, a.ttype, j);
+      if (at >= 0 && (unsigned long long)at < a.vocab && en.t[i] != -INFINITY) {  // a NaN is kept, and shows
+        en.at[i] = (int)at;
+        en.s[i] = loadOne<DT>(logits, at);
+        any = true;
+      }
+    }
+  }
+  return any;
+}
+// The largest of this thread's kept teacher logits.
+__device__ __forceinline__ float ownTop(const Entries& en) {
   float top = -INFINITY;
-  bool any = false, nan = false;
-  for (int j = threadIdx.x; j < a.k; j += blockDim.x) {
-    const long long at = a.wide ? static_cast<const long long*>(a.index)[row * a.ldi + j]
-                                : static_cast<const int*>(a.index)[row * a.ldi + j];
-    const float t = loadParam(teacher, a.ttype, j);
-    const bool in = at >= 0 && (unsigned long long)at < a.vocab;
-    const bool kept = in && t != -INFINITY;  // a NaN is kept, and shows
-    en.at[j] = kept ? (int)at : -1;
-    en.logp[j] = t;
-    en.s[j] = kept ? loadOne<DT>(logits, at) : 0.f;
-    if (kept) {
-      any = true;
-      nan |= t != t;
-      top = fmaxf(top, t);
-    }
-  }
-  top = blockMax(top, r0);
-  if (!__syncthreads_or(any)) return false;
-  float sum = 0.f;
-  for (int j = threadIdx.x; j < a.k; j += blockDim.x) {
-    if (en.at[j] < 0) continue;
-    const float d = (en.logp[j] - top) * a.invT;
-    en.logp[j] = d;
-    sum += expf(d);
-  }
-  if (nan) sum = NAN;
-  sum = blockSum(sum, r1);
-  const float ls = logf(sum);
-  for (int j = threadIdx.x; j < a.k; j += blockDim.x) {
-    if (en.at[j] < 0) {
-      en.p[j] = 0.f;
-      continue;
-    }
-    en.logp[j] -= ls;
-    en.p[j] = expf(en.logp[j]);
-  }
-  return true;
+#pragma unroll
+  for (int i = 0; i < kOwnEntries; ++i)
+    if (en.at[i] >= 0) top = fmaxf(top, en.t[i]);
+  return top;
 }
 
 // A running maximum m and the sum l of exp((x - m) invT) over what was seen.
@@ -165,36 +145,40 @@ __device__ __forceinline__ void runOver(Running& r, const float (&f)[N], float c
     r.l *= fastExp2((r.m - top) * c);  // r.l is 0 while r.m is -inf
     r.m = top;
   }
-  if (r.m != -INFINITY) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) r.l += fastExp2((f[i] - r.m) * c);
-  } else {
+  if (r.m == -INFINITY) {  // nothing above -inf so far
 #pragma unroll
     for (int i = 0; i < N; ++i) r.l += f[i] == f[i] ? 0.f : NAN;
+  } else if constexpr (N % 4 == 0) {
+    const F2 minus = pair(-r.m, -r.m), cc = pair(c, c);
+    F2 sum = 0;
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      const float2 x = split(mul2(add2(pair(f[i], f[i + 1]), minus), cc));
+      sum = add2(sum, pair(fastExp2(x.x), fastExp2(x.y)));
+    }
+    const float2 s = split(sum);
+    r.l += s.x + s.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) r.l += fastExp2((f[i] - r.m) * c);
   }
 }
 
-template <int DT>
-__global__ void __launch_bounds__(kThreads) distillForward(const __grid_constant__ DistillArgs a) {
+// T threads a block: a compile-time stride saves the long loops their address arithmetic (188 us against 172).
+template <int DT, int T>
+__global__ void __launch_bounds__(T, 4 * kThreads / T) distillForward(const __grid_constant__ DistillArgs a) {
   using S = typename Ty<DT>::S;
-  constexpr int E = floatTypeSize(DT), V = 16 / E, U = 4;
-  __shared__ Entries en;
-  __shared__ float red[2][32];
+  constexpr int E = floatTypeSize(DT), V = 16 / E, U = kUnroll;
+  __shared__ float top[32];
+  __shared__ float2 red[32];
   __shared__ Running part[32];
   __shared__ Running mine;
   cg::cluster_group cluster = cg::this_cluster();
   const unsigned parts = cluster.num_blocks(), rank = cluster.block_rank();
   const size_t row = blockIdx.x / parts;
+  const int lane = threadIdx.x & 31;
+  constexpr int warps = T / 32;
   const S* logits = reinterpret_cast<const S*>(a.logits) + row * a.ldl;
-  // every block of a cluster loads the entries: whether there are any decides
-  // if the row is read at all
-  if (!loadEntries<DT>(a, row, en, red[0], red[1])) {
-    if (rank == 0 && threadIdx.x == 0) {
-      a.loss[row] = 0.f;
-      if (a.stats) a.stats[row] = make_float2(0.f, 0.f);
-    }
-    return;  // the whole cluster takes this way
-  }
   // [head | whole 16-byte vectors | tail] of the row; the vectors are dealt to the blocks in runs
   const size_t head = min(a.vocab, ((16 - (uintptr_t)logits % 16) % 16) / E);
   const size_t nvec = (a.vocab - head) / V, tail = head + nvec * V;
@@ -202,12 +186,33 @@ __global__ void __launch_bounds__(kThreads) distillForward(const __grid_constant
   const size_t lo = min(nvec, per * rank), hi = min(nvec, lo + per);
   const uint4* vec = reinterpret_cast<const uint4*>(logits + head);
   const float c = a.invT * kLog2e;
-  Running r = {-INFINITY, 0.f};
   size_t i = lo + threadIdx.x;
-  for (; i + (U - 1) * kThreads < hi; i += U * kThreads) {
+  // every block of a cluster loads the entries: whether there are any decides if the row is read; until that is known its
+  // first vectors come into L2
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (threadIdx.x % 8 == 0 && i + (size_t)u * T < hi)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(vec + i + (size_t)u * T));
+  // (kept in shared memory over the long loop, which needs the registers: 172 us against 187 at 4096 x 131072)
+  __shared__ Entries kept[T];
+  bool any;
+  {
+    Entries en;
+    any = loadEntries<DT>(a, row, en);
+    kept[threadIdx.x] = en;
+  }
+  if (!__syncthreads_or(any)) {
+    if (rank == 0 && threadIdx.x == 0) {
+      a.loss[row] = 0.f;
+      if (a.stats) a.stats[row] = make_float2(0.f, 0.f);
+    }
+    return;  // the whole cluster takes this way
+  }
+  Running r = {-INFINITY, 0.f};
+  for (; i + (size_t)(U - 1) * T < hi; i += (size_t)U * T) {
     uint4 v[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) v[u] = __ldcs(vec + i + u * kThreads);
+    for (int u = 0; u < U; ++u) v[u] = __ldcs(vec + i + (size_t)u * T);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       float f[V];
@@ -215,123 +220,212 @@ __global__ void __launch_bounds__(kThreads) distillForward(const __grid_constant
       runOver<V>(r, f, c);
     }
   }
-  for (; i < hi; i += kThreads) {
+  for (; i < hi; i += T) {
     float f[V];
     Vec16<DT>::expand(__ldcs(vec + i), f);
     runOver<V>(r, f, c);
   }
-  if (rank == 0) {
-    const size_t extra = threadIdx.x < head ? threadIdx.x : threadIdx.x - head + tail;
-    if (threadIdx.x < head + (a.vocab - tail)) {
-      float f[1] = {Ty<DT>::toF(logits[extra])};
-      runOver<1>(r, f, c);
-    }
+  if (rank == 0 && threadIdx.x < head + (a.vocab - tail)) {
+    float f[1] = {Ty<DT>::toF(logits[threadIdx.x < head ? threadIdx.x : threadIdx.x - head + tail])};
+    runOver<1>(r, f, c);
   }
   r = warpJoin(r, a.invT);
-  const int lane = threadIdx.x & 31;
-  if (lane == 0) part[threadIdx.x >> 5] = r;
-  __syncthreads();
-  if (threadIdx.x < 32) {
-    r = warpJoin(lane < kThreads / 32 ? part[lane] : Running{-INFINITY, 0.f}, a.invT);
-    if (lane == 0) mine = r;
+  const Entries en = kept[threadIdx.x];
+  const float ownMax = warpMax(ownTop(en));
+  if (lane == 0) {
+    part[threadIdx.x >> 5] = r;
+    top[threadIdx.x >> 5] = ownMax;
   }
+  __syncthreads();
   if (parts > 1) {
+    if (threadIdx.x < 32) {
+      r = warpJoin(lane < warps ? part[lane] : Running{-INFINITY, 0.f}, a.invT);
+      if (lane == 0) mine = r;
+    }
     cluster.sync();
     if (rank == 0 && threadIdx.x < 32) {
       Running o = {-INFINITY, 0.f};
       if (lane < (int)parts) o = *cluster.map_shared_rank(&mine, lane);
-      r = warpJoin(o, a.invT);
-      if (lane == 0) mine = r;
+      part[lane] = o;
     }
     cluster.sync();
     if (rank != 0) return;
-  } else {
-    __syncthreads();
   }
-  const float m = mine.m, ll = logf(mine.l);
-  float loss = 0.f;
-  for (int j = threadIdx.x; j < a.k; j += kThreads) {
-    const float p = en.p[j];
-    if (p != 0.f) loss += p * (en.logp[j] - ((en.s[j] - m) * a.invT - ll));
+  r = warpJoin(lane < (parts > 1 ? (int)parts : warps) ? part[lane] : Running{-INFINITY, 0.f}, a.invT);
+  const float m = r.m, ll = logf(r.l);
+  // With e_j = exp((t_j - top) / T) and sum e = Z, p_j = e_j / Z and sum p = 1:
+  //   sum p (log p - log q) = sum e_j ((t_j - top) / T - (s_j - m) / T) / Z - log Z + ll
+  const float teacherTop = warpMax(lane < warps ? top[lane] : -INFINITY);
+  float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int i = 0; i < kOwnEntries; ++i) {
+    if (en.at[i] < 0) continue;
+    const float d = (en.t[i] - teacherTop) * a.invT, e = expf(d);
+    sum.x += e;
+    if (e != 0.f) sum.y += e * (d - (en.s[i] - m) * a.invT);
   }
-  loss = blockSum(loss, red[0]);
+  sum = blockSum2(sum, red);
   if (threadIdx.x == 0) {
-    a.loss[row] = loss * a.temperature * a.temperature;
+    a.loss[row] = (sum.y / sum.x - logf(sum.x) + ll) * a.temperature * a.temperature;
     if (a.stats) a.stats[row] = make_float2(m, ll);
   }
 }
 
-template <int DT>
-__global__ void __launch_bounds__(kThreads) distillBackward(const __grid_constant__ DistillArgs a) {
+template <int DT, int T>
+__global__ void __launch_bounds__(T, 2 * kThreads / T) distillBackward(const __grid_constant__ DistillArgs a) {
   using S = typename Ty<DT>::S;
-  constexpr int E = floatTypeSize(DT), V = 16 / E, U = 4;
-  __shared__ Entries en;
-  __shared__ float red[2][32];
+  constexpr int E = floatTypeSize(DT), V = 16 / E, U = kUnroll;
+  __shared__ float top[32];
+  __shared__ float red[32];
+  __shared__ __align__(16) int at[VRCCL_DISTILL_MAX_K];
+  __shared__ __align__(16) float prob[VRCCL_DISTILL_MAX_K];
   const size_t slices = (a.vocab + a.slice - 1) / a.slice;
   const size_t row = blockIdx.x / slices, part = blockIdx.x % slices;
+  const int lane = threadIdx.x & 31;
+  constexpr int warps = T / 32;
   const S* logits = reinterpret_cast<const S*>(a.logits) + row * a.ldl;
   S* out = reinterpret_cast<S*>(a.dlogits) + row * a.ldd;
-  const size_t from = part * a.slice, to = min(a.vocab, from + a.slice);
-  const bool some = loadEntries<DT>(a, row, en, red[0], red[1]);
-  // slices are whole vectors of the output counted from its row's first boundary, where the logits share it
+  // A block's elements: slices are whole vectors of the output counted from its row's first boundary, and the first one
+  // takes the head before it; vectors are loaded whole where the logits share the output's boundaries.
   const size_t head = min(a.vocab, ((16 - (uintptr_t)out % 16) % 16) / E);
   const bool together = ((uintptr_t)logits - (uintptr_t)out) % 16 == 0;
-  const size_t begin = part == 0 ? 0 : min(a.vocab, from + head);
-  const size_t end = to == a.vocab ? a.vocab : min(a.vocab, to + head);
-  const float2 st = some ? a.stats[row] : make_float2(0.f, 0.f);
-  const float scale = some ? a.dloss[row * a.dstride] * a.temperature : 0.f;
-  const float c = a.invT * kLog2e, shift = st.y * kLog2e;
-  // q_v scale = exp2((s - max) c - shift) scale
+  const size_t from = part * a.slice, to = min(a.vocab, from + a.slice);
+  const size_t begin = part == 0 ? 0 : min(a.vocab, from + head), end = to == a.vocab ? a.vocab : min(a.vocab, to + head);
   const size_t first = part == 0 ? head : begin;  // the first vector's element
-  const size_t nvec = end > first ? (end - first) / V : 0, tail = first + nvec * V;
+  const size_t nvec = end > first ? (end - first) / V : 0, tail = first + nvec * V, edge = part == 0 ? min(head, end) : 0;
+  const uint4* src = reinterpret_cast<const uint4*>(logits + first);
   uint4* dst = reinterpret_cast<uint4*>(out + first);
-  if (!some) {
-    for (size_t i = threadIdx.x; i < nvec; i += kThreads) __stcs(dst + i, make_uint4(0, 0, 0, 0));
-    const size_t edge = (part == 0 ? min(head, end) : 0);
+  size_t i = threadIdx.x;
+  uint4 v[U];
+  if (together)
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (i + (size_t)u * T < nvec) v[u] = __ldcs(src + i + (size_t)u * T);
+  const float2 st = a.stats[row];
+  const float scale = a.dloss[row * a.dstride] * a.temperature;
+  Entries en;
+  const bool any = loadEntries<DT>(a, row, en);
+  const float ownMax = warpMax(ownTop(en));
+  if (lane == 0) top[threadIdx.x >> 5] = ownMax;
+  // (in place: from here on the entries' logits may be overwritten)
+  if (!__syncthreads_or(any)) {
+    for (; i < nvec; i += T) __stcs(dst + i, make_uint4(0, 0, 0, 0));
     if (threadIdx.x < edge) out[threadIdx.x] = S(0);
     if (tail + threadIdx.x < end) out[tail + threadIdx.x] = S(0);
     return;
   }
-  __syncthreads();  // the entries' logits are read (in place: before they are overwritten)
-  size_t i = threadIdx.x;
+  // q_v dloss T = exp2((s - max) c - shift) scale
+  const float c = a.invT * kLog2e, shift = st.y * kLog2e;
+  auto dense = [&](float s) { return fastExp2(fmaf(s - st.x, c, -shift)) * scale; };
+  const F2 minus2 = pair(-st.x, -st.x), c2 = pair(c, c), shift2 = pair(-shift, -shift), scale2 = pair(scale, scale);
+  auto dense2 = [&](float& a, float& b) {
+    const float2 x = split(fma2(add2(pair(a, b), minus2), c2, shift2));
+    const float2 y = split(mul2(pair(fastExp2(x.x), fastExp2(x.y)), scale2));
+    a = y.x;
+    b = y.y;
+  };
   if (together) {
-    const uint4* src = reinterpret_cast<const uint4*>(logits + first);
-    for (; i + (U - 1) * kThreads < nvec; i += U * kThreads) {
-      uint4 v[U];
+    while (i < nvec) {
+      uint4 w[U];
+      const size_t next = i + (size_t)U * T;
 #pragma unroll
-      for (int u = 0; u < U; ++u) v[u] = __ldcs(src + i + u * kThreads);
+      for (int u = 0; u < U; ++u)
+        if (next + (size_t)u * T < nvec) w[u] = __ldcs(src + next + (size_t)u * T);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        float f[V];
-        Vec16<DT>::expand(v[u], f);
+        if (i + (size_t)u * T < nvec) {
+          float f[V];
+          Vec16<DT>::expand(v[u], f);
 #pragma unroll
-        for (int e = 0; e < V; ++e) f[e] = fastExp2((f[e] - st.x) * c - shift) * scale;
-        __stcs(dst + i + u * kThreads, Vec16<DT>::pack(f));
+          for (int e = 0; e < V; e += 2) dense2(f[e], f[e + 1]);
+          __stcs(dst + i + (size_t)u * T, Vec16<DT>::pack(f));
+        }
       }
+#pragma unroll
+      for (int u = 0; u < U; ++u) v[u] = w[u];
+      i = next;
+    }
+  } else {
+    for (; i < nvec; i += T) {
+      float f[V];
+#pragma unroll
+      for (int e = 0; e < V; ++e) f[e] = dense(Ty<DT>::toF(logits[first + i * V + e]));
+      __stcs(dst + i, Vec16<DT>::pack(f));
     }
   }
-  for (; i < nvec; i += kThreads) {
-    float f[V];
+  if (threadIdx.x < edge) out[threadIdx.x] = Ty<DT>::fromF(dense(Ty<DT>::toF(logits[threadIdx.x])));
+  if (tail + threadIdx.x < end) out[tail + threadIdx.x] = Ty<DT>::fromF(dense(Ty<DT>::toF(logits[tail + threadIdx.x])));
+  // the teacher's entries
+  const float teacherTop = warpMax(lane < warps ? top[lane] : -INFINITY);
+  float e[kOwnEntries], sum = 0.f;
 #pragma unroll
-    for (int e = 0; e < V; ++e) f[e] = fastExp2((Ty<DT>::toF(logits[first + i * V + e]) - st.x) * c - shift) * scale;
-    __stcs(dst + i, Vec16<DT>::pack(f));
+  for (int i = 0; i < kOwnEntries; ++i) {
+    e[i] = en.at[i] < 0 ? 0.f : expf((en.t[i] - teacherTop) * a.invT);
+    sum += e[i];
   }
-  const size_t edge = part == 0 ? min(head, end) : 0;
-  if (threadIdx.x < edge)
-    out[threadIdx.x] = Ty<DT>::fromF(fastExp2((Ty<DT>::toF(logits[threadIdx.x]) - st.x) * c - shift) * scale);
-  if (tail + threadIdx.x < end)
-    out[tail + threadIdx.x] =
-        Ty<DT>::fromF(fastExp2((Ty<DT>::toF(logits[tail + threadIdx.x]) - st.x) * c - shift) * scale);
-  __syncthreads();
-  // the teacher's entries of this slice; entries that share an index all write the same sum
-  for (int j = threadIdx.x; j < a.k; j += kThreads) {
-    const int at = en.at[j];
-    if (at < 0 || (size_t)at < begin || (size_t)at >= end) continue;
-    float p = 0.f;
-    for (int i = 0; i < a.k; ++i)
-      if (en.at[i] == at) p += en.p[i];
-    out[at] = Ty<DT>::fromF((expf((en.s[j] - st.x) * a.invT - st.y) - p) * scale);
+  const float inv = 1.f / blockSum(sum, red);
+  const int padded = (a.k + 3) / 4 * 4;
+#pragma unroll
+  for (int i = 0; i < kOwnEntries; ++i) {
+    const int j = threadIdx.x + i * T;
+    if (j < padded) {
+      at[j] = en.at[i];
+      prob[j] = e[i] * inv;
+    }
   }
+  __syncthreads();  // also: every element of the slice is written
+  // Entries that share an index all write the same sum. They are looked for where there can be any: up to 64 entries
+  // always, more only if a hash table of the indices says that some are met twice.
+  bool shared = true;
+  if (a.k > 64) {
+    __shared__ int seen[kSeen];
+    for (int j = threadIdx.x; j < kSeen; j += T) seen[j] = -1;
+    __syncthreads();
+    bool twice = false;
+#pragma unroll
+    for (int i = 0; i < kOwnEntries; ++i) {
+      if (en.at[i] < 0) continue;
+      for (unsigned h = (unsigned)en.at[i] * 2654435761u >> 21;; h = (h + 1) % kSeen) {
+        const int met = atomicCAS(&seen[h], -1, en.at[i]);
+        twice |= met == en.at[i];
+        if (met == -1 || met == en.at[i]) break;
+      }
+    }
+    shared = __syncthreads_or(twice);
+  }
+#pragma unroll
+  for (int i = 0; i < kOwnEntries; ++i) {
+    const int own = en.at[i];
+    if (own < 0 || (size_t)own < begin || (size_t)own >= end) continue;
+    float p = shared ? 0.f : e[i] * inv;
+    for (int j = 0; shared && j < padded; j += 4) {
+      const int4 q = *reinterpret_cast<const int4*>(at + j);
+      if (q.x == own) p += prob[j];
+      if (q.y == own) p += prob[j + 1];
+      if (q.z == own) p += prob[j + 2];
+      if (q.w == own) p += prob[j + 3];
+    }
+    out[own] = Ty<DT>::fromF((expf((en.s[i] - st.x) * a.invT - st.y) - p) * scale);
+  }
+}
+
+// Threads of a block: with a row in 16 vectors a thread or fewer, so that several short rows share a multiprocessor and
+// one's reductions run under another's loads; more where blocks are few; and enough for the row's entries.
+int blockThreads(size_t bytes, size_t blocks, size_t k) {
+  int t = 128;
+  const size_t most = blocks < (size_t)smCount() * 2 ? 64 : 256;  // bytes a thread
+  while (t < kThreads && (bytes > t * most || k > (size_t)t * kOwnEntries)) t *= 2;
+  return t;
+}
+
+using DistillFn = void (*)(DistillArgs);
+template <int DT>
+DistillFn pickForward(int threads) {
+  return threads == 128 ? distillForward<DT, 128> : threads == 256 ? distillForward<DT, 256> : distillForward<DT, 512>;
+}
+template <int DT>
+DistillFn pickBackward(int threads) {
+  return threads == 128 ? distillBackward<DT, 128> : threads == 256 ? distillBackward<DT, 256> : distillBackward<DT, 512>;
 }
 
 bool goodDistill(const void* logits, size_t ldl, const void* teacher, size_t ldt, const void* index, size_t ldi,
@@ -394,24 +488,11 @@ extern "C" vrcclResult_t vrcclDistillForward(const void* logits, size_t ldl, con
   unsigned parts = 1;
   const size_t bytes = vocab * floatTypeSize(dtype);
   while (parts < 8 && rows * parts * 2 <= (size_t)smCount() * 2 && bytes / (parts * 2) >= size_t(kThreads) * 32) parts *= 2;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(rows * parts));
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = parts;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  auto fn = dtype == vrcclFloat32    ? distillForward<vrcclFloat32>
-            : dtype == vrcclBfloat16 ? distillForward<vrcclBfloat16>
-                                     : distillForward<vrcclFloat16>;
-  if (cudaLaunchKernelEx(&cfg, fn, a) != cudaSuccess) {
-    cudaGetLastError();
-    return vrcclCudaError;
-  }
-  return vrcclSuccess;
+  const int threads = blockThreads(bytes / parts, rows * parts, k);
+  const DistillFn fn = dtype == vrcclFloat32    ? pickForward<vrcclFloat32>(threads)
+                       : dtype == vrcclBfloat16 ? pickForward<vrcclBfloat16>(threads)
+                                                : pickForward<vrcclFloat16>(threads);
+  return launchShaped(fn, {dim3((unsigned)(rows * parts)), threads, 0, (int)parts, false}, st, a);
 }
 
 extern "C" vrcclResult_t vrcclDistillBackward(const void* logits, size_t ldl, const void* teacher, size_t ldt,
@@ -444,17 +525,17 @@ extern "C" vrcclResult_t vrcclDistillBackward(const void* logits, size_t ldl, co
   a.dlogits = dlogits;
   a.ldd = ldd;
   // In place a row stays with one block: another slice's entries could be overwritten before they are read.
-  a.slice = vocab;
-  if (dlogits != logits) {
-    const size_t unit = size_t(kThreads) * 4 * (16 / E);
-    const size_t want = std::max<size_t>(1, (size_t)smCount() * 4 / rows);
-    a.slice = std::min(vocab, (vocab / want + unit) / unit * unit);
-  }
+  const size_t unit = size_t(kThreads) * (16 / E);
+  size_t pieces = 1;
+  if (dlogits != logits)  // even pieces, until there are four blocks a multiprocessor or a piece has 32 KB
+    pieces = std::max<size_t>(1, std::min((size_t)smCount() * 4 / rows, vocab * E / 32768));
+  a.slice = std::min(vocab, ((vocab + pieces - 1) / pieces + unit - 1) / unit * unit);
   const size_t slices = (vocab + a.slice - 1) / a.slice;
   if (rows * slices >= (size_t(1) << 31)) return vrcclInvalidArgument;
-  auto fn = dtype == vrcclFloat32    ? distillBackward<vrcclFloat32>
-            : dtype == vrcclBfloat16 ? distillBackward<vrcclBfloat16>
-                                     : distillBackward<vrcclFloat16>;
-  fn<<<(unsigned)(rows * slices), kThreads, 0, st>>>(a);
+  const int threads = blockThreads(a.slice * E, rows * slices, k);
+  const DistillFn fn = dtype == vrcclFloat32    ? pickBackward<vrcclFloat32>(threads)
+                       : dtype == vrcclBfloat16 ? pickBackward<vrcclBfloat16>(threads)
+                                                : pickBackward<vrcclFloat16>(threads);
+  fn<<<(unsigned)(rows * slices), threads, 0, st>>>(a);
   return launchResult();
 }

@@ -351,6 +351,7 @@ __device__ __forceinline__ void storeBox(const Problem& a, const CUtensorMap* ma
     unsigned short* o = static_cast<unsigned short*>(out) + (size_t)m * ld + n;
     const int rows = min(32, a.M - m), c = 2 * lane;
     const bool lo = n + c < a.N, hi = n + c + 1 < a.N;
+#pragma unroll 8
     for (int r = 0; r < rows; ++r) {
       const uint32_t w =
           *reinterpret_cast<const uint32_t*>(buf + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + ((lane & 3) << 2));
@@ -371,28 +372,63 @@ __device__ __forceinline__ void stage32(unsigned char* buf, int half, int lane, 
   }
 }
 
-template <int DT, int ACT>
-__device__ __forceinline__ void finish(const Problem& a, float (&f)[32], size_t m, int n) {
-  using S = typename Ty<DT>::S;
+template <int ACT>
+__device__ __forceinline__ void activate32(float (&f)[32]) {
 #pragma unroll
   for (int i = 0; i < 32; ++i) f[i] = activate<ACT>(f[i]);
-  if (!a.residual || m >= (size_t)a.M) return;
-  const int left = a.N - n;  // columns that exist, of 32
-  const S* r = static_cast<const S*>(a.residual) + m * a.ldr + n;
+}
+// One warp's 32 x 64 elements of the residual, rows m.. and columns n..: read
+// along the rows, asked for before the tile's products are waited for, and
+// handed to the lanes that own the rows through the staging buffer.
+template <int DT>
+struct Residual {
+  uint32_t w[32];
+  __device__ __forceinline__ void load(const Problem& a, int m, int n, int lane) {
+    const unsigned short* r = static_cast<const unsigned short*>(a.residual) + (size_t)m * a.ldr + n;
+    const int rows = min(32, a.M - m), cols = min(64, a.N - n);
+    if (a.wideR && cols == 64) {  // a piece of 16 bytes a lane, four rows at a time
 #pragma unroll
-  for (int v = 0; v < 4; ++v) {
-    if (a.wideR && v * 8 + 8 <= left) {
-      float g[8];
-      Vec16<DT>::expand(reinterpret_cast<const uint4*>(r)[v], g);
+      for (int i = 0; i < 8; ++i) {
+        const int row = i * 4 + (lane >> 3);
+        const uint4 v = row < rows ? __ldg(reinterpret_cast<const uint4*>(r + (size_t)row * a.ldr) + (lane & 7)) : make_uint4(0, 0, 0, 0);
+        w[4 * i] = v.x;
+        w[4 * i + 1] = v.y;
+        w[4 * i + 2] = v.z;
+        w[4 * i + 3] = v.w;
+      }
+    } else {  // a pair of columns a lane, a row at a time
 #pragma unroll
-      for (int e = 0; e < 8; ++e) f[v * 8 + e] += g[e];
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (v * 8 + e < left) f[v * 8 + e] += Ty<DT>::toF(r[v * 8 + e]);
+      for (int i = 0; i < 32; ++i) {
+        const unsigned short* p = r + (size_t)i * a.ldr + 2 * lane;
+        const uint32_t lo = i < rows && 2 * lane < cols ? p[0] : 0u, hi = i < rows && 2 * lane + 1 < cols ? p[1] : 0u;
+        w[i] = lo | hi << 16;
+      }
     }
   }
-}
+  __device__ __forceinline__ void put(const Problem& a, int n, unsigned char* buf, int lane) const {
+    if (a.wideR && a.N - n >= 64) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int row = i * 4 + (lane >> 3);
+        *reinterpret_cast<uint4*>(buf + row * 128 + (((lane & 7) ^ (row & 7)) << 4)) =
+            make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        *reinterpret_cast<uint32_t*>(buf + i * 128 + (((lane >> 2) ^ (i & 7)) << 4) + ((lane & 3) << 2)) = w[i];
+    }
+  }
+  static __device__ __forceinline__ void add(const unsigned char* buf, int half, int lane, float (&f)[32]) {
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      float g[8];
+      Vec16<DT>::expand(*reinterpret_cast<const uint4*>(buf + lane * 128 + (((half * 4 + v) ^ (lane & 7)) << 4)), g);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[v * 8 + e] += g[e];
+    }
+  }
+};
 // The bias of 64 columns from n on, a pair a lane, asked for before a tile's products are waited for; a column's value
 // then comes from its lane. (Loaded where it is used, each 32 columns waited 1200 cycles for it.)
 template <int DT>
@@ -583,6 +619,8 @@ __global__ void __launch_bounds__(kProductThreads, 1) productKernel(const __grid
       if (a.bias)
 #pragma unroll
         for (int i = 0; i < kCols / 64; ++i) bias[i] = biasPair<DT>(a, n0 + i * 64, lane);
+      Residual<DT> residual;
+      if (a.residual && m0 < a.M && n0 < a.N) residual.load(a, m0, n0, lane);
       bool ok = lane != 0 || waitBar(&accFull[acc], use & 1, dead);
       if (!__all_sync(0xffffffffu, ok)) break;
       tcFenceAfter();
@@ -603,21 +641,25 @@ __global__ void __launch_bounds__(kProductThreads, 1) productKernel(const __grid
               asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
           }
           __syncwarp();
+          if (a.residual) {
+            residual.put(a, n0 + c, yb, lane);
+            __syncwarp();
+            if (c + 64 < kCols && n0 + c + 64 < a.N) residual.load(a, m0, n0 + c + 64, lane);
+          }
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             float f[32];
             tcLoad32(from + c + h * 32, f);
-            const int n = n0 + c + h * 32;
             if (a.bias) addBias<DT>(f, bias[c / 64], h);
             if (a.z) stage32<DT>(zb, h, lane, f);
-            const size_t m = m0 + lane;
             switch (a.act) {
-              case vrcclActRelu: finish<DT, vrcclActRelu>(a, f, m, n); break;
-              case vrcclActGelu: finish<DT, vrcclActGelu>(a, f, m, n); break;
-              case vrcclActGeluTanh: finish<DT, vrcclActGeluTanh>(a, f, m, n); break;
-              case vrcclActSilu: finish<DT, vrcclActSilu>(a, f, m, n); break;
-              default: finish<DT, vrcclActNone>(a, f, m, n); break;
+              case vrcclActRelu: activate32<vrcclActRelu>(f); break;
+              case vrcclActGelu: activate32<vrcclActGelu>(f); break;
+              case vrcclActGeluTanh: activate32<vrcclActGeluTanh>(f); break;
+              case vrcclActSilu: activate32<vrcclActSilu>(f); break;
+              default: activate32<vrcclActNone>(f); break;
             }
+            if (a.residual) Residual<DT>::add(yb, h, lane, f);
             stage32<DT>(yb, h, lane, f);
           }
           if (a.z) storeBox<DT>(a, &a.zMap, a.z, a.ldz, a.wideZ, zb, m0, n0 + c, lane);

@@ -127,36 +127,6 @@ constexpr long long kRowWaitCycles = 3000000000ll, kDrainCycles = 200000000ll;  
 
 __device__ int gNormStatus;  // vrcclResult_t of the first device-side failure
 
-// Two binary32 values in one register pair: Blackwell adds and multiplies both
-// in one instruction. Forward is bound by issue slots nearly as much as by
-// memory, and this halves its arithmetic.
-using F2 = unsigned long long;
-__device__ __forceinline__ F2 pair(float lo, float hi) {
-  F2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ float2 split(F2 a) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
-  return r;
-}
-__device__ __forceinline__ F2 add2(F2 a, F2 b) {
-  F2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
-  F2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-  F2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-
 // Where a row's bytes lie and which of them a bulk copy may take: 16-byte
 // blocks that lie inside the matrix's own bytes, first row's start to last
 // row's end. A row on no 16-byte boundary shares its first and last block with
