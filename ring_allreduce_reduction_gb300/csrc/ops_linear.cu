@@ -969,24 +969,48 @@ __global__ void __launch_bounds__(kFewThreads) linearFew(const __grid_constant__
 
 // ------------------------------------------------------------ operands and the bias gradient
 
+// Eight consecutive elements from a row that starts on any element, those past `left` as zeros.
+__device__ __forceinline__ uint4 gather8(const unsigned short* p, int left) {
+  unsigned short e[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) e[i] = i < left ? p[i] : (unsigned short)0;
+  return make_uint4(e[0] | (uint32_t)e[1] << 16, e[2] | (uint32_t)e[3] << 16, e[4] | (uint32_t)e[5] << 16,
+                    e[6] | (uint32_t)e[7] << 16);
+}
+
 // Copies whose rows start on 16-byte boundaries, which TMA needs; one launch
-// for all operands of a call. What is left of a row's last 16 bytes stays as it
-// is: no copy reads past the row's last element.
+// for all operands of a call. A thread gathers eight elements (its warp's
+// loads lie next to one another, in L1 after the first) and writes them as one
+// piece.
 struct PackJob {
   const unsigned short* src;
   unsigned short* dst;
-  size_t lds, ldd, rows, cols;
+  size_t lds, groups;      // groups: pieces of the copy
+  unsigned cols, perRow;   // perRow: pieces a row
 };
+constexpr int kPackTurn = 2;  // pieces a thread has in flight
 struct PackArgs {
   PackJob job[3];
 };
 __global__ void __launch_bounds__(256) packRows(const __grid_constant__ PackArgs a) {
-  const PackJob& j = a.job[blockIdx.z];
+  const PackJob& j = a.job[blockIdx.y];
   letNextIn();
   waitForPrevious();
-  for (size_t r = blockIdx.y; r < j.rows; r += gridDim.y)
-    for (size_t c = (size_t)blockIdx.x * 256 + threadIdx.x; c < j.cols; c += (size_t)gridDim.x * 256)
-      j.dst[r * j.ldd + c] = j.src[r * j.lds + c];
+  const size_t step = (size_t)gridDim.x * 256;
+  for (size_t g0 = (size_t)blockIdx.x * 256 + threadIdx.x; g0 < j.groups; g0 += kPackTurn * step) {
+    uint4 v[kPackTurn];
+#pragma unroll
+    for (int u = 0; u < kPackTurn; ++u) {
+      const size_t g = g0 + u * step;
+      if (g >= j.groups) continue;
+      const size_t r = j.groups >> 32 ? g / j.perRow : (unsigned)g / j.perRow;
+      const unsigned c = (unsigned)(g - r * j.perRow) * 8;
+      v[u] = gather8(j.src + r * j.lds + c, (int)min(8u, j.cols - c));
+    }
+#pragma unroll
+    for (int u = 0; u < kPackTurn; ++u)
+      if (g0 + u * step < j.groups) reinterpret_cast<uint4*>(j.dst)[g0 + u * step] = v[u];
+  }
 }
 
 struct SlopeArgs {
@@ -997,75 +1021,65 @@ struct SlopeArgs {
   size_t lddy, ldz, lddz, rows;
   int cols;
 };
-constexpr int kSlopeRows = 8;  // row groups of a block; 32 lanes of V columns across
+constexpr int kSlopeRows = 8;  // row groups of a block; 32 lanes of 8 columns across
 constexpr int kSlopeTurn = 4;  // rows a thread has in flight
 
 // dz = dy act'(z), rounded to the element type: the tensor cores take their
-// operands in it. The bias gradient sums the unrounded values.
+// operands in it. The bias gradient sums the unrounded values. A thread has
+// eight columns; WIDE: rows of dy and z start on 16-byte boundaries (and end
+// on them), else their elements are gathered. dz always does.
 template <int DT, int ACT, bool WIDE>
 __global__ void __launch_bounds__(256) linearSlope(const __grid_constant__ SlopeArgs a) {
   using S = typename Ty<DT>::S;
-  constexpr int V = WIDE ? 8 : 1;
-  __shared__ float part[kSlopeRows][32 * V];
+  __shared__ float part[kSlopeRows][256];
   const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
-  const int c = (blockIdx.x * 32 + lane) * V;
-  float sum[V] = {};
+  const int c = (blockIdx.x * 32 + lane) * 8;
+  float sum[8] = {};
   letNextIn();
   if (c < a.cols) {
+    const int left = min(8, a.cols - c);
     const size_t step = (size_t)gridDim.y * kSlopeRows;
-    using Raw = std::conditional_t<WIDE, uint4, S>;
     for (size_t r0 = (size_t)blockIdx.y * kSlopeRows + g; r0 < a.rows; r0 += kSlopeTurn * step) {
-      Raw d[kSlopeTurn], z[kSlopeTurn];  // the rows of a turn are all asked for before the first is used
+      uint4 d[kSlopeTurn], z[kSlopeTurn];  // the rows of a turn are all asked for before the first is used
 #pragma unroll
       for (int u = 0; u < kSlopeTurn; ++u) {
         const size_t r = r0 + u * step;
         if (r < a.rows) {
-          d[u] = __ldg(reinterpret_cast<const Raw*>(static_cast<const S*>(a.dy) + r * a.lddy + c));
-          if constexpr (ACT != vrcclActNone)
-            z[u] = __ldcs(reinterpret_cast<const Raw*>(static_cast<const S*>(a.z) + r * a.ldz + c));
+          const unsigned short* dy = static_cast<const unsigned short*>(a.dy) + r * a.lddy + c;
+          d[u] = WIDE ? __ldg(reinterpret_cast<const uint4*>(dy)) : gather8(dy, left);
+          if constexpr (ACT != vrcclActNone) {
+            const unsigned short* zp = static_cast<const unsigned short*>(a.z) + r * a.ldz + c;
+            z[u] = WIDE ? __ldcs(reinterpret_cast<const uint4*>(zp)) : gather8(zp, left);
+          }
         }
       }
 #pragma unroll
       for (int u = 0; u < kSlopeTurn; ++u) {
         const size_t r = r0 + u * step;
         if (r >= a.rows) break;
-        float f[V], h[V];
-        if constexpr (WIDE)
-          Vec16<DT>::expand(d[u], f);
-        else
-          f[0] = Ty<DT>::toF(d[u]);
+        float f[8], h[8];
+        Vec16<DT>::expand(d[u], f);
         if constexpr (ACT != vrcclActNone) {
-          if constexpr (WIDE)
-            Vec16<DT>::expand(z[u], h);
-          else
-            h[0] = Ty<DT>::toF(z[u]);
+          Vec16<DT>::expand(z[u], h);
 #pragma unroll
-          for (int e = 0; e < V; ++e) f[e] *= slope<ACT>(h[e]);
+          for (int e = 0; e < 8; ++e) f[e] *= slope<ACT>(h[e]);
         }
 #pragma unroll
-        for (int e = 0; e < V; ++e) sum[e] += f[e];
-        if (a.dz) {
-          S* dz = static_cast<S*>(a.dz) + r * a.lddz + c;
-          if constexpr (WIDE)
-            *reinterpret_cast<uint4*>(dz) = Vec16<DT>::pack(f);
-          else
-            dz[0] = Ty<DT>::fromF(f[0]);
-        }
+        for (int e = 0; e < 8; ++e) sum[e] += f[e];
+        if (a.dz) *reinterpret_cast<uint4*>(static_cast<S*>(a.dz) + r * a.lddz + c) = Vec16<DT>::pack(f);
       }
     }
   }
   if (!a.partial) return;
 #pragma unroll
-  for (int e = 0; e < V; ++e) part[g][lane * V + e] = sum[e];
+  for (int e = 0; e < 8; ++e) part[g][lane * 8 + e] = sum[e];
   __syncthreads();
-  for (int i = threadIdx.x; i < 32 * V; i += 256) {
-    const int col = blockIdx.x * 32 * V + i;
-    if (col >= a.cols) continue;
-    float s = 0.f;
+  const int col = blockIdx.x * 256 + threadIdx.x;
+  if (col >= a.cols) return;
+  float s = 0.f;
 #pragma unroll
-    for (int k = 0; k < kSlopeRows; ++k) s += part[k][i];
-    a.partial[(size_t)blockIdx.y * a.cols + col] = s;
-  }
+  for (int k = 0; k < kSlopeRows; ++k) s += part[k][threadIdx.x];
+  a.partial[(size_t)blockIdx.y * a.cols + col] = s;
 }
 
 template <int DT>
@@ -1142,19 +1156,18 @@ struct Packing {
     if (rowsAligned(o.p, o.ld, 2)) return true;
     unsigned short* q = static_cast<unsigned short*>(ws.take(packedBytes(o.rows, o.cols)));
     if (!q) return false;
-    args.job[jobs++] = {static_cast<const unsigned short*>(o.p), q, o.ld, packedLd(o.cols), o.rows, o.cols};
+    const size_t perRow = packedLd(o.cols) / 8;
+    args.job[jobs++] = {static_cast<const unsigned short*>(o.p), q, o.ld, o.rows * perRow, (unsigned)o.cols, (unsigned)perRow};
     o.p = q;
     o.ld = packedLd(o.cols);
     return true;
   }
   vrcclResult_t launch(bool after, cudaStream_t st) const {
     if (!jobs) return vrcclSuccess;
-    size_t rows = 0, cols = 0;
-    for (int i = 0; i < jobs; ++i) {
-      rows = std::max(rows, args.job[i].rows);
-      cols = std::max(cols, args.job[i].cols);
-    }
-    const dim3 grid((unsigned)std::min<size_t>((cols + 255) / 256, 64), (unsigned)std::min<size_t>(rows, 4096), (unsigned)jobs);
+    size_t most = 0;
+    for (int i = 0; i < jobs; ++i) most = std::max(most, args.job[i].groups);
+    const size_t blocks = std::min((most + 256 * kPackTurn - 1) / (256 * kPackTurn), (size_t)smCount() * 8);
+    const dim3 grid((unsigned)std::max<size_t>(1, blocks), (unsigned)jobs);
     return launchShaped(packRows, {grid, 256, 0, 0, after}, st, args);
   }
 };
@@ -1419,8 +1432,7 @@ vrcclResult_t backward(const void* dy, size_t lddy, const void* z, size_t ldz, c
     if (dbias && !(s.partial = static_cast<float*>(ws.take(biasBytes(rows, outs)))))
       return vrcclInvalidArgument;
     const bool wide = outs % 8 == 0 && rowsAligned(dy, lddy, 2) && (act == vrcclActNone || rowsAligned(z, ldz, 2));
-    const int across = wide ? 256 : 32;
-    const dim3 grid((unsigned)((outs + across - 1) / across), (unsigned)slopeBlocks(rows, outs));
+    const dim3 grid((unsigned)((outs + 255) / 256), (unsigned)slopeBlocks(rows, outs));
     if (wide)
       launchSlope<DT, true>(act, grid, s, st);
     else
