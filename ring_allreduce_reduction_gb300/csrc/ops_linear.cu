@@ -31,12 +31,27 @@ namespace {
 
 // ------------------------------------------------------------ activations
 
-// 1 / (1 + exp(x)); exp may overflow: the reciprocal of infinity is 0
-__device__ __forceinline__ float logistic(float x) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + __expf(x)));
-  return r;
+// Two values at a time (F2). What an epilogue or the pass over dy and z has to
+// compute for an element shares its multiprocessor with loads, stores and
+// MMAs; in pairs it takes half the instructions.
+__device__ __forceinline__ F2 both(float x) { return pair(x, x); }
+// 2^x on the special function unit, relative error about 2^-22; 2^inf = inf
+__device__ __forceinline__ F2 exp2Pair(F2 x) {
+  const float2 v = split(x);
+  float a, b;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(a) : "f"(v.x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(b) : "f"(v.y));
+  return pair(a, b);
 }
+// 1 / x, relative error about 2^-23; 1 / inf = 0
+__device__ __forceinline__ F2 reciprocal(F2 x) {
+  const float2 v = split(x);
+  float a, b;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(a) : "f"(v.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(b) : "f"(v.y));
+  return pair(a, b);
+}
+constexpr float kLog2e = 1.4426950408889634f;
 
 // Phi(z), the normal distribution, and exp(-z^2/2), which its slope needs too:
 // Abramowitz and Stegun, Handbook of Mathematical Functions, 7.1.26,
@@ -44,45 +59,66 @@ __device__ __forceinline__ float logistic(float x) {
 // whose error is below 1.5e-7: half that in Phi, about one unit of binary32 at
 // 1. It costs two special-function instructions and a dozen others where erff
 // costs some forty, which made the gradient's pass over dy and z compute bound.
-__device__ __forceinline__ float normalPhi(float z, float* density = nullptr) {
-  const float x = fabsf(z) * 0.70710678118654752f;
-  float t;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(fmaf(0.3275911f, x, 1.f)));
-  const float e = __expf(-0.5f * z * z);
-  const float p = t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 1.061405429f, -1.453152027f), 1.421413741f), -0.284496736f), 0.254829592f);
-  if (density) *density = e;
-  const float tail = 0.5f * p * e;  // Phi(-|z|)
-  return z > 0.f ? 1.f - tail : tail;
+__device__ __forceinline__ F2 normalPhi(F2 z, F2& density) {
+  const float2 v = split(z);
+  const F2 x = pair(fabsf(v.x), fabsf(v.y));
+  const F2 t = reciprocal(fma2(x, both(0.3275911f * 0.70710678118654752f), both(1.f)));
+  density = exp2Pair(mul2(mul2(z, z), both(-0.5f * kLog2e)));
+  F2 p = fma2(t, both(1.061405429f * 0.5f), both(-1.453152027f * 0.5f));
+  p = fma2(t, p, both(1.421413741f * 0.5f));
+  p = fma2(t, p, both(-0.284496736f * 0.5f));
+  p = fma2(t, p, both(0.254829592f * 0.5f));
+  const float2 tail = split(mul2(mul2(p, t), density));  // Phi(-|z|)
+  return pair(v.x > 0.f ? 1.f - tail.x : tail.x, v.y > 0.f ? 1.f - tail.y : tail.y);
+}
+// 1 / (1 + exp(-w)) with w = 2 sqrt(2/pi) (z + 0.044715 z^3): (1 + tanh(w / 2)) / 2, which loses nothing where the tanh
+// nears -1; w itself, and for silu w = z.
+constexpr float kTanhScale = 1.5957691216057308f;
+template <int ACT>
+__device__ __forceinline__ F2 logisticOf(F2 z) {
+  F2 w = mul2(z, both(-kLog2e));
+  if constexpr (ACT == vrcclActGeluTanh)
+    w = mul2(z, fma2(mul2(z, z), both(-kTanhScale * kLog2e * 0.044715f), both(-kTanhScale * kLog2e)));
+  return reciprocal(add2(exp2Pair(w), both(1.f)));
 }
 
 template <int ACT>
-__device__ __forceinline__ float activate(float z) {
-  if constexpr (ACT == vrcclActRelu) return z > 0.f ? z : (z != z ? z : 0.f);
-  if constexpr (ACT == vrcclActGelu) return z * normalPhi(z);
-  // (1 + tanh u) / 2 = 1 / (1 + exp(-2u)), which loses nothing where tanh u nears -1
-  if constexpr (ACT == vrcclActGeluTanh)
-    return z * logistic(-1.5957691216057308f * (z + 0.044715f * z * z * z));
-  if constexpr (ACT == vrcclActSilu) return z * logistic(-z);
+__device__ __forceinline__ F2 activate(F2 z) {
+  if constexpr (ACT == vrcclActRelu) {
+    const float2 v = split(z);
+    return pair(v.x > 0.f ? v.x : (v.x != v.x ? v.x : 0.f), v.y > 0.f ? v.y : (v.y != v.y ? v.y : 0.f));
+  }
+  if constexpr (ACT == vrcclActGelu) {
+    F2 density;
+    return mul2(z, normalPhi(z, density));
+  }
+  if constexpr (ACT == vrcclActGeluTanh || ACT == vrcclActSilu) return mul2(z, logisticOf<ACT>(z));
   return z;
 }
 template <int ACT>
-__device__ __forceinline__ float slope(float z) {
-  if constexpr (ACT == vrcclActRelu) return z > 0.f ? 1.f : 0.f;
+__device__ __forceinline__ F2 slope(F2 z) {
+  if constexpr (ACT == vrcclActRelu) {
+    const float2 v = split(z);
+    return pair(v.x > 0.f ? 1.f : 0.f, v.y > 0.f ? 1.f : 0.f);
+  }
   if constexpr (ACT == vrcclActGelu) {
-    float e;
-    const float phi = normalPhi(z, &e);
-    return phi + z * e * 0.39894228040143268f;
+    F2 density;
+    const F2 phi = normalPhi(z, density);
+    return fma2(mul2(z, density), both(0.39894228040143268f), phi);
   }
-  // with y = z s(w), w = 2 sqrt(2/pi) (z + 0.044715 z^3), s(w) = 1 / (1 + exp(-w)):  y' = s + z s (1 - s) w'
-  if constexpr (ACT == vrcclActGeluTanh) {
-    const float s = logistic(-1.5957691216057308f * (z + 0.044715f * z * z * z));
-    return s + z * s * (1.f - s) * 1.5957691216057308f * (1.f + 0.134145f * z * z);
+  // y = z s(w): y' = s + z s (1 - s) w'
+  if constexpr (ACT == vrcclActGeluTanh || ACT == vrcclActSilu) {
+    const F2 s = logisticOf<ACT>(z);
+    F2 zw = z;
+    if constexpr (ACT == vrcclActGeluTanh)
+      zw = mul2(z, fma2(mul2(z, z), both(kTanhScale * 3.f * 0.044715f), both(kTanhScale)));
+    return fma2(mul2(s, fma2(s, both(-1.f), both(1.f))), zw, s);
   }
-  if constexpr (ACT == vrcclActSilu) {
-    const float s = logistic(-z);
-    return s * (1.f + z * (1.f - s));
-  }
-  return 1.f;
+  return both(1.f);
+}
+template <int ACT>
+__device__ __forceinline__ float activate(float z) {
+  return split(activate<ACT>(both(z))).x;
 }
 
 __device__ __forceinline__ float activateBy(int act, float z) {
@@ -281,7 +317,7 @@ struct Problem {
   bool wideD, wideZ;     // d / z may be stored by TMA
   bool wideR;            // the residual's rows start on 16-byte boundaries
   int act;
-  int tilesM, tiles, steps;
+  int tilesM, tilesN, tiles, steps;
 };
 
 // A launch computes one product or two (a linear layer's two gradients, which
@@ -310,6 +346,15 @@ struct Walk {
     }
   }
   __device__ __forceinline__ bool more() const { return tile < end; }
+  // The tile's place: columns of GROUP tiles down, so that the tiles at work at a time make up a square of the result and
+  // read few different rows of either operand.
+  template <int GROUP>
+  __device__ __forceinline__ void place(const Problem& a, int& m, int& n) const {
+    const int column = GROUP * a.tilesN, group = tile / column, r = tile - group * column;
+    const int down = min(GROUP, a.tilesM - group * GROUP);
+    n = r / down;
+    m = group * GROUP + r - n * down;
+  }
   __device__ __forceinline__ void next(const ProductArgs& a, int unit) {
     tile += stride;
     settle(a, unit);
@@ -332,6 +377,7 @@ struct ProductShape {
   static constexpr int kStages = BN == 64 ? 3 : 5;
   static constexpr int kSmem = kStages * kStageBytes + kEpilogueWarps * 2 * kStoreBytes + 1024;
   static constexpr int kTmemCols = 2 * BN;
+  static constexpr int kGroup = CG == 2 ? 8 : 12;  // tiles of a column (Walk::place): about the root of the tiles at work
 };
 
 // Writes one warp's finished 32 x 64 elements from its staging buffer (rows of
@@ -375,7 +421,11 @@ __device__ __forceinline__ void stage32(unsigned char* buf, int half, int lane, 
 template <int ACT>
 __device__ __forceinline__ void activate32(float (&f)[32]) {
 #pragma unroll
-  for (int i = 0; i < 32; ++i) f[i] = activate<ACT>(f[i]);
+  for (int i = 0; i < 32; i += 2) {
+    const float2 y = split(activate<ACT>(pair(f[i], f[i + 1])));
+    f[i] = y.x;
+    f[i + 1] = y.y;
+  }
 }
 // One warp's 32 x 64 elements of the residual, rows m.. and columns n..: read
 // along the rows, asked for before the tile's products are waited for, and
@@ -548,7 +598,10 @@ __global__ void __launch_bounds__(kProductThreads, 1) productKernel(const __grid
     bool ok = true;
     for (Walk w(args, unit, gridDim.x / CG); w.more() && ok; w.next(args, unit)) {
       const Problem& a = args.p[w.which];
-      const int m = w.tile % a.tilesM * (CG * kBM) + (int)rank * kBM, n = w.tile / a.tilesM * BN + (int)rank * Sh::kBRows;
+      int m, n;
+      w.place<Sh::kGroup>(a, m, n);
+      m = m * (CG * kBM) + (int)rank * kBM;
+      n = n * BN + (int)rank * Sh::kBRows;
       for (int k = 0; k < a.steps; ++k) {
         if (round > 0 && !(ok = __all_sync(0xffffffffu, waitBar(&empty[stage], (round - 1) & 1, dead)))) break;
         if (one) {
@@ -612,8 +665,10 @@ __global__ void __launch_bounds__(kProductThreads, 1) productKernel(const __grid
     int turn = 0, which = 0;
     for (Walk w(args, unit, gridDim.x / CG); w.more(); w.next(args, unit), ++turn) {
       const Problem& a = args.p[w.which];
-      const int m0 = w.tile % a.tilesM * (CG * kBM) + (int)rank * kBM + quarter * 32;
-      const int n0 = w.tile / a.tilesM * BN + part * kCols;
+      int m0, n0;
+      w.place<Sh::kGroup>(a, m0, n0);
+      m0 = m0 * (CG * kBM) + (int)rank * kBM + quarter * 32;
+      n0 = n0 * BN + part * kCols;
       const int acc = turn & 1, use = turn >> 1;
       uint32_t bias[kCols / 64];
       if (a.bias)
@@ -766,6 +821,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) productSplit(const __grid_
   __syncthreads();
   tcFenceAfter();
   const uint32_t tmem = __shfl_sync(0xffffffffu, tmemSlot, 0);
+  letNextIn();
   waitForPrevious();
   const int m0 = tile % a.tilesM * kBM, n0 = tile / a.tilesM * BN;
   const int rows = SWAP ? a.N : a.M, cols = SWAP ? a.M : a.N;  // of the result
@@ -1029,12 +1085,12 @@ constexpr int kSlopeTurn = 4;  // rows a thread has in flight
 // eight columns; WIDE: rows of dy and z start on 16-byte boundaries (and end
 // on them), else their elements are gathered. dz always does.
 template <int DT, int ACT, bool WIDE>
-__global__ void __launch_bounds__(256) linearSlope(const __grid_constant__ SlopeArgs a) {
+__global__ void __launch_bounds__(256, 4) linearSlope(const __grid_constant__ SlopeArgs a) {
   using S = typename Ty<DT>::S;
   __shared__ float part[kSlopeRows][256];
   const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
   const int c = (blockIdx.x * 32 + lane) * 8;
-  float sum[8] = {};
+  F2 sum[4] = {};
   letNextIn();
   if (c < a.cols) {
     const int left = min(8, a.cols - c);
@@ -1059,20 +1115,23 @@ __global__ void __launch_bounds__(256) linearSlope(const __grid_constant__ Slope
         if (r >= a.rows) break;
         float f[8], h[8];
         Vec16<DT>::expand(d[u], f);
-        if constexpr (ACT != vrcclActNone) {
-          Vec16<DT>::expand(z[u], h);
+        if constexpr (ACT != vrcclActNone) Vec16<DT>::expand(z[u], h);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) f[e] *= slope<ACT>(h[e]);
+        for (int e = 0; e < 4; ++e) {
+          F2 x = pair(f[2 * e], f[2 * e + 1]);
+          if constexpr (ACT != vrcclActNone) x = mul2(x, slope<ACT>(pair(h[2 * e], h[2 * e + 1])));
+          sum[e] = add2(sum[e], x);
+          const float2 y = split(x);
+          f[2 * e] = y.x;
+          f[2 * e + 1] = y.y;
         }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) sum[e] += f[e];
         if (a.dz) *reinterpret_cast<uint4*>(static_cast<S*>(a.dz) + r * a.lddz + c) = Vec16<DT>::pack(f);
       }
     }
   }
   if (!a.partial) return;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) part[g][lane * 8 + e] = sum[e];
+  for (int e = 0; e < 4; ++e) *reinterpret_cast<float2*>(&part[g][lane * 8 + 2 * e]) = split(sum[e]);
   __syncthreads();
   const int col = blockIdx.x * 256 + threadIdx.x;
   if (col >= a.cols) return;
@@ -1221,6 +1280,7 @@ vrcclResult_t launchProducts(const Product* q, int n, bool after, cudaStream_t s
     p.wideD = p.N % 8 == 0 && rowsAligned(p.d, p.ldd, 2);
     p.wideZ = p.z && p.N % 8 == 0 && rowsAligned(p.z, p.ldz, 2);
     p.tilesM = (p.M + CG * kBM - 1) / (CG * kBM);
+    p.tilesN = (p.N + BN - 1) / BN;
     p.tiles = (int)tileCount(p, CG * kBM, BN);
     p.steps = (p.K + Sh::kBK - 1) / Sh::kBK;
     total += p.tiles;
@@ -1307,19 +1367,22 @@ enum Tile { kPair256, kBlock128, kBlock64, kSplit64, kSwap32, kSwap64 };
 struct Choice {
   Tile tile;
   int parts;
+  double cycles;
 };
 Choice chooseTile(const Product* q, int n) {
-  if (n == 1 && q->p.M <= 64 && !q->p.aMN && !q->p.bMN) {
-    const bool narrow = q->p.M <= 32;
-    return {narrow ? kSwap32 : kSwap64, splitParts((q->p.N + kBM - 1) / kBM, (q->p.K + 127) / 128)};
-  }
-  struct {
+  struct Kind {
     Tile tile;
     int bm, bn, blocks, step, end;
-  } static const kinds[3] = {{kPair256, 256, 256, 2, 520, 6000}, {kBlock128, 128, 128, 1, 420, 3000}, {kBlock64, 128, 64, 1, 341, 2200}};
-  Choice best = {kPair256, 1};
-  double least = 1e300;
-  for (const auto& k : kinds) {
+  };
+  static const Kind kinds[3] = {{kPair256, 256, 256, 2, 520, 6000}, {kBlock128, 128, 128, 1, 420, 3000}, {kBlock64, 128, 64, 1, 341, 2200}};
+  constexpr double kJoin = 3000;  // the sums' way through distributed shared memory
+  if (n == 1 && q->p.M <= 64 && !q->p.aMN) {
+    const int parts = splitParts((q->p.N + kBM - 1) / kBM, (q->p.K + 127) / 128);
+    const long long rounds = ((q->p.N + kBM - 1) / kBM * (long long)parts + smCount() - 1) / smCount();
+    return {q->p.M <= 32 ? kSwap32 : kSwap64, parts, (double)rounds * ((q->p.K + 63) / 64 / parts * 300 + 2200) + kJoin};
+  }
+  Choice best = {kPair256, 1, 1e300};
+  for (const Kind& k : kinds) {
     const int units = smCount() / k.blocks;
     double cycles = 0, longest = 0;
     long long tiles = 0;
@@ -1332,14 +1395,11 @@ Choice chooseTile(const Product* q, int n) {
       tiles += t;
     }
     cycles = std::max(n == 1 ? cycles : cycles + longest / 4, longest) + k.end;
-    if (cycles < least) {
-      least = cycles;
-      best = {k.tile, 1};
-    }
+    if (cycles < best.cycles) best = {k.tile, 1, cycles};
     if (k.tile == kBlock64 && n == 1) {
       const int parts = splitParts(tiles, (q->p.K + 127) / 128);
-      const double split = longest / parts + k.end + 3000;
-      if (parts > 1 && split < least) best = {kSplit64, parts};
+      const double split = longest / parts + k.end + kJoin;
+      if (parts > 1 && split < best.cycles) best = {kSplit64, parts, split};
     }
   }
   return best;
@@ -1348,12 +1408,16 @@ Choice chooseTile(const Product* q, int n) {
 // `after`: the stream's last kernel is this call's own and lets the next one in.
 template <int DT>
 vrcclResult_t products(const Product* q, int n, bool after, cudaStream_t st) {
-  if (n == 2 && tileCount(q[0].p, 256, 256) + tileCount(q[1].p, 256, 256) > 60000) {
-    // more than a launch counts: they fill the GPU one by one
-    const vrcclResult_t r = products<DT>(q, 1, after, st);
-    return r == vrcclSuccess ? products<DT>(q + 1, 1, false, st) : r;
-  }
   const Choice c = chooseTile(q, n);
+  if (n == 2) {
+    // One by one where that is shorter (a few rows' dx is one long contraction that wants splitting, their dW is none at
+    // all: 16 rows of 4096 x 4096) or where there are more tiles than a launch counts. A launch costs some 3000 cycles.
+    const bool many = tileCount(q[0].p, 128, 64) + tileCount(q[1].p, 128, 64) > 60000;
+    if (many || chooseTile(q, 1).cycles + chooseTile(q + 1, 1).cycles + 3000 < c.cycles) {
+      const vrcclResult_t r = products<DT>(q, 1, after, st);
+      return r == vrcclSuccess ? products<DT>(q + 1, 1, true, st) : r;
+    }
+  }
   switch (c.tile) {
     case kPair256: return launchProducts<DT, 2, 256>(q, n, after, st);
     case kBlock128: return launchProducts<DT, 1, 128>(q, n, after, st);
