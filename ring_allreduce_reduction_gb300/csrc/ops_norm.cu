@@ -35,7 +35,7 @@ struct NormArgs {
   int cols;
   int ptype;
   bool wideParams;  // gamma and beta start on 16-byte boundaries
-  int stages, teams, teamThreads;
+  int stages, teams;
   float eps;
 };
 
@@ -122,7 +122,7 @@ __device__ __forceinline__ void loadParams(const void* p, int ptype, bool wide, 
 constexpr int kTeamElems = 16;
 constexpr int kTeamCols = 512 * kTeamElems;
 constexpr int kMaxStages = 8;
-constexpr int kTeamSmem = 192 * 1024;  // of the 227 KB a block may have
+constexpr int kTeamSmem = 192 * 1024, kWideSmem = 224 * 1024;  // of the 227 KB a block may have
 constexpr long long kRowWaitCycles = 3000000000ll, kDrainCycles = 200000000ll;  // a second and more
 
 __device__ int gNormStatus;  // vrcclResult_t of the first device-side failure
@@ -131,7 +131,7 @@ __device__ int gNormStatus;  // vrcclResult_t of the first device-side failure
 // blocks that lie inside the matrix's own bytes, first row's start to last
 // row's end. A row on no 16-byte boundary shares its first and last block with
 // the gap before and after it, which is copied and ignored; the few elements in
-// blocks that the matrix's ends cut are read straight from memory.
+// blocks that the matrix's ends cut are copied one by one (edges).
 struct Window {
   uintptr_t row, lo, hi;
 };
@@ -150,8 +150,10 @@ __device__ __forceinline__ Window window(const void* p, size_t ld, size_t row, s
 __host__ __device__ constexpr int slotBytes(int cols, int E) { return ((cols * E + 15) / 16 + 1) * 16; }
 
 // The 16 elements of thread t of a team of T: element q is column
-// ((q / V) T + t) V + q % V, V a whole 16-byte vector (VEC) or 1.
-template <int DT, bool VEC>
+// ((q / V) T + t) V + q % V, V a whole 16-byte vector (VEC) or 1. T is a
+// constant: offsets are then part of the instructions (with a T of any multiple
+// of 32 an element of a row on no boundary took 120 of them).
+template <int DT, bool VEC, int T>
 struct Team {
   static constexpr int E = floatTypeSize(DT), V = VEC ? 16 / E : 1, NV = kTeamElems / V;
   using S = typename Ty<DT>::S;
@@ -165,49 +167,55 @@ struct Team {
     const Window w = window(p, ld, row, rows, cols, E);
     if (w.hi > w.lo) bulkLoadOnce(slot + (w.lo - (w.row & ~(uintptr_t)15)), (const void*)w.lo, w.hi - w.lo, bar, policy);
   }
+  // What a bulk copy may not take of a row (see Window), copied by the thread that is about to announce it: its arrival
+  // at the row's barrier makes them visible with the rest.
+  static __device__ __forceinline__ void edges(unsigned char* slot, const void* p, size_t ld, size_t row, size_t rows,
+                                               int cols) {
+    if constexpr (!VEC) {
+      if (row != 0 && row != rows - 1) return;
+      const Window w = window(p, ld, row, rows, cols, E);
+      S* v = reinterpret_cast<S*>(slot + (w.row & 15));
+      for (uintptr_t at = w.row; at < w.lo && at < w.row + (uintptr_t)cols * E; at += E) v[(at - w.row) / E] = *(const S*)at;
+      for (uintptr_t at = max(w.hi, w.row); at < w.row + (uintptr_t)cols * E; at += E) v[(at - w.row) / E] = *(const S*)at;
+    }
+  }
   static __device__ __forceinline__ unsigned fetchBytes(const void* p, size_t ld, size_t row, size_t rows, int cols) {
     if constexpr (VEC) return cols * E;
     const Window w = window(p, ld, row, rows, cols, E);
     return w.hi - w.lo;
   }
-  static __device__ __forceinline__ void take(const unsigned char* slot, const void* p, size_t ld, size_t row,
-                                              size_t rows, int cols, int t, int T, float (&f)[kTeamElems]) {
+  // Elements FROM .. FROM + N of the thread's 16 (whole vectors).
+  template <int FROM, int N>
+  static __device__ __forceinline__ void takeSome(const unsigned char* slot, const void* p, size_t ld, size_t row,
+                                                  size_t rows, int cols, int t, float (&f)[N]) {
     if constexpr (VEC) {
       const uint4* v = reinterpret_cast<const uint4*>(slot);
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const int i = j * T + t;
+      for (int j = 0; j < N / V; ++j) {
+        const int i = (FROM / V + j) * T + t;
         float g[V];
         Vec16<DT>::expand(i * V < cols ? v[i] : make_uint4(0, 0, 0, 0), g);
 #pragma unroll
         for (int e = 0; e < V; ++e) f[j * V + e] = g[e];
       }
     } else {
-      const unsigned skew = ((unsigned)(uintptr_t)p + (unsigned)row * (unsigned)ld * E) & 15;
-      const S* v = reinterpret_cast<const S*>(slot + skew);
-      const bool cut = (row == 0 && skew != 0) || (row == rows - 1 && ((skew + (unsigned)cols * E) & 15) != 0);
-      if (!cut) {
+      const S* v = reinterpret_cast<const S*>(slot + (((unsigned)(uintptr_t)p + (unsigned)row * (unsigned)ld * E) & 15)) + t;
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-          const int c = j * T + t;
-          f[j] = c < cols ? Ty<DT>::toF(v[c]) : 0.f;
-        }
-      } else {
-        const Window w = window(p, ld, row, rows, cols, E);
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-          const int c = j * T + t;
-          const uintptr_t at = w.row + (uintptr_t)c * E;
-          f[j] = c < cols ? Ty<DT>::toF(at < w.lo || at >= w.hi ? *(const S*)at : v[c]) : 0.f;
-        }
+      for (int j = 0; j < N; ++j) {
+        f[j] = 0.f;
+        if ((FROM + j) * T + t < cols) f[j] = Ty<DT>::toF(v[(FROM + j) * T]);
       }
     }
   }
-  static __device__ __forceinline__ void store(void* row, int cols, int t, int T, const float (&f)[kTeamElems]) {
+  static __device__ __forceinline__ void take(const unsigned char* slot, const void* p, size_t ld, size_t row,
+                                              size_t rows, int cols, int t, float (&f)[kTeamElems]) {
+    takeSome<0, kTeamElems>(slot, p, ld, row, rows, cols, t, f);
+  }
+  static __device__ __forceinline__ void storeSome(void* row, int cols, int t, int from, const float* f, int n) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int i = j * T + t;
-      if (i * V >= cols) continue;
+    for (int j = 0; j < n / V; ++j) {
+      const int i = (from / V + j) * T + t;
+      if (i * V >= cols) break;
       if constexpr (VEC) {
         float g[V];
 #pragma unroll
@@ -218,7 +226,10 @@ struct Team {
       }
     }
   }
-  static __device__ __forceinline__ void params(const void* p, int ptype, bool wide, float dflt, int cols, int t, int T,
+  static __device__ __forceinline__ void store(void* row, int cols, int t, const float (&f)[kTeamElems]) {
+    storeSome(row, cols, t, 0, f, kTeamElems);
+  }
+  static __device__ __forceinline__ void params(const void* p, int ptype, bool wide, float dflt, int cols, int t,
                                                 float (&f)[kTeamElems]) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -231,11 +242,12 @@ struct Team {
       for (int e = 0; e < V; ++e) f[j * V + e] = g[e];
     }
   }
-  static __device__ __forceinline__ bool held(int q, int cols, int t, int T) { return (q / V * T + t) * V < cols; }
+  static __device__ __forceinline__ bool held(int q, int cols, int t) { return (q / V * T + t) * V < cols; }
 };
 
-__device__ __forceinline__ void teamSync(int team, int T) {
-  if (T == 32)
+template <int T>
+__device__ __forceinline__ void teamSync(int team) {
+  if constexpr (T == 32)
     __syncwarp();
   else
     asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(T) : "memory");
@@ -277,16 +289,17 @@ __device__ __forceinline__ float sumHalf(float x) {
   return x;
 }
 
-template <int DT, bool VEC>
+template <int DT, bool VEC, int T>
 __global__ void __launch_bounds__(512) normForwardTeams(const __grid_constant__ NormArgs a) {
-  using M = Team<DT, VEC>;
+  using M = Team<DT, VEC, T>;
   constexpr int E = M::E, NP = kTeamElems / 2;
   extern __shared__ __align__(128) unsigned char ring[];
   __shared__ unsigned long long full[16 * kMaxStages];
   __shared__ float2 red[16][2][2][16];  // team, turn, row, warp: (sum, squares about the warp's mean)
   __shared__ int deadWord[16];
-  const int T = a.teamThreads, team = threadIdx.x / T, t = threadIdx.x - team * T, lane = t & 31;
-  const int cols = a.cols, stages = a.stages, slot = slotBytes(cols, E), warps = T >> 5;
+  const int team = threadIdx.x / T, t = threadIdx.x % T, lane = t & 31;
+  const int cols = a.cols, stages = a.stages, slot = slotBytes(cols, E);
+  constexpr int warps = T / 32;
   unsigned char* mine = ring + (size_t)team * stages * slot;
   unsigned long long* bar = full + team * kMaxStages;
   int* dead = &deadWord[team];
@@ -300,6 +313,7 @@ __global__ void __launch_bounds__(512) normForwardTeams(const __grid_constant__ 
   }
   auto refill = [&](int s, size_t row) {
     if (row >= a.rows) return;
+    M::edges(mine + (size_t)s * slot, a.x, a.ldx, row, a.rows, cols);
     expectBytes(&bar[s], M::fetchBytes(a.x, a.ldx, row, a.rows, cols));
     M::fetch(mine + (size_t)s * slot, a.x, a.ldx, row, a.rows, cols, &bar[s], policy);
   };
@@ -308,10 +322,10 @@ __global__ void __launch_bounds__(512) normForwardTeams(const __grid_constant__ 
   F2 g[NP], b[NP];
   {
     float p[kTeamElems];
-    M::params(a.gamma, a.ptype, a.wideParams, 1.f, cols, t, T, p);
+    M::params(a.gamma, a.ptype, a.wideParams, 1.f, cols, t, p);
 #pragma unroll
     for (int i = 0; i < NP; ++i) g[i] = pair(p[2 * i], p[2 * i + 1]);
-    M::params(a.beta, a.ptype, a.wideParams, 0.f, cols, t, T, p);
+    M::params(a.beta, a.ptype, a.wideParams, 0.f, cols, t, p);
 #pragma unroll
     for (int i = 0; i < NP; ++i) b[i] = pair(p[2 * i], p[2 * i + 1]);
   }
@@ -325,16 +339,16 @@ __global__ void __launch_bounds__(512) normForwardTeams(const __grid_constant__ 
   };
   const float ownCount = warpCount(t >> 5), ownInv = ownCount > 0.f ? 1.f / ownCount : 0.f;
   const float joinCount = (lane & 15) < warps ? warpCount(lane & 15) : 0.f, joinInv = joinCount > 0.f ? 1.f / joinCount : 0.f;
-  teamSync(team, T);
+  teamSync<T>(team);
   int stage = 0, round = 0, turn = 0;
   for (size_t row = first; row < a.rows; row += 2 * stride) {
     const bool two = row + stride < a.rows;
     float f[2][kTeamElems];
     waitRow(&bar[stage], round & 1, dead);
-    M::take(mine + (size_t)stage * slot, a.x, a.ldx, row, a.rows, cols, t, T, f[0]);
+    M::take(mine + (size_t)stage * slot, a.x, a.ldx, row, a.rows, cols, t, f[0]);
     if (two) {
       waitRow(&bar[stage + 1], round & 1, dead);
-      M::take(mine + (size_t)(stage + 1) * slot, a.x, a.ldx, row + stride, a.rows, cols, t, T, f[1]);
+      M::take(mine + (size_t)(stage + 1) * slot, a.x, a.ldx, row + stride, a.rows, cols, t, f[1]);
     } else {
 #pragma unroll
       for (int i = 0; i < kTeamElems; ++i) f[1][i] = 0.f;
@@ -362,10 +376,10 @@ __global__ void __launch_bounds__(512) normForwardTeams(const __grid_constant__ 
       for (int i = 0; i < NP; ++i) {
         const F2 d = add2(x[r][i], minus);
         if constexpr (VEC) {
-          if (M::held(2 * i, cols, t, T)) acc = fma2(d, d, acc);
+          if (M::held(2 * i, cols, t)) acc = fma2(d, d, acc);
         } else {
           const float2 q = split(d);
-          acc = fma2(d, pair(M::held(2 * i, cols, t, T) ? q.x : 0.f, M::held(2 * i + 1, cols, t, T) ? q.y : 0.f), acc);
+          acc = fma2(d, pair(M::held(2 * i, cols, t) ? q.x : 0.f, M::held(2 * i + 1, cols, t) ? q.y : 0.f), acc);
         }
       }
       const float2 q = split(acc);
@@ -374,7 +388,7 @@ __global__ void __launch_bounds__(512) normForwardTeams(const __grid_constant__ 
     const float squares = sumTwo(s[0], s[1], high);
     turn ^= 1;
     if ((lane & 15) == 0) red[team][turn][high][t >> 5] = make_float2(both, squares);
-    teamSync(team, T);
+    teamSync<T>(team);
     if (*reinterpret_cast<volatile int*>(dead)) {
       abandon(bar, stages, stage, round, t == 0, dead);
       break;
@@ -403,7 +417,7 @@ __global__ void __launch_bounds__(512) normForwardTeams(const __grid_constant__ 
         f[r][2 * i] = q.x;
         f[r][2 * i + 1] = q.y;
       }
-      M::store(static_cast<char*>(a.y) + (row + r * stride) * a.ldy * E, cols, t, T, f[r]);
+      M::store(static_cast<char*>(a.y) + (row + r * stride) * a.ldy * E, cols, t, f[r]);
     }
     if ((stage += 2) == stages) {
       stage = 0;
@@ -414,16 +428,17 @@ __global__ void __launch_bounds__(512) normForwardTeams(const __grid_constant__ 
 
 // Backward: x and dy rows arrive together, a row a turn; the columns' two sums
 // stay in registers to the end, where the block's teams add them up.
-template <int DT, bool VEC>
+template <int DT, bool VEC, int T>
 __global__ void __launch_bounds__(512) normBackwardTeams(const __grid_constant__ NormArgs a) {
-  using M = Team<DT, VEC>;
+  using M = Team<DT, VEC, T>;
   constexpr int E = M::E, NP = kTeamElems / 2;
   extern __shared__ __align__(128) unsigned char ring[];
   __shared__ unsigned long long full[16 * kMaxStages];
   __shared__ float2 red[16][2][16];
   __shared__ int deadWord[16];
-  const int T = a.teamThreads, team = threadIdx.x / T, t = threadIdx.x - team * T, lane = t & 31;
-  const int cols = a.cols, stages = a.stages, slot = slotBytes(cols, E), warps = T >> 5;
+  const int team = threadIdx.x / T, t = threadIdx.x % T, lane = t & 31;
+  const int cols = a.cols, stages = a.stages, slot = slotBytes(cols, E);
+  constexpr int warps = T / 32;
   unsigned char* mine = ring + (size_t)team * stages * 2 * slot;
   unsigned long long* bar = full + team * kMaxStages;
   int* dead = &deadWord[team];
@@ -438,6 +453,8 @@ __global__ void __launch_bounds__(512) normBackwardTeams(const __grid_constant__
   auto refill = [&](int s, size_t row) {
     if (row >= a.rows) return;
     unsigned char* q = mine + (size_t)s * 2 * slot;
+    M::edges(q, a.x, a.ldx, row, a.rows, cols);
+    M::edges(q + slot, a.dy, a.lddy, row, a.rows, cols);
     expectBytes(&bar[s], M::fetchBytes(a.x, a.ldx, row, a.rows, cols) + M::fetchBytes(a.dy, a.lddy, row, a.rows, cols));
     M::fetch(q, a.x, a.ldx, row, a.rows, cols, &bar[s], policy);
     M::fetch(q + slot, a.dy, a.lddy, row, a.rows, cols, &bar[s], policy);
@@ -447,7 +464,7 @@ __global__ void __launch_bounds__(512) normBackwardTeams(const __grid_constant__
   F2 g[NP], dg[NP], db[NP];
   {
     float p[kTeamElems];
-    M::params(a.gamma, a.ptype, a.wideParams, 1.f, cols, t, T, p);
+    M::params(a.gamma, a.ptype, a.wideParams, 1.f, cols, t, p);
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
       g[i] = pair(p[2 * i], p[2 * i + 1]);
@@ -461,7 +478,7 @@ __global__ void __launch_bounds__(512) normBackwardTeams(const __grid_constant__
     nextMean = a.mean[first];
     nextRstd = a.rstd[first];
   }
-  teamSync(team, T);
+  teamSync<T>(team);
   int stage = 0, round = 0, turn = 0;
   for (size_t row = first; row < a.rows; row += stride) {
     const float mean = nextMean, rstd = nextRstd;
@@ -472,10 +489,10 @@ __global__ void __launch_bounds__(512) normBackwardTeams(const __grid_constant__
     {
       float f[kTeamElems];
       const F2 scale = pair(rstd, rstd), shift = pair(-mean, -mean);
-      M::take(q, a.x, a.ldx, row, a.rows, cols, t, T, f);
+      M::take(q, a.x, a.ldx, row, a.rows, cols, t, f);
 #pragma unroll
       for (int i = 0; i < NP; ++i) xh[i] = mul2(add2(pair(f[2 * i], f[2 * i + 1]), shift), scale);
-      M::take(q + slot, a.dy, a.lddy, row, a.rows, cols, t, T, f);
+      M::take(q + slot, a.dy, a.lddy, row, a.rows, cols, t, f);
       F2 sg = 0, sx = 0;  // dy is zero in columns that do not exist
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
@@ -492,7 +509,7 @@ __global__ void __launch_bounds__(512) normBackwardTeams(const __grid_constant__
     const float part = sumTwo(s.x, s.y, lane >= 16);
     turn ^= 1;
     if ((lane & 15) == 0) reinterpret_cast<float*>(&red[team][turn][t >> 5])[lane >> 4] = part;
-    teamSync(team, T);
+    teamSync<T>(team);
     if (*reinterpret_cast<volatile int*>(dead)) {
       abandon(bar, stages, stage, round, t == 0, dead);
       break;
@@ -512,7 +529,7 @@ __global__ void __launch_bounds__(512) normBackwardTeams(const __grid_constant__
       f[2 * i] = u.x;
       f[2 * i + 1] = u.y;
     }
-    M::store(static_cast<char*>(a.y) + row * a.ldy * E, cols, t, T, f);
+    M::store(static_cast<char*>(a.y) + row * a.ldy * E, cols, t, f);
     if (++stage == stages) {
       stage = 0;
       ++round;
@@ -524,7 +541,7 @@ __global__ void __launch_bounds__(512) normBackwardTeams(const __grid_constant__
   __syncthreads();  // no team reads its ring any more
 #pragma unroll
   for (int i = 0; i < kTeamElems; ++i) {
-    if (!M::held(i, cols, t, T)) continue;
+    if (!M::held(i, cols, t)) continue;
     float* q = sum + (size_t)team * 2 * cols + (i / M::V * T + t) * M::V + i % M::V;
     const float2 u = split(dg[i / 2]), v = split(db[i / 2]);
     q[0] = i & 1 ? u.y : u.x;
@@ -539,8 +556,252 @@ __global__ void __launch_bounds__(512) normBackwardTeams(const __grid_constant__
   }
 }
 
-// ------------------------------------------------------------ a row a block
-// Rows of up to 32768 elements, one a block, EPT elements a thread.
+// ------------------------------------------------------------ a whole block for a row
+// Rows of up to 16384 elements: a team of up to 1024 threads, which leaves each
+// 64 registers. What the smaller teams keep in registers is divided: forward
+// holds the row and reads the parameters from shared memory, backward holds the
+// columns' sums and passes over the row's stage twice (so that a stage is
+// refilled a row later, when the next barrier shows that all are through).
+constexpr int kWideCols = 1024 * kTeamElems;
+
+// A thread's own parameters in shared memory, pair i at [i T + t]: laid out so
+// that a warp reads its pairs side by side (by column, vectors of eight would
+// put its lanes 32 bytes apart and a read would take eight turns).
+template <int DT, bool VEC, int T>
+__device__ __forceinline__ void keepParams(F2* own, const void* p, int ptype, bool wide, float dflt, int cols, int t) {
+  float f[kTeamElems];
+  Team<DT, VEC, T>::params(p, ptype, wide, dflt, cols, t, f);
+#pragma unroll
+  for (int i = 0; i < kTeamElems / 2; ++i) own[i * T + t] = pair(f[2 * i], f[2 * i + 1]);
+}
+
+template <int DT, bool VEC, int T>
+__global__ void __launch_bounds__(T, 1) normForwardWide(const __grid_constant__ NormArgs a) {
+  using M = Team<DT, VEC, T>;
+  constexpr int E = M::E, NP = kTeamElems / 2;
+  extern __shared__ __align__(128) unsigned char ring[];
+  __shared__ unsigned long long full[kMaxStages];
+  __shared__ float2 red[2][32];
+  __shared__ int dead;
+  constexpr int warps = T / 32;
+  const int t = threadIdx.x, lane = t & 31;
+  const int cols = a.cols, stages = a.stages, slot = slotBytes(cols, E);
+  F2* gamma = reinterpret_cast<F2*>(ring + (size_t)stages * slot);
+  F2* beta = gamma + NP * T;
+  const size_t stride = gridDim.x;
+  unsigned long long policy = 0;
+  if (t == 0) {
+    for (int s = 0; s < stages; ++s) mbarInit(&full[s], 1);
+    dead = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    policy = evictFirstPolicy();
+  }
+  auto refill = [&](int s, size_t row) {
+    if (row >= a.rows) return;
+    M::edges(ring + (size_t)s * slot, a.x, a.ldx, row, a.rows, cols);
+    expectBytes(&full[s], M::fetchBytes(a.x, a.ldx, row, a.rows, cols));
+    M::fetch(ring + (size_t)s * slot, a.x, a.ldx, row, a.rows, cols, &full[s], policy);
+  };
+  if (t == 0)
+    for (int s = 0; s < stages; ++s) refill(s, blockIdx.x + s * stride);
+  keepParams<DT, VEC, T>(gamma, a.gamma, a.ptype, a.wideParams, 1.f, cols, t);
+  keepParams<DT, VEC, T>(beta, a.beta, a.ptype, a.wideParams, 0.f, cols, t);
+  const float inv = 1.f / (float)cols;
+  auto warpCount = [&](int w) {
+    int n = 0;
+    for (int j = 0; j < M::NV; ++j) n += min(32, max(0, (cols + M::V - 1) / M::V - j * T - w * 32)) * M::V;
+    return (float)n;
+  };
+  const float ownCount = warpCount(t >> 5), ownInv = ownCount > 0.f ? 1.f / ownCount : 0.f;
+  const float joinCount = lane < warps ? warpCount(lane) : 0.f, joinInv = joinCount > 0.f ? 1.f / joinCount : 0.f;
+  __syncthreads();
+  int stage = 0, round = 0, turn = 0;
+  for (size_t row = blockIdx.x; row < a.rows; row += stride) {
+    waitRow(&full[stage], round & 1, &dead);
+    F2 x[NP];
+    float s;
+    {
+      float f[kTeamElems];
+      M::take(ring + (size_t)stage * slot, a.x, a.ldx, row, a.rows, cols, t, f);
+      F2 acc = 0;
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        x[i] = pair(f[2 * i], f[2 * i + 1]);
+        acc = add2(acc, x[i]);
+      }
+      const float2 q = split(acc);
+      s = warpSum(q.x + q.y);
+    }
+    float squares;
+    {
+      const F2 minus = pair(-s * ownInv, -s * ownInv);
+      float q = 0.f;
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        const float2 d = split(add2(x[i], minus));
+        q += M::held(2 * i, cols, t) ? d.x * d.x : 0.f;
+        q += M::held(2 * i + 1, cols, t) ? d.y * d.y : 0.f;
+      }
+      squares = warpSum(q);
+    }
+    turn ^= 1;
+    if (lane == 0) red[turn][t >> 5] = make_float2(s, squares);
+    __syncthreads();
+    if (*reinterpret_cast<volatile int*>(&dead)) {
+      abandon(full, stages, stage, round, t == 0, &dead);
+      break;
+    }
+    if (t == 0) refill(stage, row + stages * stride);
+    const float2 w = lane < warps ? red[turn][lane] : make_float2(0.f, 0.f);
+    const float mean = warpSum(w.x) * inv, d = w.x * joinInv - mean;
+    const float rstd = rsqrtf(warpSum(w.y + joinCount * d * d) * inv + a.eps);
+    if (t == 0) {
+      if (a.mean) a.mean[row] = mean;
+      if (a.rstd) a.rstd[row] = rstd;
+    }
+    float f[kTeamElems];
+    const F2 scale = pair(rstd, rstd), shift = pair(-mean, -mean);
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const float2 q = split(fma2(mul2(add2(x[i], shift), scale), gamma[i * T + t], beta[i * T + t]));
+      f[2 * i] = q.x;
+      f[2 * i + 1] = q.y;
+    }
+    M::store(static_cast<char*>(a.y) + row * a.ldy * E, cols, t, f);
+    if (++stage == stages) {
+      stage = 0;
+      ++round;
+    }
+  }
+}
+
+// fn(0), fn(N), ... over a thread's elements, the argument a constant.
+template <int N, int FROM = 0, typename Fn>
+__device__ __forceinline__ void chunks(Fn& fn) {
+  if constexpr (FROM < kTeamElems) {
+    fn(std::integral_constant<int, FROM>{});
+    chunks<N, FROM + N>(fn);
+  }
+}
+
+template <int DT, bool VEC, int T>
+__global__ void __launch_bounds__(T, 1) normBackwardWide(const __grid_constant__ NormArgs a) {
+  using M = Team<DT, VEC, T>;
+  constexpr int E = M::E, NP = kTeamElems / 2, kChunk = VEC ? 8 : 4;
+  extern __shared__ __align__(128) unsigned char ring[];
+  __shared__ unsigned long long full[kMaxStages];
+  __shared__ float2 red[2][32];
+  __shared__ int dead;
+  constexpr int warps = T / 32;
+  const int t = threadIdx.x, lane = t & 31;
+  const int cols = a.cols, stages = a.stages, slot = slotBytes(cols, E);
+  F2* gamma = reinterpret_cast<F2*>(ring + (size_t)stages * 2 * slot);
+  const size_t stride = gridDim.x;
+  unsigned long long policy = 0;
+  if (t == 0) {
+    for (int s = 0; s < stages; ++s) mbarInit(&full[s], 1);
+    dead = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    policy = evictFirstPolicy();
+  }
+  auto refill = [&](int s, size_t row) {
+    if (row >= a.rows) return;
+    unsigned char* q = ring + (size_t)s * 2 * slot;
+    M::edges(q, a.x, a.ldx, row, a.rows, cols);
+    M::edges(q + slot, a.dy, a.lddy, row, a.rows, cols);
+    expectBytes(&full[s], M::fetchBytes(a.x, a.ldx, row, a.rows, cols) + M::fetchBytes(a.dy, a.lddy, row, a.rows, cols));
+    M::fetch(q, a.x, a.ldx, row, a.rows, cols, &full[s], policy);
+    M::fetch(q + slot, a.dy, a.lddy, row, a.rows, cols, &full[s], policy);
+  };
+  if (t == 0)
+    for (int s = 0; s < stages; ++s) refill(s, blockIdx.x + s * stride);
+  keepParams<DT, VEC, T>(gamma, a.gamma, a.ptype, a.wideParams, 1.f, cols, t);
+  F2 dg[NP], db[NP];
+#pragma unroll
+  for (int i = 0; i < NP; ++i) dg[i] = db[i] = 0;
+  const float inv = 1.f / (float)cols;
+  letNextIn();
+  __syncthreads();
+  int stage = 0, round = 0, turn = 0, behind = 0;
+  for (size_t row = blockIdx.x; row < a.rows; row += stride) {
+    const float mean = a.mean[row], rstd = a.rstd[row];
+    waitRow(&full[stage], round & 1, &dead);
+    const unsigned char* q = ring + (size_t)stage * 2 * slot;
+    const F2 scale = pair(rstd, rstd), shift = pair(-mean, -mean);
+    F2 sg = 0, sx = 0;
+    // a few elements at a time: more at once would not fit beside the sums, and what spills finds no L1 (shared memory
+    // has it)
+    auto sums = [&](auto from) {
+      constexpr int kFrom = decltype(from)::value;
+      float fx[kChunk], fd[kChunk];
+      M::template takeSome<kFrom, kChunk>(q, a.x, a.ldx, row, a.rows, cols, t, fx);
+      M::template takeSome<kFrom, kChunk>(q + slot, a.dy, a.lddy, row, a.rows, cols, t, fd);
+#pragma unroll
+      for (int i = 0; i < kChunk / 2; ++i) {
+        const int p = kFrom / 2 + i;
+        const F2 xh = mul2(add2(pair(fx[2 * i], fx[2 * i + 1]), shift), scale), d = pair(fd[2 * i], fd[2 * i + 1]);
+        const F2 gd = mul2(d, gamma[p * T + t]);
+        sg = add2(sg, gd);
+        sx = fma2(gd, xh, sx);
+        dg[p] = fma2(d, xh, dg[p]);
+        db[p] = add2(db[p], d);
+      }
+      asm volatile("" ::: "memory");
+    };
+    chunks<kChunk>(sums);
+    const float2 u = split(sg), w = split(sx);
+    const float2 s = warpSum2(make_float2(u.x + u.y, w.x + w.y));
+    turn ^= 1;
+    if (lane == 0) red[turn][t >> 5] = s;
+    __syncthreads();
+    if (*reinterpret_cast<volatile int*>(&dead)) {
+      abandon(full, stages, stage, round, t == 0, &dead);
+      break;
+    }
+    // all are through with the row before this one: its stage takes the row `stages` after it
+    if (t == 0 && stages > 1 && row != blockIdx.x) refill(behind, row + (stages - 1) * stride);
+    behind = stage;
+    const float2 m = warpSum2(lane < warps ? red[turn][lane] : make_float2(0.f, 0.f));
+    const F2 n1 = pair(-m.x * inv, -m.x * inv), n2 = pair(-m.y * inv, -m.y * inv);
+    auto outputs = [&](auto from) {
+      constexpr int kFrom = decltype(from)::value;
+      float fx[kChunk], fd[kChunk];
+      M::template takeSome<kFrom, kChunk>(q, a.x, a.ldx, row, a.rows, cols, t, fx);
+      M::template takeSome<kFrom, kChunk>(q + slot, a.dy, a.lddy, row, a.rows, cols, t, fd);
+#pragma unroll
+      for (int i = 0; i < kChunk / 2; ++i) {
+        const F2 xh = mul2(add2(pair(fx[2 * i], fx[2 * i + 1]), shift), scale), g = gamma[(kFrom / 2 + i) * T + t];
+        const float2 v = split(mul2(scale, fma2(xh, n2, fma2(pair(fd[2 * i], fd[2 * i + 1]), g, n1))));
+        fx[2 * i] = v.x;
+        fx[2 * i + 1] = v.y;
+      }
+      M::storeSome(static_cast<char*>(a.y) + row * a.ldy * E, cols, t, kFrom, fx, kChunk);
+      asm volatile("" ::: "memory");
+    };
+    chunks<kChunk>(outputs);
+    if (stages == 1) {  // (binary32 rows of 11400 elements and more: there is room for one)
+      __syncthreads();
+      if (t == 0) refill(0, row + stride);
+    }
+    if (++stage == stages) {
+      stage = 0;
+      ++round;
+    }
+  }
+  if (!a.partial) return;
+  float* p = a.partial + (size_t)blockIdx.x * 2 * cols;
+#pragma unroll
+  for (int i = 0; i < kTeamElems; ++i) {
+    if (!M::held(i, cols, t)) continue;
+    const int c = (i / M::V * T + t) * M::V + i % M::V;
+    const float2 u = split(dg[i / 2]), v = split(db[i / 2]);
+    p[c] = i & 1 ? u.y : u.x;
+    p[cols + c] = i & 1 ? v.y : v.x;
+  }
+}
+
+// ------------------------------------------------------------ longer rows
+// Rows of up to 32768 elements forward, one a block, EPT elements a thread, the parameters read where they are used.
 template <int DT, bool VEC, int EPT>
 __global__ void __launch_bounds__(1024) normForward(const __grid_constant__ NormArgs a) {
   using H = Held<DT, VEC, EPT>;
@@ -621,70 +882,6 @@ __global__ void __launch_bounds__(1024) normForwardLong(const __grid_constant__ 
   }
 }
 
-// Rows of up to 16384 elements backward, one a block at a time.
-template <int DT, bool VEC, int EPT>
-__global__ void __launch_bounds__(1024) normBackward(const __grid_constant__ NormArgs a) {
-  using H = Held<DT, VEC, EPT>;
-  constexpr int V = H::V, NV = H::NV, E = floatTypeSize(DT);
-  __shared__ float2 red[2][32];
-  const int T = blockDim.x, t = threadIdx.x;
-  const float inv = 1.f / (float)a.cols;
-  float dg[EPT], db[EPT];
-#pragma unroll
-  for (int i = 0; i < EPT; ++i) dg[i] = db[i] = 0.f;
-  int turn = 0;
-  for (size_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-    H hx, hd;
-    hx.load(static_cast<const char*>(a.x) + row * a.ldx * E, t, T, a.cols);
-    hd.load(static_cast<const char*>(a.dy) + row * a.lddy * E, t, T, a.cols);
-    const float mean = a.mean[row], rstd = a.rstd[row];
-    float fx[V], fd[V], g[V];
-    float2 s = make_float2(0.f, 0.f);
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int c = (j * T + t) * V;
-      if (c < a.cols) {
-        loadParams<V>(a.gamma, a.ptype, a.wideParams, c, 1.f, g);
-        hx.get(j, fx);
-        hd.get(j, fd);
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const float xh = (fx[e] - mean) * rstd, gd = fd[e] * g[e];
-          s.x += gd;
-          s.y += gd * xh;
-          dg[j * V + e] += fd[e] * xh;
-          db[j * V + e] += fd[e];
-        }
-      }
-    }
-    s = blockSum2(s, red[turn ^= 1]);
-    const float m1 = s.x * inv, m2 = s.y * inv;
-    void* out = static_cast<char*>(a.y) + row * a.ldy * E;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int i = j * T + t;
-      if (i * V < a.cols) {
-        loadParams<V>(a.gamma, a.ptype, a.wideParams, i * V, 1.f, g);
-        hx.get(j, fx);
-        hd.get(j, fd);
-#pragma unroll
-        for (int e = 0; e < V; ++e) fx[e] = rstd * (fd[e] * g[e] - m1 - (fx[e] - mean) * rstd * m2);
-        H::put(out, i, fx);
-      }
-    }
-  }
-  if (!a.partial) return;
-  float* p = a.partial + (size_t)blockIdx.x * 2 * a.cols;
-#pragma unroll
-  for (int i = 0; i < EPT; ++i) {
-    const int c = ((i / V) * T + t) * V + i % V;
-    if (c < a.cols) {
-      p[c] = dg[i];
-      p[a.cols + c] = db[i];
-    }
-  }
-}
-
 // Rows longer than a block holds: the row's two sums, then dx, each a pass
 // over the row; the weight's gradient by normColumns.
 template <int DT>
@@ -744,15 +941,21 @@ __global__ void __launch_bounds__(1024) normJoin(const float* partial, int block
 
 // ------------------------------------------------------------ host
 
-enum Walk { kTeams, kBlockRow, kLongRow };
+enum Walk { kTeams, kWide, kBlockRow, kLongRow };
 struct Shape {
   Walk walk;
   bool vec;
-  int per;       // kBlockRow: elements a thread
   int threads;   // of a block
   int teams, teamThreads, stages, smem;
   int resident;  // blocks a multiprocessor
 };
+// The thread counts that kernels are made for.
+constexpr int kTeamSizes[] = {32, 64, 96, 128, 192, 256, 320, 384, 512, 640, 768, 1024};
+int teamThreads(int cols) {
+  for (int t : kTeamSizes)
+    if (t * kTeamElems >= cols) return t;
+  return 0;
+}
 Shape normShape(size_t rows, int cols, int elem, bool aligned, bool forward) {
   Shape s = {};
   s.vec = aligned && cols % (16 / elem) == 0;
@@ -761,18 +964,24 @@ Shape normShape(size_t rows, int cols, int elem, bool aligned, bool forward) {
   if (cols <= kTeamCols) {
     // one block of up to 512 threads a multiprocessor: 128 registers each. With few rows, fewer teams to a block.
     s.walk = kTeams;
-    s.teamThreads = up(cols, kTeamElems);
+    s.teamThreads = teamThreads(cols);
     s.teams = (int)std::min<size_t>(512 / s.teamThreads, std::max<size_t>(1, (rows + smCount() - 1) / smCount()));
     s.threads = s.teams * s.teamThreads;
     const int row = slotBytes(cols, elem) * (forward ? 1 : 2);
     s.stages = std::min(kMaxStages, kTeamSmem / (s.teams * row)) & (forward ? ~1 : ~0);
     s.smem = s.teams * s.stages * row;
     s.resident = 1;
-  } else if (cols <= (forward ? kMaxHeldCols : kMaxHeldCols / 2)) {
+  } else if (cols <= kWideCols) {
+    s.walk = kWide;
+    s.threads = teamThreads(cols);
+    const int row = slotBytes(cols, elem) * (forward ? 1 : 2), params = s.threads * kTeamElems * 4 * (forward ? 2 : 1);
+    s.stages = std::min(4, (kWideSmem - params) / row);
+    s.smem = s.stages * row + params;
+    s.resident = 1;
+  } else if (forward && cols <= kMaxHeldCols) {
     s.walk = kBlockRow;
-    s.per = cols <= 16384 ? 16 : 32;
-    s.threads = up(cols, s.per);
-    s.resident = forward ? 1 << 20 : 1;
+    s.threads = up(cols, 32);
+    s.resident = 1 << 20;
   } else {
     s.walk = kLongRow;
     s.threads = 1024;
@@ -792,14 +1001,19 @@ int mostBlocks(size_t rows, int cols) {
 }
 
 using NormFn = void (*)(NormArgs);
-template <int DT, bool VEC, bool FWD>
-NormFn pickWalk(const Shape& s) {
-  if constexpr (FWD) {
-    if (s.walk == kTeams) return normForwardTeams<DT, VEC>;
-    return s.per == 16 ? normForward<DT, VEC, 16> : normForward<DT, VEC, 32>;
-  } else {
-    return s.walk == kTeams ? normBackwardTeams<DT, VEC> : normBackward<DT, VEC, 16>;
-  }
+template <int DT, bool VEC, bool FWD, int I = 0>
+NormFn pickTeams(int threads) {
+  constexpr int T = kTeamSizes[I];
+  if constexpr (T < 1024)
+    if (threads > T) return pickTeams<DT, VEC, FWD, I + 1>(threads);
+  if constexpr (FWD && T <= 512)
+    return normForwardTeams<DT, VEC, T>;
+  else if constexpr (FWD)
+    return normForwardWide<DT, VEC, T>;
+  else if constexpr (T <= 512)
+    return normBackwardTeams<DT, VEC, T>;
+  else
+    return normBackwardWide<DT, VEC, T>;
 }
 template <int DT, bool FWD>
 NormFn pickKernel(const Shape& s) {
@@ -807,7 +1021,10 @@ NormFn pickKernel(const Shape& s) {
     if constexpr (FWD) return normForwardLong<DT>;
     else return normBackwardLong<DT>;
   }
-  return s.vec ? pickWalk<DT, true, FWD>(s) : pickWalk<DT, false, FWD>(s);
+  if constexpr (FWD)
+    if (s.walk == kBlockRow) return s.vec ? normForward<DT, true, 32> : normForward<DT, false, 32>;
+  const int threads = s.walk == kTeams ? s.teamThreads : s.threads;
+  return s.vec ? pickTeams<DT, true, FWD>(threads) : pickTeams<DT, false, FWD>(threads);
 }
 template <bool FWD>
 vrcclResult_t launchNorm(int dt, const Shape& s, unsigned blocks, NormArgs& a, cudaStream_t st) {
@@ -821,7 +1038,6 @@ vrcclResult_t launchNorm(int dt, const Shape& s, unsigned blocks, NormArgs& a, c
   }
   a.stages = s.stages;
   a.teams = s.teams;
-  a.teamThreads = s.teamThreads;
   fn<<<blocks, s.threads, s.smem, st>>>(a);
   return launchResult();
 }

@@ -160,6 +160,13 @@ def test_norm_without_parameters(torch, v):
     _norm_check(torch, v, 19, 520, "bfloat16", "float32", affine=False)
 
 
+@pytest.mark.parametrize("dtype", FLOATS)
+@pytest.mark.parametrize("rows,cols,pad", [(400, 8200, 0), (333, 11440, 3), (310, 14336, 0), (170, 16384, 8), (457, 9001, 1)])
+def test_norm_wide_rows_several_turns(torch, v, rows, cols, pad, dtype):
+    """A block a row, more rows than multiprocessors, one shared-memory stage and several."""
+    _norm_check(torch, v, rows, cols, dtype, "float32", pad)
+
+
 def test_norm_many_rows(torch, v):
     """More rows than blocks, several turns each."""
     _norm_check(torch, v, 5003, 264, "float16", "float32")
