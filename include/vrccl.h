@@ -530,8 +530,9 @@ vrcclResult_t vrcclAllReduceNoAlloc(const void* const* sendbufs, void* const* re
  * `workspace`) and may be captured in a CUDA graph.
  *
  * Matrices are row-major with a row stride in elements (ldx, ...), which may
- * exceed the row's length; only the elements of the rows are read or
- * written. Pointers must be aligned to their element's size; rows that all
+ * exceed the row's length; only the elements of the rows are written, and
+ * beside them nothing is read but what shares a 16-byte block with a row
+ * between the matrix's first element and its last (it is ignored). Pointers must be aligned to their element's size; rows that all
  * start on 16-byte boundaries are faster. The operators take vrcclFloat32,
  * vrcclBfloat16 and vrcclFloat16 (the linear layer only the latter two).
  * Sums and statistics are held in binary32 and each result is rounded once
