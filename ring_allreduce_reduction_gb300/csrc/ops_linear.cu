@@ -303,7 +303,7 @@ __device__ __forceinline__ uint64_t operandDesc(uint32_t addr, bool mn, int dept
 constexpr int kBM = 128;  // rows of A a block
 constexpr int kEpilogueWarps = 8;
 constexpr int kProductThreads = 32 * (2 + kEpilogueWarps);  // TMA warp, MMA warp, epilogue warps
-constexpr int kStoreBytes = 32 * 64 * 2;                    // one warp's 32 rows x 64 columns on the way out
+constexpr int kStoreBytes = 32 * 32 * 2;                    // one warp's 32 rows x 32 columns on the way out
 
 struct Problem {
   CUtensorMap a, b, dMap, zMap;
@@ -374,15 +374,18 @@ struct ProductShape {
   // 128 x 128 tiles 107 us against 147), but as much again under a narrow one's.
   static constexpr int kBK = BN <= 64 ? 128 : 64;
   static constexpr int kStageBytes = (kBM + kBRows) * kBK * 2;
-  static constexpr int kStages = BN == 64 ? 3 : 5;
+  static constexpr int kStages = BN == 64 ? 3 : 6;
   static constexpr int kSmem = kStages * kStageBytes + kEpilogueWarps * 2 * kStoreBytes + 1024;
   static constexpr int kTmemCols = 2 * BN;
   static constexpr int kGroup = CG == 2 ? 8 : 12;  // tiles of a column (Walk::place): about the root of the tiles at work
 };
 
-// Writes one warp's finished 32 x 64 elements from its staging buffer (rows of
-// 128 bytes, 16-byte pieces swizzled by the row) to memory.
-template <int DT>
+// A warp's staging buffer: 32 rows of 64 bytes, their 16-byte pieces swizzled
+// as a TMA map of 64-byte swizzle has them, so that lanes that each write or
+// read a piece of their own row meet different banks.
+__device__ __forceinline__ int pieceAt(int row, int piece) { return row * 64 + ((piece ^ (row >> 1 & 3)) << 4); }
+
+// Writes one warp's finished 32 x 32 elements from its staging buffer to memory.
 __device__ __forceinline__ void storeBox(const Problem& a, const CUtensorMap* map, void* out, size_t ld, bool wide,
                                          const unsigned char* buf, int m, int n, int lane) {
   if (wide) {
@@ -394,27 +397,22 @@ __device__ __forceinline__ void storeBox(const Problem& a, const CUtensorMap* ma
     }
   } else {
     __syncwarp();
-    unsigned short* o = static_cast<unsigned short*>(out) + (size_t)m * ld + n;
-    const int rows = min(32, a.M - m), c = 2 * lane;
-    const bool lo = n + c < a.N, hi = n + c + 1 < a.N;
+    unsigned short* o = static_cast<unsigned short*>(out) + (size_t)m * ld + n + lane;
+    const int rows = n + lane < a.N ? min(32, a.M - m) : 0;
 #pragma unroll 8
-    for (int r = 0; r < rows; ++r) {
-      const uint32_t w =
-          *reinterpret_cast<const uint32_t*>(buf + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + ((lane & 3) << 2));
-      if (lo) o[(size_t)r * ld + c] = (unsigned short)(w & 0xffffu);
-      if (hi) o[(size_t)r * ld + c + 1] = (unsigned short)(w >> 16);
-    }
+    for (int r = 0; r < rows; ++r)
+      o[(size_t)r * ld] = *reinterpret_cast<const unsigned short*>(buf + pieceAt(r, lane >> 3) + ((lane & 7) << 1));
     __syncwarp();
   }
 }
 template <int DT>
-__device__ __forceinline__ void stage32(unsigned char* buf, int half, int lane, const float (&f)[32]) {
+__device__ __forceinline__ void stage32(unsigned char* buf, int lane, const float (&f)[32]) {
 #pragma unroll
   for (int v = 0; v < 4; ++v) {
     float g[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) g[e] = f[v * 8 + e];
-    *reinterpret_cast<uint4*>(buf + lane * 128 + (((half * 4 + v) ^ (lane & 7)) << 4)) = Vec16<DT>::pack(g);
+    *reinterpret_cast<uint4*>(buf + pieceAt(lane, v)) = Vec16<DT>::pack(g);
   }
 }
 
@@ -427,53 +425,55 @@ __device__ __forceinline__ void activate32(float (&f)[32]) {
     f[i + 1] = y.y;
   }
 }
-// One warp's 32 x 64 elements of the residual, rows m.. and columns n..: read
+// One warp's 32 x 32 elements of the residual, rows m.. and columns n..: read
 // along the rows, asked for before the tile's products are waited for, and
 // handed to the lanes that own the rows through the staging buffer.
 template <int DT>
 struct Residual {
-  uint32_t w[32];
+  uint32_t w[16];
+  static __device__ __forceinline__ bool pieces(const Problem& a, int n) { return a.wideR && a.N - n >= 32; }
   __device__ __forceinline__ void load(const Problem& a, int m, int n, int lane) {
     const unsigned short* r = static_cast<const unsigned short*>(a.residual) + (size_t)m * a.ldr + n;
-    const int rows = min(32, a.M - m), cols = min(64, a.N - n);
-    if (a.wideR && cols == 64) {  // a piece of 16 bytes a lane, four rows at a time
+    const int rows = min(32, a.M - m);
+    if (pieces(a, n)) {  // a piece of 16 bytes a lane, eight rows at a time
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int row = i * 4 + (lane >> 3);
-        const uint4 v = row < rows ? __ldg(reinterpret_cast<const uint4*>(r + (size_t)row * a.ldr) + (lane & 7)) : make_uint4(0, 0, 0, 0);
+      for (int i = 0; i < 4; ++i) {
+        const int row = i * 8 + (lane >> 2);
+        const uint4 v = row < rows ? __ldg(reinterpret_cast<const uint4*>(r + (size_t)row * a.ldr) + (lane & 3)) : make_uint4(0, 0, 0, 0);
         w[4 * i] = v.x;
         w[4 * i + 1] = v.y;
         w[4 * i + 2] = v.z;
         w[4 * i + 3] = v.w;
       }
-    } else {  // a pair of columns a lane, a row at a time
+    } else {  // a column a lane, two rows at a time
+      const bool exists = n + lane < a.N;
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const unsigned short* p = r + (size_t)i * a.ldr + 2 * lane;
-        const uint32_t lo = i < rows && 2 * lane < cols ? p[0] : 0u, hi = i < rows && 2 * lane + 1 < cols ? p[1] : 0u;
+      for (int i = 0; i < 16; ++i) {
+        const unsigned short* p = r + (size_t)(2 * i) * a.ldr + lane;
+        const uint32_t lo = exists && 2 * i < rows ? p[0] : 0u, hi = exists && 2 * i + 1 < rows ? p[a.ldr] : 0u;
         w[i] = lo | hi << 16;
       }
     }
   }
   __device__ __forceinline__ void put(const Problem& a, int n, unsigned char* buf, int lane) const {
-    if (a.wideR && a.N - n >= 64) {
+    if (pieces(a, n)) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int row = i * 4 + (lane >> 3);
-        *reinterpret_cast<uint4*>(buf + row * 128 + (((lane & 7) ^ (row & 7)) << 4)) =
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<uint4*>(buf + pieceAt(i * 8 + (lane >> 2), lane & 3)) =
             make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-      }
     } else {
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
-        *reinterpret_cast<uint32_t*>(buf + i * 128 + (((lane >> 2) ^ (i & 7)) << 4) + ((lane & 3) << 2)) = w[i];
+      for (int i = 0; i < 16; ++i) {
+        *reinterpret_cast<unsigned short*>(buf + pieceAt(2 * i, lane >> 3) + ((lane & 7) << 1)) = (unsigned short)(w[i] & 0xffffu);
+        *reinterpret_cast<unsigned short*>(buf + pieceAt(2 * i + 1, lane >> 3) + ((lane & 7) << 1)) = (unsigned short)(w[i] >> 16);
+      }
     }
   }
-  static __device__ __forceinline__ void add(const unsigned char* buf, int half, int lane, float (&f)[32]) {
+  static __device__ __forceinline__ void add(const unsigned char* buf, int lane, float (&f)[32]) {
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
       float g[8];
-      Vec16<DT>::expand(*reinterpret_cast<const uint4*>(buf + lane * 128 + (((half * 4 + v) ^ (lane & 7)) << 4)), g);
+      Vec16<DT>::expand(*reinterpret_cast<const uint4*>(buf + pieceAt(lane, v)), g);
 #pragma unroll
       for (int e = 0; e < 8; ++e) f[v * 8 + e] += g[e];
     }
@@ -564,7 +564,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) productKernel(const __grid
   unsigned char* smem = dyn + ((1024 - (smemAddr(dyn) & 1023)) & 1023);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t rank = CG == 2 ? clusterRank() : 0;
-  constexpr int kWorkers = BN >= 128 ? kEpilogueWarps : 4;  // warps that have 64 columns to finish
+  constexpr int kWorkers = kEpilogueWarps;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -660,7 +660,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) productKernel(const __grid
   } else if (warp - 2 < kWorkers) {
     const int quarter = warp & 3;  // the TMEM lanes this warp may read
     const int part = (warp - 2) >> 2;
-    constexpr int kCols = BN / (kWorkers / 4);  // columns a warp finishes, 64 at a time
+    constexpr int kCols = BN / (kWorkers / 4);  // columns a warp finishes, 32 at a time
     unsigned char* buf = smem + kStages * Sh::kStageBytes + (warp - 2) * 2 * kStoreBytes;
     int turn = 0, which = 0;
     for (Walk w(args, unit, gridDim.x / CG); w.more(); w.next(args, unit), ++turn) {
@@ -670,10 +670,10 @@ __global__ void __launch_bounds__(kProductThreads, 1) productKernel(const __grid
       m0 = m0 * (CG * kBM) + (int)rank * kBM + quarter * 32;
       n0 = n0 * BN + part * kCols;
       const int acc = turn & 1, use = turn >> 1;
-      uint32_t bias[kCols / 64];
+      uint32_t bias[(kCols + 63) / 64];
       if (a.bias)
 #pragma unroll
-        for (int i = 0; i < kCols / 64; ++i) bias[i] = biasPair<DT>(a, n0 + i * 64, lane);
+        for (int i = 0; i < (kCols + 63) / 64; ++i) bias[i] = biasPair<DT>(a, n0 + i * 64, lane);
       Residual<DT> residual;
       if (a.residual && m0 < a.M && n0 < a.N) residual.load(a, m0, n0, lane);
       bool ok = lane != 0 || waitBar(&accFull[acc], use & 1, dead);
@@ -682,8 +682,9 @@ __global__ void __launch_bounds__(kProductThreads, 1) productKernel(const __grid
       const uint32_t from = tmem + ((uint32_t)(quarter * 32) << 16) + acc * BN + part * kCols;
       if (m0 < a.M) {
 #pragma unroll
-        for (int c = 0; c < kCols; c += 64) {
-          if (n0 + c >= a.N) break;
+        for (int c = 0; c < kCols; c += 32) {
+          const int n = n0 + c;
+          if (n >= a.N) break;
           // the buffers take turns; the store that last read one has to be done with it
           unsigned char* zb = buf + which * kStoreBytes;
           if (a.z) which ^= 1;
@@ -697,28 +698,27 @@ __global__ void __launch_bounds__(kProductThreads, 1) productKernel(const __grid
           }
           __syncwarp();
           if (a.residual) {
-            residual.put(a, n0 + c, yb, lane);
+            residual.put(a, n, yb, lane);
             __syncwarp();
-            if (c + 64 < kCols && n0 + c + 64 < a.N) residual.load(a, m0, n0 + c + 64, lane);
+            if (c + 32 < kCols && n + 32 < a.N) residual.load(a, m0, n + 32, lane);
           }
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float f[32];
-            tcLoad32(from + c + h * 32, f);
-            if (a.bias) addBias<DT>(f, bias[c / 64], h);
-            if (a.z) stage32<DT>(zb, h, lane, f);
-            switch (a.act) {
-              case vrcclActRelu: activate32<vrcclActRelu>(f); break;
-              case vrcclActGelu: activate32<vrcclActGelu>(f); break;
-              case vrcclActGeluTanh: activate32<vrcclActGeluTanh>(f); break;
-              case vrcclActSilu: activate32<vrcclActSilu>(f); break;
-              default: activate32<vrcclActNone>(f); break;
-            }
-            if (a.residual) Residual<DT>::add(yb, h, lane, f);
-            stage32<DT>(yb, h, lane, f);
+          float f[32];
+          tcLoad32(from + c, f);
+          if (a.bias) addBias<DT>(f, bias[c / 64], c / 32 & 1);
+          if (a.z) {
+            stage32<DT>(zb, lane, f);
+            storeBox(a, &a.zMap, a.z, a.ldz, a.wideZ, zb, m0, n, lane);
           }
-          if (a.z) storeBox<DT>(a, &a.zMap, a.z, a.ldz, a.wideZ, zb, m0, n0 + c, lane);
-          storeBox<DT>(a, &a.dMap, a.d, a.ldd, a.wideD, yb, m0, n0 + c, lane);
+          switch (a.act) {
+            case vrcclActRelu: activate32<vrcclActRelu>(f); break;
+            case vrcclActGelu: activate32<vrcclActGelu>(f); break;
+            case vrcclActGeluTanh: activate32<vrcclActGeluTanh>(f); break;
+            case vrcclActSilu: activate32<vrcclActSilu>(f); break;
+            default: break;
+          }
+          if (a.residual) Residual<DT>::add(yb, lane, f);
+          stage32<DT>(yb, lane, f);
+          storeBox(a, &a.dMap, a.d, a.ldd, a.wideD, yb, m0, n, lane);
         }
       }
       tcFenceBefore();
@@ -1168,15 +1168,18 @@ EncodeFn encodeFn() {
   return fn;
 }
 
-// Tiles of 64 x boxRows out of a [rows, cols] matrix of 2-byte elements whose
-// rows start on 16-byte boundaries; what lies outside reads as zero.
-bool makeMap(CUtensorMap* map, int dtype, const void* p, size_t ld, size_t rows, size_t cols, int boxRows) {
+// Tiles of boxCols (64: operands, 32: results) x boxRows out of a [rows, cols]
+// matrix of 2-byte elements whose rows start on 16-byte boundaries, swizzled
+// over their rows' bytes; what lies outside reads as zero.
+bool makeMap(CUtensorMap* map, int dtype, const void* p, size_t ld, size_t rows, size_t cols, int boxRows,
+             int boxCols = 64) {
   const EncodeFn fn = encodeFn();
   if (!fn) return false;
   const cuuint64_t dims[2] = {cols, rows}, strides[1] = {ld * 2};
-  const cuuint32_t box[2] = {64, (cuuint32_t)boxRows}, step[2] = {1, 1};
+  const cuuint32_t box[2] = {(cuuint32_t)boxCols, (cuuint32_t)boxRows}, step[2] = {1, 1};
   return fn(map, dtype == vrcclBfloat16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
-            const_cast<void*>(p), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            const_cast<void*>(p), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            boxCols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1286,8 +1289,8 @@ vrcclResult_t launchProducts(const Product* q, int n, bool after, cudaStream_t s
     total += p.tiles;
     if (!makeMap(&p.a, DT, A.p, A.ld, A.rows, A.cols, A.mn ? Sh::kBK : kBM) ||
         !makeMap(&p.b, DT, B.p, B.ld, B.rows, B.cols, B.mn ? Sh::kBK : Sh::kBRows) ||
-        (p.wideD && !makeMap(&p.dMap, DT, p.d, p.ldd, p.M, p.N, 32)) ||
-        (p.wideZ && !makeMap(&p.zMap, DT, p.z, p.ldz, p.M, p.N, 32)))
+        (p.wideD && !makeMap(&p.dMap, DT, p.d, p.ldd, p.M, p.N, 32, 32)) ||
+        (p.wideZ && !makeMap(&p.zMap, DT, p.z, p.ldz, p.M, p.N, 32, 32)))
       return vrcclInternalError;
   }
   const int units = (int)std::min<long long>(total, std::min(smCount() / CG, kMaxUnits));
