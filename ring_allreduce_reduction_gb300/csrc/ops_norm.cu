@@ -242,6 +242,28 @@ struct Team {
       for (int e = 0; e < V; ++e) f[j * V + e] = g[e];
     }
   }
+  // The thread's two sums of its columns to p[0 .. cols) and p[cols .. 2 cols).
+  static __device__ __forceinline__ void layOut(float* p, const F2 (&dg)[kTeamElems / 2], const F2 (&db)[kTeamElems / 2],
+                                                int cols, int t) {
+    if constexpr (VEC) {
+#pragma unroll
+      for (int q = 0; q < kTeamElems; q += 4) {
+        if (!held(q, cols, t)) continue;
+        float* at = p + (q / V * T + t) * V + q % V;
+        const float2 a = split(dg[q / 2]), b = split(dg[q / 2 + 1]), c = split(db[q / 2]), d = split(db[q / 2 + 1]);
+        *reinterpret_cast<float4*>(at) = make_float4(a.x, a.y, b.x, b.y);
+        *reinterpret_cast<float4*>(at + cols) = make_float4(c.x, c.y, d.x, d.y);
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < kTeamElems; ++q) {
+        if (!held(q, cols, t)) continue;
+        const float2 a = split(dg[q / 2]), c = split(db[q / 2]);
+        p[q * T + t] = q & 1 ? a.y : a.x;
+        p[cols + q * T + t] = q & 1 ? c.y : c.x;
+      }
+    }
+  }
   static __device__ __forceinline__ bool held(int q, int cols, int t) { return (q / V * T + t) * V < cols; }
 };
 
@@ -539,20 +561,182 @@ __global__ void __launch_bounds__(512) normBackwardTeams(const __grid_constant__
   // the teams own the same columns: every team lays its sums out, and the block adds them in the teams' order
   float* sum = reinterpret_cast<float*>(ring);
   __syncthreads();  // no team reads its ring any more
-#pragma unroll
-  for (int i = 0; i < kTeamElems; ++i) {
-    if (!M::held(i, cols, t)) continue;
-    float* q = sum + (size_t)team * 2 * cols + (i / M::V * T + t) * M::V + i % M::V;
-    const float2 u = split(dg[i / 2]), v = split(db[i / 2]);
-    q[0] = i & 1 ? u.y : u.x;
-    q[cols] = i & 1 ? v.y : v.x;
-  }
+  M::layOut(sum + (size_t)team * 2 * cols, dg, db, cols, t);
   __syncthreads();
   float* p = a.partial + (size_t)blockIdx.x * 2 * cols;
   for (int c = threadIdx.x; c < 2 * cols; c += blockDim.x) {
     float x = sum[c];
     for (int w = 1; w < a.teams; ++w) x += sum[(size_t)w * 2 * cols + c];
     p[c] = x;
+  }
+}
+
+// ------------------------------------------------------------ narrow rows
+// Rows of at most 32 whole vectors (heads, and their like): G lanes a row, one
+// vector each, 32 / G rows a warp at a time and kNarrowTurn such steps in
+// flight. Such rows reduce within a warp; there is nothing to wait for.
+constexpr int kNarrowTurn = 4, kNarrowThreads = 256;
+
+template <int G>
+__device__ __forceinline__ float sumLanes(float x) {
+#pragma unroll
+  for (int o = G / 2; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
+template <int DT, int G>
+__global__ void __launch_bounds__(kNarrowThreads) normForwardNarrow(const __grid_constant__ NormArgs a) {
+  constexpr int E = floatTypeSize(DT), V = 16 / E, R = 32 / G, U = kNarrowTurn;
+  const int lane = threadIdx.x & 31, own = lane % G;
+  const bool held = own * V < a.cols;
+  const size_t warps = (size_t)gridDim.x * (kNarrowThreads / 32);
+  const float inv = 1.f / (float)a.cols;
+  F2 g[V / 2], b[V / 2];
+  {
+    float p[V];
+    if (held) {
+      loadParams<V>(a.gamma, a.ptype, a.wideParams, own * V, 1.f, p);
+#pragma unroll
+      for (int e = 0; e < V / 2; ++e) g[e] = pair(p[2 * e], p[2 * e + 1]);
+      loadParams<V>(a.beta, a.ptype, a.wideParams, own * V, 0.f, p);
+#pragma unroll
+      for (int e = 0; e < V / 2; ++e) b[e] = pair(p[2 * e], p[2 * e + 1]);
+    }
+  }
+  for (size_t r0 = ((size_t)blockIdx.x * (kNarrowThreads / 32) + (threadIdx.x >> 5)) * R * U; r0 < a.rows; r0 += warps * R * U) {
+    uint4 raw[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const size_t row = r0 + u * R + lane / G;
+      raw[u] = held && row < a.rows ? __ldcs(reinterpret_cast<const uint4*>(static_cast<const char*>(a.x) + row * a.ldx * E) + own)
+                                    : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const size_t row = r0 + u * R + lane / G;
+      float f[V];
+      Vec16<DT>::expand(raw[u], f);
+      F2 x[V / 2], acc = 0;
+#pragma unroll
+      for (int e = 0; e < V / 2; ++e) {
+        x[e] = pair(f[2 * e], f[2 * e + 1]);
+        acc = add2(acc, x[e]);
+      }
+      float2 q = split(acc);
+      const float mean = sumLanes<G>(q.x + q.y) * inv;
+      const F2 shift = pair(-mean, -mean);
+      acc = 0;
+#pragma unroll
+      for (int e = 0; e < V / 2; ++e) {
+        x[e] = add2(x[e], shift);
+        acc = fma2(x[e], x[e], acc);
+      }
+      q = split(acc);
+      const float rstd = rsqrtf(sumLanes<G>(held ? q.x + q.y : 0.f) * inv + a.eps);
+      if (row >= a.rows) continue;
+      if (own == 0) {
+        if (a.mean) a.mean[row] = mean;
+        if (a.rstd) a.rstd[row] = rstd;
+      }
+      if (held) {
+        const F2 scale = pair(rstd, rstd);
+#pragma unroll
+        for (int e = 0; e < V / 2; ++e) {
+          const float2 y = split(fma2(mul2(x[e], scale), g[e], b[e]));
+          f[2 * e] = y.x;
+          f[2 * e + 1] = y.y;
+        }
+        __stcs(reinterpret_cast<uint4*>(static_cast<char*>(a.y) + row * a.ldy * E) + own, Vec16<DT>::pack(f));
+      }
+    }
+  }
+}
+
+template <int DT, int G>
+__global__ void __launch_bounds__(kNarrowThreads) normBackwardNarrow(const __grid_constant__ NormArgs a) {
+  constexpr int E = floatTypeSize(DT), V = 16 / E, R = 32 / G, U = kNarrowTurn;
+  __shared__ float sum[kNarrowThreads / 32][2][32 * V];
+  const int lane = threadIdx.x & 31, own = lane % G, w = threadIdx.x >> 5;
+  const bool held = own * V < a.cols;
+  const size_t warps = (size_t)gridDim.x * (kNarrowThreads / 32);
+  const float inv = 1.f / (float)a.cols;
+  F2 g[V / 2], dg[V / 2], db[V / 2];
+  {
+    float p[V] = {};
+    if (held) loadParams<V>(a.gamma, a.ptype, a.wideParams, own * V, 1.f, p);
+#pragma unroll
+    for (int e = 0; e < V / 2; ++e) {
+      g[e] = pair(p[2 * e], p[2 * e + 1]);
+      dg[e] = db[e] = 0;
+    }
+  }
+  letNextIn();
+  for (size_t r0 = ((size_t)blockIdx.x * (kNarrowThreads / 32) + w) * R * U; r0 < a.rows; r0 += warps * R * U) {
+    uint4 rx[U], rd[U];
+    float mean[U], rstd[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const size_t row = r0 + u * R + lane / G;
+      const bool there = held && row < a.rows;
+      rx[u] = there ? __ldcs(reinterpret_cast<const uint4*>(static_cast<const char*>(a.x) + row * a.ldx * E) + own) : make_uint4(0, 0, 0, 0);
+      rd[u] = there ? __ldcs(reinterpret_cast<const uint4*>(static_cast<const char*>(a.dy) + row * a.lddy * E) + own) : make_uint4(0, 0, 0, 0);
+      mean[u] = row < a.rows ? a.mean[row] : 0.f;
+      rstd[u] = row < a.rows ? a.rstd[row] : 0.f;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const size_t row = r0 + u * R + lane / G;
+      float fx[V], fd[V];
+      Vec16<DT>::expand(rx[u], fx);
+      Vec16<DT>::expand(rd[u], fd);  // zero where nothing is held: such lanes add nothing to any sum
+      const F2 shift = pair(-mean[u], -mean[u]), scale = pair(rstd[u], rstd[u]);
+      F2 xh[V / 2], gd[V / 2], sg = 0, sx = 0;
+#pragma unroll
+      for (int e = 0; e < V / 2; ++e) {
+        const F2 d = pair(fd[2 * e], fd[2 * e + 1]);
+        xh[e] = mul2(add2(pair(fx[2 * e], fx[2 * e + 1]), shift), scale);
+        gd[e] = mul2(d, g[e]);
+        sg = add2(sg, gd[e]);
+        sx = fma2(gd[e], xh[e], sx);
+        dg[e] = fma2(d, xh[e], dg[e]);
+        db[e] = add2(db[e], d);
+      }
+      const float2 q = split(sg), r = split(sx);
+      const float m1 = sumLanes<G>(q.x + q.y) * inv, m2 = sumLanes<G>(r.x + r.y) * inv;
+      if (held && row < a.rows) {
+        const F2 n1 = pair(-m1, -m1), n2 = pair(-m2, -m2);
+#pragma unroll
+        for (int e = 0; e < V / 2; ++e) {
+          const float2 v = split(mul2(scale, fma2(xh[e], n2, add2(gd[e], n1))));
+          fx[2 * e] = v.x;
+          fx[2 * e + 1] = v.y;
+        }
+        __stcs(reinterpret_cast<uint4*>(static_cast<char*>(a.y) + row * a.ldy * E) + own, Vec16<DT>::pack(fx));
+      }
+    }
+  }
+  if (!a.partial) return;
+  // the warp's row groups hold the same columns, then the block's warps do
+#pragma unroll
+  for (int e = 0; e < V / 2; ++e) {
+#pragma unroll
+    for (int o = G; o < 32; o *= 2) {
+      dg[e] = add2(dg[e], __shfl_xor_sync(0xffffffffu, dg[e], o));
+      db[e] = add2(db[e], __shfl_xor_sync(0xffffffffu, db[e], o));
+    }
+    if (lane < G) {
+      *reinterpret_cast<F2*>(&sum[w][0][own * V + 2 * e]) = dg[e];
+      *reinterpret_cast<F2*>(&sum[w][1][own * V + 2 * e]) = db[e];
+    }
+  }
+  __syncthreads();
+  float* p = a.partial + (size_t)blockIdx.x * 2 * a.cols;
+  for (int i = threadIdx.x; i < 2 * a.cols; i += kNarrowThreads) {
+    const int which = i >= a.cols, c = i - which * a.cols;
+    float x = sum[0][which][c];
+#pragma unroll
+    for (int k = 1; k < kNarrowThreads / 32; ++k) x += sum[k][which][c];
+    p[i] = x;
   }
 }
 
@@ -789,15 +973,7 @@ __global__ void __launch_bounds__(T, 1) normBackwardWide(const __grid_constant__
     }
   }
   if (!a.partial) return;
-  float* p = a.partial + (size_t)blockIdx.x * 2 * cols;
-#pragma unroll
-  for (int i = 0; i < kTeamElems; ++i) {
-    if (!M::held(i, cols, t)) continue;
-    const int c = (i / M::V * T + t) * M::V + i % M::V;
-    const float2 u = split(dg[i / 2]), v = split(db[i / 2]);
-    p[c] = i & 1 ? u.y : u.x;
-    p[cols + c] = i & 1 ? v.y : v.x;
-  }
+  M::layOut(a.partial + (size_t)blockIdx.x * 2 * cols, dg, db, cols, t);
 }
 
 // ------------------------------------------------------------ longer rows
@@ -941,7 +1117,7 @@ __global__ void __launch_bounds__(1024) normJoin(const float* partial, int block
 
 // ------------------------------------------------------------ host
 
-enum Walk { kTeams, kWide, kBlockRow, kLongRow };
+enum Walk { kNarrow, kTeams, kWide, kBlockRow, kLongRow };
 struct Shape {
   Walk walk;
   bool vec;
@@ -961,7 +1137,15 @@ Shape normShape(size_t rows, int cols, int elem, bool aligned, bool forward) {
   s.vec = aligned && cols % (16 / elem) == 0;
   s.teams = 1;
   auto up = [](int n, int per) { return std::max(32, (n + per * 32 - 1) / (per * 32) * 32); };
-  if (cols <= kTeamCols) {
+  if (s.vec && cols <= 32 * (16 / elem)) {
+    s.walk = kNarrow;
+    s.threads = kNarrowThreads;
+    int lanes = 4;
+    while (lanes * (16 / elem) < cols) lanes *= 2;
+    s.teamThreads = lanes;
+    s.teams = kNarrowThreads / lanes * kNarrowTurn;  // rows a block takes at a time
+    s.resident = 4;
+  } else if (cols <= kTeamCols) {
     // one block of up to 512 threads a multiprocessor: 128 registers each. With few rows, fewer teams to a block.
     s.walk = kTeams;
     s.teamThreads = teamThreads(cols);
@@ -1015,6 +1199,15 @@ NormFn pickTeams(int threads) {
   else
     return normBackwardWide<DT, VEC, T>;
 }
+template <int DT, bool FWD, int G = 4>
+NormFn pickNarrow(int lanes) {
+  if constexpr (G < 32)
+    if (lanes > G) return pickNarrow<DT, FWD, 2 * G>(lanes);
+  if constexpr (FWD)
+    return normForwardNarrow<DT, G>;
+  else
+    return normBackwardNarrow<DT, G>;
+}
 template <int DT, bool FWD>
 NormFn pickKernel(const Shape& s) {
   if (s.walk == kLongRow) {
@@ -1023,6 +1216,7 @@ NormFn pickKernel(const Shape& s) {
   }
   if constexpr (FWD)
     if (s.walk == kBlockRow) return s.vec ? normForward<DT, true, 32> : normForward<DT, false, 32>;
+  if (s.walk == kNarrow) return pickNarrow<DT, FWD>(s.teamThreads);
   const int threads = s.walk == kTeams ? s.teamThreads : s.threads;
   return s.vec ? pickTeams<DT, true, FWD>(threads) : pickTeams<DT, false, FWD>(threads);
 }

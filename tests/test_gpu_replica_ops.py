@@ -167,6 +167,14 @@ def test_norm_wide_rows_several_turns(torch, v, rows, cols, pad, dtype):
     _norm_check(torch, v, rows, cols, dtype, "float32", pad)
 
 
+@pytest.mark.parametrize("dtype", FLOATS)
+@pytest.mark.parametrize("rows,cols,pad,ypad", [(1, 16, 0, 0), (3, 32, 8, 0), (1001, 64, 0, 8), (130, 128, 0, 0), (20003, 40, 0, 0),
+                                               (9999, 200, 8, 16), (40001, 8, 0, 0)])
+def test_norm_narrow_rows(torch, v, rows, cols, pad, ypad, dtype):
+    """Several rows a warp, with lanes that hold nothing, and more rows than the grid takes at once."""
+    _norm_check(torch, v, rows, cols, dtype, "float32", pad, 0, ypad, 0)
+
+
 def test_norm_many_rows(torch, v):
     """More rows than blocks, several turns each."""
     _norm_check(torch, v, 5003, 264, "float16", "float32")
