@@ -657,6 +657,61 @@ def test_distill_no_entries(torch, v):
     v.vrcclDistillForward(None, None, None, None, None, 0, 50, 4, "bfloat16", "float32", "int32")
 
 
+# ------------------------------------------------------------ far apart
+
+@pytest.mark.parametrize("gap", [0, 3])
+def test_offsets_beyond_32_bits(torch, v, gap):
+    """Rows so far apart that the last one's offset exceeds 2^32 elements."""
+    rows, ld = 2100, (1 << 21) + gap
+    buf = torch.empty(rows * ld, device="cuda", dtype=torch.bfloat16)
+    far = lambda cols: buf.view(rows, ld)[:, :cols]  # noqa: E731
+    g, u = _rng(41), U["bfloat16"]
+    a = torch.as_tensor(g.standard_normal((rows, 264))).cuda().bfloat16()
+    x = far(264).copy_(a)
+    # layer norm, in place, forward and backward, against the same rows side by side
+    near, back = torch.empty_like(a), torch.empty_like(a)
+    mean, rstd, dg, db, dg2, db2 = (torch.empty(n, device="cuda") for n in (rows, rows, 264, 264, 264, 264))
+    v.vrcclLayerNormForward(a, None, None, near, mean, rstd, rows, 264, "bfloat16", "float32")
+    ws = torch.empty(v.vrcclLayerNormWorkspace(rows, 264), device="cuda", dtype=torch.uint8)
+    v.vrcclLayerNormBackward(a, a, None, mean, rstd, back, dg, db, rows, 264, "bfloat16", "float32", ws, ws.numel())
+    v.vrcclLayerNormBackward(x, a, None, mean, rstd, x, dg2, db2, rows, 264, "bfloat16", "float32", ws, ws.numel(),
+                             lddy=ld, lddx=ld)
+    _close(_host(x), _host(back), 2 * u * np.abs(_host(back)) + 64 * EPS, "dx")
+    _close(_host(dg2), _host(dg), rows * EPS * np.abs(_host(a) ** 2).sum(0), "dgamma")
+    x.copy_(a)
+    v.vrcclLayerNormForward(x, None, None, x, None, None, rows, 264, "bfloat16", "float32", ldx=ld, ldy=ld)
+    _close(_host(x), _host(near), 2 * u * np.abs(_host(near)) + 64 * EPS, "y")
+    # linear layer
+    w = torch.as_tensor(g.standard_normal((72, 264)) / 16).cuda().bfloat16()
+    x.copy_(a)
+    y, y2 = torch.empty(rows, 72, device="cuda", dtype=torch.bfloat16), torch.empty(rows, 72, device="cuda", dtype=torch.bfloat16)
+    ws = _scratch(torch, v, "backward", rows, 72, 264, "bfloat16", "none")
+    v.vrcclLinearForward(a, w, None, None, y, None, rows, 72, 264, "bfloat16")
+    v.vrcclLinearForward(x, w, None, None, y2, None, rows, 72, 264, "bfloat16", "none", ws, ws.numel(), ldx=ld)
+    assert torch.equal(y, y2)
+    dw, dw2 = torch.empty_like(w), torch.empty_like(w)
+    v.vrcclLinearBackward(y, None, a, None, None, dw, None, rows, 72, 264, "bfloat16", "none", ws, ws.numel())
+    v.vrcclLinearBackward(y, None, x, None, None, dw2, None, rows, 72, 264, "bfloat16", "none", ws, ws.numel(), ldx=ld)
+    assert torch.equal(dw, dw2)
+    v.vrcclLinearBackward(y, None, None, w, back, None, None, rows, 72, 264, "bfloat16", "none", ws, ws.numel())
+    v.vrcclLinearBackward(y, None, None, w, x, None, None, rows, 72, 264, "bfloat16", "none", ws, ws.numel(), lddx=ld)
+    assert torch.equal(back, x)
+    # distillation
+    x.copy_(a)
+    t = torch.as_tensor(g.standard_normal((rows, 5))).float().cuda()
+    idx = torch.as_tensor(g.integers(0, 264, (rows, 5))).cuda()
+    one = torch.ones(1, device="cuda")
+    out = []
+    for s, stride in ((a.clone(), 264), (x, ld)):
+        loss, stats = torch.empty(rows, device="cuda"), torch.empty(rows, 2, device="cuda")
+        v.vrcclDistillForward(s, t, idx, loss, stats, rows, 264, 5, "bfloat16", "float32", "int64", ldl=stride)
+        v.vrcclDistillBackward(s, t, idx, stats, one, s, rows, 264, 5, "bfloat16", "float32", "int64", dloss_stride=0,
+                               ldl=stride, ldd=stride)
+        out.append((_host(loss), _host(s)))
+    _close(out[1][0], out[0][0], 1e-5 * np.abs(out[0][0]) + 1e-6, "loss")
+    _close(out[1][1], out[0][1], 2 * u * np.abs(out[0][1]) + 1e-6, "dlogits")
+
+
 # ------------------------------------------------------------ streams, graphs, repeats
 
 def _everything(torch, v, stream=None):
