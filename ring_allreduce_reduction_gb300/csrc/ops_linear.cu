@@ -937,7 +937,9 @@ __global__ void __launch_bounds__(kProductThreads, 1) productSplit(const __grid_
 // One or two rows: 4096 x 4096 in 7.6 us where the split product takes 10.4. Up to eight where W would first have to be
 // copied for TMA, which alone reads and writes it once more.
 constexpr int kFewRows = 2, kFewRowsUnaligned = 8;
-constexpr int kFewOuts = 4;  // outputs a block: x is read once for four rows of W
+// Outputs a block, as many rows of W a thread has in flight: eight for one row of x (4096 x 4096 in 6.2 us against 8.2 with
+// four), four for more (8.2 us against 8.4 with eight, whose sums crowd the registers).
+constexpr int fewOuts(int rows) { return rows == 1 ? 8 : 4; }
 constexpr int kFewThreads = 256;
 
 struct FewArgs {
@@ -969,25 +971,25 @@ __device__ __forceinline__ float laneSums(float (&v)[N], int lane) {
   return v[0];
 }
 
-// MR rows of x against four rows of W a block, the contraction dealt to the
+// MR rows of x against a few rows of W a block, the contraction dealt to the
 // threads in 16-byte vectors (WIDE) or single elements, joined at the end.
 template <int DT, int MR, bool WIDE>
 __global__ void __launch_bounds__(kFewThreads) linearFew(const __grid_constant__ FewArgs a) {
   using S = typename Ty<DT>::S;
-  constexpr int V = WIDE ? 8 : 1;
-  __shared__ float part[kFewThreads / 32][kFewOuts * MR];
+  constexpr int V = WIDE ? 8 : 1, kOuts = fewOuts(MR);
+  __shared__ float part[kFewThreads / 32][kOuts * MR];
   const S* x = static_cast<const S*>(a.x);
   const S* w = static_cast<const S*>(a.w);
-  const int n0 = blockIdx.x * kFewOuts;
-  float acc[kFewOuts][MR] = {};
+  const int n0 = blockIdx.x * kOuts;
+  float acc[kOuts][MR] = {};
   const int nvec = a.ins / V;
   for (int i = threadIdx.x; i < nvec; i += kFewThreads) {
-    float wf[kFewOuts][V];
+    float wf[kOuts][V];
 #pragma unroll
-    for (int o = 0; o < kFewOuts; ++o) {
+    for (int o = 0; o < kOuts; ++o) {
       const S* row = w + (size_t)min(n0 + o, a.outs - 1) * a.ldw + (size_t)i * V;
       if constexpr (WIDE)
-        Vec16<DT>::expand(__ldcs(reinterpret_cast<const uint4*>(row)), wf[o]);
+        Vec16<DT>::expand(__ldg(reinterpret_cast<const uint4*>(row)), wf[o]);
       else
         wf[o][0] = Ty<DT>::toF(*row);
     }
@@ -1000,16 +1002,16 @@ __global__ void __launch_bounds__(kFewThreads) linearFew(const __grid_constant__
       else
         xf[0] = Ty<DT>::toF(*row);
 #pragma unroll
-      for (int o = 0; o < kFewOuts; ++o)
+      for (int o = 0; o < kOuts; ++o)
 #pragma unroll
         for (int e = 0; e < V; ++e) acc[o][m] += wf[o][e] * xf[e];
     }
   }
-  const float s = laneSums(reinterpret_cast<float(&)[kFewOuts * MR]>(acc), threadIdx.x & 31);
-  constexpr int kLanes = 32 / (kFewOuts * MR);  // lanes that hold the same sum
+  const float s = laneSums(reinterpret_cast<float(&)[kOuts * MR]>(acc), threadIdx.x & 31);
+  constexpr int kLanes = 32 / (kOuts * MR);  // lanes that hold the same sum
   if (threadIdx.x % kLanes == 0) part[threadIdx.x >> 5][(threadIdx.x & 31) / kLanes] = s;
   __syncthreads();
-  if (threadIdx.x < kFewOuts * MR) {
+  if (threadIdx.x < kOuts * MR) {
     const int n = n0 + threadIdx.x / MR, m = threadIdx.x % MR;
     if (n >= a.outs || m >= a.rows) return;
     float s = 0.f;
@@ -1434,7 +1436,7 @@ vrcclResult_t products(const Product* q, int n, bool after, cudaStream_t st) {
 
 template <int DT, int MR, bool WIDE>
 void launchFew(const FewArgs& a, cudaStream_t st) {
-  linearFew<DT, MR, WIDE><<<(unsigned)((a.outs + kFewOuts - 1) / kFewOuts), kFewThreads, 0, st>>>(a);
+  linearFew<DT, MR, WIDE><<<(unsigned)((a.outs + fewOuts(MR) - 1) / fewOuts(MR)), kFewThreads, 0, st>>>(a);
 }
 template <int DT>
 vrcclResult_t few(const FewArgs& a, bool wide, cudaStream_t st) {
