@@ -45,6 +45,8 @@ inline vrcclResult_t launchResult() {
 int normStatus(int* code);
 // Multiprocessors of the current device (asked for once a device).
 int smCount();
+// Lets a kernel's blocks ask for all the dynamic shared memory there is on the current device; once a kernel and device.
+vrcclResult_t allowSharedMemory(const void* fn);
 
 // A kernel that may be launched while the one before it on its stream still
 // runs (LaunchShape::after): waits for that one's results. And in the one before: the

@@ -1262,17 +1262,8 @@ long long tileCount(const Problem& p, int bm, int bn) {
 template <int DT, int CG, int BN>
 vrcclResult_t launchProducts(const Product* q, int n, bool after, cudaStream_t st) {
   using Sh = ProductShape<CG, BN>;
-  static bool raised[64] = {};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return vrcclCudaError;
-  if (!raised[dev]) {
-    if (cudaFuncSetAttribute(productKernel<DT, CG, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem) !=
-        cudaSuccess) {
-      cudaGetLastError();
-      return vrcclCudaError;
-    }
-    raised[dev] = true;
-  }
+  const vrcclResult_t allowed = allowSharedMemory((const void*)productKernel<DT, CG, BN>);
+  if (allowed != vrcclSuccess) return allowed;
   ProductArgs args;
   memset(&args, 0, sizeof(args));
   long long total = 0;
@@ -1328,17 +1319,8 @@ template <int DT, int BN, bool SWAP>
 vrcclResult_t launchSplit(const Product& q, int parts, bool after, cudaStream_t st) {
   using Sh = ProductShape<1, BN>;
   using Sp = SplitShape<BN, SWAP>;
-  static bool raised[64] = {};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return vrcclCudaError;
-  if (!raised[dev]) {
-    if (cudaFuncSetAttribute(productSplit<DT, BN, SWAP>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sp::kSmem) !=
-        cudaSuccess) {
-      cudaGetLastError();
-      return vrcclCudaError;
-    }
-    raised[dev] = true;
-  }
+  const vrcclResult_t allowed = allowSharedMemory((const void*)productSplit<DT, BN, SWAP>);
+  if (allowed != vrcclSuccess) return allowed;
   Problem p = q.p;
   const Operand &A = SWAP ? q.B : q.A, &B = SWAP ? q.A : q.B;
   if (SWAP) {

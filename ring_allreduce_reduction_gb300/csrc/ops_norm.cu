@@ -17,6 +17,10 @@
 // sums in registers; it writes them once, as one row of a [blocks, 2, cols]
 // workspace, and a second kernel adds those rows in order. No atomics: the
 // same call gives the same bits.
+#include <mutex>
+#include <utility>
+#include <vector>
+
 #include "ops_common.cuh"
 
 namespace vrccl {
@@ -1152,7 +1156,10 @@ Shape normShape(size_t rows, int cols, int elem, bool aligned, bool forward) {
     s.teams = (int)std::min<size_t>(512 / s.teamThreads, std::max<size_t>(1, (rows + smCount() - 1) / smCount()));
     s.threads = s.teams * s.teamThreads;
     const int row = slotBytes(cols, elem) * (forward ? 1 : 2);
+    // no more stages than a team has rows (and two: forward takes two rows at a time)
+    const size_t turns = (rows + (size_t)smCount() * s.teams - 1) / ((size_t)smCount() * s.teams);
     s.stages = std::min(kMaxStages, kTeamSmem / (s.teams * row)) & (forward ? ~1 : ~0);
+    s.stages = (int)std::min<size_t>(s.stages, std::max<size_t>(2, (turns + 1) & ~size_t(1)));
     s.smem = s.teams * s.stages * row;
     s.resident = 1;
   } else if (cols <= kWideCols) {
@@ -1225,10 +1232,9 @@ vrcclResult_t launchNorm(int dt, const Shape& s, unsigned blocks, NormArgs& a, c
   const NormFn fn = dt == vrcclFloat32    ? pickKernel<vrcclFloat32, FWD>(s)
                     : dt == vrcclBfloat16 ? pickKernel<vrcclBfloat16, FWD>(s)
                                           : pickKernel<vrcclFloat16, FWD>(s);
-  if (s.smem > 32 * 1024 &&  // (beside static shared memory, 48 KB come without asking)
-      cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, s.smem) != cudaSuccess) {
-    cudaGetLastError();
-    return vrcclCudaError;
+  if (s.smem > 32 * 1024) {  // (beside static shared memory, 48 KB come without asking)
+    const vrcclResult_t r = allowSharedMemory((const void*)fn);
+    if (r != vrcclSuccess) return r;
   }
   a.stages = s.stages;
   a.teams = s.teams;
@@ -1243,6 +1249,22 @@ bool goodSizes(size_t rows, size_t cols, int dtype, int ptype) {
 }  // namespace
 
 int normStatus(int* code) { return cudaMemcpyFromSymbol(code, gNormStatus, sizeof(*code)); }
+
+vrcclResult_t allowSharedMemory(const void* fn) {
+  static std::mutex mu;
+  static std::vector<std::pair<const void*, int>> done;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return vrcclCudaError;
+  std::lock_guard<std::mutex> lk(mu);
+  const auto key = std::make_pair(fn, dev);
+  if (std::find(done.begin(), done.end(), key) != done.end()) return vrcclSuccess;
+  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, maxDynamicSmem(fn, dev)) != cudaSuccess) {
+    cudaGetLastError();
+    return vrcclCudaError;
+  }
+  done.push_back(key);
+  return vrcclSuccess;
+}
 
 int smCount() {
   static int count[64] = {};
