@@ -658,7 +658,7 @@ vrcclResult_t vrcclReplicaGetAsyncError(vrcclResult_t* asyncErr);
  *   stats    out, [rows, 2] binary32, 8-byte aligned, or NULL: the row's
  *            largest logit and the logarithm of the sum of
  *            exp((logits - largest) / T); 0, 0 for a row without entries.
- *   temperature  > 0, and its reciprocal finite.
+ *   temperature  1e-18 to 1e18.
  */
 vrcclResult_t vrcclDistillForward(const void* logits, size_t ldl, const void* teacher, size_t ldt, const void* index,
                                   size_t ldi, float* loss, float* stats, size_t rows, size_t vocab, size_t k,

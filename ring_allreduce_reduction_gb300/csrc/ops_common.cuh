@@ -21,9 +21,11 @@ __host__ __device__ constexpr int floatTypeSize(int dt) { return dt == vrcclFloa
 inline bool isOperatorType(int dt) { return dt == vrcclFloat32 || dt == vrcclBfloat16 || dt == vrcclFloat16; }
 
 // A [rows, cols] operand: present, its address a multiple of its elements'
-// size, its row stride no shorter than a row.
-inline bool goodMatrix(const void* p, size_t ld, size_t cols, int elemSize) {
-  return p && (uintptr_t)p % elemSize == 0 && ld >= cols && ld < kMaxExtent;
+// size, its row stride no shorter than a row, and all of it within 2^46
+// elements (so that no offset, in bytes, comes near 64 bits).
+inline bool goodMatrix(const void* p, size_t ld, size_t rows, size_t cols, int elemSize) {
+  return p && (uintptr_t)p % elemSize == 0 && ld >= cols && ld < kMaxExtent &&
+         (rows == 0 || ld <= (size_t(1) << 46) / rows);
 }
 inline bool goodVector(const void* p, int elemSize) { return p && (uintptr_t)p % elemSize == 0; }
 // Every row of a matrix starts on a 16-byte boundary.
@@ -32,15 +34,34 @@ inline bool rowsAligned(const void* p, size_t ld, int elemSize) {
 }
 // Bytes of the matrix from its first element to its last.
 inline size_t spanBytes(size_t ld, size_t rows, size_t cols, int elemSize) {
-  return rows == 0 ? 0 : ((rows - 1) * ld + cols) * elemSize;
+  return rows == 0 || cols == 0 ? 0 : ((rows - 1) * ld + cols) * elemSize;
 }
-inline bool overlap(const void* a, size_t an, const void* b, size_t bn) {
-  return a && b && an && bn && (uintptr_t)a < (uintptr_t)b + bn && (uintptr_t)b < (uintptr_t)a + an;
+// What a call reads or writes; nothing where p is NULL.
+struct Span {
+  const void* p;
+  size_t bytes;
+};
+inline bool overlap(const Span& a, const Span& b) {
+  return a.p && b.p && a.bytes && b.bytes && (uintptr_t)a.p < (uintptr_t)b.p + b.bytes &&
+         (uintptr_t)b.p < (uintptr_t)a.p + a.bytes;
+}
+// No output touches an input or another output. (An input that an output may
+// take the place of is left out by its caller where it does.)
+template <int O, int I>
+inline bool apart(const Span (&out)[O], const Span (&in)[I]) {
+  for (int i = 0; i < O; ++i) {
+    for (int j = 0; j < I; ++j)
+      if (overlap(out[i], in[j])) return false;
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i], out[j])) return false;
+  }
+  return true;
+}
+// `in`, unless `out` lies in its place.
+inline Span unlessInPlace(const Span& in, size_t ldin, const void* out, size_t ldout) {
+  return in.p == out && ldin == ldout ? Span{nullptr, 0} : in;
 }
 
-inline vrcclResult_t launchResult() {
-  return cudaGetLastError() == cudaSuccess ? vrcclSuccess : vrcclCudaError;
-}
 // A failed wait of the layer norm's kernels (each translation unit holds its own device-side word).
 int normStatus(int* code);
 // Multiprocessors of the current device (asked for once a device).

@@ -431,13 +431,13 @@ DistillFn pickBackward(int threads) {
 bool goodDistill(const void* logits, size_t ldl, const void* teacher, size_t ldt, const void* index, size_t ldi,
                  size_t rows, size_t vocab, size_t k, int dtype, int ttype, int itype) {
   const int is = itype == vrcclInt64 ? 8 : 4;
-  return goodMatrix(logits, ldl, vocab, floatTypeSize(dtype)) && goodMatrix(teacher, ldt, k, floatTypeSize(ttype)) &&
-         goodMatrix(index, ldi, k, is);
+  return goodMatrix(logits, ldl, rows, vocab, floatTypeSize(dtype)) && goodMatrix(teacher, ldt, rows, k, floatTypeSize(ttype)) &&
+         goodMatrix(index, ldi, rows, k, is);
 }
 bool goodTypes(size_t rows, size_t vocab, size_t k, int dtype, int ttype, int itype, float temperature) {
   return rows < (size_t(1) << 31) && vocab < (size_t(1) << 31) && k <= VRCCL_DISTILL_MAX_K && isOperatorType(dtype) &&
-         isOperatorType(ttype) && (itype == vrcclInt32 || itype == vrcclInt64) && temperature > 0.f &&
-         temperature <= 3.0e38f && 1.f / temperature <= 3.0e38f;
+         isOperatorType(ttype) && (itype == vrcclInt32 || itype == vrcclInt64) && temperature >= 1e-18f &&
+         temperature <= 1e18f;  // its square and its reciprocal are then normal numbers
 }
 DistillArgs distillArgs(const void* logits, size_t ldl, const void* teacher, size_t ldt, const void* index, size_t ldi,
                         size_t rows, size_t vocab, size_t k, int ttype, int itype, float temperature) {
@@ -481,6 +481,11 @@ extern "C" vrcclResult_t vrcclDistillForward(const void* logits, size_t ldl, con
   }
   if (!goodDistill(logits, ldl, teacher, ldt, index, ldi, rows, vocab, k, dtype, teacherType, indexType))
     return vrcclInvalidArgument;
+  const Span out[] = {{loss, rows * 4}, {stats, rows * 8}};
+  const Span in[] = {{logits, spanBytes(ldl, rows, vocab, floatTypeSize(dtype))},
+                     {teacher, spanBytes(ldt, rows, k, floatTypeSize(teacherType))},
+                     {index, spanBytes(ldi, rows, k, indexType == vrcclInt64 ? 8 : 4)}};
+  if (!apart(out, in)) return vrcclInvalidArgument;
   DistillArgs a = distillArgs(logits, ldl, teacher, ldt, index, ldi, rows, vocab, k, teacherType, indexType, temperature);
   a.loss = loss;
   a.stats = reinterpret_cast<float2*>(stats);
@@ -504,7 +509,7 @@ extern "C" vrcclResult_t vrcclDistillBackward(const void* logits, size_t ldl, co
   if (rows == 0 || vocab == 0) return vrcclSuccess;
   const int E = floatTypeSize(dtype);
   cudaStream_t st = (cudaStream_t)stream;
-  if (!goodMatrix(dlogits, ldd, vocab, E)) return vrcclInvalidArgument;
+  if (!goodMatrix(dlogits, ldd, rows, vocab, E)) return vrcclInvalidArgument;
   if (k == 0) {  // no row has an entry
     if (cudaMemset2DAsync(dlogits, ldd * E, 0, vocab * E, rows, st) != cudaSuccess) {
       cudaGetLastError();
@@ -515,9 +520,14 @@ extern "C" vrcclResult_t vrcclDistillBackward(const void* logits, size_t ldl, co
   if (!goodDistill(logits, ldl, teacher, ldt, index, ldi, rows, vocab, k, dtype, teacherType, indexType) ||
       !goodVector(stats, 8) || !goodVector(dloss, 4) || dlossStride >= kMaxExtent)
     return vrcclInvalidArgument;
-  if (!(dlogits == logits && ldd == ldl) &&
-      overlap(dlogits, spanBytes(ldd, rows, vocab, E), logits, spanBytes(ldl, rows, vocab, E)))
-    return vrcclInvalidArgument;
+  if (rows - 1 > (size_t(1) << 46) / std::max<size_t>(1, dlossStride)) return vrcclInvalidArgument;
+  const Span out[] = {{dlogits, spanBytes(ldd, rows, vocab, E)}};
+  const Span in[] = {unlessInPlace({logits, spanBytes(ldl, rows, vocab, E)}, ldl, dlogits, ldd),
+                     {teacher, spanBytes(ldt, rows, k, floatTypeSize(teacherType))},
+                     {index, spanBytes(ldi, rows, k, indexType == vrcclInt64 ? 8 : 4)},
+                     {stats, rows * 8},
+                     {dloss, ((rows - 1) * dlossStride + 1) * 4}};
+  if (!apart(out, in)) return vrcclInvalidArgument;
   DistillArgs a = distillArgs(logits, ldl, teacher, ldt, index, ldi, rows, vocab, k, teacherType, indexType, temperature);
   a.stats = const_cast<float2*>(reinterpret_cast<const float2*>(stats));
   a.dloss = dloss;
@@ -538,6 +548,5 @@ extern "C" vrcclResult_t vrcclDistillBackward(const void* logits, size_t ldl, co
   const DistillFn fn = dtype == vrcclFloat32    ? pickBackward<vrcclFloat32>(threads)
                        : dtype == vrcclBfloat16 ? pickBackward<vrcclBfloat16>(threads)
                                                 : pickBackward<vrcclFloat16>(threads);
-  fn<<<(unsigned)(rows * slices), threads, 0, st>>>(a);
-  return launchResult();
+  return launchShaped(fn, {dim3((unsigned)(rows * slices)), threads, 0, 0, false}, st, a);
 }

@@ -21,6 +21,7 @@
 // linearFew streams W with wide loads over all multiprocessors instead.
 #include <cuda.h>
 
+#include <atomic>
 #include <cstring>
 #include <utility>
 
@@ -1156,17 +1157,20 @@ __global__ void __launch_bounds__(1024) linearBiasJoin(const float* partial, int
 using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
                               const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                               CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+// (Asked for again after a failure: the driver may not have been there yet.)
 EncodeFn encodeFn() {
-  static const EncodeFn fn = [] {
+  static std::atomic<EncodeFn> known{nullptr};
+  EncodeFn fn = known.load(std::memory_order_relaxed);
+  if (!fn) {
     void* p = nullptr;
     cudaDriverEntryPointQueryResult q;
     if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
         q != cudaDriverEntryPointSuccess) {
       cudaGetLastError();
-      p = nullptr;
+      return nullptr;
     }
-    return (EncodeFn)p;
-  }();
+    known.store(fn = (EncodeFn)p, std::memory_order_relaxed);
+  }
   return fn;
 }
 
@@ -1417,18 +1421,14 @@ vrcclResult_t products(const Product* q, int n, bool after, cudaStream_t st) {
 }
 
 template <int DT, int MR, bool WIDE>
-void launchFew(const FewArgs& a, cudaStream_t st) {
-  linearFew<DT, MR, WIDE><<<(unsigned)((a.outs + fewOuts(MR) - 1) / fewOuts(MR)), kFewThreads, 0, st>>>(a);
+vrcclResult_t launchFew(const FewArgs& a, cudaStream_t st) {
+  return launchShaped(linearFew<DT, MR, WIDE>, {dim3((unsigned)((a.outs + fewOuts(MR) - 1) / fewOuts(MR))), kFewThreads, 0, 0, false}, st, a);
 }
 template <int DT>
 vrcclResult_t few(const FewArgs& a, bool wide, cudaStream_t st) {
-  if (wide && a.rows <= 2)
-    a.rows == 1 ? launchFew<DT, 1, true>(a, st) : launchFew<DT, 2, true>(a, st);
-  else if (a.rows <= 2)
-    a.rows == 1 ? launchFew<DT, 1, false>(a, st) : launchFew<DT, 2, false>(a, st);
-  else
-    a.rows <= 4 ? launchFew<DT, 4, false>(a, st) : launchFew<DT, 8, false>(a, st);
-  return launchResult();
+  if (wide && a.rows <= 2) return a.rows == 1 ? launchFew<DT, 1, true>(a, st) : launchFew<DT, 2, true>(a, st);
+  if (a.rows <= 2) return a.rows == 1 ? launchFew<DT, 1, false>(a, st) : launchFew<DT, 2, false>(a, st);
+  return a.rows <= 4 ? launchFew<DT, 4, false>(a, st) : launchFew<DT, 8, false>(a, st);
 }
 
 // Row blocks of linearSlope: enough for two waves of blocks.
@@ -1442,14 +1442,13 @@ int slopeBlocks(size_t rows, size_t cols) {
 size_t biasBytes(size_t rows, size_t outs) { return (size_t(slopeBlocks(rows, outs)) * outs * 4 + 255) / 256 * 256; }
 
 template <int DT, bool WIDE>
-void launchSlope(int act, dim3 grid, const SlopeArgs& a, cudaStream_t st) {
-  switch (act) {
-    case vrcclActRelu: linearSlope<DT, vrcclActRelu, WIDE><<<grid, 256, 0, st>>>(a); break;
-    case vrcclActGelu: linearSlope<DT, vrcclActGelu, WIDE><<<grid, 256, 0, st>>>(a); break;
-    case vrcclActGeluTanh: linearSlope<DT, vrcclActGeluTanh, WIDE><<<grid, 256, 0, st>>>(a); break;
-    case vrcclActSilu: linearSlope<DT, vrcclActSilu, WIDE><<<grid, 256, 0, st>>>(a); break;
-    default: linearSlope<DT, vrcclActNone, WIDE><<<grid, 256, 0, st>>>(a); break;
-  }
+vrcclResult_t launchSlope(int act, dim3 grid, const SlopeArgs& a, cudaStream_t st) {
+  void (*fn)(SlopeArgs) = act == vrcclActRelu       ? linearSlope<DT, vrcclActRelu, WIDE>
+                          : act == vrcclActGelu     ? linearSlope<DT, vrcclActGelu, WIDE>
+                          : act == vrcclActGeluTanh ? linearSlope<DT, vrcclActGeluTanh, WIDE>
+                          : act == vrcclActSilu     ? linearSlope<DT, vrcclActSilu, WIDE>
+                                                    : linearSlope<DT, vrcclActNone, WIDE>;
+  return launchShaped(fn, {grid, 256, 0, 0, false}, st, a);
 }
 
 bool goodLinear(size_t rows, size_t outs, size_t ins, int dtype, int act) {
@@ -1484,10 +1483,8 @@ vrcclResult_t backward(const void* dy, size_t lddy, const void* z, size_t ldz, c
       return vrcclInvalidArgument;
     const bool wide = outs % 8 == 0 && rowsAligned(dy, lddy, 2) && (act == vrcclActNone || rowsAligned(z, ldz, 2));
     const dim3 grid((unsigned)((outs + 255) / 256), (unsigned)slopeBlocks(rows, outs));
-    if (wide)
-      launchSlope<DT, true>(act, grid, s, st);
-    else
-      launchSlope<DT, false>(act, grid, s, st);
+    const vrcclResult_t r = wide ? launchSlope<DT, true>(act, grid, s, st) : launchSlope<DT, false>(act, grid, s, st);
+    if (r != vrcclSuccess) return r;
     partial = s.partial;
     blocks = (int)grid.y;
     after = true;
@@ -1513,7 +1510,7 @@ vrcclResult_t backward(const void* dy, size_t lddy, const void* z, size_t ldz, c
   if (dbias)
     return launchShaped(linearBiasJoin<DT>, {dim3((unsigned)((outs + 31) / 32)), 1024, 0, 0, true}, st, partial, blocks,
                         (int)outs, dbias);
-  return launchResult();
+  return vrcclSuccess;
 }
 
 vrcclResult_t zeroRows(void* p, size_t ld, size_t rows, size_t cols, cudaStream_t st) {
@@ -1546,17 +1543,14 @@ extern "C" vrcclResult_t vrcclLinearForward(const void* x, size_t ldx, const voi
   if (!goodLinear(rows, outs, ins, dtype, act)) return vrcclInvalidArgument;
   if (dtype == vrcclFloat32) return vrcclInvalidUsage;
   if (rows == 0 || outs == 0) return vrcclSuccess;
-  if ((ins && (!goodMatrix(x, ldx, ins, 2) || !goodMatrix(w, ldw, ins, 2))) || !goodMatrix(y, ldy, outs, 2) ||
-      (bias && !goodVector(bias, 2)) || (residual && !goodMatrix(residual, ldr, outs, 2)) ||
-      (z && !goodMatrix(z, ldz, outs, 2)) || (workspace && !goodVector(workspace, 256)))
+  if ((ins && (!goodMatrix(x, ldx, rows, ins, 2) || !goodMatrix(w, ldw, outs, ins, 2))) || !goodMatrix(y, ldy, rows, outs, 2) ||
+      (bias && !goodVector(bias, 2)) || (residual && !goodMatrix(residual, ldr, rows, outs, 2)) ||
+      (z && !goodMatrix(z, ldz, rows, outs, 2)) || (workspace && !goodVector(workspace, 256)))
     return vrcclInvalidArgument;
-  const size_t ySpan = spanBytes(ldy, rows, outs, 2), zSpan = spanBytes(ldz, rows, outs, 2);
-  const size_t xSpan = spanBytes(ldx, rows, ins, 2), wSpan = spanBytes(ldw, outs, ins, 2);
-  if (overlap(y, ySpan, x, xSpan) || overlap(y, ySpan, w, wSpan) || overlap(z, zSpan, x, xSpan) ||
-      overlap(z, zSpan, w, wSpan) || overlap(z, zSpan, y, ySpan) || overlap(z, zSpan, residual, spanBytes(ldr, rows, outs, 2)) ||
-      overlap(y, ySpan, bias, outs * 2) || overlap(z, zSpan, bias, outs * 2) ||
-      (!(residual == y && ldr == ldy) && overlap(y, ySpan, residual, spanBytes(ldr, rows, outs, 2))))
-    return vrcclInvalidArgument;
+  const Span spanR = {residual, spanBytes(ldr, rows, outs, 2)}, spanZ = {z, spanBytes(ldz, rows, outs, 2)};
+  const Span out[] = {{y, spanBytes(ldy, rows, outs, 2)}, spanZ, {workspace, workspaceBytes}};
+  const Span in[] = {{x, spanBytes(ldx, rows, ins, 2)}, {w, spanBytes(ldw, outs, ins, 2)}, {bias, outs * 2}, unlessInPlace(spanR, ldr, y, ldy)};
+  if (!apart(out, in) || overlap(spanZ, spanR) || overlap(out[2], spanR)) return vrcclInvalidArgument;
   cudaStream_t st = (cudaStream_t)stream;
   const bool apart = rowsAligned(x, ldx, 2) && rowsAligned(w, ldw, 2);
   if (rows <= (size_t)(apart ? kFewRows : kFewRowsUnaligned) || ins == 0) {
@@ -1611,7 +1605,7 @@ extern "C" vrcclResult_t vrcclLinearBackward(const void* dy, size_t lddy, const 
   if (!goodLinear(rows, outs, ins, dtype, act)) return vrcclInvalidArgument;
   if (dtype == vrcclFloat32) return vrcclInvalidUsage;
   const bool acts = act != vrcclActNone;
-  if ((dx && !goodMatrix(dx, lddx, ins, 2)) || (dw && !goodMatrix(dw, lddw, ins, 2)) || (dbias && !goodVector(dbias, 2)) ||
+  if ((dx && !goodMatrix(dx, lddx, rows, ins, 2)) || (dw && !goodMatrix(dw, lddw, outs, ins, 2)) || (dbias && !goodVector(dbias, 2)) ||
       (workspace && !goodVector(workspace, 256)))
     return vrcclInvalidArgument;
   cudaStream_t st = (cudaStream_t)stream;
@@ -1624,22 +1618,13 @@ extern "C" vrcclResult_t vrcclLinearBackward(const void* dy, size_t lddy, const 
     if (rows == 0) return zeroRows(dbias, outs, 1, outs, st);
     dx = dw = nullptr;  // ins == 0: the bias gradient is all there is
   }
-  const size_t gSpan = spanBytes(lddy, rows, outs, 2), zSpan = spanBytes(ldz, rows, outs, 2);
-  const size_t xSpan = spanBytes(ldx, rows, ins, 2), wSpan = spanBytes(ldw, outs, ins, 2);
-  if (!goodMatrix(dy, lddy, outs, 2) || (acts && !goodMatrix(z, ldz, outs, 2)) || (dw && !goodMatrix(x, ldx, ins, 2)) ||
-      (dx && !goodMatrix(w, ldw, ins, 2)))
+  if (!goodMatrix(dy, lddy, rows, outs, 2) || (acts && !goodMatrix(z, ldz, rows, outs, 2)) || (dw && !goodMatrix(x, ldx, rows, ins, 2)) ||
+      (dx && !goodMatrix(w, ldw, outs, ins, 2)))
     return vrcclInvalidArgument;
-  struct {
-    void* p;
-    size_t n;
-  } out[3] = {{dx, spanBytes(lddx, rows, ins, 2)}, {dw, spanBytes(lddw, outs, ins, 2)}, {dbias, outs * 2}};
-  for (int i = 0; i < 3; ++i) {
-    if (overlap(out[i].p, out[i].n, dy, gSpan) || (acts && overlap(out[i].p, out[i].n, z, zSpan)) ||
-        overlap(out[i].p, out[i].n, x, xSpan) || overlap(out[i].p, out[i].n, w, wSpan))
-      return vrcclInvalidArgument;
-    for (int j = 0; j < i; ++j)
-      if (overlap(out[i].p, out[i].n, out[j].p, out[j].n)) return vrcclInvalidArgument;
-  }
+  const Span out[] = {{dx, spanBytes(lddx, rows, ins, 2)}, {dw, spanBytes(lddw, outs, ins, 2)}, {dbias, outs * 2}, {workspace, workspaceBytes}};
+  const Span in[] = {{dy, spanBytes(lddy, rows, outs, 2)}, {acts ? z : nullptr, spanBytes(ldz, rows, outs, 2)},
+                     {dw ? x : nullptr, spanBytes(ldx, rows, ins, 2)}, {dx ? w : nullptr, spanBytes(ldw, outs, ins, 2)}};
+  if (!apart(out, in)) return vrcclInvalidArgument;
   size_t need = dbias ? biasBytes(rows, outs) : 0;
   if (dx || dw) need += acts ? packedBytes(rows, outs) : packNeed(dy, lddy, rows, outs);
   if (dx) need += packNeed(w, ldw, outs, ins);

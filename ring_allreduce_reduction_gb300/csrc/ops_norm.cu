@@ -18,8 +18,6 @@
 // workspace, and a second kernel adds those rows in order. No atomics: the
 // same call gives the same bits.
 #include <mutex>
-#include <utility>
-#include <vector>
 
 #include "ops_common.cuh"
 
@@ -1238,8 +1236,7 @@ vrcclResult_t launchNorm(int dt, const Shape& s, unsigned blocks, NormArgs& a, c
   }
   a.stages = s.stages;
   a.teams = s.teams;
-  fn<<<blocks, s.threads, s.smem, st>>>(a);
-  return launchResult();
+  return launchShaped(fn, {dim3(blocks), s.threads, s.smem, 0, false}, st, a);
 }
 
 bool goodSizes(size_t rows, size_t cols, int dtype, int ptype) {
@@ -1252,17 +1249,24 @@ int normStatus(int* code) { return cudaMemcpyFromSymbol(code, gNormStatus, sizeo
 
 vrcclResult_t allowSharedMemory(const void* fn) {
   static std::mutex mu;
-  static std::vector<std::pair<const void*, int>> done;
+  static struct {
+    const void* fn;
+    int dev;
+  } done[256];
+  static int count = 0;
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return vrcclCudaError;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    return vrcclCudaError;
+  }
   std::lock_guard<std::mutex> lk(mu);
-  const auto key = std::make_pair(fn, dev);
-  if (std::find(done.begin(), done.end(), key) != done.end()) return vrcclSuccess;
+  for (int i = 0; i < count; ++i)
+    if (done[i].fn == fn && done[i].dev == dev) return vrcclSuccess;
   if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, maxDynamicSmem(fn, dev)) != cudaSuccess) {
     cudaGetLastError();
     return vrcclCudaError;
   }
-  done.push_back(key);
+  if (count < 256) done[count++] = {fn, dev};
   return vrcclSuccess;
 }
 
@@ -1292,11 +1296,14 @@ extern "C" vrcclResult_t vrcclLayerNormForward(const void* x, size_t ldx, const 
   if (!goodSizes(rows, cols, dtype, paramType) || !(eps >= 0.f)) return vrcclInvalidArgument;
   if (rows == 0 || cols == 0) return vrcclSuccess;
   const int E = floatTypeSize(dtype), PE = floatTypeSize(paramType);
-  if (!goodMatrix(x, ldx, cols, E) || !goodMatrix(y, ldy, cols, E)) return vrcclInvalidArgument;
+  if (!goodMatrix(x, ldx, rows, cols, E) || !goodMatrix(y, ldy, rows, cols, E)) return vrcclInvalidArgument;
   if ((gamma && !goodVector(gamma, PE)) || (beta && !goodVector(beta, PE)) || (mean && !goodVector(mean, 4)) ||
       (rstd && !goodVector(rstd, 4)))
     return vrcclInvalidArgument;
-  if (!(x == y && ldx == ldy) && overlap(x, spanBytes(ldx, rows, cols, E), y, spanBytes(ldy, rows, cols, E)))
+  const Span out[] = {{y, spanBytes(ldy, rows, cols, E)}, {mean, rows * 4}, {rstd, rows * 4}};
+  const Span in[] = {unlessInPlace({x, spanBytes(ldx, rows, cols, E)}, ldx, y, ldy), {gamma, cols * PE}, {beta, cols * PE}};
+  if (!apart(out, in) || overlap(out[1], {x, spanBytes(ldx, rows, cols, E)}) ||
+      overlap(out[2], {x, spanBytes(ldx, rows, cols, E)}))
     return vrcclInvalidArgument;
   const Shape s = normShape(rows, (int)cols, E, rowsAligned(x, ldx, E) && rowsAligned(y, ldy, E), true);
   NormArgs a = {};
@@ -1342,18 +1349,20 @@ extern "C" vrcclResult_t vrcclLayerNormBackward(const void* dy, size_t lddy, con
     }
     return vrcclSuccess;
   }
-  if (!goodMatrix(dy, lddy, cols, E) || !goodMatrix(x, ldx, cols, E) || !goodMatrix(dx, lddx, cols, E) ||
+  if (!goodMatrix(dy, lddy, rows, cols, E) || !goodMatrix(x, ldx, rows, cols, E) || !goodMatrix(dx, lddx, rows, cols, E) ||
       !goodVector(mean, 4) || !goodVector(rstd, 4))
-    return vrcclInvalidArgument;
-  const size_t outSpan = spanBytes(lddx, rows, cols, E);
-  if ((!(dx == dy && lddx == lddy) && overlap(dx, outSpan, dy, spanBytes(lddy, rows, cols, E))) ||
-      (!(dx == x && lddx == ldx) && overlap(dx, outSpan, x, spanBytes(ldx, rows, cols, E))))
     return vrcclInvalidArgument;
   const Shape s =
       normShape(rows, (int)cols, E, rowsAligned(dy, lddy, E) && rowsAligned(x, ldx, E) && rowsAligned(dx, lddx, E), false);
   const int blocks = normBlocks(rows, s);
-  if (weights && (!goodVector(workspace, 16) || workspaceBytes < size_t(blocks) * 2 * cols * sizeof(float)))
-    return vrcclInvalidArgument;
+  const size_t need = weights ? size_t(mostBlocks(rows, (int)cols)) * 2 * cols * sizeof(float) : 0;  // what the query says
+  if (weights && (!goodVector(workspace, 16) || workspaceBytes < need)) return vrcclInvalidArgument;
+  const Span spanDy = {dy, spanBytes(lddy, rows, cols, E)}, spanX = {x, spanBytes(ldx, rows, cols, E)};
+  const Span other[] = {{dgamma, cols * PE}, {dbeta, cols * PE}, {workspace, need}};
+  const Span all[] = {{dx, spanBytes(lddx, rows, cols, E)}, other[0], other[1], other[2]};
+  const Span in[] = {{gamma, cols * PE}, {mean, rows * 4}, {rstd, rows * 4}, unlessInPlace(spanDy, lddy, dx, lddx), unlessInPlace(spanX, ldx, dx, lddx)};
+  const Span matrices[] = {spanDy, spanX};
+  if (!apart(all, in) || !apart(other, matrices)) return vrcclInvalidArgument;
   NormArgs a = {};
   a.x = x;
   a.dy = dy;
@@ -1371,12 +1380,11 @@ extern "C" vrcclResult_t vrcclLayerNormBackward(const void* dy, size_t lddy, con
   a.wideParams = ((uintptr_t)gamma & 15) == 0;
   if (s.walk == kLongRow && weights) {
     const dim3 grid((unsigned)((cols + 255) / 256), (unsigned)blocks);
-    if (dtype == vrcclFloat32)
-      normColumns<vrcclFloat32><<<grid, 256, 0, st>>>(a);
-    else if (dtype == vrcclBfloat16)
-      normColumns<vrcclBfloat16><<<grid, 256, 0, st>>>(a);
-    else
-      normColumns<vrcclFloat16><<<grid, 256, 0, st>>>(a);
+    const NormFn columns = dtype == vrcclFloat32    ? normColumns<vrcclFloat32>
+                           : dtype == vrcclBfloat16 ? normColumns<vrcclBfloat16>
+                                                    : normColumns<vrcclFloat16>;
+    const vrcclResult_t r = launchShaped(columns, {grid, 256, 0, 0, false}, st, a);
+    if (r != vrcclSuccess) return r;
   }
   const vrcclResult_t r = launchNorm<false>(dtype, s, (unsigned)blocks, a, st);
   if (r != vrcclSuccess) return r;

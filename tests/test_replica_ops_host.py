@@ -104,6 +104,47 @@ def test_distill_refusals(lib):
     assert _call(lib.vrcclDistillBackward, bwd, vocab=0) == 0
 
 
+def test_outputs_that_overlap_are_refused(lib):
+    """An output may not touch an input, another output or the workspace, other than in place as documented."""
+    norm = dict(x=A[0], ldx=64, gamma=A[1], beta=A[2], y=A[3], ldy=64, mean=A[4], rstd=A[5], rows=4, cols=64, dtype=BF16,
+                ptype=F32, eps=1e-5, stream=None)
+    for change in (dict(mean=A[3] + 64), dict(rstd=A[4] + 8), dict(y=A[1]), dict(y=A[2] + 128), dict(mean=A[0] + 8),
+                   dict(x=A[3], ldx=72), dict(rstd=A[1])):
+        assert _call(lib.vrcclLayerNormForward, norm, **change) == 1, change
+    back = dict(dy=A[0], lddy=64, x=A[1], ldx=64, gamma=A[2], mean=A[3], rstd=A[4], dx=A[5], lddx=64, dgamma=A[6],
+                dbeta=A[7], rows=4, cols=64, dtype=BF16, ptype=F32, ws=A[8], bytes=1 << 20, stream=None)
+    for change in (dict(ws=A[5]), dict(ws=A[0]), dict(dgamma=A[1] + 4), dict(dbeta=A[6] + 16), dict(dx=A[3]), dict(dgamma=A[2]),
+                   dict(dbeta=A[8] + 64)):
+        assert _call(lib.vrcclLayerNormBackward, back, **change) == 1, change
+    lin = dict(x=A[0], ldx=64, w=A[1], ldw=64, bias=A[2], r=A[3], ldr=32, y=A[4], ldy=32, z=A[5], ldz=32, rows=20, outs=32,
+               ins=64, dtype=BF16, act=2, ws=A[6], bytes=1 << 20, stream=None)
+    for change in (dict(z=A[3]), dict(ws=A[4]), dict(ws=A[0]), dict(ws=A[3]), dict(z=A[2])):
+        assert _call(lib.vrcclLinearForward, lin, **change) == 1, change
+    grad = dict(dy=A[0], lddy=32, z=A[1], ldz=32, x=A[2], ldx=64, w=A[3], ldw=64, dx=A[4], lddx=64, dw=A[5], lddw=64,
+                db=A[6], rows=20, outs=32, ins=64, dtype=BF16, act=2, ws=A[7], bytes=1 << 20, stream=None)
+    for change in (dict(ws=A[4]), dict(ws=A[1]), dict(db=A[5] + 2), dict(dx=A[1]), dict(db=A[2])):
+        assert _call(lib.vrcclLinearBackward, grad, **change) == 1, change
+    dis = dict(s=A[0], ldl=100, t=A[1], ldt=8, idx=A[2], ldi=8, loss=A[3], stats=A[4], rows=4, vocab=100, k=8, dtype=BF16,
+               ttype=F32, itype=I64, T=1.0, stream=None)
+    for change in (dict(loss=A[0] + 4), dict(stats=A[1]), dict(loss=A[4] + 8), dict(stats=A[2])):
+        assert _call(lib.vrcclDistillForward, dis, **change) == 1, change
+    dback = dict(s=A[0], ldl=100, t=A[1], ldt=8, idx=A[2], ldi=8, stats=A[3], dloss=A[4], stride=1, ds=A[5], ldd=100, rows=4,
+                 vocab=100, k=8, dtype=BF16, ttype=F32, itype=I64, T=1.0, stream=None)
+    for change in (dict(ds=A[1]), dict(ds=A[2]), dict(ds=A[3]), dict(ds=A[4])):
+        assert _call(lib.vrcclDistillBackward, dback, **change) == 1, change
+
+
+def test_extents_beyond_64_bits_are_refused(lib):
+    """Rows times row stride must stay addressable; a temperature's square and reciprocal normal numbers."""
+    norm = dict(x=A[0], ldx=1 << 39, gamma=None, beta=None, y=A[3], ldy=64, mean=None, rstd=None, rows=1 << 30, cols=64,
+                dtype=BF16, ptype=F32, eps=1e-5, stream=None)
+    assert _call(lib.vrcclLayerNormForward, norm) == 1
+    dis = dict(s=A[0], ldl=100, t=A[1], ldt=8, idx=A[2], ldi=8, loss=A[3], stats=A[4], rows=4, vocab=100, k=8, dtype=BF16,
+               ttype=F32, itype=I64, T=1.0, stream=None)
+    for change in (dict(T=1e-19), dict(T=1e19), dict(ldl=1 << 39, rows=1 << 20), dict(ldi=1 << 39, rows=1 << 20)):
+        assert _call(lib.vrcclDistillForward, dis, **change) == 1, change
+
+
 def _along(f, x, d, h=1e-6):
     return (f(x + h * d) - f(x - h * d)) / (2 * h)
 
