@@ -11,14 +11,22 @@
 // cores read either from the same 128-byte-swizzled tiles, so no operand is
 // ever transposed in memory.
 //
-// Warp roles of a block: one thread issues the TMA copies of 64-deep slices
-// of A and B into a ring of shared-memory stages, one issues the MMAs, four
-// warps read finished accumulators out of TMEM, apply the epilogue and store.
-// TMEM holds two accumulators, so a tile's epilogue runs under the next one's
-// products.
+// Warp roles of a block: one warp issues the TMA copies of slices of A and B
+// into a ring of shared-memory stages, one issues the MMAs, eight read finished
+// accumulators out of TMEM, apply the epilogue and store by TMA. TMEM holds two
+// accumulators, so a tile's epilogue runs under the next one's products.
+//
+// Large products are bound by the tensor cores, and, a second into a run, by
+// the 1400 W limit: 8192 cubed 560 us (1.96 PFLOP/s, 0.99 of a library product's
+// burst), over seconds 600 us. Beside a library's plain product in the same
+// state: 8192 x 8192 x 2048 156 us, here 168 us with the bias, 171 with
+// gelu-tanh, 183 where z is stored too (268 MB written in all); both gradients
+// of 8192 x 4096 x 4096 331 us for the library's 331.
 //
 // A call with few rows (one token and its like) is bound by reading W once:
-// linearFew streams W with wide loads over all multiprocessors instead.
+// linearFew streams W with wide loads, productSplit (below) feeds it to the
+// tensor cores from all multiprocessors: 1, 16 and 64 rows of 4096 x 4096 in
+// 6.2, 8.4 and 10.4 us (33.5 MB: 5.0 us from memory).
 #include <cuda.h>
 
 #include <atomic>
@@ -1086,7 +1094,8 @@ constexpr int kSlopeTurn = 4;  // rows a thread has in flight
 // dz = dy act'(z), rounded to the element type: the tensor cores take their
 // operands in it. The bias gradient sums the unrounded values. A thread has
 // eight columns; WIDE: rows of dy and z start on 16-byte boundaries (and end
-// on them), else their elements are gathered. dz always does.
+// on them), else their elements are gathered. dz always does. Bound by memory:
+// for 8192 x 4096 bf16 with gelu (201 MB) it adds 31 us to the products.
 template <int DT, int ACT, bool WIDE>
 __global__ void __launch_bounds__(256, 4) linearSlope(const __grid_constant__ SlopeArgs a) {
   using S = typename Ty<DT>::S;
