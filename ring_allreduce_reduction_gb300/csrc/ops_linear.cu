@@ -385,7 +385,7 @@ struct ProductShape {
   static constexpr int kStageBytes = (kBM + kBRows) * kBK * 2;
   static constexpr int kStages = BN == 64 ? 3 : 6;
   static constexpr int kSmem = kStages * kStageBytes + kEpilogueWarps * 2 * kStoreBytes + 1024;
-  static constexpr int kTmemCols = 2 * BN;
+  static constexpr int kTmemCols = BN == 192 ? 512 : 2 * BN;  // a power of two
   static constexpr int kGroup = CG == 2 ? 8 : 12;  // tiles of a column (Walk::place): about the root of the tiles at work
 };
 
@@ -1361,9 +1361,11 @@ int splitParts(long long tiles, long long steps) {
 
 // Which tile: the one whose last unit ends first, by measured cycles: a step
 // of 64 contraction elements and a tile's epilogue (which runs under the next
-// tile's steps where they take longer). At 4096 cubed: pairs 83 us, 128 x 128
-// tiles 107, 128 x 64 tiles 171; at 1024 cubed 12.4, 8.8 and 8.3.
-enum Tile { kPair256, kBlock128, kBlock64, kSplit64, kSwap32, kSwap64 };
+// tile's steps where they take longer). At 4096 cubed: pairs 81 us, 128 x 128
+// tiles 102, 128 x 64 tiles 166; at 1024 cubed 12.4, 10.3 and 8.3. A pair's tile
+// of 192 columns is for counts that leave most of a round of 256-wide ones
+// empty: 1921 x 2544 x 2808, 80 of those on 76 pairs, 41 us, 37 with 112.
+enum Tile { kPair256, kPair192, kBlock128, kBlock64, kSplit64, kSwap32, kSwap64 };
 struct Choice {
   Tile tile;
   int parts;
@@ -1374,7 +1376,7 @@ Choice chooseTile(const Product* q, int n) {
     Tile tile;
     int bm, bn, blocks, step, end;
   };
-  static const Kind kinds[3] = {{kPair256, 256, 256, 2, 520, 6000}, {kBlock128, 128, 128, 1, 420, 3000}, {kBlock64, 128, 64, 1, 341, 2200}};
+  static const Kind kinds[4] = {{kPair256, 256, 256, 2, 520, 6000}, {kPair192, 256, 192, 2, 420, 5000}, {kBlock128, 128, 128, 1, 420, 3000}, {kBlock64, 128, 64, 1, 341, 2200}};
   constexpr double kJoin = 3000;  // the sums' way through distributed shared memory
   if (n == 1 && q->p.M <= 64 && !q->p.aMN) {
     const int parts = splitParts((q->p.N + kBM - 1) / kBM, (q->p.K + 127) / 128);
@@ -1383,6 +1385,8 @@ Choice chooseTile(const Product* q, int n) {
   }
   Choice best = {kPair256, 1, 1e300};
   for (const Kind& k : kinds) {
+    // (half of its 192 rows of B is no whole number of the 64-wide boxes an MN-major operand comes in)
+    if (k.tile == kPair192 && (q[0].p.bMN || q[n - 1].p.bMN)) continue;
     const int units = smCount() / k.blocks;
     double cycles = 0, longest = 0;
     long long tiles = 0;
@@ -1420,6 +1424,7 @@ vrcclResult_t products(const Product* q, int n, bool after, cudaStream_t st) {
   }
   switch (c.tile) {
     case kPair256: return launchProducts<DT, 2, 256>(q, n, after, st);
+    case kPair192: return launchProducts<DT, 2, 192>(q, n, after, st);
     case kBlock128: return launchProducts<DT, 1, 128>(q, n, after, st);
     case kBlock64: return launchProducts<DT, 1, 64>(q, n, after, st);
     case kSplit64: return launchSplit<DT, 64, false>(q[0], c.parts, after, st);

@@ -376,6 +376,13 @@ def test_linear_many_tiles(torch, v, rows, outs, ins):
     _linear_back(torch, v, rows, outs, ins, "bfloat16", "none")
 
 
+@pytest.mark.parametrize("rows,outs,ins", [(744, 3584, 600), (750, 3561, 611)])
+def test_linear_tiles_of_192_columns(torch, v, rows, outs, ins):
+    for act in ("gelu_tanh", "none"):
+        _linear_check(torch, v, rows, outs, ins, "bfloat16", act)
+    _linear_check(torch, v, rows, outs, ins, "float16", "silu", 5, 1)
+
+
 @pytest.mark.parametrize("rows,outs,ins", [(3, 4096, 512), (5, 1000, 1000), (16, 1024, 4096), (20, 130, 2056), (32, 136, 136),
                                            (33, 1000, 2048), (64, 64, 4096), (65, 520, 1536), (128, 1024, 2048),
                                            (250, 300, 1100), (512, 512, 4096), (130, 72, 4104)])
