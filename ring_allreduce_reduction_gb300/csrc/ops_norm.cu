@@ -190,6 +190,7 @@ struct Team {
       S* v = reinterpret_cast<S*>(slot + (w.row & 15));
       for (uintptr_t at = w.row; at < w.lo && at < w.row + (uintptr_t)cols * E; at += E) v[(at - w.row) / E] = *(const S*)at;
       for (uintptr_t at = max(w.hi, w.row); at < w.row + (uintptr_t)cols * E; at += E) v[(at - w.row) / E] = *(const S*)at;
+      fenceProxyAsync();  // a later row's copy into this slot comes after these writes
     }
   }
   static __device__ __forceinline__ unsigned fetchBytes(const void* p, size_t ld, size_t row, size_t rows, int cols) {
