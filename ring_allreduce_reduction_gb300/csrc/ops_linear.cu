@@ -19,9 +19,9 @@
 // Large products are bound by the tensor cores, and, a second into a run, by
 // the 1400 W limit: 8192 cubed 560 us (1.96 PFLOP/s, 0.99 of a library product's
 // burst), over seconds 600 us. Beside a library's plain product in the same
-// state: 8192 x 8192 x 2048 156 us, here 168 us with the bias, 171 with
-// gelu-tanh, 183 where z is stored too (268 MB written in all); both gradients
-// of 8192 x 4096 x 4096 331 us for the library's 331.
+// state: 8192 x 8192 x 2048 159 us, here 169 us with the bias, 173 with
+// gelu-tanh, 182 where z is stored too (268 MB written in all); both gradients
+// of 8192 x 4096 x 4096 339 us for the library's 335.
 //
 // A call with few rows (one token and its like) is bound by reading W once:
 // linearFew streams W with wide loads, productSplit (below) feeds it to the
@@ -355,7 +355,7 @@ struct Walk {
     }
   }
   __device__ __forceinline__ bool more() const { return tile < end; }
-  // The tile's place: columns of GROUP tiles down, so that the tiles at work at a time make up a square of the result and
+  // The tile's place: columns of GROUP tiles down, so that the tiles at work at a time make up a block of the result and
   // read few different rows of either operand.
   template <int GROUP>
   __device__ __forceinline__ void place(const Problem& a, int& m, int& n) const {
@@ -379,14 +379,16 @@ template <int CG, int BN>
 struct ProductShape {
   static constexpr int kBRows = BN / CG;
   // Contraction elements a stage. Waiting for a stage and signalling it free costs its MMA warp some 150 cycles: nothing
-  // under the MMAs of the wider tiles (which gain more from five shallow stages than from two deep ones: 4096 cubed on
+  // under the MMAs of the wider tiles (which gain more from many shallow stages than from two deep ones: 4096 cubed on
   // 128 x 128 tiles 107 us against 147), but as much again under a narrow one's.
   static constexpr int kBK = BN <= 64 ? 128 : 64;
   static constexpr int kStageBytes = (kBM + kBRows) * kBK * 2;
   static constexpr int kStages = BN == 64 ? 3 : 6;
   static constexpr int kSmem = kStages * kStageBytes + kEpilogueWarps * 2 * kStoreBytes + 1024;
   static constexpr int kTmemCols = BN == 192 ? 512 : 2 * BN;  // a power of two
-  static constexpr int kGroup = CG == 2 ? 8 : 12;  // tiles of a column (Walk::place): about the root of the tiles at work
+  // Tiles of a column (Walk::place). Pairs, over seconds, 8 against 16: 8192 x 8192 x 2048 with gelu-tanh and z 187.3 and
+  // 183.6 us, 4096 cubed 89.3 and 87.5, both gradients of 8192 x 4096 x 4096 with gelu 356.4 and 358.4.
+  static constexpr int kGroup = CG == 2 ? 16 : 12;
 };
 
 // A warp's staging buffer: 32 rows of 64 bytes, their 16-byte pieces swizzled
@@ -573,7 +575,6 @@ __global__ void __launch_bounds__(kProductThreads, 1) productKernel(const __grid
   unsigned char* smem = dyn + ((1024 - (smemAddr(dyn) & 1023)) & 1023);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t rank = CG == 2 ? clusterRank() : 0;
-  constexpr int kWorkers = kEpilogueWarps;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -582,7 +583,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) productKernel(const __grid
     }
     for (int s = 0; s < 2; ++s) {
       mbarInit(&accFull[s], 1);
-      mbarInit(&accEmpty[s], kWorkers * CG);
+      mbarInit(&accEmpty[s], kEpilogueWarps * CG);
     }
     mbarInit(&drained, 1);
     deadWord = 0;
@@ -666,10 +667,10 @@ __global__ void __launch_bounds__(kProductThreads, 1) productKernel(const __grid
       }
     }
     __syncwarp();
-  } else if (warp - 2 < kWorkers) {
+  } else {
     const int quarter = warp & 3;  // the TMEM lanes this warp may read
     const int part = (warp - 2) >> 2;
-    constexpr int kCols = BN / (kWorkers / 4);  // columns a warp finishes, 32 at a time
+    constexpr int kCols = BN / (kEpilogueWarps / 4);  // columns a warp finishes, 32 at a time
     unsigned char* buf = smem + kStages * Sh::kStageBytes + (warp - 2) * 2 * kStoreBytes;
     int turn = 0, which = 0;
     for (Walk w(args, unit, gridDim.x / CG); w.more(); w.next(args, unit), ++turn) {
