@@ -27,6 +27,9 @@ Modules:
                   down).
 * ``phases``      the reduce-scatter and all-gather phases of the ring run
                   alone (ReduceScatter, AllGather), with a predictor.
+* ``replica``     the operators of a replica (layer norm, linear layer,
+                  distillation) and their gradients in 64 bits; its pins
+                  are in ``tests/test_replica_ops_host.py``.
 * ``closed_form`` the order-free definition (float64 / exact integers) and
                   the error bounds it is compared under.
 
