@@ -31,6 +31,7 @@
 #include <mutex>
 
 #include "ops_common.cuh"
+#include "ops_rows.h"
 
 namespace vrccl {
 namespace {
@@ -49,6 +50,7 @@ struct NormArgs {
   int ptype;
   bool wideParams;  // gamma and beta start on 16-byte boundaries
   int stages, teams;
+  unsigned cutX, cutDy;  // cutRows of x and dy
   float eps;
 };
 
@@ -140,26 +142,6 @@ constexpr long long kRowWaitCycles = 3000000000ll, kDrainCycles = 200000000ll;  
 
 __device__ int gNormStatus;  // vrcclResult_t of the first device-side failure
 
-// Where a row's bytes lie and which of them a bulk copy may take: 16-byte
-// blocks that lie inside the matrix's own bytes, first row's start to last
-// row's end. A row on no 16-byte boundary shares its first and last block with
-// the gap before and after it, which is copied and ignored; the few elements in
-// blocks that the matrix's ends cut are copied one by one (edges).
-struct Window {
-  uintptr_t row, lo, hi;
-};
-__device__ __forceinline__ Window window(const void* p, size_t ld, size_t row, size_t rows, int cols, int E) {
-  Window w;
-  const uintptr_t base = (uintptr_t)p;
-  w.row = base + row * ld * E;
-  const uintptr_t end = w.row + (uintptr_t)cols * E;
-  w.lo = w.row & ~(uintptr_t)15;
-  w.hi = (end + 15) & ~(uintptr_t)15;
-  if (row == 0 && w.lo < base) w.lo += 16;
-  if (row == rows - 1 && w.hi > end) w.hi -= 16;
-  if (w.hi < w.lo) w.hi = w.lo;
-  return w;
-}
 __host__ __device__ constexpr int slotBytes(int cols, int E) { return ((cols * E + 15) / 16 + 1) * 16; }
 
 // The 16 elements of thread t of a team of T: element q is column
@@ -172,30 +154,31 @@ struct Team {
   using S = typename Ty<DT>::S;
 
   static __device__ __forceinline__ void fetch(unsigned char* slot, const void* p, size_t ld, size_t row, size_t rows,
-                                               int cols, unsigned long long* bar, unsigned long long policy) {
+                                               int cols, unsigned cut, unsigned long long* bar, unsigned long long policy) {
     if constexpr (VEC) {
       bulkLoadOnce(slot, static_cast<const char*>(p) + row * ld * E, cols * E, bar, policy);
       return;
     }
-    const Window w = window(p, ld, row, rows, cols, E);
+    const Window w = rowWindow((uintptr_t)p, ld, row, rows, cols, E, cut);
     if (w.hi > w.lo) bulkLoadOnce(slot + (w.lo - (w.row & ~(uintptr_t)15)), (const void*)w.lo, w.hi - w.lo, bar, policy);
   }
-  // What a bulk copy may not take of a row (see Window), copied by the thread that is about to announce it: its arrival
+  // What a bulk copy may not take of a row (Window), copied by the thread that is about to announce it: its arrival
   // at the row's barrier makes them visible with the rest.
   static __device__ __forceinline__ void edges(unsigned char* slot, const void* p, size_t ld, size_t row, size_t rows,
-                                               int cols) {
+                                               int cols, unsigned cut) {
     if constexpr (!VEC) {
-      if (row != 0 && row != rows - 1) return;
-      const Window w = window(p, ld, row, rows, cols, E);
+      if (!maybeCut(row, rows, cut)) return;
+      const Window w = rowWindow((uintptr_t)p, ld, row, rows, cols, E, cut);
       S* v = reinterpret_cast<S*>(slot + (w.row & 15));
-      for (uintptr_t at = w.row; at < w.lo && at < w.row + (uintptr_t)cols * E; at += E) v[(at - w.row) / E] = *(const S*)at;
-      for (uintptr_t at = max(w.hi, w.row); at < w.row + (uintptr_t)cols * E; at += E) v[(at - w.row) / E] = *(const S*)at;
+      for (uintptr_t at = w.row; at < w.headEnd(); at += E) v[(at - w.row) / E] = *(const S*)at;
+      for (uintptr_t at = w.tailBegin(); at < w.end; at += E) v[(at - w.row) / E] = *(const S*)at;
       fenceProxyAsync();  // a later row's copy into this slot comes after these writes
     }
   }
-  static __device__ __forceinline__ unsigned fetchBytes(const void* p, size_t ld, size_t row, size_t rows, int cols) {
+  static __device__ __forceinline__ unsigned fetchBytes(const void* p, size_t ld, size_t row, size_t rows, int cols,
+                                                    unsigned cut) {
     if constexpr (VEC) return cols * E;
-    const Window w = window(p, ld, row, rows, cols, E);
+    const Window w = rowWindow((uintptr_t)p, ld, row, rows, cols, E, cut);
     return w.hi - w.lo;
   }
   // Elements FROM .. FROM + N of the thread's 16 (whole vectors).
@@ -349,9 +332,9 @@ __global__ void __launch_bounds__(512) normForwardTeams(const __grid_constant__ 
   }
   auto refill = [&](int s, size_t row) {
     if (row >= a.rows) return;
-    M::edges(mine + (size_t)s * slot, a.x, a.ldx, row, a.rows, cols);
-    expectBytes(&bar[s], M::fetchBytes(a.x, a.ldx, row, a.rows, cols));
-    M::fetch(mine + (size_t)s * slot, a.x, a.ldx, row, a.rows, cols, &bar[s], policy);
+    M::edges(mine + (size_t)s * slot, a.x, a.ldx, row, a.rows, cols, a.cutX);
+    expectBytes(&bar[s], M::fetchBytes(a.x, a.ldx, row, a.rows, cols, a.cutX));
+    M::fetch(mine + (size_t)s * slot, a.x, a.ldx, row, a.rows, cols, a.cutX, &bar[s], policy);
   };
   if (t == 0)
     for (int s = 0; s < stages; ++s) refill(s, first + s * stride);
@@ -492,11 +475,11 @@ __global__ void __launch_bounds__(512) normBackwardTeams(const __grid_constant__
   auto refill = [&](int s, size_t row) {
     if (row >= a.rows) return;
     unsigned char* q = mine + (size_t)s * 2 * slot;
-    M::edges(q, a.x, a.ldx, row, a.rows, cols);
-    M::edges(q + slot, a.dy, a.lddy, row, a.rows, cols);
-    expectBytes(&bar[s], M::fetchBytes(a.x, a.ldx, row, a.rows, cols) + M::fetchBytes(a.dy, a.lddy, row, a.rows, cols));
-    M::fetch(q, a.x, a.ldx, row, a.rows, cols, &bar[s], policy);
-    M::fetch(q + slot, a.dy, a.lddy, row, a.rows, cols, &bar[s], policy);
+    M::edges(q, a.x, a.ldx, row, a.rows, cols, a.cutX);
+    M::edges(q + slot, a.dy, a.lddy, row, a.rows, cols, a.cutDy);
+    expectBytes(&bar[s], M::fetchBytes(a.x, a.ldx, row, a.rows, cols, a.cutX) + M::fetchBytes(a.dy, a.lddy, row, a.rows, cols, a.cutDy));
+    M::fetch(q, a.x, a.ldx, row, a.rows, cols, a.cutX, &bar[s], policy);
+    M::fetch(q + slot, a.dy, a.lddy, row, a.rows, cols, a.cutDy, &bar[s], policy);
   };
   if (t == 0)
     for (int s = 0; s < stages; ++s) refill(s, first + s * stride);
@@ -799,9 +782,9 @@ __global__ void __launch_bounds__(T, 1) normForwardWide(const __grid_constant__ 
   }
   auto refill = [&](int s, size_t row) {
     if (row >= a.rows) return;
-    M::edges(ring + (size_t)s * slot, a.x, a.ldx, row, a.rows, cols);
-    expectBytes(&full[s], M::fetchBytes(a.x, a.ldx, row, a.rows, cols));
-    M::fetch(ring + (size_t)s * slot, a.x, a.ldx, row, a.rows, cols, &full[s], policy);
+    M::edges(ring + (size_t)s * slot, a.x, a.ldx, row, a.rows, cols, a.cutX);
+    expectBytes(&full[s], M::fetchBytes(a.x, a.ldx, row, a.rows, cols, a.cutX));
+    M::fetch(ring + (size_t)s * slot, a.x, a.ldx, row, a.rows, cols, a.cutX, &full[s], policy);
   };
   if (t == 0)
     for (int s = 0; s < stages; ++s) refill(s, blockIdx.x + s * stride);
@@ -908,11 +891,11 @@ __global__ void __launch_bounds__(T, 1) normBackwardWide(const __grid_constant__
   auto refill = [&](int s, size_t row) {
     if (row >= a.rows) return;
     unsigned char* q = ring + (size_t)s * 2 * slot;
-    M::edges(q, a.x, a.ldx, row, a.rows, cols);
-    M::edges(q + slot, a.dy, a.lddy, row, a.rows, cols);
-    expectBytes(&full[s], M::fetchBytes(a.x, a.ldx, row, a.rows, cols) + M::fetchBytes(a.dy, a.lddy, row, a.rows, cols));
-    M::fetch(q, a.x, a.ldx, row, a.rows, cols, &full[s], policy);
-    M::fetch(q + slot, a.dy, a.lddy, row, a.rows, cols, &full[s], policy);
+    M::edges(q, a.x, a.ldx, row, a.rows, cols, a.cutX);
+    M::edges(q + slot, a.dy, a.lddy, row, a.rows, cols, a.cutDy);
+    expectBytes(&full[s], M::fetchBytes(a.x, a.ldx, row, a.rows, cols, a.cutX) + M::fetchBytes(a.dy, a.lddy, row, a.rows, cols, a.cutDy));
+    M::fetch(q, a.x, a.ldx, row, a.rows, cols, a.cutX, &full[s], policy);
+    M::fetch(q + slot, a.dy, a.lddy, row, a.rows, cols, a.cutDy, &full[s], policy);
   };
   if (t == 0)
     for (int s = 0; s < stages; ++s) refill(s, blockIdx.x + s * stride);
@@ -1329,6 +1312,7 @@ extern "C" vrcclResult_t vrcclLayerNormForward(const void* x, size_t ldx, const 
   a.mean = mean;
   a.rstd = rstd;
   a.ldx = ldx;
+  a.cutX = cutRows(ldx, E);
   a.ldy = ldy;
   a.rows = rows;
   a.cols = (int)cols;
@@ -1387,7 +1371,9 @@ extern "C" vrcclResult_t vrcclLayerNormBackward(const void* dy, size_t lddy, con
   a.rstd = const_cast<float*>(rstd);
   a.partial = weights ? static_cast<float*>(workspace) : nullptr;
   a.ldx = ldx;
+  a.cutX = cutRows(ldx, E);
   a.lddy = lddy;
+  a.cutDy = cutRows(lddy, E);
   a.ldy = lddx;
   a.rows = rows;
   a.cols = (int)cols;

@@ -1,0 +1,59 @@
+"""Address arithmetic of the operators' rows (csrc/ops_rows.h), compiled for
+the host: what a row's bulk copy takes."""
+import ctypes
+import os
+import shutil
+import subprocess
+
+import pytest
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "ring_allreduce_reduction_gb300", "csrc")
+
+SOURCE = r"""
+#include "ops_rows.h"
+using namespace vrccl;
+extern "C" void rowWindowOf(uintptr_t base, size_t ld, size_t row, size_t rows, size_t cols, size_t elem, uintptr_t* out) {
+  const unsigned cut = cutRows(ld, elem);
+  const Window w = rowWindow(base, ld, row, rows, cols, elem, cut);
+  out[0] = w.row; out[1] = w.end; out[2] = w.lo; out[3] = w.hi;
+  out[4] = w.headEnd(); out[5] = w.tailBegin(); out[6] = maybeCut(row, rows, cut);
+}
+"""
+
+
+@pytest.fixture(scope="module")
+def rows_lib(tmp_path_factory):
+    d = tmp_path_factory.mktemp("rows")
+    (d / "rows.cc").write_text(SOURCE)
+    cxx = shutil.which("g++") or shutil.which("c++")
+    assert cxx, "the library's build needs a host compiler too"
+    subprocess.run([cxx, "-std=c++17", "-O1", "-shared", "-fPIC", f"-I{CSRC}", str(d / "rows.cc"), "-o", str(d / "rows.so")],
+                   check=True)
+    return ctypes.CDLL(str(d / "rows.so"))
+
+
+@pytest.mark.parametrize("elem", [2, 4])
+def test_copies_of_short_rows_stay_inside_the_matrix(rows_lib, elem):
+    """Every copied 16-byte block lies between the matrix's first and last
+    byte, and copy and single elements together make up the row."""
+    fn = rows_lib.rowWindowOf
+    fn.argtypes = [ctypes.c_size_t] * 6 + [ctypes.POINTER(ctypes.c_size_t)]
+    out = (ctypes.c_size_t * 7)()
+    for skew in range(0, 16, elem):
+        base = 4096 + skew
+        for cols in range(1, 20):
+            for ld in (cols, cols + 1, cols + 3, cols + 8):
+                for rows in (1, 2, 3, 9, 17):
+                    last = base + ((rows - 1) * ld + cols) * elem
+                    for row in range(rows):
+                        fn(base, ld, row, rows, cols, elem, out)
+                        at, end, lo, hi, head, tail, cut = out
+                        where = (skew, cols, ld, rows, row)
+                        assert (at, end) == (base + row * ld * elem, base + (row * ld + cols) * elem), where
+                        assert lo % 16 == 0 and hi % 16 == 0 and lo <= hi, where
+                        assert lo == hi or (base <= lo and hi <= last), where
+                        copied = set(range(max(lo, at), min(hi, end)))
+                        single = list(range(at, head)) + list(range(tail, end))
+                        assert len(single) == len(set(single)) and not copied & set(single), where
+                        assert copied | set(single) == set(range(at, end)), where
+                        assert cut or not single, where
