@@ -636,7 +636,9 @@ vrcclResult_t vrcclLinearBackward(const void* dy, size_t lddy, const void* z, si
 
 /* vrcclReplicaGetAsyncError -- vrcclSuccess, or vrcclTimeout after an
  * operator's kernel on the current device gave up a wait (its outputs are
- * then undefined). Waits for the device's work. */
+ * then undefined). Waits for the device's work on every stream (so not while
+ * one is being captured). The status is the device's, of the whole process,
+ * and is not cleared: once vrcclTimeout, every later query reports it. */
 vrcclResult_t vrcclReplicaGetAsyncError(vrcclResult_t* asyncErr);
 
 /* Most teacher entries a row of the distillation loss may have. */

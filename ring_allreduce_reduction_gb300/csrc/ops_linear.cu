@@ -1655,7 +1655,9 @@ extern "C" vrcclResult_t vrcclLinearBackward(const void* dy, size_t lddy, const 
 extern "C" vrcclResult_t vrcclReplicaGetAsyncError(vrcclResult_t* asyncErr) {
   if (!asyncErr) return vrcclInvalidArgument;
   int code = 0, norm = 0;
-  if (cudaMemcpyFromSymbol(&code, gLinearStatus, sizeof(code)) != cudaSuccess || normStatus(&norm) != cudaSuccess) {
+  // (the copies alone run on the legacy default stream, which does not wait for non-blocking ones)
+  if (cudaDeviceSynchronize() != cudaSuccess ||
+      cudaMemcpyFromSymbol(&code, gLinearStatus, sizeof(code)) != cudaSuccess || normStatus(&norm) != cudaSuccess) {
     cudaGetLastError();
     return vrcclCudaError;
   }
