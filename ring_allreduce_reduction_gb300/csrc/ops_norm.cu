@@ -271,23 +271,24 @@ __device__ __forceinline__ void teamSync(int team) {
   else
     asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(T) : "memory");
 }
-// Sets *dead when the copy has not come after a time in which it must have.
-__device__ __forceinline__ void waitRow(unsigned long long* bar, unsigned parity, int* dead,
+// Sets *dead (givenUpWord) when the copy has not come after a time in which it must have.
+__device__ __forceinline__ void waitRow(unsigned long long* bar, unsigned parity, int* dead, int turn,
                                         long long limit = kRowWaitCycles) {
   if (mbarTryWait(bar, parity)) return;
   const long long t0 = clock64();
   while (!mbarTryWait(bar, parity))
     if (clock64() - t0 > limit) {
-      *reinterpret_cast<volatile int*>(dead) = 1;
+      *reinterpret_cast<volatile int*>(dead) = givenUpWord(turn);
       return;
     }
 }
 // Given up with the ring at (stage, round): records it, and lets no copy that
 // is in flight land after the block has gone.
-__device__ __noinline__ void abandon(unsigned long long* full, int stages, int stage, int round, bool first, int* dead) {
+__device__ __noinline__ void abandon(unsigned long long* full, int stages, int stage, int round, bool first, int* dead,
+                                     int turn) {
   if (!first) return;
   atomicCAS(&gNormStatus, 0, (int)vrcclTimeout);
-  for (int s = 0; s < stages; ++s) waitRow(&full[s], (round + (s < stage ? 1 : 0)) & 1, dead, kDrainCycles);
+  for (int s = 0; s < stages; ++s) waitRow(&full[s], (round + (s < stage ? 1 : 0)) & 1, dead, turn, kDrainCycles);
 }
 __device__ __forceinline__ void expectBytes(unsigned long long* bar, unsigned bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smemAddr(bar)), "r"(bytes) : "memory");
@@ -360,13 +361,13 @@ __global__ void __launch_bounds__(512) normForwardTeams(const __grid_constant__ 
   const float joinCount = (lane & 15) < warps ? warpCount(lane & 15) : 0.f, joinInv = joinCount > 0.f ? 1.f / joinCount : 0.f;
   teamSync<T>(team);
   int stage = 0, round = 0, turn = 0;
-  for (size_t row = first; row < a.rows; row += 2 * stride) {
+  for (size_t row = first; row < a.rows; row += 2 * stride, turn ^= 1) {
     const bool two = row + stride < a.rows;
     float f[2][kTeamElems];
-    waitRow(&bar[stage], round & 1, dead);
+    waitRow(&bar[stage], round & 1, dead, turn);
     M::take(mine + (size_t)stage * slot, a.x, a.ldx, row, a.rows, cols, t, f[0]);
     if (two) {
-      waitRow(&bar[stage + 1], round & 1, dead);
+      waitRow(&bar[stage + 1], round & 1, dead, turn);
       M::take(mine + (size_t)(stage + 1) * slot, a.x, a.ldx, row + stride, a.rows, cols, t, f[1]);
     } else {
 #pragma unroll
@@ -405,11 +406,10 @@ __global__ void __launch_bounds__(512) normForwardTeams(const __grid_constant__ 
       s[r] = q.x + q.y;
     }
     const float squares = sumTwo(s[0], s[1], high);
-    turn ^= 1;
     if ((lane & 15) == 0) red[team][turn][high][t >> 5] = make_float2(both, squares);
     teamSync<T>(team);
-    if (*reinterpret_cast<volatile int*>(dead)) {
-      abandon(bar, stages, stage, round, t == 0, dead);
+    if (givenUp(*reinterpret_cast<volatile int*>(dead), turn)) {
+      abandon(bar, stages, stage, round, t == 0, dead, turn);
       break;
     }
     if (t == 0) {
@@ -502,9 +502,9 @@ __global__ void __launch_bounds__(512) normBackwardTeams(const __grid_constant__
   }
   teamSync<T>(team);
   int stage = 0, round = 0, turn = 0;
-  for (size_t row = first; row < a.rows; row += stride) {
+  for (size_t row = first; row < a.rows; row += stride, turn ^= 1) {
     const float mean = nextMean, rstd = nextRstd;
-    waitRow(&bar[stage], round & 1, dead);
+    waitRow(&bar[stage], round & 1, dead, turn);
     const unsigned char* q = mine + (size_t)stage * 2 * slot;
     F2 xh[NP], gd[NP];
     float2 s;
@@ -529,11 +529,10 @@ __global__ void __launch_bounds__(512) normBackwardTeams(const __grid_constant__
       s = make_float2(u.x + u.y, w.x + w.y);
     }
     const float part = sumTwo(s.x, s.y, lane >= 16);
-    turn ^= 1;
     if ((lane & 15) == 0) reinterpret_cast<float*>(&red[team][turn][t >> 5])[lane >> 4] = part;
     teamSync<T>(team);
-    if (*reinterpret_cast<volatile int*>(dead)) {
-      abandon(bar, stages, stage, round, t == 0, dead);
+    if (givenUp(*reinterpret_cast<volatile int*>(dead), turn)) {
+      abandon(bar, stages, stage, round, t == 0, dead, turn);
       break;
     }
     if (t == 0) refill(stage, row + stages * stride);
@@ -800,8 +799,8 @@ __global__ void __launch_bounds__(T, 1) normForwardWide(const __grid_constant__ 
   const float joinCount = lane < warps ? warpCount(lane) : 0.f, joinInv = joinCount > 0.f ? 1.f / joinCount : 0.f;
   __syncthreads();
   int stage = 0, round = 0, turn = 0;
-  for (size_t row = blockIdx.x; row < a.rows; row += stride) {
-    waitRow(&full[stage], round & 1, &dead);
+  for (size_t row = blockIdx.x; row < a.rows; row += stride, turn ^= 1) {
+    waitRow(&full[stage], round & 1, &dead, turn);
     F2 x[NP];
     float s;
     {
@@ -828,11 +827,10 @@ __global__ void __launch_bounds__(T, 1) normForwardWide(const __grid_constant__ 
       }
       squares = warpSum(q);
     }
-    turn ^= 1;
     if (lane == 0) red[turn][t >> 5] = make_float2(s, squares);
     __syncthreads();
-    if (*reinterpret_cast<volatile int*>(&dead)) {
-      abandon(full, stages, stage, round, t == 0, &dead);
+    if (givenUp(*reinterpret_cast<volatile int*>(&dead), turn)) {
+      abandon(full, stages, stage, round, t == 0, &dead, turn);
       break;
     }
     if (t == 0) refill(stage, row + stages * stride);
@@ -907,9 +905,9 @@ __global__ void __launch_bounds__(T, 1) normBackwardWide(const __grid_constant__
   letNextIn();
   __syncthreads();
   int stage = 0, round = 0, turn = 0, behind = 0;
-  for (size_t row = blockIdx.x; row < a.rows; row += stride) {
+  for (size_t row = blockIdx.x; row < a.rows; row += stride, turn ^= 1) {
     const float mean = a.mean[row], rstd = a.rstd[row];
-    waitRow(&full[stage], round & 1, &dead);
+    waitRow(&full[stage], round & 1, &dead, turn);
     const unsigned char* q = ring + (size_t)stage * 2 * slot;
     const F2 scale = pair(rstd, rstd), shift = pair(-mean, -mean);
     F2 sg = 0, sx = 0;
@@ -935,11 +933,10 @@ __global__ void __launch_bounds__(T, 1) normBackwardWide(const __grid_constant__
     chunks<kChunk>(sums);
     const float2 u = split(sg), w = split(sx);
     const float2 s = warpSum2(make_float2(u.x + u.y, w.x + w.y));
-    turn ^= 1;
     if (lane == 0) red[turn][t >> 5] = s;
     __syncthreads();
-    if (*reinterpret_cast<volatile int*>(&dead)) {
-      abandon(full, stages, stage, round, t == 0, &dead);
+    if (givenUp(*reinterpret_cast<volatile int*>(&dead), turn)) {
+      abandon(full, stages, stage, round, t == 0, &dead, turn);
       break;
     }
     // all are through with the row before this one: its stage takes the row `stages` after it

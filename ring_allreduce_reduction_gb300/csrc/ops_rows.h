@@ -1,6 +1,6 @@
-// Where the bytes of a matrix's rows lie: address arithmetic that the
-// operators' kernels and their host checks share. Plain C++, so that it can be
-// tested without a GPU.
+// Where the bytes of a matrix's rows lie, and when a team of threads leaves
+// its loop over them: arithmetic of the operators' kernels in plain C++, so
+// that it can be tested without a GPU.
 #pragma once
 
 #include <cstddef>
@@ -44,5 +44,14 @@ VRCCL_HD Window rowWindow(uintptr_t base, size_t ld, size_t row, size_t rows, un
   }
   return w;
 }
+
+// A team's word for a wait that was given up says in which turn it was, by the
+// turn's parity (0 or 1). A turn has one barrier, after which every thread
+// reads the word: it finds what was written before the barrier, or what a
+// faster thread has already written in the next turn (not in a later one: that
+// is another barrier on). The latter is the next turn's to act on, or the
+// threads of a team would leave their loop at different barriers.
+VRCCL_HD int givenUpWord(int turn) { return turn + 1; }
+VRCCL_HD bool givenUp(int word, int turn) { return word == givenUpWord(turn); }
 
 }  // namespace vrccl

@@ -1,5 +1,5 @@
-"""Address arithmetic of the operators' rows (csrc/ops_rows.h), compiled for
-the host: what a row's bulk copy takes."""
+"""Arithmetic of the operators' rows (csrc/ops_rows.h), compiled for the host:
+what a row's bulk copy takes, and when a team gives up."""
 import ctypes
 import os
 import shutil
@@ -18,6 +18,8 @@ extern "C" void rowWindowOf(uintptr_t base, size_t ld, size_t row, size_t rows, 
   out[0] = w.row; out[1] = w.end; out[2] = w.lo; out[3] = w.hi;
   out[4] = w.headEnd(); out[5] = w.tailBegin(); out[6] = maybeCut(row, rows, cut);
 }
+extern "C" int wordOf(int turn) { return givenUpWord(turn); }
+extern "C" int leaves(int word, int turn) { return givenUp(word, turn); }
 """
 
 
@@ -57,3 +59,14 @@ def test_copies_of_short_rows_stay_inside_the_matrix(rows_lib, elem):
                         assert len(single) == len(set(single)) and not copied & set(single), where
                         assert copied | set(single) == set(range(at, end)), where
                         assert cut or not single, where
+
+
+def test_a_team_gives_up_at_one_barrier(rows_lib):
+    """Whatever a faster thread has written in the next turn, a thread that
+    reads the word late stays with it; at that turn's barrier all leave."""
+    for turn in (0, 1):  # a turn's parity
+        word = 0
+        assert not rows_lib.leaves(word, turn)  # the fast thread goes on
+        word = rows_lib.wordOf(turn ^ 1)  # and gives up the next turn's wait
+        assert not rows_lib.leaves(word, turn)  # the slow one reads only now
+        assert rows_lib.leaves(word, turn ^ 1)  # both, past the next barrier
