@@ -686,8 +686,8 @@ __global__ void __launch_bounds__(kProductThreads, 1) productKernel(const __grid
         for (int i = 0; i < (kCols + 63) / 64; ++i) bias[i] = biasPair<DT>(a, n0 + i * 64, lane);
       Residual<DT> residual;
       if (a.residual && m0 < a.M && n0 < a.N) residual.load(a, m0, n0, lane);
-      bool ok = lane != 0 || waitBar(&accFull[acc], use & 1, dead);
-      if (!__all_sync(0xffffffffu, ok)) break;
+      // (every lane waits: the barrier orders the products before the loads of the thread that has seen it)
+      if (!__all_sync(0xffffffffu, waitBar(&accFull[acc], use & 1, dead))) break;
       tcFenceAfter();
       const uint32_t from = tmem + ((uint32_t)(quarter * 32) << 16) + acc * BN + part * kCols;
       if (m0 < a.M) {

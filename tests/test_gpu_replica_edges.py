@@ -33,3 +33,24 @@ def test_async_error_waits_for_every_stream(torch, v):  # noqa: F811
         torch.cuda._sleep(400_000_000)  # a fifth of a second
     assert v.vrcclReplicaGetAsyncError() == 0
     assert side.query()
+
+
+# ------------------------------------------------------------ linear layer
+
+@pytest.mark.parametrize("rows,outs,ins", [(4096, 4096, 256), (2048, 1536, 64), (5000, 136, 136)])
+def test_linear_tiles_in_a_row_give_the_same_bits(torch, v, rows, outs, ins):  # noqa: F811
+    """Every lane of an epilogue reads finished products: many short tiles a
+    block, again and again, against the first pass and against 64 bits."""
+    g = torch.Generator("cuda").manual_seed(1)
+    x, w = (torch.randn(n, ins, generator=g, device="cuda").bfloat16() for n in (rows, outs))
+    y = torch.empty(rows, outs, device="cuda", dtype=torch.bfloat16)
+    first = None
+    for _ in range(20):
+        y.fill_(float("nan"))
+        v.vrcclLinearForward(x, w, None, None, y, None, rows, outs, ins, "bfloat16")
+        first = y.clone() if first is None else first
+        assert torch.equal(y, first)
+    X, W = x.double(), w.double()
+    want = X @ W.t()
+    off = (y.double() - want).abs() - U["bfloat16"] * 1.01 * want.abs() - (ins + 16) * 2 * EPS * (X.abs() @ W.abs().t())
+    assert off.max().item() <= 0
