@@ -118,10 +118,13 @@ __device__ __forceinline__ F2 slope(F2 z) {
   // y = z s(w): y' = s + z s (1 - s) w'
   if constexpr (ACT == vrcclActGeluTanh || ACT == vrcclActSilu) {
     const F2 s = logisticOf<ACT>(z);
-    F2 zw = z;
-    if constexpr (ACT == vrcclActGeluTanh)
-      zw = mul2(z, fma2(mul2(z, z), both(kTanhScale * 3.f * 0.044715f), both(kTanhScale)));
-    return fma2(mul2(s, fma2(s, both(-1.f), both(1.f))), zw, s);
+    const F2 bell = mul2(mul2(s, fma2(s, both(-1.f), both(1.f))), z);  // exactly 0 long before z^2 is large
+    if constexpr (ACT == vrcclActGeluTanh) {
+      const float2 q = split(mul2(z, z));  // held below infinity, which bell's 0 would make NaN of
+      const F2 zz = pair(fminf(q.x, 1e30f), fminf(q.y, 1e30f));
+      return fma2(bell, fma2(zz, both(kTanhScale * 3.f * 0.044715f), both(kTanhScale)), s);
+    }
+    return add2(bell, s);
   }
   return both(1.f);
 }

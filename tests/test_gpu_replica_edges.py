@@ -54,3 +54,26 @@ def test_linear_tiles_in_a_row_give_the_same_bits(torch, v, rows, outs, ins):  #
     want = X @ W.t()
     off = (y.double() - want).abs() - U["bfloat16"] * 1.01 * want.abs() - (ins + 16) * 2 * EPS * (X.abs() @ W.abs().t())
     assert off.max().item() <= 0
+
+
+@pytest.mark.parametrize("act", ["relu", "gelu", "gelu_tanh", "silu"])
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
+def test_linear_slope_of_large_arguments(torch, v, dtype, act):  # noqa: F811
+    """Every finite z has a finite slope: 0 or 1 once it is large, however its
+    powers overflow."""
+    top = float(torch.finfo(getattr(torch, dtype)).max)
+    z = np.array([s * m for m in (1.0, 9.0, 40.0, 3e3, 6e4, 1e9, 2e13, 1e15, 1e19, 3e19, 1e30, 3e38) if m <= top
+                  for s in (1, -1)] + [top, -top])
+    rows, n = 16, z.size
+    Z = Mat(torch, rows, n, dtype, np.tile(z, (rows, 1)))
+    dy = Mat(torch, rows, n, dtype, _rng(5).standard_normal((rows, n)))
+    db = torch.empty(n, device="cuda", dtype=getattr(torch, dtype))
+    ws = torch.empty(v.vrcclLinearWorkspace("backward", rows, n, 8, dtype, act), device="cuda", dtype=torch.uint8)
+    v.vrcclLinearBackward(dy.ptr, Z.ptr, None, None, None, None, db, rows, n, 8, dtype, act, ws, ws.numel())
+    z, D = Z.get()[0], dy.get()
+    with np.errstate(over="ignore", invalid="ignore"):
+        slope = np.where(z > 100, 1.0, np.where(z < -100, 0.0, o.slope(np.clip(z, -100, 100), act)))
+    want = (D * slope).sum(0)
+    # as in _linear_back, with arguments no larger than where the slope is still moving
+    es = (32 * EPS * np.abs(D) * (1 + np.minimum(np.abs(z), 50))).sum(0)
+    _close(_host(db), want, U[dtype] * np.abs(want) * 1.01 + es + (rows + 16) * EPS * np.abs(D * slope).sum(0) + TINY[dtype], "dbias")
