@@ -77,3 +77,34 @@ def test_linear_slope_of_large_arguments(torch, v, dtype, act):  # noqa: F811
     # as in _linear_back, with arguments no larger than where the slope is still moving
     es = (32 * EPS * np.abs(D) * (1 + np.minimum(np.abs(z), 50))).sum(0)
     _close(_host(db), want, U[dtype] * np.abs(want) * 1.01 + es + (rows + 16) * EPS * np.abs(D * slope).sum(0) + TINY[dtype], "dbias")
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
+def test_linear_gelu_is_rounded_once(torch, v, dtype):  # noqa: F811
+    """gelu and its slope to one rounding of the type, in the tail too.
+
+    Phi(-x) = exp(-x^2/2) R(x): the exponent, of at most 26 binary digits
+    here (|z| <= 6), is rounded twice (52 EPS of it, times log 2, 36); the two
+    special functions, the reciprocal and the polynomial add some 28 EPS.
+    The slope adds a product with the same density."""
+    u, some = U[dtype], 64 * EPS
+    grid = torch.linspace(-6, 6, 4001, dtype=torch.float64).to(getattr(torch, dtype)).unique()
+    z = grid.double().numpy()
+    n = z.size
+    # Phi of either sign without cancellation, by its definition in 64 bits
+    phi = 0.5 * torch.special.erfc(torch.as_tensor(-z / np.sqrt(2))).numpy()
+    dense = z * np.exp(-z * z / 2) / np.sqrt(2 * np.pi)
+    w = torch.zeros(n, 8, device="cuda", dtype=grid.dtype)
+    w[:, 0] = grid.cuda()
+    for rows in (1, 20, 300):
+        x, y = torch.zeros(rows, 8, device="cuda", dtype=grid.dtype), torch.empty(rows, n, device="cuda", dtype=grid.dtype)
+        x[:, 0] = 1
+        ws = torch.empty(max(256, v.vrcclLinearWorkspace("forward", rows, n, 8, dtype, "gelu")), device="cuda", dtype=torch.uint8)
+        v.vrcclLinearForward(x, w, None, None, y, None, rows, n, 8, dtype, "gelu", ws, ws.numel())
+        want = np.tile(z * phi, (rows, 1))
+        _close(_host(y), want, (u + some) * np.abs(want) + TINY[dtype] / 2, f"gelu, {rows} rows")
+    db = torch.empty(n, device="cuda", dtype=grid.dtype)
+    one = torch.ones(1, n, device="cuda", dtype=grid.dtype)
+    ws = torch.empty(v.vrcclLinearWorkspace("backward", 1, n, 8, dtype, "gelu"), device="cuda", dtype=torch.uint8)
+    v.vrcclLinearBackward(one, grid.cuda(), None, None, None, None, db, 1, n, 8, dtype, "gelu", ws, ws.numel())
+    _close(_host(db), phi + dense, u * np.abs(phi + dense) + 2 * some * (phi + np.abs(dense)) + TINY[dtype] / 2, "slope")
