@@ -649,10 +649,11 @@ vrcclResult_t vrcclReplicaGetAsyncError(vrcclResult_t* asyncErr);
  * its top logits: with temperature T, p = softmax(teacher / T) over a row's
  * kept entries and q = softmax(logits / T) over the vocabulary,
  *   loss = T^2 * sum over entries of p * (log p - log q[index]).
- * An entry is kept if its index lies in [0, vocab) and its logit is above
- * -inf; entries that share an index add up. A row without kept entries has
- * loss 0 (a padding position; its logits are not read). Masked student
- * logits may be -inf or the type's lowest value.
+ * An entry is kept if its index lies in [0, vocab) and its logit is not
+ * -inf; entries that share an index add up. A NaN is kept, so that it shows:
+ * the row's loss and the gradients of its entries are then NaN. A row without
+ * kept entries has loss 0 and gradient 0 (a padding position), whatever its
+ * logits hold. Masked student logits may be -inf or the type's lowest value.
  *   logits   [rows, vocab] of dtype.
  *   teacher  [rows, k] of teacherType;  index [rows, k] of indexType
  *            (vrcclInt32 or vrcclInt64), k <= VRCCL_DISTILL_MAX_K.

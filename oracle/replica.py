@@ -72,7 +72,7 @@ def linear_backward(dy, z, x, w, act):
 # ------------------------------------------------------------ distillation
 
 def _row(logits, teacher, index, T):
-    """(kept, p, log p, log q at every entry of the vocabulary) of one row."""
+    """(kept, p, log p, log q at every entry of the vocabulary) of one row; a NaN logit of the teacher's is kept."""
     kept = (index >= 0) & (index < logits.size) & ~(teacher == -np.inf)
     t = teacher[kept]
     t = (t - t.max(initial=-np.inf)) / T

@@ -2,7 +2,7 @@
 //
 // A row holds the student's logits s over the whole vocabulary and the
 // teacher's logits t at k of its entries. With temperature T, over the kept
-// entries j (index inside the vocabulary, t_j above -inf):
+// entries j (index inside the vocabulary, t_j not -inf; a NaN is kept, and shows):
 //
 //   p_j  = exp(t_j / T) / sum_i exp(t_i / T)
 //   q_v  = exp(s_v / T) / sum_u exp(s_u / T)
@@ -15,7 +15,8 @@
 // their sum would round away the fraction of a large logit. An entry whose
 // p_j is 0 in binary32 adds nothing, whatever q is there. A row without a kept
 // entry (a padding position) has loss 0 and gradient 0 whatever its logits
-// hold, and they are not read.
+// hold; forward reads none of them, backward the first few, which it asks for
+// before it knows.
 //
 // Both directions are bound by memory: forward reads the logits once (each
 // thread keeps a running maximum and a sum rescaled when the maximum grows,

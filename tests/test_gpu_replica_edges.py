@@ -5,7 +5,8 @@ import numpy as np
 import pytest
 
 from oracle import replica as o
-from test_gpu_replica_ops import EPS, FLOATS, TINY, U, Mat, _close, _host, _norm_check, _rng, torch, v  # noqa: F401
+from test_gpu_replica_ops import (EPS, FLOATS, TINY, U, Mat, _close, _distill_check, _distill_inputs, _host, _norm_check,  # noqa: F401
+                                  _rng, torch, v)  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -108,3 +109,18 @@ def test_linear_gelu_is_rounded_once(torch, v, dtype):  # noqa: F811
     ws = torch.empty(v.vrcclLinearWorkspace("backward", 1, n, 8, dtype, "gelu"), device="cuda", dtype=torch.uint8)
     v.vrcclLinearBackward(one, grid.cuda(), None, None, None, None, db, 1, n, 8, dtype, "gelu", ws, ws.numel())
     _close(_host(db), phi + dense, u * np.abs(phi + dense) + 2 * some * (phi + np.abs(dense)) + TINY[dtype] / 2, "slope")
+
+
+# ------------------------------------------------------------ distillation
+
+@pytest.mark.parametrize("ttype", FLOATS)
+@pytest.mark.parametrize("vocab", [700, 70001])
+def test_distill_nan_teacher_is_kept(torch, v, vocab, ttype):  # noqa: F811
+    """A NaN among the teacher's logits makes the row's loss and its entries' gradients NaN, and nothing else."""
+    s, t, idx = _distill_inputs(4, vocab, 6, 9)
+    t[1, 2] = np.nan
+    t[2, 0], idx[2, 0] = np.nan, -1  # (outside the vocabulary: not kept)
+    with np.errstate(invalid="ignore"):
+        loss, d = _distill_check(torch, v, s, t, idx, "float32", ttype)
+    assert np.array_equal(np.isnan(loss), [False, True, False, False])
+    assert np.array_equal(np.flatnonzero(np.isnan(d[1])), np.sort(idx[1])) and np.isfinite(d[[0, 2, 3]]).all()
