@@ -541,8 +541,11 @@ vrcclResult_t vrcclAllReduceNoAlloc(const void* const* sendbufs, void* const* re
  *
  * Errors of all of them: vrcclInvalidArgument (a null or misaligned pointer,
  * a row stride below the row's length, an enum or a size out of range, a
- * workspace that is too small, an output that overlaps an input other than
- * as the call allows); vrcclCudaError (launch failure).
+ * workspace that is too small, an output that overlaps an input or another
+ * output other than as the call allows); vrcclCudaError (launch failure).
+ * Matrices of one row stride in bytes may lie side by side in a wider buffer
+ * (column slices), and vectors between a matrix's rows; of two strides the
+ * whole address ranges may not meet.
  */
 
 /*

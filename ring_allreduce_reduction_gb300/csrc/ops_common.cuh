@@ -10,6 +10,7 @@
 #include <cstdint>
 
 #include "device_common.cuh"
+#include "ops_rows.h"
 
 namespace vrccl {
 
@@ -32,19 +33,6 @@ inline bool goodVector(const void* p, int elemSize) { return p && (uintptr_t)p %
 inline bool rowsAligned(const void* p, size_t ld, int elemSize) {
   return ((uintptr_t)p | (uintptr_t)(ld * elemSize)) % 16 == 0;
 }
-// Bytes of the matrix from its first element to its last.
-inline size_t spanBytes(size_t ld, size_t rows, size_t cols, int elemSize) {
-  return rows == 0 || cols == 0 ? 0 : ((rows - 1) * ld + cols) * elemSize;
-}
-// What a call reads or writes; nothing where p is NULL.
-struct Span {
-  const void* p;
-  size_t bytes;
-};
-inline bool overlap(const Span& a, const Span& b) {
-  return a.p && b.p && a.bytes && b.bytes && (uintptr_t)a.p < (uintptr_t)b.p + b.bytes &&
-         (uintptr_t)b.p < (uintptr_t)a.p + a.bytes;
-}
 // No output touches an input or another output. (An input that an output may
 // take the place of is left out by its caller where it does.)
 template <int O, int I>
@@ -59,7 +47,7 @@ inline bool apart(const Span (&out)[O], const Span (&in)[I]) {
 }
 // `in`, unless `out` lies in its place.
 inline Span unlessInPlace(const Span& in, size_t ldin, const void* out, size_t ldout) {
-  return in.p == out && ldin == ldout ? Span{nullptr, 0} : in;
+  return in.p == out && ldin == ldout ? vectorSpan(nullptr, 0) : in;
 }
 
 // A failed wait of the layer norm's kernels (each translation unit holds its own device-side word).

@@ -488,10 +488,10 @@ extern "C" vrcclResult_t vrcclDistillForward(const void* logits, size_t ldl, con
   }
   if (!goodDistill(logits, ldl, teacher, ldt, index, ldi, rows, vocab, k, dtype, teacherType, indexType))
     return vrcclInvalidArgument;
-  const Span out[] = {{loss, rows * 4}, {stats, rows * 8}};
-  const Span in[] = {{logits, spanBytes(ldl, rows, vocab, floatTypeSize(dtype))},
-                     {teacher, spanBytes(ldt, rows, k, floatTypeSize(teacherType))},
-                     {index, spanBytes(ldi, rows, k, indexType == vrcclInt64 ? 8 : 4)}};
+  const Span out[] = {vectorSpan(loss, rows * 4), vectorSpan(stats, rows * 8)};
+  const Span in[] = {matrixSpan(logits, ldl, rows, vocab, floatTypeSize(dtype)),
+                     matrixSpan(teacher, ldt, rows, k, floatTypeSize(teacherType)),
+                     matrixSpan(index, ldi, rows, k, indexType == vrcclInt64 ? 8 : 4)};
   if (!apart(out, in)) return vrcclInvalidArgument;
   DistillArgs a = distillArgs(logits, ldl, teacher, ldt, index, ldi, rows, vocab, k, teacherType, indexType, temperature);
   a.loss = loss;
@@ -528,12 +528,12 @@ extern "C" vrcclResult_t vrcclDistillBackward(const void* logits, size_t ldl, co
       !goodVector(stats, 8) || !goodVector(dloss, 4) || dlossStride >= kMaxExtent)
     return vrcclInvalidArgument;
   if (rows - 1 > (size_t(1) << 46) / std::max<size_t>(1, dlossStride)) return vrcclInvalidArgument;
-  const Span out[] = {{dlogits, spanBytes(ldd, rows, vocab, E)}};
-  const Span in[] = {unlessInPlace({logits, spanBytes(ldl, rows, vocab, E)}, ldl, dlogits, ldd),
-                     {teacher, spanBytes(ldt, rows, k, floatTypeSize(teacherType))},
-                     {index, spanBytes(ldi, rows, k, indexType == vrcclInt64 ? 8 : 4)},
-                     {stats, rows * 8},
-                     {dloss, ((rows - 1) * dlossStride + 1) * 4}};
+  const Span out[] = {matrixSpan(dlogits, ldd, rows, vocab, E)};
+  const Span in[] = {unlessInPlace(matrixSpan(logits, ldl, rows, vocab, E), ldl, dlogits, ldd),
+                     matrixSpan(teacher, ldt, rows, k, floatTypeSize(teacherType)),
+                     matrixSpan(index, ldi, rows, k, indexType == vrcclInt64 ? 8 : 4),
+                     vectorSpan(stats, rows * 8),
+                     matrixSpan(dloss, dlossStride, rows, 1, 4)};
   if (!apart(out, in)) return vrcclInvalidArgument;
   DistillArgs a = distillArgs(logits, ldl, teacher, ldt, index, ldi, rows, vocab, k, teacherType, indexType, temperature);
   a.stats = const_cast<float2*>(reinterpret_cast<const float2*>(stats));

@@ -1573,9 +1573,10 @@ extern "C" vrcclResult_t vrcclLinearForward(const void* x, size_t ldx, const voi
       (bias && !goodVector(bias, 2)) || (residual && !goodMatrix(residual, ldr, rows, outs, 2)) ||
       (z && !goodMatrix(z, ldz, rows, outs, 2)) || (workspace && !goodVector(workspace, 256)))
     return vrcclInvalidArgument;
-  const Span spanR = {residual, spanBytes(ldr, rows, outs, 2)}, spanZ = {z, spanBytes(ldz, rows, outs, 2)};
-  const Span out[] = {{y, spanBytes(ldy, rows, outs, 2)}, spanZ, {workspace, workspaceBytes}};
-  const Span in[] = {{x, spanBytes(ldx, rows, ins, 2)}, {w, spanBytes(ldw, outs, ins, 2)}, {bias, outs * 2}, unlessInPlace(spanR, ldr, y, ldy)};
+  const Span spanR = matrixSpan(residual, ldr, rows, outs, 2), spanZ = matrixSpan(z, ldz, rows, outs, 2);
+  const Span out[] = {matrixSpan(y, ldy, rows, outs, 2), spanZ, vectorSpan(workspace, workspaceBytes)};
+  const Span in[] = {matrixSpan(x, ldx, rows, ins, 2), matrixSpan(w, ldw, outs, ins, 2), vectorSpan(bias, outs * 2),
+                     unlessInPlace(spanR, ldr, y, ldy)};
   if (!apart(out, in) || overlap(spanZ, spanR) || overlap(out[2], spanR)) return vrcclInvalidArgument;
   cudaStream_t st = (cudaStream_t)stream;
   const bool apart = rowsAligned(x, ldx, 2) && rowsAligned(w, ldw, 2);
@@ -1647,9 +1648,10 @@ extern "C" vrcclResult_t vrcclLinearBackward(const void* dy, size_t lddy, const 
   if (!goodMatrix(dy, lddy, rows, outs, 2) || (acts && !goodMatrix(z, ldz, rows, outs, 2)) || (dw && !goodMatrix(x, ldx, rows, ins, 2)) ||
       (dx && !goodMatrix(w, ldw, outs, ins, 2)))
     return vrcclInvalidArgument;
-  const Span out[] = {{dx, spanBytes(lddx, rows, ins, 2)}, {dw, spanBytes(lddw, outs, ins, 2)}, {dbias, outs * 2}, {workspace, workspaceBytes}};
-  const Span in[] = {{dy, spanBytes(lddy, rows, outs, 2)}, {acts ? z : nullptr, spanBytes(ldz, rows, outs, 2)},
-                     {dw ? x : nullptr, spanBytes(ldx, rows, ins, 2)}, {dx ? w : nullptr, spanBytes(ldw, outs, ins, 2)}};
+  const Span out[] = {matrixSpan(dx, lddx, rows, ins, 2), matrixSpan(dw, lddw, outs, ins, 2), vectorSpan(dbias, outs * 2),
+                      vectorSpan(workspace, workspaceBytes)};
+  const Span in[] = {matrixSpan(dy, lddy, rows, outs, 2), matrixSpan(acts ? z : nullptr, ldz, rows, outs, 2),
+                     matrixSpan(dw ? x : nullptr, ldx, rows, ins, 2), matrixSpan(dx ? w : nullptr, ldw, outs, ins, 2)};
   if (!apart(out, in)) return vrcclInvalidArgument;
   size_t need = dbias ? biasBytes(rows, outs) : 0;
   if (dx || dw) need += acts ? packedBytes(rows, outs) : packNeed(dy, lddy, rows, outs);

@@ -1295,10 +1295,10 @@ extern "C" vrcclResult_t vrcclLayerNormForward(const void* x, size_t ldx, const 
   if ((gamma && !goodVector(gamma, PE)) || (beta && !goodVector(beta, PE)) || (mean && !goodVector(mean, 4)) ||
       (rstd && !goodVector(rstd, 4)))
     return vrcclInvalidArgument;
-  const Span out[] = {{y, spanBytes(ldy, rows, cols, E)}, {mean, rows * 4}, {rstd, rows * 4}};
-  const Span in[] = {unlessInPlace({x, spanBytes(ldx, rows, cols, E)}, ldx, y, ldy), {gamma, cols * PE}, {beta, cols * PE}};
-  if (!apart(out, in) || overlap(out[1], {x, spanBytes(ldx, rows, cols, E)}) ||
-      overlap(out[2], {x, spanBytes(ldx, rows, cols, E)}))
+  const Span out[] = {matrixSpan(y, ldy, rows, cols, E), vectorSpan(mean, rows * 4), vectorSpan(rstd, rows * 4)};
+  const Span spanX = matrixSpan(x, ldx, rows, cols, E);
+  const Span in[] = {unlessInPlace(spanX, ldx, y, ldy), vectorSpan(gamma, cols * PE), vectorSpan(beta, cols * PE)};
+  if (!apart(out, in) || overlap(out[1], spanX) || overlap(out[2], spanX))
     return vrcclInvalidArgument;
   const Shape s = normShape(rows, (int)cols, E, rowsAligned(x, ldx, E) && rowsAligned(y, ldy, E), true);
   NormArgs a = {};
@@ -1353,10 +1353,11 @@ extern "C" vrcclResult_t vrcclLayerNormBackward(const void* dy, size_t lddy, con
   const int blocks = normBlocks(rows, s);
   const size_t need = weights ? size_t(mostBlocks(rows, (int)cols)) * 2 * cols * sizeof(float) : 0;  // what the query says
   if (weights && (!goodVector(workspace, 16) || workspaceBytes < need)) return vrcclInvalidArgument;
-  const Span spanDy = {dy, spanBytes(lddy, rows, cols, E)}, spanX = {x, spanBytes(ldx, rows, cols, E)};
-  const Span other[] = {{dgamma, cols * PE}, {dbeta, cols * PE}, {workspace, need}};
-  const Span all[] = {{dx, spanBytes(lddx, rows, cols, E)}, other[0], other[1], other[2]};
-  const Span in[] = {{gamma, cols * PE}, {mean, rows * 4}, {rstd, rows * 4}, unlessInPlace(spanDy, lddy, dx, lddx), unlessInPlace(spanX, ldx, dx, lddx)};
+  const Span spanDy = matrixSpan(dy, lddy, rows, cols, E), spanX = matrixSpan(x, ldx, rows, cols, E);
+  const Span other[] = {vectorSpan(dgamma, cols * PE), vectorSpan(dbeta, cols * PE), vectorSpan(workspace, need)};
+  const Span all[] = {matrixSpan(dx, lddx, rows, cols, E), other[0], other[1], other[2]};
+  const Span in[] = {vectorSpan(gamma, cols * PE), vectorSpan(mean, rows * 4), vectorSpan(rstd, rows * 4),
+                     unlessInPlace(spanDy, lddy, dx, lddx), unlessInPlace(spanX, ldx, dx, lddx)};
   const Span matrices[] = {spanDy, spanX};
   if (!apart(all, in) || !apart(other, matrices)) return vrcclInvalidArgument;
   NormArgs a = {};

@@ -1,6 +1,6 @@
-// Where the bytes of a matrix's rows lie, and when a team of threads leaves
-// its loop over them: arithmetic of the operators' kernels in plain C++, so
-// that it can be tested without a GPU.
+// Where the bytes of a matrix's rows lie, which operands share any, and when a
+// team of threads leaves its loop over rows: arithmetic of the operators'
+// kernels and host checks in plain C++, so that it can be tested without a GPU.
 #pragma once
 
 #include <cstddef>
@@ -13,6 +13,29 @@
 #endif
 
 namespace vrccl {
+
+// What a call reads or writes: rows of `width` bytes, `pitch` apart (0: one run); nothing where p is NULL. bytes: from the
+// first to the last.
+struct Span {
+  const void* p;
+  size_t bytes, pitch, width;
+};
+inline Span vectorSpan(const void* p, size_t bytes) { return {p, bytes, 0, bytes}; }
+inline Span matrixSpan(const void* p, size_t ld, size_t rows, size_t cols, size_t elemSize) {
+  if (rows == 0 || cols == 0) return vectorSpan(p, 0);
+  return {p, ((rows - 1) * ld + cols) * elemSize, rows > 1 ? ld * elemSize : 0, cols * elemSize};
+}
+// Whether two of them share a byte. Operands of one pitch may lie side by side
+// (column slices of a wider buffer), a run between the rows of a matrix; of two
+// pitches the whole ranges count.
+inline bool overlap(const Span& a, const Span& b) {
+  const uintptr_t pa = (uintptr_t)a.p, pb = (uintptr_t)b.p;
+  if (!a.p || !b.p || !a.bytes || !b.bytes || pa >= pb + b.bytes || pb >= pa + a.bytes) return false;
+  const size_t pitch = a.pitch ? a.pitch : b.pitch;
+  if (pitch == 0 || (a.pitch && b.pitch && a.pitch != b.pitch)) return true;
+  const size_t from = pb >= pa ? (pb - pa) % pitch : (pitch - (pa - pb) % pitch) % pitch;  // where b's rows start in a's pitch
+  return from < a.width || from + b.width > pitch;
+}
 
 // Where a row's bytes lie and which of them a bulk copy may take: the 16-byte
 // blocks it touches that lie inside the matrix's own bytes, first row's start

@@ -124,3 +124,97 @@ def test_distill_nan_teacher_is_kept(torch, v, vocab, ttype):  # noqa: F811
         loss, d = _distill_check(torch, v, s, t, idx, "float32", ttype)
     assert np.array_equal(np.isnan(loss), [False, True, False, False])
     assert np.array_equal(np.flatnonzero(np.isnan(d[1])), np.sort(idx[1])) and np.isfinite(d[[0, 2, 3]]).all()
+
+
+# ------------------------------------------------------------ column slices of one buffer
+
+class Slices:
+    """Matrices of one dtype side by side in one buffer (`together`), or each
+    at the same place of a buffer of its own."""
+
+    def __init__(self, torch, rows, widths, dtype, gap, together):  # noqa: F811
+        at, self.ld = {}, gap
+        for name, n in widths.items():
+            at[name] = (self.ld, n)
+            self.ld += n + gap
+        self.ld += (-self.ld) % 8 if gap % 8 == 0 else 0
+        new = lambda: torch.full((rows, self.ld), Mat.CANARY, device="cuda", dtype=getattr(torch, dtype))  # noqa: E731
+        one = new()
+        self.bufs = [one] if together else []
+        self.t, self.at = {}, at
+        for name, (c, n) in at.items():
+            buf = one if together else new()
+            if not together:
+                self.bufs.append(buf)
+            self.t[name] = buf[:, c:c + n]
+
+    def __getitem__(self, name):
+        return self.t[name].data_ptr()
+
+    def gaps_intact(self):
+        bad = 0
+        for buf in self.bufs:
+            a = buf.clone()
+            for c, n in self.at.values():
+                a[:, c:c + n] = Mat.CANARY
+            bad += (a != Mat.CANARY).sum().item()
+        return bad == 0
+
+
+@pytest.mark.parametrize("gap", [0, 8, 3])
+@pytest.mark.parametrize("rows,cols", [(40, 264), (700, 64), (333, 1001), (5, 9000), (3, 33001)])
+def test_norm_column_slices(torch, v, rows, cols, gap):  # noqa: F811
+    got = []
+    for together in (False, True):
+        b = Slices(torch, rows, {"x": cols, "y": cols, "dy": cols, "dx": cols}, "bfloat16", gap, together)
+        g = torch.Generator("cuda").manual_seed(3)
+        for n in ("x", "dy"):
+            b.t[n].copy_(torch.randn(rows, cols, generator=g, device="cuda"))
+        mean, rstd = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+        dg, db = torch.empty(cols, device="cuda"), torch.empty(cols, device="cuda")
+        ws = torch.empty(v.vrcclLayerNormWorkspace(rows, cols), device="cuda", dtype=torch.uint8)
+        v.vrcclLayerNormForward(b["x"], None, None, b["y"], mean, rstd, rows, cols, "bfloat16", "float32", ldx=b.ld, ldy=b.ld)
+        v.vrcclLayerNormBackward(b["dy"], b["x"], None, mean, rstd, b["dx"], dg, db, rows, cols, "bfloat16", "float32", ws,
+                                 ws.numel(), lddy=b.ld, ldx=b.ld, lddx=b.ld)
+        assert b.gaps_intact()
+        got.append([t.clone() for t in (*b.t.values(), mean, rstd, dg, db)])
+    assert all(torch.equal(a, c) for a, c in zip(*got))
+
+
+@pytest.mark.parametrize("gap", [0, 8, 3])
+@pytest.mark.parametrize("rows,outs,ins", [(1, 72, 64), (7, 40, 136), (33, 130, 65), (300, 264, 72), (1500, 1000, 96)])
+def test_linear_column_slices(torch, v, rows, outs, ins, gap):  # noqa: F811
+    got = []
+    for together in (False, True):
+        b = Slices(torch, rows, {"x": ins, "z": outs, "y": outs, "r": outs, "dy": outs, "dx": ins}, "bfloat16", gap, together)
+        g = torch.Generator("cuda").manual_seed(4)
+        for n in ("x", "r", "dy"):
+            b.t[n].copy_(torch.randn(b.t[n].shape, generator=g, device="cuda"))
+        w = (torch.randn(outs, ins, generator=g, device="cuda") / 8).bfloat16()
+        dw = torch.empty_like(w)
+        ws = torch.empty(v.vrcclLinearWorkspace("backward", rows, outs, ins, "bfloat16", "silu"), device="cuda", dtype=torch.uint8)
+        v.vrcclLinearForward(b["x"], w, None, b["r"], b["y"], b["z"], rows, outs, ins, "bfloat16", "silu", ws, ws.numel(),
+                             ldx=b.ld, ldr=b.ld, ldy=b.ld, ldz=b.ld)
+        v.vrcclLinearBackward(b["dy"], b["z"], b["x"], w, b["dx"], dw, None, rows, outs, ins, "bfloat16", "silu", ws,
+                              ws.numel(), lddy=b.ld, ldz=b.ld, ldx=b.ld, lddx=b.ld)
+        assert b.gaps_intact()
+        got.append([t.clone() for t in (*b.t.values(), dw)])
+    assert all(torch.equal(a, c) for a, c in zip(*got))
+
+
+@pytest.mark.parametrize("gap", [0, 8, 3])
+@pytest.mark.parametrize("rows,vocab", [(40, 1000), (3, 70001)])
+def test_distill_column_slices(torch, v, rows, vocab, gap):  # noqa: F811
+    got = []
+    _, t, idx = _distill_inputs(rows, vocab, 12, 6)
+    t, idx = torch.as_tensor(t).float().cuda(), torch.as_tensor(idx).cuda()
+    for together in (False, True):
+        b = Slices(torch, rows, {"s": vocab, "ds": vocab}, "bfloat16", gap, together)
+        b.t["s"].copy_(torch.randn(rows, vocab, generator=torch.Generator("cuda").manual_seed(5), device="cuda"))
+        loss, stats = torch.empty(rows, device="cuda"), torch.empty(rows, 2, device="cuda")
+        v.vrcclDistillForward(b["s"], t, idx, loss, stats, rows, vocab, 12, "bfloat16", "float32", "int64", ldl=b.ld)
+        v.vrcclDistillBackward(b["s"], t, idx, stats, loss, b["ds"], rows, vocab, 12, "bfloat16", "float32", "int64",
+                               ldl=b.ld, ldd=b.ld)
+        assert b.gaps_intact()
+        got.append([t.clone() for t in (*b.t.values(), loss, stats)])
+    assert all(torch.equal(a, c) for a, c in zip(*got))

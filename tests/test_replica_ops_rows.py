@@ -1,5 +1,6 @@
 """Arithmetic of the operators' rows (csrc/ops_rows.h), compiled for the host:
-what a row's bulk copy takes, and when a team gives up."""
+what a row's bulk copy takes, which operands share bytes, and when a team
+gives up."""
 import ctypes
 import os
 import shutil
@@ -17,6 +18,9 @@ extern "C" void rowWindowOf(uintptr_t base, size_t ld, size_t row, size_t rows, 
   const Window w = rowWindow(base, ld, row, rows, cols, elem, cut);
   out[0] = w.row; out[1] = w.end; out[2] = w.lo; out[3] = w.hi;
   out[4] = w.headEnd(); out[5] = w.tailBegin(); out[6] = maybeCut(row, rows, cut);
+}
+extern "C" int meet(uintptr_t p, size_t ld, size_t rows, size_t cols, uintptr_t q, size_t le, size_t rowsq, size_t colsq) {
+  return overlap(matrixSpan((void*)p, ld, rows, cols, 2), matrixSpan((void*)q, le, rowsq, colsq, 2));
 }
 extern "C" int wordOf(int turn) { return givenUpWord(turn); }
 extern "C" int leaves(int word, int turn) { return givenUp(word, turn); }
@@ -70,3 +74,28 @@ def test_a_team_gives_up_at_one_barrier(rows_lib):
         word = rows_lib.wordOf(turn ^ 1)  # and gives up the next turn's wait
         assert not rows_lib.leaves(word, turn)  # the slow one reads only now
         assert rows_lib.leaves(word, turn ^ 1)  # both, past the next barrier
+
+
+def test_operands_side_by_side_do_not_overlap(rows_lib):
+    """overlap() against the sets of elements: exact for one stride and for
+    runs, never false where two strides share an element."""
+    rows_lib.meet.argtypes = [ctypes.c_size_t] * 8
+    elements = lambda at, ld, rows, cols: {at + 2 * (r * ld + c) for r in range(rows) for c in range(cols)}  # noqa: E731
+    accepted = 0
+    shapes = [(ld, rows, cols) for ld in (6, 7) for rows in (1, 2, 4) for cols in (1, 3, 6)]
+    for a in shapes:
+        for b in shapes:
+            for at in range(2048 - 60, 2048 + 60, 2):
+                share = bool(elements(2048, *a) & elements(at, *b))
+                got = bool(rows_lib.meet(2048, *a, at, *b))
+                if a[0] == b[0] or (a[1] == 1 or b[1] == 1):
+                    one = a[1] == 1 or b[1] == 1  # a run that reaches past a row's gap counts as touching it
+                    assert got == share or (one and got), (a, b, at)
+                    accepted += not got
+                else:
+                    assert got or not share, (a, b, at)
+    assert accepted > 1000
+    # column slices of one buffer, and a run between the rows
+    assert not rows_lib.meet(4096, 512, 100, 256, 4096 + 512, 512, 100, 256)
+    assert rows_lib.meet(4096, 512, 100, 256, 4096 + 510, 512, 100, 256)
+    assert not rows_lib.meet(4096, 512, 100, 256, 4096 + 7 * 1024 + 512, 1, 1, 100)
