@@ -112,8 +112,11 @@ def _ptr(x) -> int:
 
 
 # The current stream's handle without a Stream object, which takes 3 us to
-# make: as long as a launch.
-_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch.cuda.current_device
+# make: as long as a launch. (A torch built without CUDA has no such function;
+# the calls that need no GPU work there all the same.)
+_current_device = torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
 def _stream(s) -> int | None:
