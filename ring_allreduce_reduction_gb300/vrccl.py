@@ -112,9 +112,9 @@ def _ptr(x) -> int:
 
 
 # The current stream's handle without a Stream object, which takes 3 us to
-# make: as long as a launch. (A torch built without CUDA has no such function;
+# make: as long as a launch. (A torch built without CUDA has no such functions;
 # the calls that need no GPU work there all the same.)
-_current_device = torch.cuda.current_device
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                       lambda device: torch.cuda.current_stream(device).cuda_stream)
 
@@ -305,18 +305,89 @@ def vrcclCommLoadTuning(comm, path: str) -> int:
 
 
 # ------------------------------------------------------------ operators of a replica
-# Matrices default to rows without gaps (ld = the row's length); a buffer may
-# be None where include/vrccl.h allows NULL.
+# A buffer may be None where include/vrccl.h allows NULL. A tensor has to be of
+# the element type that the call names and the GPU's to read (on it, or pinned
+# on the host); a matrix whose row stride is not given is taken as it lies: a
+# [rows, cols] view by its own stride, anything else without gaps. A raw
+# address is passed on as it is, its row stride the row's length by default.
 
-def _opt(x) -> int | None:
-    return None if x is None else x.data_ptr() if isinstance(x, torch.Tensor) else int(x)
+_F32 = torch.float32
+
+
+class _Types(dict):
+    """By name, torch dtype and enum value: (enum value, torch dtype)."""
+
+    def __missing__(self, dtype) -> tuple:
+        return _enum(DTYPES, dtype, "dtype"), None  # an integer out of range: the library's to refuse
+
+
+_DT = _Types({key: (val, getattr(torch, name)) for name, val in DTYPES.items()
+              for key in (name, getattr(torch, name), val)})
+
+
+def _misfit(x: torch.Tensor, td) -> None:
+    if td is not None and x.dtype is not td:
+        raise ValueError(f"a tensor of {x.dtype} where the call names {td}")
+    if not x.is_cuda and not x.is_pinned():
+        raise ValueError(f"a tensor on {x.device}, where the GPU does not read")
+
+
+def _address(x) -> int | None:
+    return None if x is None else int(x)
+
+
+# (What is no tensor has no `dtype`: cheaper to find out than to ask for the
+# type first. The host's time for a call is a launch's.)
+def _mat(x, td, rows: int, cols: int, ld: int | None) -> tuple:
+    """(address, row stride) of a [rows, cols] matrix of torch dtype td."""
+    try:
+        if x.dtype is not td or not x.is_cuda:
+            _misfit(x, td)
+    except AttributeError:
+        return _address(x), cols if ld is None else ld
+    return x.data_ptr(), _ld(x, rows, cols) if ld is None else ld
+
+
+def _vec(x, td, n: int) -> int | None:
+    """Address of a vector of n: a tensor without gaps."""
+    try:
+        if x.dtype is not td or not x.is_cuda:
+            _misfit(x, td)
+    except AttributeError:
+        return _address(x)
+    if not x.is_contiguous() or x.numel() < n:
+        raise ValueError(f"a tensor of {tuple(x.shape)}, strides {x.stride()}, for a vector of {n}")
+    return x.data_ptr()
+
+
+def _ld(x: torch.Tensor, rows: int, cols: int) -> int:
+    """Row stride of a [rows, cols] matrix where the call gives none."""
+    if x.is_contiguous():
+        if x.numel() < rows * cols:
+            raise ValueError(f"a tensor of {tuple(x.shape)} for {rows} rows of {cols}")
+        return cols
+    if x.shape != (rows, cols) or (cols > 1 and x.stride(1) != 1):
+        raise ValueError(f"no row stride given for a tensor of {tuple(x.shape)}, strides {x.stride()}")
+    return x.stride(0)
+
+
+def _scratch(x, nbytes: int) -> int | None:
+    """Address of a workspace."""
+    if not isinstance(x, torch.Tensor):
+        return _address(x)
+    if not x.is_cuda:
+        _misfit(x, None)
+    if not x.is_contiguous() or x.nbytes < nbytes:
+        raise ValueError(f"a workspace of {x.nbytes} bytes (strides {x.stride()}) passed as {nbytes}")
+    return x.data_ptr()
 
 
 def vrcclLayerNormForward(x, gamma, beta, y, mean, rstd, rows: int, cols: int, dtype, ptype, eps: float = 1e-5,
                           ldx: int | None = None, ldy: int | None = None, stream=None) -> None:
-    _check(_lib.vrcclLayerNormForward(_opt(x), cols if ldx is None else ldx, _opt(gamma), _opt(beta), _opt(y),
-                                      cols if ldy is None else ldy, _opt(mean), _opt(rstd), rows, cols,
-                                      _enum(DTYPES, dtype, "dtype"), _enum(DTYPES, ptype, "dtype"), eps,
+    (e, td), (pe, ptd) = _DT[dtype], _DT[ptype]
+    (x, ldx), (y, ldy) = _mat(x, td, rows, cols, ldx), _mat(y, td, rows, cols, ldy)
+    _check(_lib.vrcclLayerNormForward(x, ldx, _vec(gamma, ptd, cols), _vec(beta, ptd, cols), y, ldy,
+                                      _vec(mean, _F32, rows), _vec(rstd, _F32, rows), rows, cols, e, pe, eps,
                                       _stream(stream)), "vrcclLayerNormForward")
 
 
@@ -329,11 +400,14 @@ def vrcclLayerNormWorkspace(rows: int, cols: int) -> int:
 def vrcclLayerNormBackward(dy, x, gamma, mean, rstd, dx, dgamma, dbeta, rows: int, cols: int, dtype, ptype,
                            workspace=None, workspace_bytes: int = 0, lddy: int | None = None, ldx: int | None = None,
                            lddx: int | None = None, stream=None) -> None:
-    _check(_lib.vrcclLayerNormBackward(_opt(dy), cols if lddy is None else lddy, _opt(x),
-                                       cols if ldx is None else ldx, _opt(gamma), _opt(mean), _opt(rstd), _opt(dx),
-                                       cols if lddx is None else lddx, _opt(dgamma), _opt(dbeta), rows, cols,
-                                       _enum(DTYPES, dtype, "dtype"), _enum(DTYPES, ptype, "dtype"), _opt(workspace),
-                                       workspace_bytes, _stream(stream)), "vrcclLayerNormBackward")
+    (e, td), (pe, ptd) = _DT[dtype], _DT[ptype]
+    dy, lddy = _mat(dy, td, rows, cols, lddy)
+    (x, ldx), (dx, lddx) = _mat(x, td, rows, cols, ldx), _mat(dx, td, rows, cols, lddx)
+    _check(_lib.vrcclLayerNormBackward(dy, lddy, x, ldx, _vec(gamma, ptd, cols), _vec(mean, _F32, rows),
+                                       _vec(rstd, _F32, rows), dx, lddx, _vec(dgamma, ptd, cols),
+                                       _vec(dbeta, ptd, cols), rows, cols, e, pe,
+                                       _scratch(workspace, workspace_bytes), workspace_bytes, _stream(stream)),
+           "vrcclLayerNormBackward")
 
 
 def vrcclLinearWorkspace(direction: str, rows: int, outs: int, ins: int, dtype, act="none") -> int:
@@ -348,23 +422,27 @@ def vrcclLinearWorkspace(direction: str, rows: int, outs: int, ins: int, dtype, 
 def vrcclLinearForward(x, w, bias, residual, y, z, rows: int, outs: int, ins: int, dtype, act="none", workspace=None,
                        workspace_bytes: int = 0, ldx: int | None = None, ldw: int | None = None,
                        ldr: int | None = None, ldy: int | None = None, ldz: int | None = None, stream=None) -> None:
-    _check(_lib.vrcclLinearForward(_opt(x), ins if ldx is None else ldx, _opt(w), ins if ldw is None else ldw,
-                                   _opt(bias), _opt(residual), outs if ldr is None else ldr, _opt(y),
-                                   outs if ldy is None else ldy, _opt(z), outs if ldz is None else ldz, rows, outs,
-                                   ins, _enum(DTYPES, dtype, "dtype"), _enum(ACTS, act, "activation"),
-                                   _opt(workspace), workspace_bytes, _stream(stream)), "vrcclLinearForward")
+    e, td = _DT[dtype]
+    (x, ldx), (w, ldw) = _mat(x, td, rows, ins, ldx), _mat(w, td, outs, ins, ldw)
+    residual, ldr = _mat(residual, td, rows, outs, ldr)
+    (y, ldy), (z, ldz) = _mat(y, td, rows, outs, ldy), _mat(z, td, rows, outs, ldz)
+    _check(_lib.vrcclLinearForward(x, ldx, w, ldw, _vec(bias, td, outs), residual, ldr, y, ldy, z, ldz, rows, outs,
+                                   ins, e, _enum(ACTS, act, "activation"), _scratch(workspace, workspace_bytes),
+                                   workspace_bytes, _stream(stream)), "vrcclLinearForward")
 
 
 def vrcclLinearBackward(dy, z, x, w, dx, dw, dbias, rows: int, outs: int, ins: int, dtype, act="none",
                         workspace=None, workspace_bytes: int = 0, lddy: int | None = None, ldz: int | None = None,
                         ldx: int | None = None, ldw: int | None = None, lddx: int | None = None,
                         lddw: int | None = None, stream=None) -> None:
-    _check(_lib.vrcclLinearBackward(_opt(dy), outs if lddy is None else lddy, _opt(z), outs if ldz is None else ldz,
-                                    _opt(x), ins if ldx is None else ldx, _opt(w), ins if ldw is None else ldw,
-                                    _opt(dx), ins if lddx is None else lddx, _opt(dw), ins if lddw is None else lddw,
-                                    _opt(dbias), rows, outs, ins, _enum(DTYPES, dtype, "dtype"),
-                                    _enum(ACTS, act, "activation"), _opt(workspace), workspace_bytes,
-                                    _stream(stream)), "vrcclLinearBackward")
+    e, td = _DT[dtype]
+    (dy, lddy), (z, ldz) = _mat(dy, td, rows, outs, lddy), _mat(z, td, rows, outs, ldz)
+    (x, ldx), (w, ldw) = _mat(x, td, rows, ins, ldx), _mat(w, td, outs, ins, ldw)
+    (dx, lddx), (dw, lddw) = _mat(dx, td, rows, ins, lddx), _mat(dw, td, outs, ins, lddw)
+    _check(_lib.vrcclLinearBackward(dy, lddy, z, ldz, x, ldx, w, ldw, dx, lddx, dw, lddw, _vec(dbias, td, outs), rows,
+                                    outs, ins, e, _enum(ACTS, act, "activation"),
+                                    _scratch(workspace, workspace_bytes), workspace_bytes, _stream(stream)),
+           "vrcclLinearBackward")
 
 
 def vrcclReplicaGetAsyncError() -> int:
@@ -376,23 +454,25 @@ def vrcclReplicaGetAsyncError() -> int:
 def vrcclDistillForward(logits, teacher, index, loss, stats, rows: int, vocab: int, k: int, dtype, teacher_dtype,
                         index_dtype, temperature: float = 1.0, ldl: int | None = None, ldt: int | None = None,
                         ldi: int | None = None, stream=None) -> None:
-    _check(_lib.vrcclDistillForward(_opt(logits), vocab if ldl is None else ldl, _opt(teacher),
-                                    k if ldt is None else ldt, _opt(index), k if ldi is None else ldi, _opt(loss),
-                                    _opt(stats), rows, vocab, k, _enum(DTYPES, dtype, "dtype"),
-                                    _enum(DTYPES, teacher_dtype, "dtype"), _enum(DTYPES, index_dtype, "dtype"),
-                                    temperature, _stream(stream)), "vrcclDistillForward")
+    (e, td), (te, ttd), (ie, itd) = _DT[dtype], _DT[teacher_dtype], _DT[index_dtype]
+    logits, ldl = _mat(logits, td, rows, vocab, ldl)
+    (teacher, ldt), (index, ldi) = _mat(teacher, ttd, rows, k, ldt), _mat(index, itd, rows, k, ldi)
+    _check(_lib.vrcclDistillForward(logits, ldl, teacher, ldt, index, ldi, _vec(loss, _F32, rows),
+                                    _vec(stats, _F32, 2 * rows), rows, vocab, k, e, te, ie, temperature,
+                                    _stream(stream)), "vrcclDistillForward")
 
 
 def vrcclDistillBackward(logits, teacher, index, stats, dloss, dlogits, rows: int, vocab: int, k: int, dtype,
                          teacher_dtype, index_dtype, temperature: float = 1.0, dloss_stride: int = 1,
                          ldl: int | None = None, ldt: int | None = None, ldi: int | None = None,
                          ldd: int | None = None, stream=None) -> None:
-    _check(_lib.vrcclDistillBackward(_opt(logits), vocab if ldl is None else ldl, _opt(teacher),
-                                     k if ldt is None else ldt, _opt(index), k if ldi is None else ldi, _opt(stats),
-                                     _opt(dloss), dloss_stride, _opt(dlogits), vocab if ldd is None else ldd, rows,
-                                     vocab, k, _enum(DTYPES, dtype, "dtype"), _enum(DTYPES, teacher_dtype, "dtype"),
-                                     _enum(DTYPES, index_dtype, "dtype"), temperature, _stream(stream)),
-           "vrcclDistillBackward")
+    (e, td), (te, ttd), (ie, itd) = _DT[dtype], _DT[teacher_dtype], _DT[index_dtype]
+    (logits, ldl), (dlogits, ldd) = _mat(logits, td, rows, vocab, ldl), _mat(dlogits, td, rows, vocab, ldd)
+    (teacher, ldt), (index, ldi) = _mat(teacher, ttd, rows, k, ldt), _mat(index, itd, rows, k, ldi)
+    dloss = _vec(dloss, _F32, rows) if dloss_stride == 1 else _mat(dloss, _F32, rows, 1, dloss_stride)[0]
+    _check(_lib.vrcclDistillBackward(logits, ldl, teacher, ldt, index, ldi, _vec(stats, _F32, 2 * rows), dloss,
+                                     dloss_stride, dlogits, ldd, rows, vocab, k, e, te, ie, temperature,
+                                     _stream(stream)), "vrcclDistillBackward")
 
 
 def raw_call(name: str, *args) -> int:

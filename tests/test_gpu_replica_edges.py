@@ -218,3 +218,41 @@ def test_distill_column_slices(torch, v, rows, vocab, gap):  # noqa: F811
         assert b.gaps_intact()
         got.append([t.clone() for t in (*b.t.values(), loss, stats)])
     assert all(torch.equal(a, c) for a, c in zip(*got))
+
+
+# ------------------------------------------------------------ tensors through the binding
+
+def test_views_are_taken_as_they_lie(torch, v):  # noqa: F811
+    """Padded views without a row stride beside them give what the call with the stride gives."""
+    rows, cols, outs, k = 30, 264, 72, 5
+    g = torch.Generator("cuda").manual_seed(8)
+    view = lambda n, pad=24: torch.randn(rows, n + pad, generator=g, device="cuda").bfloat16()[:, :n]  # noqa: E731
+    x = view(cols)
+    w = torch.randn(outs, cols + 8, generator=g, device="cuda").bfloat16()[:, :cols]
+    out = []
+    for strides in (True, False):
+        kw = lambda **d: d if strides else {}  # noqa: E731
+        y, z, r = (torch.zeros(rows, n + 16, device="cuda", dtype=torch.bfloat16)[:, :n] for n in (cols, outs, outs))
+        mean, rstd = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+        v.vrcclLayerNormForward(x, None, None, y, mean, rstd, rows, cols, "bfloat16", "float32", **kw(ldx=cols + 24, ldy=cols + 16))
+        v.vrcclLinearForward(y, w, None, None, z, None, rows, outs, cols, torch.bfloat16, "silu",
+                             **kw(ldx=cols + 16, ldw=cols + 8, ldy=outs + 16))
+        t = (torch.arange(rows * 8, device="cuda").float() % 7).view(rows, 8)[:, :k]
+        idx = (torch.arange(rows * 9, device="cuda") * 5 % outs).view(rows, 9)[:, :k]
+        assert t.stride(0) == 8 and idx.stride(0) == 9
+        loss, stats = torch.empty(rows, device="cuda"), torch.empty(rows, 2, device="cuda")
+        v.vrcclDistillForward(z, t, idx, loss, stats, rows, outs, k, "bfloat16", "float32", "int64",
+                              **kw(ldl=outs + 16, ldt=8, ldi=9))
+        v.vrcclDistillBackward(z, t, idx, stats, loss, r, rows, outs, k, "bfloat16", "float32", "int64",
+                               **kw(ldl=outs + 16, ldt=8, ldi=9, ldd=outs + 16))
+        out.append([a.clone() for a in (y, mean, rstd, z, loss, stats, r)])
+    assert all(torch.equal(a, b) for a, b in zip(*out))
+    with pytest.raises(ValueError):  # no row stride to be had
+        v.vrcclLayerNormForward(x.t().contiguous().t(), None, None, x, None, None, rows, cols, "bfloat16", "float32")
+    with pytest.raises(ValueError):  # too few elements
+        v.vrcclLayerNormForward(x, torch.ones(cols - 1, device="cuda"), None, x, None, None, rows, cols, "bfloat16", "float32")
+    # pinned memory on the host is the GPU's to write
+    pinned = torch.zeros(rows, pin_memory=True)
+    v.vrcclLayerNormForward(x, None, None, y, pinned, None, rows, cols, "bfloat16", "float32")
+    torch.cuda.synchronize()
+    assert torch.equal(pinned, mean.cpu())
