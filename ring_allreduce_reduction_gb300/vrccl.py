@@ -307,7 +307,7 @@ def vrcclCommLoadTuning(comm, path: str) -> int:
 # ------------------------------------------------------------ operators of a replica
 # A buffer may be None where include/vrccl.h allows NULL. A tensor has to be of
 # the element type that the call names and the GPU's to read (on it, or pinned
-# on the host); a matrix whose row stride is not given is taken as it lies: a
+# on the host), a vector without gaps; a matrix whose row stride is not given is taken as it lies: a
 # [rows, cols] view by its own stride, anything else without gaps. A raw
 # address is passed on as it is, its row stride the row's length by default.
 
@@ -332,49 +332,51 @@ def _misfit(x: torch.Tensor, td) -> None:
         raise ValueError(f"a tensor on {x.device}, where the GPU does not read")
 
 
-def _address(x) -> int | None:
-    return None if x is None else int(x)
-
-
-# (What is no tensor has no `dtype`: cheaper to find out than to ask for the
-# type first. The host's time for a call is a launch's.)
+# (Written for the host's time, which bounds a small call: what is no tensor
+# has no `dtype`, cheaper to find out than to ask for the type first.)
 def _mat(x, td, rows: int, cols: int, ld: int | None) -> tuple:
     """(address, row stride) of a [rows, cols] matrix of torch dtype td."""
+    if x is None:
+        return None, cols if ld is None else ld
     try:
         if x.dtype is not td or not x.is_cuda:
             _misfit(x, td)
     except AttributeError:
-        return _address(x), cols if ld is None else ld
-    return x.data_ptr(), _ld(x, rows, cols) if ld is None else ld
-
-
-def _vec(x, td, n: int) -> int | None:
-    """Address of a vector of n: a tensor without gaps."""
-    try:
-        if x.dtype is not td or not x.is_cuda:
-            _misfit(x, td)
-    except AttributeError:
-        return _address(x)
-    if not x.is_contiguous() or x.numel() < n:
-        raise ValueError(f"a tensor of {tuple(x.shape)}, strides {x.stride()}, for a vector of {n}")
-    return x.data_ptr()
-
-
-def _ld(x: torch.Tensor, rows: int, cols: int) -> int:
-    """Row stride of a [rows, cols] matrix where the call gives none."""
-    if x.is_contiguous():
-        if x.numel() < rows * cols:
+        return int(x), cols if ld is None else ld
+    if ld is None:
+        if not x.is_contiguous():
+            ld = _row_stride(x, rows, cols)
+        elif x.numel() < rows * cols:
             raise ValueError(f"a tensor of {tuple(x.shape)} for {rows} rows of {cols}")
-        return cols
+        else:
+            ld = cols
+    return x.data_ptr(), ld
+
+
+def _row_stride(x: torch.Tensor, rows: int, cols: int) -> int:
     if x.shape != (rows, cols) or (cols > 1 and x.stride(1) != 1):
         raise ValueError(f"no row stride given for a tensor of {tuple(x.shape)}, strides {x.stride()}")
     return x.stride(0)
 
 
+def _vec(x, td) -> int | None:
+    """Address of a vector: a tensor without gaps."""
+    if x is None:
+        return None
+    try:
+        if x.dtype is not td or not x.is_cuda:
+            _misfit(x, td)
+    except AttributeError:
+        return int(x)
+    if not x.is_contiguous():
+        raise ValueError(f"a vector with gaps (strides {x.stride()})")
+    return x.data_ptr()
+
+
 def _scratch(x, nbytes: int) -> int | None:
     """Address of a workspace."""
     if not isinstance(x, torch.Tensor):
-        return _address(x)
+        return None if x is None else int(x)
     if not x.is_cuda:
         _misfit(x, None)
     if not x.is_contiguous() or x.nbytes < nbytes:
@@ -386,8 +388,8 @@ def vrcclLayerNormForward(x, gamma, beta, y, mean, rstd, rows: int, cols: int, d
                           ldx: int | None = None, ldy: int | None = None, stream=None) -> None:
     (e, td), (pe, ptd) = _DT[dtype], _DT[ptype]
     (x, ldx), (y, ldy) = _mat(x, td, rows, cols, ldx), _mat(y, td, rows, cols, ldy)
-    _check(_lib.vrcclLayerNormForward(x, ldx, _vec(gamma, ptd, cols), _vec(beta, ptd, cols), y, ldy,
-                                      _vec(mean, _F32, rows), _vec(rstd, _F32, rows), rows, cols, e, pe, eps,
+    _check(_lib.vrcclLayerNormForward(x, ldx, _vec(gamma, ptd), _vec(beta, ptd), y, ldy,
+                                      _vec(mean, _F32), _vec(rstd, _F32), rows, cols, e, pe, eps,
                                       _stream(stream)), "vrcclLayerNormForward")
 
 
@@ -403,9 +405,9 @@ def vrcclLayerNormBackward(dy, x, gamma, mean, rstd, dx, dgamma, dbeta, rows: in
     (e, td), (pe, ptd) = _DT[dtype], _DT[ptype]
     dy, lddy = _mat(dy, td, rows, cols, lddy)
     (x, ldx), (dx, lddx) = _mat(x, td, rows, cols, ldx), _mat(dx, td, rows, cols, lddx)
-    _check(_lib.vrcclLayerNormBackward(dy, lddy, x, ldx, _vec(gamma, ptd, cols), _vec(mean, _F32, rows),
-                                       _vec(rstd, _F32, rows), dx, lddx, _vec(dgamma, ptd, cols),
-                                       _vec(dbeta, ptd, cols), rows, cols, e, pe,
+    _check(_lib.vrcclLayerNormBackward(dy, lddy, x, ldx, _vec(gamma, ptd), _vec(mean, _F32),
+                                       _vec(rstd, _F32), dx, lddx, _vec(dgamma, ptd),
+                                       _vec(dbeta, ptd), rows, cols, e, pe,
                                        _scratch(workspace, workspace_bytes), workspace_bytes, _stream(stream)),
            "vrcclLayerNormBackward")
 
@@ -426,7 +428,7 @@ def vrcclLinearForward(x, w, bias, residual, y, z, rows: int, outs: int, ins: in
     (x, ldx), (w, ldw) = _mat(x, td, rows, ins, ldx), _mat(w, td, outs, ins, ldw)
     residual, ldr = _mat(residual, td, rows, outs, ldr)
     (y, ldy), (z, ldz) = _mat(y, td, rows, outs, ldy), _mat(z, td, rows, outs, ldz)
-    _check(_lib.vrcclLinearForward(x, ldx, w, ldw, _vec(bias, td, outs), residual, ldr, y, ldy, z, ldz, rows, outs,
+    _check(_lib.vrcclLinearForward(x, ldx, w, ldw, _vec(bias, td), residual, ldr, y, ldy, z, ldz, rows, outs,
                                    ins, e, _enum(ACTS, act, "activation"), _scratch(workspace, workspace_bytes),
                                    workspace_bytes, _stream(stream)), "vrcclLinearForward")
 
@@ -439,7 +441,7 @@ def vrcclLinearBackward(dy, z, x, w, dx, dw, dbias, rows: int, outs: int, ins: i
     (dy, lddy), (z, ldz) = _mat(dy, td, rows, outs, lddy), _mat(z, td, rows, outs, ldz)
     (x, ldx), (w, ldw) = _mat(x, td, rows, ins, ldx), _mat(w, td, outs, ins, ldw)
     (dx, lddx), (dw, lddw) = _mat(dx, td, rows, ins, lddx), _mat(dw, td, outs, ins, lddw)
-    _check(_lib.vrcclLinearBackward(dy, lddy, z, ldz, x, ldx, w, ldw, dx, lddx, dw, lddw, _vec(dbias, td, outs), rows,
+    _check(_lib.vrcclLinearBackward(dy, lddy, z, ldz, x, ldx, w, ldw, dx, lddx, dw, lddw, _vec(dbias, td), rows,
                                     outs, ins, e, _enum(ACTS, act, "activation"),
                                     _scratch(workspace, workspace_bytes), workspace_bytes, _stream(stream)),
            "vrcclLinearBackward")
@@ -457,8 +459,8 @@ def vrcclDistillForward(logits, teacher, index, loss, stats, rows: int, vocab: i
     (e, td), (te, ttd), (ie, itd) = _DT[dtype], _DT[teacher_dtype], _DT[index_dtype]
     logits, ldl = _mat(logits, td, rows, vocab, ldl)
     (teacher, ldt), (index, ldi) = _mat(teacher, ttd, rows, k, ldt), _mat(index, itd, rows, k, ldi)
-    _check(_lib.vrcclDistillForward(logits, ldl, teacher, ldt, index, ldi, _vec(loss, _F32, rows),
-                                    _vec(stats, _F32, 2 * rows), rows, vocab, k, e, te, ie, temperature,
+    _check(_lib.vrcclDistillForward(logits, ldl, teacher, ldt, index, ldi, _vec(loss, _F32),
+                                    _vec(stats, _F32), rows, vocab, k, e, te, ie, temperature,
                                     _stream(stream)), "vrcclDistillForward")
 
 
@@ -469,8 +471,8 @@ def vrcclDistillBackward(logits, teacher, index, stats, dloss, dlogits, rows: in
     (e, td), (te, ttd), (ie, itd) = _DT[dtype], _DT[teacher_dtype], _DT[index_dtype]
     (logits, ldl), (dlogits, ldd) = _mat(logits, td, rows, vocab, ldl), _mat(dlogits, td, rows, vocab, ldd)
     (teacher, ldt), (index, ldi) = _mat(teacher, ttd, rows, k, ldt), _mat(index, itd, rows, k, ldi)
-    dloss = _vec(dloss, _F32, rows) if dloss_stride == 1 else _mat(dloss, _F32, rows, 1, dloss_stride)[0]
-    _check(_lib.vrcclDistillBackward(logits, ldl, teacher, ldt, index, ldi, _vec(stats, _F32, 2 * rows), dloss,
+    dloss = _vec(dloss, _F32) if dloss_stride == 1 else _mat(dloss, _F32, rows, 1, dloss_stride)[0]
+    _check(_lib.vrcclDistillBackward(logits, ldl, teacher, ldt, index, ldi, _vec(stats, _F32), dloss,
                                      dloss_stride, dlogits, ldd, rows, vocab, k, e, te, ie, temperature,
                                      _stream(stream)), "vrcclDistillBackward")
 

@@ -249,8 +249,8 @@ def test_views_are_taken_as_they_lie(torch, v):  # noqa: F811
     assert all(torch.equal(a, b) for a, b in zip(*out))
     with pytest.raises(ValueError):  # no row stride to be had
         v.vrcclLayerNormForward(x.t().contiguous().t(), None, None, x, None, None, rows, cols, "bfloat16", "float32")
-    with pytest.raises(ValueError):  # too few elements
-        v.vrcclLayerNormForward(x, torch.ones(cols - 1, device="cuda"), None, x, None, None, rows, cols, "bfloat16", "float32")
+    with pytest.raises(ValueError):  # a vector with gaps
+        v.vrcclLayerNormForward(x, torch.ones(cols, 2, device="cuda")[:, 0], None, x, None, None, rows, cols, "bfloat16", "float32")
     # pinned memory on the host is the GPU's to write
     pinned = torch.zeros(rows, pin_memory=True)
     v.vrcclLayerNormForward(x, None, None, y, pinned, None, rows, cols, "bfloat16", "float32")

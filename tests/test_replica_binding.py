@@ -59,18 +59,20 @@ def test_tensors_that_do_not_fit_are_refused(v, monkeypatch):
             fn(**dict(base, **change))
 
 
-def test_row_strides_of_tensors(v):
+def test_row_strides_of_tensors(v, monkeypatch):
     import torch
+    f32 = torch.float32
+    monkeypatch.setattr(v, "_misfit", lambda x, td: None)  # (host tensors stand in for the GPU's)
     wide = torch.zeros(6, 80)
-    assert v._ld(wide[:, :64], 6, 64) == 80
-    assert v._ld(wide[:, 8:72], 6, 64) == 80
-    assert v._ld(wide[::2, :64], 3, 64) == 160
-    assert v._ld(wide, 6, 80) == 80
-    assert v._ld(wide.view(2, 3, 80), 6, 80) == 80
-    assert v._ld(wide[:1, :64], 1, 64) >= 64
-    assert v._mat(4096, None, 6, 64, None) == (4096, 64) and v._mat(None, None, 6, 64, 70) == (None, 70)
+    for x, rows, cols, ld in ((wide[:, :64], 6, 64, 80), (wide[:, 8:72], 6, 64, 80), (wide[::2, :64], 3, 64, 160),
+                              (wide, 6, 80, 80), (wide.view(2, 3, 80), 6, 80, 80), (wide[:1, :64], 1, 64, 64)):
+        assert v._mat(x, f32, rows, cols, None) == (x.data_ptr(), ld)
+    assert v._mat(wide, f32, 3, 64, 160) == (wide.data_ptr(), 160)  # as the call says
+    assert v._mat(4096, f32, 6, 64, None) == (4096, 64) and v._mat(None, f32, 6, 64, 70) == (None, 70)
     for x, rows, cols in ((wide.t(), 80, 6), (wide[:, ::2], 6, 40), (wide[:, :64], 3, 128), (wide, 7, 80),
                           (wide.view(2, 3, 80)[:, :, :64], 6, 64)):
         with pytest.raises(ValueError):
-            v._ld(x, rows, cols)
-    assert v._vec(None, torch.float32, 4) is None and v._vec(4096, torch.float32, 4) == 4096
+            v._mat(x, f32, rows, cols, None)
+    with pytest.raises(ValueError):
+        v._vec(wide[:, 0], f32)
+    assert v._vec(None, f32) is None and v._vec(4096, f32) == 4096
