@@ -613,7 +613,8 @@ vrcclResult_t vrcclLinearWorkspace(int backward, size_t rows, size_t outs, size_
  *   dtype     vrcclBfloat16 or vrcclFloat16, of every operand. Products and
  *             sums are binary32. vrcclFloat32 -> vrcclInvalidUsage: the
  *             tensor cores would round its operands to 10 fraction bits.
- *   workspace 256-byte aligned; may be NULL where none is needed.
+ *   workspace 256-byte aligned wherever one is passed; may be NULL where none
+ *             is needed.
  */
 vrcclResult_t vrcclLinearForward(const void* x, size_t ldx, const void* w, size_t ldw, const void* bias,
                                  const void* residual, size_t ldr, void* y, size_t ldy, void* z, size_t ldz,

@@ -26,7 +26,7 @@
 // backward over independent blocks, since the saved statistics are all an
 // element needs.
 //
-// Measured, of a copy's 6.7 TB/s: 4096 x 131072 bf16 forward 167 us (6.4 TB/s),
+// Measured, of a copy's 6.7 TB/s: 4096 x 131072 bf16 forward 168 us (6.4 TB/s),
 // backward 337 us (6.4); fp32 forward 7.0. With 2-byte logits the passes run
 // near their issue slots, hence the packed arithmetic and the constant strides.
 // Shorter rows leave the reductions between loads in sight: 8192 x 32000 bf16
@@ -132,9 +132,10 @@ __device__ __forceinline__ Running warpJoin(Running r, float invT) {
   return r;
 }
 
-// exp for the long sums: 2^(x log2 e) on the special function unit, relative
-// error below 2^-21 for the arguments that matter (x <= 0); the statistics it
-// feeds are sums of many terms whose errors average out.
+// exp for the long sums: 2^x on the special function unit, relative error about
+// 2^-22 of its own; the rounding of its argument adds |x| 2^-24, so that a
+// term of 2^-100 is off by 2^-17 of itself. The terms that make up a sum have
+// small arguments, and their errors average out.
 __device__ __forceinline__ float fastExp2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -171,7 +172,8 @@ __device__ __forceinline__ void runOver(Running& r, const float (&f)[N], float c
   }
 }
 
-// T threads a block: a compile-time stride saves the long loops their address arithmetic (188 us against 172).
+// T threads a block: a compile-time stride saves the long loops their address arithmetic (162 us against 174 at
+// 4096 x 131072 bf16).
 template <int DT, int T>
 __global__ void __launch_bounds__(T, 4 * kThreads / T) distillForward(const __grid_constant__ DistillArgs a) {
   using S = typename Ty<DT>::S;
@@ -200,7 +202,7 @@ __global__ void __launch_bounds__(T, 4 * kThreads / T) distillForward(const __gr
   for (int u = 0; u < U; ++u)
     if (threadIdx.x % 8 == 0 && i + (size_t)u * T < hi)
       asm volatile("prefetch.global.L2 [%0];" ::"l"(vec + i + (size_t)u * T));
-  // (kept in shared memory over the long loop, which needs the registers: 172 us against 187 at 4096 x 131072)
+  // (kept in shared memory over the long loop, which needs the registers: 162 us against 167 at 4096 x 131072)
   __shared__ Entries kept[T];
   bool any;
   {

@@ -17,16 +17,18 @@
 // accumulators, so a tile's epilogue runs under the next one's products.
 //
 // Large products are bound by the tensor cores, and, a second into a run, by
-// the 1400 W limit: 8192 cubed 560 us (1.96 PFLOP/s, 0.99 of a library product's
-// burst), over seconds 600 us. Beside a library's plain product in the same
-// state: 8192 x 8192 x 2048 159 us, here 169 us with the bias, 173 with
-// gelu-tanh, 182 where z is stored too (268 MB written in all); both gradients
-// of 8192 x 4096 x 4096 339 us for the library's 335.
+// the 1400 W limit. Beside a library's plain product in the same state, normal
+// inputs: 8192 cubed 583 us after a pause (1.89 PFLOP/s; the library 565), 662
+// over seconds (636); 8192 x 8192 x 2048 with the bias 163 us after a pause
+// (167), 167 over seconds (158), 175 with gelu-tanh, 181 where z is stored too
+// (268 MB written in all); both gradients of 8192 x 4096 x 4096 337 us over seconds
+// (335).
 //
 // A call with few rows (one token and its like) is bound by reading W once:
 // linearFew streams W with wide loads, productSplit (below) feeds it to the
-// tensor cores from all multiprocessors: 1, 16 and 64 rows of 4096 x 4096 in
-// 6.2, 8.4 and 10.4 us (33.5 MB: 5.0 us from memory).
+// tensor cores from all multiprocessors: 1, 2, 16 and 64 rows of 4096 x 4096
+// in 7.2, 8.2, 9.6 and 10.6 us (33.5 MB, 5.0 us from memory; eight weights in
+// turn, which L2 does not hold).
 #include <cuda.h>
 
 #include <atomic>
@@ -955,11 +957,11 @@ __global__ void __launch_bounds__(kProductThreads, 1) productSplit(const __grid_
 
 // ------------------------------------------------------------ few rows
 
-// One or two rows: 4096 x 4096 in 7.6 us where the split product takes 10.4. Up to eight where W would first have to be
-// copied for TMA, which alone reads and writes it once more.
+// One or two rows: 4096 x 4096 in 7.2 and 8.2 us where the split product takes 9.2 and 9.6. Up to eight where W would first
+// have to be copied for TMA, which alone reads and writes it once more.
 constexpr int kFewRows = 2, kFewRowsUnaligned = 8;
-// Outputs a block, as many rows of W a thread has in flight: eight for one row of x (4096 x 4096 in 6.2 us against 8.2 with
-// four), four for more (8.2 us against 8.4 with eight, whose sums crowd the registers).
+// Outputs a block, as many rows of W a thread has in flight: eight for one row of x (4096 x 4096 in 7.2 us against 8.8 with
+// four), four for more (two rows 8.2 us against 12.6 with eight, whose sums crowd the registers).
 constexpr int fewOuts(int rows) { return rows == 1 ? 8 : 4; }
 constexpr int kFewThreads = 256;
 
@@ -1107,7 +1109,7 @@ constexpr int kSlopeTurn = 4;  // rows a thread has in flight
 // operands in it. The bias gradient sums the unrounded values. A thread has
 // eight columns; WIDE: rows of dy and z start on 16-byte boundaries (and end
 // on them), else their elements are gathered. dz always does. Bound by memory:
-// for 8192 x 4096 bf16 with gelu (201 MB) it adds 31 us to the products.
+// for 8192 x 4096 bf16 with gelu (201 MB) it takes 36 us with cold caches and adds 21 to the products.
 template <int DT, int ACT, bool WIDE>
 __global__ void __launch_bounds__(256, 4) linearSlope(const __grid_constant__ SlopeArgs a) {
   using S = typename Ty<DT>::S;

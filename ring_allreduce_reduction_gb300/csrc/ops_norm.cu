@@ -960,7 +960,7 @@ __global__ void __launch_bounds__(T, 1) normBackwardWide(const __grid_constant__
       asm volatile("" ::: "memory");
     };
     chunks<kChunk>(outputs);
-    if (stages == 1) {  // (binary32 rows of 11400 elements and more: there is room for one)
+    if (stages == 1) {  // (binary32 rows of 11261 elements and more: there is room for one)
       __syncthreads();
       if (t == 0) refill(0, row + stride);
     }
