@@ -114,7 +114,13 @@ def _ptr(x) -> int:
 # The current stream's handle without a Stream object, which takes 3 us to
 # make: as long as a launch. (A torch built without CUDA has no such functions;
 # the calls that need no GPU work there all the same.)
-_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+def _current_device() -> int:
+    global _current_device
+    device = torch.cuda.current_device()  # initialises CUDA, or says why it cannot; later calls ask the runtime alone
+    _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    return device
+
+
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                       lambda device: torch.cuda.current_stream(device).cuda_stream)
 

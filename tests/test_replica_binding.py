@@ -76,3 +76,21 @@ def test_row_strides_of_tensors(v, monkeypatch):
     with pytest.raises(ValueError):
         v._vec(wide[:, 0], f32)
     assert v._vec(None, f32) is None and v._vec(4096, f32) == 4096
+
+
+def test_first_call_initialises_cuda(v, monkeypatch):
+    """The first question for the current stream goes through torch's own
+    initialisation, whose error is the caller's to see."""
+    import torch
+
+    def no_driver():
+        raise RuntimeError("no driver")
+
+    monkeypatch.setattr(torch.cuda, "current_device", no_driver)
+    import importlib.util
+    spec = importlib.util.spec_from_file_location(v.__name__ + "_again", v.__file__)
+    again = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(again)
+    for _ in range(2):
+        with pytest.raises(RuntimeError, match="no driver"):
+            again.vrcclLayerNormForward(4096, None, None, 8192, None, None, 4, 64, "float32", "float32")
