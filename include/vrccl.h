@@ -523,8 +523,9 @@ vrcclResult_t vrcclAllReduceNoAlloc(const void* const* sendbufs, void* const* re
 
 /* ------------------------------------------------------------------------
  * Operators of a replica: what a data-parallel rank computes between two
- * AllReduces of its gradients -- layer norm, the linear layer and a
- * distillation loss, forward and backward. They need no communicator: a call
+ * AllReduces of its gradients -- layer norm, RMS norm, dropout, the linear
+ * layer, a distillation loss and the log probabilities of given tokens, each
+ * forward and backward. They need no communicator: a call
  * runs on the current CUDA device, is asynchronous on `stream` like every
  * call here, allocates nothing (what scratch it needs the caller passes as
  * `workspace`) and may be captured in a CUDA graph.
@@ -686,6 +687,157 @@ vrcclResult_t vrcclDistillBackward(const void* logits, size_t ldl, const void* t
                                    void* dlogits, size_t ldd, size_t rows, size_t vocab, size_t k,
                                    vrcclDataType_t dtype, vrcclDataType_t teacherType, vrcclDataType_t indexType,
                                    float temperature, vrcclStream_t stream);
+
+/*
+ * vrcclDropoutForward -- y = residual + (kept ? x * scale : 0), the kept
+ * elements drawn by a counter-based generator, so that nothing of the mask is
+ * stored: the backward pass (and a recomputed forward pass) draws it again.
+ *   x, y      [rows, cols] of dtype; y may be x (same stride).
+ *   residual  [rows, cols], or NULL (0); y may be residual (same stride).
+ *   p         0 to 1, the probability of being dropped, taken as the nearest
+ *             multiple of 2^-16: drop = round(65536 p); scale = 65536 /
+ *             (65536 - drop). A dropped element adds nothing, whatever x holds.
+ *   seed      DEVICE address of one 64-bit word, read when the kernel runs (so
+ *             that a captured graph draws another mask once the word changes).
+ *   offset    which of the masks of one seed: calls that are to differ (layers,
+ *             steps) take offsets of their own.
+ *   firstRow  number of row 0. The mask of a row depends on its number, so that
+ *             a batch that is cut over calls or ranks has the mask of the whole.
+ * Element (r, c) is kept if its 16 bits are not below drop: with n = (firstRow
+ * + r) ceil(cols / 8) + c / 8 and Philox4x32-10 (Salmon et al., 2011) under
+ * the key `seed` for the counter (n, offset), low words first, the lower (c
+ * even) or upper half of the output's word c % 8 / 2. Strides, type and
+ * alignment do not enter.
+ * Errors: vrcclInvalidArgument (also p outside [0, 1] or NaN, firstRow >= 2^40).
+ */
+vrcclResult_t vrcclDropoutForward(const void* x, size_t ldx, const void* residual, size_t ldr, void* y, size_t ldy,
+                                  size_t rows, size_t cols, vrcclDataType_t dtype, float p, const uint64_t* seed,
+                                  uint64_t offset, size_t firstRow, vrcclStream_t stream);
+
+/*
+ * vrcclDropoutBackward -- dx = kept ? dy * scale : 0 under the mask that the
+ * forward call with the same p, seed, offset, firstRow and cols drew (the
+ * residual's gradient is dy itself).
+ *   dy, dx  [rows, cols] of dtype; dx may be dy (same stride).
+ */
+vrcclResult_t vrcclDropoutBackward(const void* dy, size_t lddy, void* dx, size_t lddx, size_t rows, size_t cols,
+                                   vrcclDataType_t dtype, float p, const uint64_t* seed, uint64_t offset, size_t firstRow,
+                                   vrcclStream_t stream);
+
+/* 8-bit codes of the RMS norm: int8 (-127 to 127), or e4m3 (4 exponent and 3
+ * fraction bits, largest 448). */
+typedef enum {
+  vrcclQuantInt8 = 0,
+  vrcclQuantE4M3 = 1,
+  vrcclNumQuants = 2
+} vrcclQuant_t;
+
+/*
+ * vrcclRmsNormForward -- s = x + residual, rounded to dtype, and
+ * y = s * rstd * gamma, rstd = 1 / sqrt(mean(s^2) + eps) over the columns of
+ * each row.
+ *   x, residual  [rows, cols] of dtype; residual may be NULL (s = x).
+ *   gamma        [cols] of paramType, or NULL (1).
+ *   sum          out, [rows, cols] of dtype: s, what the backward pass and the
+ *                next addition take; or NULL.
+ *   y            out, [rows, cols] of dtype, or NULL where codes are asked for.
+ *                sum and y may each be x or residual (same stride), not both
+ *                the same one.
+ *   codes        out, [rows, cols] bytes, or NULL: y in 8 bits, code = y /
+ *                scale rounded to the nearest (even) int8 or e4m3.
+ *   scales       out, binary32 [rows, ceil(cols / group)], what a code is
+ *                multiplied by: the largest |y| of the group (unrounded) over
+ *                the largest code, at least 2^-126. Not finite where a y of the
+ *                group is not.
+ *   quant, group read with codes alone: the codes' type, and how many columns
+ *                share a scale: 32, 64, 128, or 0 for the whole row.
+ *   rstd         out, [rows] binary32, what the backward pass takes; or NULL.
+ *   rows, cols   0 of either -> success, nothing launched.
+ *   eps          >= 0.
+ * vrcclAllGather carries codes as vrcclInt8 or vrcclUint8.
+ */
+vrcclResult_t vrcclRmsNormForward(const void* x, size_t ldx, const void* residual, size_t ldr, const void* gamma,
+                                  void* sum, size_t lds, void* y, size_t ldy, void* codes, size_t ldc, float* scales,
+                                  size_t ldsc, float* rstd, size_t rows, size_t cols, vrcclDataType_t dtype,
+                                  vrcclDataType_t paramType, vrcclQuant_t quant, size_t group, float eps,
+                                  vrcclStream_t stream);
+
+/* vrcclRmsNormWorkspace -- bytes of workspace the backward pass of this size
+ * needs (the partial sums of the weight's gradient). */
+vrcclResult_t vrcclRmsNormWorkspace(size_t rows, size_t cols, size_t* bytes);
+
+/*
+ * vrcclRmsNormBackward -- with xh = s * rstd and g = dy * gamma:
+ *   dx = dsum + rstd * (g - xh * mean(g * xh))      per row
+ *   dgamma = sum over rows of dy * xh
+ * dx is the gradient of x and of residual alike. Codes pass the gradient on as
+ * if they were y.
+ *   dy, s, dx  [rows, cols] of dtype; s as the forward pass wrote (or took) it;
+ *              dx may be dy, dsum or s (same stride).
+ *   dsum       [rows, cols]: the gradient that reaches s other than through
+ *              the norm, or NULL (0).
+ *   gamma      [cols] of paramType, or NULL (1).
+ *   rstd       [rows], as the forward pass wrote it.
+ *   dgamma     out, [cols] of paramType, or NULL. With rows == 0 it is set to
+ *              zero.
+ *   workspace  16-byte aligned, vrcclRmsNormWorkspace bytes; NULL where dgamma
+ *              is not asked for.
+ */
+vrcclResult_t vrcclRmsNormBackward(const void* dy, size_t lddy, const void* dsum, size_t ldds, const void* s, size_t lds,
+                                   const void* gamma, const float* rstd, void* dx, size_t lddx, void* dgamma, size_t rows,
+                                   size_t cols, vrcclDataType_t dtype, vrcclDataType_t paramType, void* workspace,
+                                   size_t workspaceBytes, vrcclStream_t stream);
+
+/* Most alternatives a row of vrcclLogProbForward lists. */
+#define VRCCL_LOGPROB_MAX_K 32
+
+/*
+ * vrcclLogProbForward -- with q = softmax(logits / T) over the vocabulary:
+ *   logprob = log q[token],  entropy = - sum of q * log q,
+ * and the k likeliest entries.
+ *   logits    [rows, vocab] of dtype.
+ *   token     [rows] of tokenType (vrcclInt32 or vrcclInt64), or NULL: none
+ *             are given (logprob is then NULL too). A row whose token lies
+ *             outside [0, vocab) is a padding position: its logits count for
+ *             nothing, its logprob, entropy and stats are 0.
+ *   logprob, entropy  out, [rows] binary32; either may be NULL.
+ *   stats     out, [rows, 2] binary32, 8-byte aligned, or NULL: the row's
+ *             largest logit and the logarithm of the sum of
+ *             exp((logits - largest) / T), what the backward pass takes.
+ *   top, topIndex  out, [rows, k] binary32 and 32-bit integers: the log
+ *             probabilities and indices of the k largest logits, the largest
+ *             first, equal ones by the lowest index (zeros of either sign are
+ *             equal; a NaN counts as the largest). Where there are fewer (k >
+ *             vocab, a padding position): -inf and -1. NULL with k == 0.
+ *   k         0 to VRCCL_LOGPROB_MAX_K.
+ *   temperature  1e-18 to 1e18.
+ * Masked logits may be -inf or the type's lowest value. A row of nothing but
+ * -inf has no distribution: logprob -inf, entropy 0, stats (-inf, 0). A NaN or
+ * +inf among the logits makes the row's values NaN.
+ */
+vrcclResult_t vrcclLogProbForward(const void* logits, size_t ldl, const void* token, float* logprob, float* entropy,
+                                  float* stats, float* top, size_t ldt, int32_t* topIndex, size_t ldi, size_t rows,
+                                  size_t vocab, size_t k, vrcclDataType_t dtype, vrcclDataType_t tokenType,
+                                  float temperature, vrcclStream_t stream);
+
+/*
+ * vrcclLogProbBackward -- the gradient of logprob and entropy,
+ *   dlogits[v] = (dlogprob * ((v == token) - q[v]) - dentropy * q[v] * (log q[v] + entropy)) / T,
+ * zero at padding positions and in rows of nothing but -inf. (The
+ * alternatives are for reading; no gradient flows through them.)
+ *   stats, entropy  as the forward pass wrote them; entropy is read with
+ *             dentropy alone.
+ *   dlogprob  binary32, row r's at dlogprob[r * dlogprobStride] (stride 0: one
+ *             value for all rows), or NULL (0); needs token.
+ *   dentropy  likewise; one of the two is given.
+ *   token     as forward (NULL if none were given).
+ *   dlogits   out, [rows, vocab] of dtype; may be logits (same stride).
+ */
+vrcclResult_t vrcclLogProbBackward(const void* logits, size_t ldl, const void* token, const float* stats,
+                                   const float* entropy, const float* dlogprob, size_t dlogprobStride,
+                                   const float* dentropy, size_t dentropyStride, void* dlogits, size_t ldd, size_t rows,
+                                   size_t vocab, vrcclDataType_t dtype, vrcclDataType_t tokenType, float temperature,
+                                   vrcclStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -1,5 +1,6 @@
-"""The operators of a replica in 64 bits: layer norm, linear layer and
-distillation loss, forward and backward, each written from its definition.
+"""The operators of a replica in 64 bits: layer norm, linear layer,
+distillation loss, dropout, RMS norm and the log probabilities of tokens,
+forward and backward, each written from its definition.
 
 Everything takes and returns float64 arrays; what the library rounds (its
 inputs' type, the saved statistics) the caller rounds before the call.
@@ -103,4 +104,108 @@ def distill_backward(logits, teacher, index, dloss, T):
             out[r] = np.exp(logq)
             np.subtract.at(out[r], index[r][kept], p)
             out[r] *= dloss[r] * T
+    return out
+
+
+# ------------------------------------------------------------ dropout
+
+def philox(key, counter, stream):
+    """The four 32-bit words of Philox4x32-10 (Salmon et al., 2011), in Python integers."""
+    low = (1 << 32) - 1
+    k = [key & low, key >> 32 & low]
+    c = [counter & low, counter >> 32 & low, stream & low, stream >> 32 & low]
+    for _ in range(10):
+        p, q = 0xD2511F53 * c[0], 0xCD9E8D57 * c[2]
+        c = [q >> 32 ^ c[1] ^ k[0], q & low, p >> 32 ^ c[3] ^ k[1], p & low]
+        k = [k[0] + 0x9E3779B9 & low, k[1] + 0xBB67AE85 & low]
+    return c
+
+
+def dropout_mask(rows, cols, p, seed, offset, first_row):
+    """(kept, scale)."""
+    drop, per = int(p * 65536 + 0.5), -(-cols // 8)
+    kept = np.zeros((rows, per * 8), bool)
+    for r in range(rows):
+        for n in range(per):
+            words = philox(seed, (first_row + r) * per + n, offset)
+            for e in range(8):
+                kept[r, 8 * n + e] = (words[e // 2] >> 16 * (e % 2) & 0xFFFF) >= drop
+    return kept[:, :cols], 65536 / (65536 - drop) if drop < 65536 else 0.0
+
+
+def dropout(x, residual, p, seed, offset=0, first_row=0):
+    kept, scale = dropout_mask(*x.shape, p, seed, offset, first_row)
+    return np.where(kept, x * scale, 0.0) + residual
+
+
+# ------------------------------------------------------------ RMS norm
+
+def rms_forward(s, gamma, eps):
+    """(y, rstd) of the sum s."""
+    rstd = 1 / np.sqrt((s ** 2).mean(1) + eps)
+    return s * rstd[:, None] * gamma, rstd
+
+
+def rms_backward(dy, dsum, s, gamma, rstd):
+    """(dx, dgamma)."""
+    xh, g = s * rstd[:, None], dy * gamma
+    dx = dsum + rstd[:, None] * (g - xh * (g * xh).sum(1, keepdims=True) / s.shape[1])
+    return dx, (dy * xh).sum(0)
+
+
+def group_scales(y, quant, group):
+    """[rows, groups]: the largest |y| of each group of columns over the largest code."""
+    group = group or y.shape[1]
+    most = np.stack([np.abs(y[:, at:at + group]).max(1) for at in range(0, y.shape[1], group)], 1)
+    return np.maximum(most / {"int8": 127.0, "e4m3": 448.0}[quant], 2.0 ** -126)
+
+
+# ------------------------------------------------------------ log probabilities of tokens
+
+def _logq(s, T):
+    """log softmax(s / T) of one row, or None where all of it is -inf."""
+    if s.size == 0 or (s == -np.inf).all():
+        return None
+    x = (s - s.max()) / T
+    return x - logsumexp(x)
+
+
+def logprob_forward(logits, token, k, T):
+    """(logprob, entropy, stats, top, index); a token of None: none are given."""
+    n, vocab = logits.shape
+    logprob, entropy, stats = np.zeros(n), np.zeros(n), np.zeros((n, 2))
+    top, index = np.full((n, k), -np.inf), np.full((n, k), -1)
+    for r, s in enumerate(logits):
+        if token is not None and not 0 <= token[r] < vocab:
+            continue
+        logq = _logq(s, T)
+        if logq is None:
+            stats[r], logprob[r] = (-np.inf, 0), -np.inf
+            logq = np.full(vocab, -np.inf)
+        else:
+            q = np.exp(logq)
+            entropy[r] = -np.sum(np.where(q > 0, q * np.where(q > 0, logq, 0), 0.0 if not np.isnan(q).any() else np.nan))
+            logprob[r] = logq[token[r]] if token is not None else 0
+            with np.errstate(invalid="ignore"):
+                stats[r] = s.max(), np.log(np.sum(np.exp((s - s.max()) / T)))
+        if k == 0:
+            continue
+        nan = np.isnan(s)
+        order = np.lexsort((np.arange(vocab), np.where(nan, 0, -s), ~nan))[:k]  # NaN first, the largest, the lowest index
+        top[r, :len(order)], index[r, :len(order)] = logq[order], order
+    return logprob, entropy, stats, top, index
+
+
+def logprob_backward(logits, token, dlogprob, dentropy, T):
+    """dlogits."""
+    out = np.zeros_like(logits)
+    for r, s in enumerate(logits):
+        logq = _logq(s, T)
+        if logq is None or (token is not None and not 0 <= token[r] < s.size):
+            continue
+        q, known = np.exp(logq), np.where(np.exp(logq) > 0, logq, 0)
+        out[r] = -dlogprob[r] * q - dentropy[r] * q * (known - np.sum(q * known))
+        if token is not None:
+            out[r, token[r]] += dlogprob[r]
+        out[r] /= T
     return out

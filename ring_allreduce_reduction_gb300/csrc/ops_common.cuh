@@ -50,8 +50,9 @@ inline Span unlessInPlace(const Span& in, size_t ldin, const void* out, size_t l
   return in.p == out && ldin == ldout ? vectorSpan(nullptr, 0) : in;
 }
 
-// A failed wait of the layer norm's kernels (each translation unit holds its own device-side word).
+// A failed wait of the layer norm's and the RMS norm's kernels (each translation unit holds its own device-side word).
 int normStatus(int* code);
+int rmsStatus(int* code);
 // Multiprocessors of the current device (asked for once a device).
 int smCount();
 // Lets a kernel's blocks ask for all the dynamic shared memory there is on the current device; once a kernel and device.
@@ -137,6 +138,39 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return d;
 }
 
+// V parameters from column c on; `wide`: one 16- or 8-byte load a group, which
+// the caller allows where the parameters start on a 16-byte boundary.
+template <int V>
+__device__ __forceinline__ void loadParams(const void* p, int ptype, bool wide, int c, float dflt, float (&f)[V]) {
+  if (!p) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) f[e] = dflt;
+    return;
+  }
+  if constexpr (V >= 4) {
+    if (wide && ptype == vrcclFloat32) {
+#pragma unroll
+      for (int e = 0; e < V; e += 4) {
+        const float4 q = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + c + e));
+        f[e] = q.x, f[e + 1] = q.y, f[e + 2] = q.z, f[e + 3] = q.w;
+      }
+      return;
+    }
+    if (wide) {
+#pragma unroll
+      for (int e = 0; e < V; e += 4) {
+        const uint2 q = __ldg(reinterpret_cast<const uint2*>(static_cast<const unsigned short*>(p) + c + e));
+        const float2 lo = ptype == vrcclBfloat16 ? unpack2<vrcclBfloat16>(q.x) : unpack2<vrcclFloat16>(q.x);
+        const float2 hi = ptype == vrcclBfloat16 ? unpack2<vrcclBfloat16>(q.y) : unpack2<vrcclFloat16>(q.y);
+        f[e] = lo.x, f[e + 1] = lo.y, f[e + 2] = hi.x, f[e + 3] = hi.y;
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < V; ++e) f[e] = loadParam(p, ptype, c + e);
+}
+
 // A 16-byte vector of elements <-> binary32.
 template <int DT>
 struct Vec16 {
@@ -195,6 +229,35 @@ __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
   F2 r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
+}
+
+// exp for the long sums: 2^x on the special function unit, relative error about
+// 2^-22 of its own; the rounding of its argument adds |x| 2^-24, so that a
+// term of 2^-100 is off by 2^-17 of itself. The terms that make up a sum have
+// small arguments, and their errors average out.
+__device__ __forceinline__ float fastExp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// The larger of two, NaN if either is.
+__device__ __forceinline__ float maxOrNan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+// The larger of the elements of two words (2-byte types); a NaN loses.
+template <int DT>
+__device__ __forceinline__ uint32_t maxPacked(uint32_t a, uint32_t b) {
+  uint32_t d;
+  if constexpr (DT == vrcclBfloat16)
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  else
+    asm("max.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
 }
 
 // ------------------------------------------------------------ reductions

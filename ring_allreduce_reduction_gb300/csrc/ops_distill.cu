@@ -132,18 +132,6 @@ __device__ __forceinline__ Running warpJoin(Running r, float invT) {
   return r;
 }
 
-// exp for the long sums: 2^x on the special function unit, relative error about
-// 2^-22 of its own; the rounding of its argument adds |x| 2^-24, so that a
-// term of 2^-100 is off by 2^-17 of itself. The terms that make up a sum have
-// small arguments, and their errors average out.
-__device__ __forceinline__ float fastExp2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-constexpr float kLog2e = 1.4426950408889634f;
-
 template <int N>
 __device__ __forceinline__ void runOver(Running& r, const float (&f)[N], float c) {  // c = invT log2(e)
   float top = f[0];

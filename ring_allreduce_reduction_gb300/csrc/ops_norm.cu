@@ -30,8 +30,7 @@
 // (3.1 TB/s), bound by issue slots.
 #include <mutex>
 
-#include "ops_common.cuh"
-#include "ops_rows.h"
+#include "ops_ring.cuh"
 
 namespace vrccl {
 namespace {
@@ -93,39 +92,6 @@ struct Held {
   }
 };
 
-// V parameters from column c on; `wide`: one 16- or 8-byte load a group, which
-// the caller allows where the parameters start on a 16-byte boundary.
-template <int V>
-__device__ __forceinline__ void loadParams(const void* p, int ptype, bool wide, int c, float dflt, float (&f)[V]) {
-  if (!p) {
-#pragma unroll
-    for (int e = 0; e < V; ++e) f[e] = dflt;
-    return;
-  }
-  if constexpr (V >= 4) {
-    if (wide && ptype == vrcclFloat32) {
-#pragma unroll
-      for (int e = 0; e < V; e += 4) {
-        const float4 q = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + c + e));
-        f[e] = q.x, f[e + 1] = q.y, f[e + 2] = q.z, f[e + 3] = q.w;
-      }
-      return;
-    }
-    if (wide) {
-#pragma unroll
-      for (int e = 0; e < V; e += 4) {
-        const uint2 q = __ldg(reinterpret_cast<const uint2*>(static_cast<const unsigned short*>(p) + c + e));
-        const float2 lo = ptype == vrcclBfloat16 ? unpack2<vrcclBfloat16>(q.x) : unpack2<vrcclFloat16>(q.x);
-        const float2 hi = ptype == vrcclBfloat16 ? unpack2<vrcclBfloat16>(q.y) : unpack2<vrcclFloat16>(q.y);
-        f[e] = lo.x, f[e + 1] = lo.y, f[e + 2] = hi.x, f[e + 3] = hi.y;
-      }
-      return;
-    }
-  }
-#pragma unroll
-  for (int e = 0; e < V; ++e) f[e] = loadParam(p, ptype, c + e);
-}
-
 // ------------------------------------------------------------ teams
 // Rows of up to 8192 elements. A block of up to 512 threads is cut into teams
 // of a few warps, 16 elements of a row a thread; every team walks rows of its
@@ -136,11 +102,7 @@ __device__ __forceinline__ void loadParams(const void* p, int ptype, bool wide, 
 // the stage, and the team's first thread refills it.
 constexpr int kTeamElems = 16;
 constexpr int kTeamCols = 512 * kTeamElems;
-constexpr int kMaxStages = 8;
 constexpr int kTeamSmem = 192 * 1024, kWideSmem = 224 * 1024;  // of the 227 KB a block may have
-constexpr long long kRowWaitCycles = 3000000000ll, kDrainCycles = 200000000ll;  // a second and more
-
-__device__ int gNormStatus;  // vrcclResult_t of the first device-side failure
 
 __host__ __device__ constexpr int slotBytes(int cols, int E) { return ((cols * E + 15) / 16 + 1) * 16; }
 
@@ -270,28 +232,6 @@ __device__ __forceinline__ void teamSync(int team) {
     __syncwarp();
   else
     asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(T) : "memory");
-}
-// Sets *dead (givenUpWord) when the copy has not come after a time in which it must have.
-__device__ __forceinline__ void waitRow(unsigned long long* bar, unsigned parity, int* dead, int turn,
-                                        long long limit = kRowWaitCycles) {
-  if (mbarTryWait(bar, parity)) return;
-  const long long t0 = clock64();
-  while (!mbarTryWait(bar, parity))
-    if (clock64() - t0 > limit) {
-      *reinterpret_cast<volatile int*>(dead) = givenUpWord(turn);
-      return;
-    }
-}
-// Given up with the ring at (stage, round): records it, and lets no copy that
-// is in flight land after the block has gone.
-__device__ __noinline__ void abandon(unsigned long long* full, int stages, int stage, int round, bool first, int* dead,
-                                     int turn) {
-  if (!first) return;
-  atomicCAS(&gNormStatus, 0, (int)vrcclTimeout);
-  for (int s = 0; s < stages; ++s) waitRow(&full[s], (round + (s < stage ? 1 : 0)) & 1, dead, turn, kDrainCycles);
-}
-__device__ __forceinline__ void expectBytes(unsigned long long* bar, unsigned bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smemAddr(bar)), "r"(bytes) : "memory");
 }
 
 // Two rows a turn, so that one row's reduction hides the other's latency and
@@ -1240,7 +1180,7 @@ bool goodSizes(size_t rows, size_t cols, int dtype, int ptype) {
 
 }  // namespace
 
-int normStatus(int* code) { return cudaMemcpyFromSymbol(code, gNormStatus, sizeof(*code)); }
+int normStatus(int* code) { return cudaMemcpyFromSymbol(code, gRingStatus, sizeof(*code)); }
 
 vrcclResult_t allowSharedMemory(const void* fn) {
   static std::mutex mu;

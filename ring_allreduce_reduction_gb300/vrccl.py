@@ -36,13 +36,15 @@ MAX_RANKS = 128
 MAX_CHANNELS = 64
 STEPS = 16
 DISTILL_MAX_K = 1024
+LOGPROB_MAX_K = 32
+QUANTS = {"int8": 0, "e4m3": 1}
 
 _TORCH_DTYPES = {torch.int32: "int32", torch.float32: "float32", torch.bfloat16: "bfloat16",
                  torch.float16: "float16", torch.int8: "int8", torch.uint8: "uint8", torch.int64: "int64",
                  torch.float64: "float64"}
 
 _c_int_p = ctypes.POINTER(ctypes.c_int)
-_p, _z, _i, _f = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.c_float
+_p, _z, _i, _f, _u64 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.c_float, ctypes.c_uint64
 _sig = {
     "vrcclCommInit": [ctypes.POINTER(ctypes.c_void_p), ctypes.c_int, ctypes.c_int],
     "vrcclAllReduce": [ctypes.POINTER(ctypes.c_void_p), ctypes.POINTER(ctypes.c_void_p), ctypes.c_size_t,
@@ -84,6 +86,13 @@ _sig = {
     "vrcclReplicaGetAsyncError": [_c_int_p],
     "vrcclDistillForward": [_p, _z, _p, _z, _p, _z, _p, _p, _z, _z, _z, _i, _i, _i, _f, _p],
     "vrcclDistillBackward": [_p, _z, _p, _z, _p, _z, _p, _p, _z, _p, _z, _z, _z, _z, _i, _i, _i, _f, _p],
+    "vrcclDropoutForward": [_p, _z, _p, _z, _p, _z, _z, _z, _i, _f, _p, _u64, _z, _p],
+    "vrcclDropoutBackward": [_p, _z, _p, _z, _z, _z, _i, _f, _p, _u64, _z, _p],
+    "vrcclRmsNormForward": [_p, _z, _p, _z, _p, _p, _z, _p, _z, _p, _z, _p, _z, _p, _z, _z, _i, _i, _i, _z, _f, _p],
+    "vrcclRmsNormWorkspace": [_z, _z, ctypes.POINTER(_z)],
+    "vrcclRmsNormBackward": [_p, _z, _p, _z, _p, _z, _p, _p, _p, _z, _p, _z, _z, _i, _i, _p, _z, _p],
+    "vrcclLogProbForward": [_p, _z, _p, _p, _p, _p, _p, _z, _p, _z, _z, _z, _z, _i, _i, _f, _p],
+    "vrcclLogProbBackward": [_p, _z, _p, _p, _p, _p, _z, _p, _z, _p, _z, _z, _z, _i, _i, _f, _p],
 }
 for _name, _args in _sig.items():
     _fn = getattr(_lib, _name)
@@ -481,6 +490,86 @@ def vrcclDistillBackward(logits, teacher, index, stats, dloss, dlogits, rows: in
     _check(_lib.vrcclDistillBackward(logits, ldl, teacher, ldt, index, ldi, _vec(stats, _F32), dloss,
                                      dloss_stride, dlogits, ldd, rows, vocab, k, e, te, ie, temperature,
                                      _stream(stream)), "vrcclDistillBackward")
+
+
+# The codes' torch type of each name and enum value.
+_CODES = {key: (val, td) for (name, val), td in zip(QUANTS.items(), (torch.int8, torch.float8_e4m3fn)) for key in (name, val)}
+
+
+def vrcclDropoutForward(x, residual, y, rows: int, cols: int, dtype, p: float, seed, offset: int = 0, first_row: int = 0,
+                        ldx: int | None = None, ldr: int | None = None, ldy: int | None = None, stream=None) -> None:
+    """``seed``: an int64 tensor of one element on the GPU."""
+    e, td = _DT[dtype]
+    (x, ldx), (residual, ldr) = _mat(x, td, rows, cols, ldx), _mat(residual, td, rows, cols, ldr)
+    y, ldy = _mat(y, td, rows, cols, ldy)
+    _check(_lib.vrcclDropoutForward(x, ldx, residual, ldr, y, ldy, rows, cols, e, p, _vec(seed, torch.int64), offset,
+                                    first_row, _stream(stream)), "vrcclDropoutForward")
+
+
+def vrcclDropoutBackward(dy, dx, rows: int, cols: int, dtype, p: float, seed, offset: int = 0, first_row: int = 0,
+                         lddy: int | None = None, lddx: int | None = None, stream=None) -> None:
+    e, td = _DT[dtype]
+    (dy, lddy), (dx, lddx) = _mat(dy, td, rows, cols, lddy), _mat(dx, td, rows, cols, lddx)
+    _check(_lib.vrcclDropoutBackward(dy, lddy, dx, lddx, rows, cols, e, p, _vec(seed, torch.int64), offset, first_row,
+                                     _stream(stream)), "vrcclDropoutBackward")
+
+
+def vrcclRmsNormForward(x, residual, gamma, sum, y, rstd, rows: int, cols: int, dtype, ptype, eps: float = 1e-5, codes=None,
+                        scales=None, quant="int8", group: int = 0, ldx: int | None = None, ldr: int | None = None,
+                        lds: int | None = None, ldy: int | None = None, ldc: int | None = None,
+                        ldscales: int | None = None, stream=None) -> None:
+    """``codes``: int8 or float8_e4m3fn (as ``quant`` says), ``scales`` [rows, groups]."""
+    (e, td), (pe, ptd) = _DT[dtype], _DT[ptype]
+    (x, ldx), (residual, ldr) = _mat(x, td, rows, cols, ldx), _mat(residual, td, rows, cols, ldr)
+    (sum, lds), (y, ldy) = _mat(sum, td, rows, cols, lds), _mat(y, td, rows, cols, ldy)
+    q = 0
+    if codes is not None or scales is not None:
+        q, ctd = _CODES[quant] if quant in _CODES else (_enum(QUANTS, quant, "quantisation"), None)
+        groups = -(-cols // group) if group > 0 else 1
+        (codes, ldc), (scales, ldscales) = _mat(codes, ctd, rows, cols, ldc), _mat(scales, _F32, rows, groups, ldscales)
+    _check(_lib.vrcclRmsNormForward(x, ldx, residual, ldr, _vec(gamma, ptd), sum, lds, y, ldy, codes, ldc or 0, scales,
+                                    ldscales or 0, _vec(rstd, _F32), rows, cols, e, pe, q, group, eps, _stream(stream)),
+           "vrcclRmsNormForward")
+
+
+def vrcclRmsNormWorkspace(rows: int, cols: int) -> int:
+    n = ctypes.c_size_t()
+    _check(_lib.vrcclRmsNormWorkspace(rows, cols, ctypes.byref(n)), "vrcclRmsNormWorkspace")
+    return n.value
+
+
+def vrcclRmsNormBackward(dy, dsum, s, gamma, rstd, dx, dgamma, rows: int, cols: int, dtype, ptype, workspace=None,
+                         workspace_bytes: int = 0, lddy: int | None = None, lddsum: int | None = None,
+                         lds: int | None = None, lddx: int | None = None, stream=None) -> None:
+    (e, td), (pe, ptd) = _DT[dtype], _DT[ptype]
+    (dy, lddy), (dsum, lddsum) = _mat(dy, td, rows, cols, lddy), _mat(dsum, td, rows, cols, lddsum)
+    (s, lds), (dx, lddx) = _mat(s, td, rows, cols, lds), _mat(dx, td, rows, cols, lddx)
+    _check(_lib.vrcclRmsNormBackward(dy, lddy, dsum, lddsum, s, lds, _vec(gamma, ptd), _vec(rstd, _F32), dx, lddx,
+                                     _vec(dgamma, ptd), rows, cols, e, pe, _scratch(workspace, workspace_bytes),
+                                     workspace_bytes, _stream(stream)), "vrcclRmsNormBackward")
+
+
+def vrcclLogProbForward(logits, token, logprob, entropy, stats, top, top_index, rows: int, vocab: int, k: int, dtype,
+                        token_dtype, temperature: float = 1.0, ldl: int | None = None, ldt: int | None = None,
+                        ldi: int | None = None, stream=None) -> None:
+    (e, td), (te, ttd) = _DT[dtype], _DT[token_dtype]
+    logits, ldl = _mat(logits, td, rows, vocab, ldl)
+    (top, ldt), (top_index, ldi) = _mat(top, _F32, rows, k, ldt), _mat(top_index, torch.int32, rows, k, ldi)
+    _check(_lib.vrcclLogProbForward(logits, ldl, _vec(token, ttd), _vec(logprob, _F32), _vec(entropy, _F32),
+                                    _vec(stats, _F32), top, ldt, top_index, ldi, rows, vocab, k, e, te, temperature,
+                                    _stream(stream)), "vrcclLogProbForward")
+
+
+def vrcclLogProbBackward(logits, token, stats, entropy, dlogprob, dentropy, dlogits, rows: int, vocab: int, dtype,
+                         token_dtype, temperature: float = 1.0, dlogprob_stride: int = 1, dentropy_stride: int = 1,
+                         ldl: int | None = None, ldd: int | None = None, stream=None) -> None:
+    (e, td), (te, ttd) = _DT[dtype], _DT[token_dtype]
+    (logits, ldl), (dlogits, ldd) = _mat(logits, td, rows, vocab, ldl), _mat(dlogits, td, rows, vocab, ldd)
+    dlogprob = _vec(dlogprob, _F32) if dlogprob_stride == 1 else _mat(dlogprob, _F32, rows, 1, dlogprob_stride)[0]
+    dentropy = _vec(dentropy, _F32) if dentropy_stride == 1 else _mat(dentropy, _F32, rows, 1, dentropy_stride)[0]
+    _check(_lib.vrcclLogProbBackward(logits, ldl, _vec(token, ttd), _vec(stats, _F32), _vec(entropy, _F32), dlogprob,
+                                     dlogprob_stride, dentropy, dentropy_stride, dlogits, ldd, rows, vocab, e, te, temperature,
+                                     _stream(stream)), "vrcclLogProbBackward")
 
 
 def raw_call(name: str, *args) -> int:
