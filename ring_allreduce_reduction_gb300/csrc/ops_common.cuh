@@ -249,14 +249,14 @@ __device__ __forceinline__ float maxOrNan(float a, float b) {
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
-// The larger of the elements of two words (2-byte types); a NaN loses.
+// The larger of the elements of two words (2-byte types), NaN if either is.
 template <int DT>
-__device__ __forceinline__ uint32_t maxPacked(uint32_t a, uint32_t b) {
+__device__ __forceinline__ uint32_t maxPackedOrNan(uint32_t a, uint32_t b) {
   uint32_t d;
   if constexpr (DT == vrcclBfloat16)
-    asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   else
-    asm("max.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
 

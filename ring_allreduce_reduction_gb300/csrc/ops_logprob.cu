@@ -8,20 +8,29 @@
 //   d logprob / d s_v = (1[v = token] - q_v) / T
 //   d H / d s_v       = -q_v (log q_v + H) / T
 //
-// Forward reads the logits once: each thread keeps its largest logit m, the
-// sum l of exp(x) and the sum w of exp(x) x, rescaled when m grows:
-// with d = (m - m') / T, w' = (w + l d) exp(d), l' = l exp(d). Terms of
-// masked entries (-inf or the type's lowest value) are exp(-inf) x = 0: x is
-// held above -1000 (base 2), where its power is 0 in binary32. A NaN stays NaN
-// through that bound.
+// Forward reads the logits once. A thread keeps its largest logit m, the sum l
+// of 2^x and the sum w of 2^x x over what it has seen, where x = s c - M, c =
+// log2(e) / T and M is m c rounded: one operation for x, rounded once, and M's
+// own rounding is taken back exactly at the end (M - m c is one more). When m
+// grows by d (in units of x), w' = (w + l d) 2^d and l' = l 2^d. The passes are
+// bound by issue slots nearly as much as by memory, so that the loop looks at
+// nothing else: a product of 0 and -inf (a masked entry), an M beyond binary32
+// or a NaN leave w not finite, and the thread then takes the step back and goes
+// on with care: x = (s - m) c, held above -1000, where 2^x and 2^x x are 0. A
+// NaN stays NaN through that bound. So do rows whose M is no longer small
+// beside 2^24.
 //
-// The k likeliest entries, in the order (larger logit, lower index), are found
-// from the largest logits m_t that the threads hold anyway: the k-th largest
-// of them is a bound that k entries reach, and so do all of the k wanted. The
-// few threads whose m_t reaches it have their elements read once more (about
-// k of 512 threads' shares, mostly from L2), a warp a share, each warp keeping its best in order, one a
-// lane; the warps' lists (and the blocks') are merged two and two. Whatever
-// the logits hold, the lists are right: ties only mean more shares to read.
+// The k likeliest entries, in the order (larger logit, lower index). A warp's
+// load reads 512 bytes of the row, and the largest logit of such a segment (or
+// of a few after one another) costs one reduction over the lanes. Of the
+// segments in the order (larger largest logit, lower index) the first k hold
+// all the k entries wanted: fewer than k have a larger logit than the k-th
+// one's, and an entry equal to that has as many of lower index before it. Those
+// segments are read once more by the whole block, and what reaches the k-th
+// one's largest (k entries do) is collected; places, of segments and of
+// entries, are counts of what is above. Of ties there may be too many to
+// collect (a row of one value): each warp then keeps its best in order, one a
+// lane, and the warps' lists are merged two and two.
 //
 // Backward reads the logits and writes the gradient; the statistics are saved,
 // so that a row may be cut into independent slices.
@@ -30,6 +39,8 @@
 // of zero; rows of nothing but -inf have no distribution: logprob -inf, entropy
 // 0, gradient 0.
 #include <cooperative_groups.h>
+
+#include <type_traits>
 
 #include "ops_common.cuh"
 
@@ -40,6 +51,9 @@ namespace cg = cooperative_groups;
 
 constexpr int kThreads = 512;  // of a block, at most
 constexpr int kUnroll = 4;     // vectors a thread asks for at once
+constexpr int kPass = 32 * kUnroll;  // vectors of a warp's pass
+constexpr int kSegments = 512;       // of a block's part of a row, at most
+constexpr int kCollected = 512;      // entries, at most
 constexpr float kFloor = -1000.f;  // 2^-1000 is 0 in binary32, and its product with -1000 too
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -56,7 +70,7 @@ struct LogProbArgs {
   void* dlogits;
   size_t ldl, ldt, ldi, ldd, lstride, hstride, vocab;
   size_t slice;  // backward: elements of a row one block takes
-  int k;
+  int k, span, shift;  // span: loads of a segment, 2^shift
   bool wide;  // 64-bit tokens
   float temperature, invT;
 };
@@ -68,83 +82,6 @@ __device__ __forceinline__ long long tokenOf(const LogProbArgs& a, size_t row) {
   return t >= 0 && (unsigned long long)t < a.vocab ? t : -2;
 }
 
-// m, the sum l of 2^x and the sum w of 2^x x, x = (s - m) c.
-struct Sums {
-  float m, l, w;
-};
-// (s - m) c, no lower than kFloor; NaN stays.
-__device__ __forceinline__ float scaled(float d, float c) { return maxOrNan(d * c, kFloor); }
-__device__ __forceinline__ Sums joined(const Sums& a, const Sums& b, float c) {
-  Sums r;
-  r.m = fmaxf(a.m, b.m);
-  if (r.m == -INFINITY) return {r.m, a.l + b.l, a.w + b.w};  // nothing above -inf: both zero, or NaN
-  const float da = a.m == r.m ? 0.f : scaled(a.m - r.m, c), db = b.m == r.m ? 0.f : scaled(b.m - r.m, c);
-  const float ea = exp2f(da), eb = exp2f(db);
-  r.l = a.l * ea + b.l * eb;
-  r.w = (a.w + a.l * da) * ea + (b.w + b.l * db) * eb;
-  return r;
-}
-__device__ __forceinline__ Sums warpJoin(Sums r, float c) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    Sums b;
-    b.m = __shfl_xor_sync(0xffffffffu, r.m, o);
-    b.l = __shfl_xor_sync(0xffffffffu, r.l, o);
-    b.w = __shfl_xor_sync(0xffffffffu, r.w, o);
-    // the same order on both sides: every lane has the same bits
-    r = (threadIdx.x & o) ? joined(b, r, c) : joined(r, b, c);
-  }
-  return r;
-}
-
-template <int DT>
-__device__ __forceinline__ float largestOf(const uint4& v) {
-  if constexpr (DT == vrcclFloat32) {
-    return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)), fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
-  } else {  // two at a time; a NaN loses
-    const uint32_t p = maxPacked<DT>(maxPacked<DT>(v.x, v.y), maxPacked<DT>(v.z, v.w));
-    const float2 f = unpack2<DT>(p);
-    return fmaxf(f.x, f.y);
-  }
-}
-
-template <int N>
-__device__ __forceinline__ void runOver(Sums& r, const float (&f)[N], float top, float c) {
-  if (top > r.m) {
-    const float d = scaled(r.m - top, c), e = fastExp2(d);  // l and w are 0 while m is -inf
-    r.w = (r.w + r.l * d) * e;
-    r.l *= e;
-    r.m = top;
-  }
-  if (r.m == -INFINITY) {  // nothing above -inf so far
-#pragma unroll
-    for (int i = 0; i < N; ++i) r.l += f[i] == f[i] ? 0.f : NAN;
-  } else if constexpr (N % 2 == 0) {
-    const F2 minus = pair(-r.m, -r.m), cc = pair(c, c);
-    F2 l = 0, w = 0;
-#pragma unroll
-    for (int i = 0; i < N; i += 2) {
-      float2 x = split(mul2(add2(pair(f[i], f[i + 1]), minus), cc));
-      x.x = maxOrNan(x.x, kFloor);
-      x.y = maxOrNan(x.y, kFloor);
-      const F2 e = pair(fastExp2(x.x), fastExp2(x.y));
-      l = add2(l, e);
-      w = fma2(e, pair(x.x, x.y), w);
-    }
-    const float2 a = split(l), b = split(w);
-    r.l += a.x + a.y;
-    r.w += b.x + b.y;
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const float x = scaled(f[i] - r.m, c), e = fastExp2(x);
-      r.l += e;
-      r.w = fmaf(e, x, r.w);
-    }
-  }
-}
-
-// ------------------------------------------------------------ the likeliest entries
 // A key orders entries as the list does: the logit's bits made ascending (zeros of either sign alike, a NaN above
 // everything) over the inverted index. 0: no entry.
 using Key = unsigned long long;
@@ -153,41 +90,161 @@ __device__ __forceinline__ uint32_t ascending(float s) {
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 __device__ __forceinline__ float fromAscending(uint32_t u) { return __uint_as_float(u & 0x80000000u ? u & 0x7fffffffu : ~u); }
+
+// m, the sum l of 2^x and the sum w of 2^x x, x = (s - m) c.
+struct Sums {
+  float m, l, w;
+};
+// (s - m) c, no lower than kFloor; NaN stays.
+__device__ __forceinline__ float scaled(float d, float c) { return maxOrNan(d * c, kFloor); }
+// Of a warp's lanes, in every lane: relative to the largest m, then added up.
+__device__ __forceinline__ Sums warpJoin(Sums r, float c) {
+  const float m = fromAscending(__reduce_max_sync(0xffffffffu, ascending(r.m)));
+  if (m != -INFINITY) {
+    const float d = r.m == m ? 0.f : scaled(r.m - m, c), e = fastExp2(d);
+    r.w = (r.w + r.l * d) * e;
+    r.l *= e;
+  }
+  const float2 s = warpSum2(make_float2(r.l, r.w));
+  return {m, s.x, s.y};
+}
+
+// The largest of a warp's lanes, NaN if one is.
+__device__ __forceinline__ float largestOfWarp(float x) {
+  float r;
+  asm("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+  return r;
+}
+template <int DT>
+__device__ __forceinline__ float largestOf(const uint4& v) {
+  if constexpr (DT == vrcclFloat32) {
+    return maxOrNan(maxOrNan(__uint_as_float(v.x), __uint_as_float(v.y)), maxOrNan(__uint_as_float(v.z), __uint_as_float(v.w)));
+  } else {  // two at a time
+    const uint32_t p = maxPackedOrNan<DT>(maxPackedOrNan<DT>(v.x, v.y), maxPackedOrNan<DT>(v.z, v.w));
+    const float2 f = unpack2<DT>(p);
+    return maxOrNan(f.x, f.y);
+  }
+}
+
+// With care: any values. Of the sums relative to m.
+template <int N>
+__device__ __forceinline__ void runOver(Sums& r, const float (&f)[N], float c) {
+  float top = f[0];
+#pragma unroll
+  for (int i = 1; i < N; ++i) top = fmaxf(top, f[i]);
+  if (top > r.m) {
+    const float d = scaled(r.m - top, c), e = fastExp2(d);  // l and w are 0 while m is -inf
+    r.w = (r.w + r.l * d) * e;
+    r.l *= e;
+    r.m = top;
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if (r.m == -INFINITY) {  // nothing above -inf so far
+      r.l += f[i] == f[i] ? 0.f : NAN;
+    } else {
+      const float x = scaled(f[i] - r.m, c), e = fastExp2(x);
+      r.l += e;
+      r.w = fmaf(e, x, r.w);
+    }
+  }
+}
+
+template <int DT>
+__device__ __noinline__ Sums withCare(Sums r, uint4 v, float c) {
+  float f[Vec16<DT>::N];
+  Vec16<DT>::expand(v, f);
+  runOver<Vec16<DT>::N>(r, f, c);
+  return r;
+}
+
+// A thread's running sums: relative to M (or to m, with care).
+struct Stream {
+  Sums s;
+  float M;
+  bool careful;
+};
+__device__ __forceinline__ Sums settled(const Stream& a, float c) {  // relative to m
+  if (a.careful || a.s.m == -INFINITY) return a.s;
+  const float d = fmaf(-a.s.m, c, a.M), e = exp2f(d);  // what M was rounded by
+  return {a.s.m, a.s.l * e, (a.s.w + a.s.l * d) * e};
+}
+template <int DT, int N>
+__device__ __forceinline__ float largestOf(const uint4 (&v)[N]) {  // NaN if one is
+  if constexpr (DT == vrcclFloat32) {
+    float top = largestOf<DT>(v[0]);
+#pragma unroll
+    for (int n = 1; n < N; ++n) top = maxOrNan(top, largestOf<DT>(v[n]));
+    return top;
+  } else {
+    uint4 p = v[0];
+#pragma unroll
+    for (int n = 1; n < N; ++n)
+      p = make_uint4(maxPackedOrNan<DT>(p.x, v[n].x), maxPackedOrNan<DT>(p.y, v[n].y), maxPackedOrNan<DT>(p.z, v[n].z), maxPackedOrNan<DT>(p.w, v[n].w));
+    return largestOf<DT>(p);
+  }
+}
+template <int DT, int N>
+__device__ __forceinline__ void runOver(Stream& a, const uint4 (&v)[N], float top, float c) {
+  constexpr int V = Vec16<DT>::N;
+  if (!a.careful) {
+    Sums r = a.s;
+    float M = a.M;
+    if (top > r.m) {
+      const float next = top * c, d = maxOrNan(M - next, kFloor), e = fastExp2(d);  // l and w are 0 while M is -inf
+      r.w = (r.w + r.l * d) * e;
+      r.l *= e;
+      r.m = top;
+      M = next;
+    }
+    const F2 cc = pair(c, c), minus = pair(-M, -M);
+    F2 l = 0, w = 0;
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      float f[V];
+      Vec16<DT>::expand(v[n], f);
+#pragma unroll
+      for (int i = 0; i < V; i += 2) {
+        const F2 x = fma2(pair(f[i], f[i + 1]), cc, minus);
+        const float2 y = split(x);
+        const F2 e = pair(fastExp2(y.x), fastExp2(y.y));
+        l = add2(l, e);
+        w = fma2(e, x, w);
+      }
+    }
+    const float2 p = split(l), q = split(w);
+    r.l += p.x + p.y;
+    r.w += q.x + q.y;
+    if (fabsf(r.w) < INFINITY && fabsf(M) < 0x1p24f) {  // (beyond, M's rounding is no small part of x)
+      a.s = r;
+      a.M = M;
+      return;
+    }
+    a.s = settled(a, c);  // as it was before these vectors
+    a.careful = true;
+  }
+#pragma unroll
+  for (int n = 0; n < N; ++n) a.s = withCare<DT>(a.s, v[n], c);
+}
+
+// ------------------------------------------------------------ the likeliest entries
 __device__ __forceinline__ Key keyOf(uint32_t value, size_t index) { return (Key)value << 32 | (uint32_t)~(uint32_t)index; }
 
-// Lists of 32, one entry a lane, the largest in lane 0.
-template <typename K>
-__device__ __forceinline__ K tidied(K a) {  // a bitonic list into order
+// Lists of 32, one entry a lane, the largest in lane 0: the 32 largest of two.
+__device__ __forceinline__ Key merged(Key a, const Key* other) {
   const int lane = threadIdx.x & 31;
+  a = max(a, other[31 - lane]);
 #pragma unroll
   for (int o = 16; o; o >>= 1) {
-    const K b = __shfl_xor_sync(0xffffffffu, a, o);
-    a = ((lane & o) == 0) == (a > b) ? a : b;
+    const Key b = __shfl_xor_sync(0xffffffffu, a, o);
+    a = (lane & o) == 0 ? max(a, b) : min(a, b);
   }
   return a;
 }
-template <typename K>
-__device__ __forceinline__ K sorted(K a) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int n = 2; n <= 32; n *= 2)
-#pragma unroll
-    for (int o = n / 2; o; o >>= 1) {
-      const K b = __shfl_xor_sync(0xffffffffu, a, o);
-      a = (((lane & o) == 0) == ((lane & n) == 0)) == (a > b) ? a : b;
-    }
-  return a;
-}
-// The 32 largest of two lists in order, in order.
-template <typename K>
-__device__ __forceinline__ K merged(K a, const K* other) {
-  const K b = other[31 - (threadIdx.x & 31)];
-  return tidied(a > b ? a : b);
-}
 // The block's warps' lists into warp 0's: each step the upper half hands its lists to the lower. All threads call it; `s`
-// holds 32 entries for each of warps / 2 warps.
-template <typename K, int WARPS>
-__device__ __forceinline__ K mergedOverWarps(K a, K* s) {
+// holds 32 entries for each of WARPS / 2 warps.
+template <int WARPS>
+__device__ __forceinline__ Key mergedOverWarps(Key a, Key* s) {
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
 #pragma unroll
   for (int half = WARPS / 2; half; half /= 2) {
@@ -213,139 +270,292 @@ __device__ __forceinline__ void insert(Key& list, Key& bound, Key candidate, int
     bound = last > bound ? last : bound;
   }
 }
-
-// T threads a block, a compile-time stride.
-template <int DT, int T>
-__global__ void __launch_bounds__(T, 3 * kThreads / T) logProbForward(const __grid_constant__ LogProbArgs a) {
-  using S = typename Ty<DT>::S;
-  constexpr int E = floatTypeSize(DT), V = 16 / E, U = kUnroll, warps = T / 32;
-  __shared__ Sums part[32];
-  __shared__ Sums mine;
-  __shared__ Key best[warps / 2 * 32];
-  __shared__ int flagged[T];
-  __shared__ int flags;
-  __shared__ uint32_t least;
-  cg::cluster_group cluster = cg::this_cluster();
-  const unsigned parts = cluster.num_blocks(), rank = cluster.block_rank();
-  const size_t row = blockIdx.x / parts;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const S* logits = reinterpret_cast<const S*>(a.logits) + row * a.ldl;
-  // [head | whole 16-byte vectors | tail] of the row; the vectors are dealt to the blocks in runs
-  const size_t head = min(a.vocab, ((16 - (uintptr_t)logits % 16) % 16) / E);
-  const size_t nvec = (a.vocab - head) / V, tail = head + nvec * V;
-  const size_t per = (nvec + parts - 1) / parts;
-  const size_t lo = min(nvec, per * rank), hi = min(nvec, lo + per);
-  const uint4* vec = reinterpret_cast<const uint4*>(logits + head);
-  const int odd = rank == 0 ? (int)(head + (a.vocab - tail)) : 0;  // single elements, the first threads'
-  auto oddIndex = [&](int i) { return (size_t)i < head ? (size_t)i : i - head + tail; };
-  const float c = a.invT * kLog2e;
-  size_t i = lo + threadIdx.x;
-  // until it is known whether the row is read, its first vectors come into L2
-#pragma unroll
-  for (int u = 0; u < U; ++u)
-    if (threadIdx.x % 8 == 0 && i + (size_t)u * T < hi)
-      asm volatile("prefetch.global.L2 [%0];" ::"l"(vec + i + (size_t)u * T));
-  const long long token = tokenOf(a, row);
-  if (token == -2) {  // the whole cluster takes this way
-    if (rank == 0 && threadIdx.x == 0) {
-      if (a.logprob) a.logprob[row] = 0.f;
-      if (a.entropy) a.entropy[row] = 0.f;
-      if (a.stats) a.stats[row] = make_float2(0.f, 0.f);
-    }
-    if (rank == 0 && threadIdx.x < a.k) {
-      a.top[row * a.ldt + threadIdx.x] = -INFINITY;
-      a.topIndex[row * a.ldi + threadIdx.x] = -1;
-    }
-    return;
+// How many of n entries are above one.
+__device__ __forceinline__ int above(const Key* v, int n, Key own) {
+  int count = 0;
+#pragma unroll 4
+  for (int j = 0; j < n; ++j) count += v[j] > own;
+  return count;
+}
+// How many of v[0 .. n) come before number i in the order (larger, lower number). n: a multiple of 4, v aligned.
+__device__ __forceinline__ int before(const uint32_t* v, int n, int i) {
+  const uint32_t own = v[i];
+  int count = 0;
+#pragma unroll 2
+  for (int j = 0; j < n; j += 4) {
+    const uint4 q = *reinterpret_cast<const uint4*>(v + j);
+    count += q.x > own || (q.x == own && j < i);
+    count += q.y > own || (q.y == own && j + 1 < i);
+    count += q.z > own || (q.z == own && j + 2 < i);
+    count += q.w > own || (q.w == own && j + 3 < i);
   }
-  Sums r = {-INFINITY, 0.f, 0.f};
-  for (; i + (size_t)(U - 1) * T < hi; i += (size_t)U * T) {
+  return count;
+}
+
+// A row's elements before its first 16-byte boundary, whole vectors, and the rest.
+template <int DT>
+struct Row {
+  using S = typename Ty<DT>::S;
+  static constexpr int V = Vec16<DT>::N;
+  const S* p;
+  const uint4* vec;
+  size_t head, nvec, vocab;
+
+  __device__ __forceinline__ Row(const LogProbArgs& a, size_t row) : vocab(a.vocab) {
+    p = reinterpret_cast<const S*>(a.logits) + row * a.ldl;
+    head = min(vocab, ((16 - (uintptr_t)p % 16) % 16) / sizeof(S));
+    nvec = (vocab - head) / V;
+    vec = reinterpret_cast<const uint4*>(p + head);
+  }
+  __device__ __forceinline__ int odd() const { return (int)(vocab - nvec * V); }  // single elements
+  __device__ __forceinline__ size_t oddIndex(int i) const { return (size_t)i < head ? (size_t)i : i + nvec * V; }
+  __device__ __forceinline__ float at(size_t i) const { return Ty<DT>::toF(p[i]); }
+};
+
+// A thread's pass (vectors i, i + 32, ... of a row, i - lane a multiple of kPass) into its sums; own: the largest of each vector.
+template <int DT>
+__device__ __forceinline__ void runPass(Stream& stream, const Row<DT>& in, size_t i, float (&own)[kUnroll], float c) {
+  constexpr int U = kUnroll;
+  if (i - (threadIdx.x & 31) + kPass <= in.nvec) {
     uint4 v[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) v[u] = __ldcs(vec + i + (size_t)u * T);
+    for (int u = 0; u < U; ++u) v[u] = __ldcs(in.vec + i + u * 32);
+#pragma unroll
+    for (int u = 0; u < U; ++u) own[u] = largestOf<DT>(v[u]);
+    runOver<DT, U>(stream, v, maxOrNan(maxOrNan(own[0], own[1]), maxOrNan(own[2], own[3])), c);
+  } else {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      float f[V];
-      Vec16<DT>::expand(v[u], f);
-      runOver<V>(r, f, largestOf<DT>(v[u]), c);
-    }
-  }
-  for (; i < hi; i += T) {
-    const uint4 v = __ldcs(vec + i);
-    float f[V];
-    Vec16<DT>::expand(v, f);
-    runOver<V>(r, f, largestOf<DT>(v), c);
-  }
-  if ((int)threadIdx.x < odd) {
-    const float f[1] = {Ty<DT>::toF(logits[oddIndex(threadIdx.x)])};
-    runOver<1>(r, f, f[0], c);
-  }
-  Key list = 0;
-  if (a.k > 0) {
-    // what this thread's largest is at least (a sum of NaN: +inf or a NaN is among its elements); 0: it has none
-    const uint32_t own = lo + threadIdx.x < hi || (int)threadIdx.x < odd ? ascending(r.l == r.l ? r.m : INFINITY) : 0;
-    const uint32_t order = mergedOverWarps<uint32_t, warps>(sorted(own), reinterpret_cast<uint32_t*>(best));
-    if (threadIdx.x == a.k - 1) least = order;
-    if (threadIdx.x == 0) flags = 0;
-    __syncthreads();
-    const uint32_t enough = least;
-    if (own && own >= enough) flagged[atomicAdd(&flags, 1)] = threadIdx.x;  // (in any order: the list does not depend on it)
-    __syncthreads();
-    Key bound = enough ? ((Key)enough << 32) - 1 : 0;
-    for (int n = warp; n < flags; n += warps) {
-      const int share = flagged[n];
-      for (size_t j = lo + share; j < hi; j += (size_t)32 * T) {
-        const size_t at = j + (size_t)lane * T;
-        float f[V];
-        Vec16<DT>::expand(at < hi ? __ldcs(vec + at) : make_uint4(0, 0, 0, 0), f);
-        bool any = false;
-        Key key[V];
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          key[e] = at < hi ? keyOf(ascending(f[e]), head + at * V + e) : 0;
-          any |= key[e] > bound;
-        }
-        if (__any_sync(0xffffffffu, any))
-#pragma unroll
-          for (int e = 0; e < V; ++e) insert(list, bound, key[e], a.k);
+      own[u] = -INFINITY;
+      if (i + u * 32 < in.nvec) {
+        const uint4 v[1] = {__ldcs(in.vec + i + u * 32)};
+        own[u] = largestOf<DT>(v[0]);
+        runOver<DT, 1>(stream, v, own[u], c);
       }
-      if (share < odd)
-        insert(list, bound, lane == 0 ? keyOf(ascending(Ty<DT>::toF(logits[oddIndex(share)])), oddIndex(share)) : 0, a.k);
     }
-    list = mergedOverWarps<Key, warps>(list, best);
   }
-  r = warpJoin(r, c);
+}
+__device__ __forceinline__ void sayPadding(const LogProbArgs& a, size_t row) {  // a warp
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) {
+    if (a.logprob) a.logprob[row] = 0.f;
+    if (a.entropy) a.entropy[row] = 0.f;
+    if (a.stats) a.stats[row] = make_float2(0.f, 0.f);
+  }
+  if (lane < a.k) {
+    a.top[row * a.ldt + lane] = -INFINITY;
+    a.topIndex[row * a.ldi + lane] = -1;
+  }
+}
+template <int DT>
+__device__ __forceinline__ void prefetchPass(const Row<DT>& in, size_t i) {  // into L2
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u)
+    if ((threadIdx.x & 7) == 0 && i + u * 32 < in.nvec) asm volatile("prefetch.global.L2 [%0];" ::"l"(in.vec + i + u * 32));
+}
+// Sums of the first threads' single elements too; the warp's, joined.
+template <int DT>
+__device__ __forceinline__ Sums endRow(const Stream& stream, const Row<DT>& in, bool singles, float c) {
+  Sums r = settled(stream, c);
+  if (singles && (int)threadIdx.x < in.odd()) {
+    const float f[1] = {in.at(in.oddIndex(threadIdx.x))};
+    runOver<1>(r, f, c);
+  }
+  return warpJoin(r, c);
+}
+
+// What a block needs for the likeliest entries.
+template <int T>
+struct Finder {
+  uint32_t tops[(kSegments > T ? kSegments : T) + 4];  // of segments, by number, or of the threads; ascending()
+  uint32_t groups[kSegments];
+  int segment[32];
+  Key collected[kCollected];  // (or the warps' lists: T / 64 of 32)
+  Key best[32];
+  uint32_t least;
+  int entries, candidates;
+};
+struct NoFinder {};
+
+// A row over the blocks of a cluster, T threads each. TOP: with the likeliest entries.
+template <int DT, int T, bool TOP>
+__global__ void __launch_bounds__(T, T == 128 ? 8 : 3 * kThreads / T) logProbForward(const __grid_constant__ LogProbArgs a) {
+  constexpr int V = Vec16<DT>::N, U = kUnroll, warps = T / 32;
+  __shared__ Sums part[32];
+  __shared__ Sums mine;
+  __shared__ __align__(16) std::conditional_t<TOP, Finder<T>, NoFinder> find;
+  cg::cluster_group cluster = cg::this_cluster();
+  const unsigned parts = cluster.num_blocks(), block = cluster.block_rank();
+  const size_t row = blockIdx.x / parts;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const Row<DT> in(a, row);
+  const int odd = block == 0 ? in.odd() : 0;  // single elements, the first threads'
+  const float c = a.invT * kLog2e;
+  // runs of passes over the row, a segment each where one is longer than a pass; a block has [firstRun, lastRun), its warps in turn
+  const unsigned perRun = TOP ? max(1, a.span / U) : 1, passes = (unsigned)((in.nvec + kPass - 1) / kPass), runs = (passes + perRun - 1) / perRun;
+  const unsigned runsEach = (runs + parts - 1) / parts, firstRun = min(runs, runsEach * block), lastRun = min(runs, firstRun + runsEach);
+  prefetchPass(in, (size_t)(firstRun + warp) * perRun * kPass + lane);  // (before it is known whether the row is read)
+  const long long token = tokenOf(a, row);
+  if (token == -2) {  // the whole cluster takes this way
+    if (block == 0 && warp == 0) sayPadding(a, row);
+    return;
+  }
+  Stream stream = {{-INFINITY, 0.f, 0.f}, -INFINITY, false};
+  for (unsigned run = firstRun + warp; run < lastRun; run += warps) {
+    float top = -INFINITY;
+    for (unsigned n = 0; n < perRun; ++n) {
+      const unsigned pass = run * perRun + n;
+      float own[U];
+      runPass<DT>(stream, in, (size_t)pass * kPass + lane, own, c);
+      if constexpr (TOP) {
+        auto keep = [&](float x, unsigned segment) {
+          x = largestOfWarp(x);
+          if (lane == 0) find.tops[segment] = ascending(x);
+        };
+        if (a.span == 1) {
+#pragma unroll
+          for (int u = 0; u < U; ++u) keep(own[u], (pass - firstRun) * U + u);
+        } else if (a.span == 2) {
+          keep(maxOrNan(own[0], own[1]), (pass - firstRun) * 2);
+          keep(maxOrNan(own[2], own[3]), (pass - firstRun) * 2 + 1);
+        } else {
+          top = maxOrNan(top, maxOrNan(maxOrNan(own[0], own[1]), maxOrNan(own[2], own[3])));
+          if (n == perRun - 1) keep(top, run - firstRun);
+        }
+      }
+    }
+  }
+  const float given = warp == 0 && block == 0 && token >= 0 ? in.at(token) : 0.f;
+  Sums r = endRow(stream, in, block == 0, c);
   if (lane == 0) part[warp] = r;
+  if constexpr (TOP) {
+    const int segments = (int)(lastRun - firstRun) * (a.span < U ? U / a.span : 1);
+    // groups of segments, 2 k at least where there are as many: the k-th of their largest is a bound for the k-th segment's
+    const int size = segments >= 8 * a.k ? 4 : segments >= 4 * a.k ? 2 : 1, groups = (segments + size - 1) / size, padded = (groups + 3) & ~3;
+    if (warp == 0) {
+      find.best[lane] = 0;
+      find.segment[lane] = -1;
+      if (lane < 4) find.tops[segments + lane] = 0;
+    }
+    if (threadIdx.x == 0) find.entries = find.least = find.candidates = 0;
+    __syncthreads();
+    for (int g = threadIdx.x; g < padded; g += T) {
+      uint32_t top = 0;
+      for (int j = 0; j < size; ++j) top = max(top, g < groups ? find.tops[g * size + j] : 0);
+      find.groups[g] = top;
+    }
+    __syncthreads();
+    for (int g = threadIdx.x; g < groups; g += T)
+      if (before(find.groups, padded, g) == a.k - 1) find.least = find.groups[g];
+    __syncthreads();
+    for (int s = threadIdx.x; s < segments; s += T)
+      if (find.tops[s] >= find.least) find.collected[atomicAdd(&find.candidates, 1)] = keyOf(find.tops[s], s);
+    __syncthreads();
+    for (int j = threadIdx.x; j < find.candidates; j += T) {
+      const int place = above(find.collected, find.candidates, find.collected[j]);
+      if (place < a.k) find.segment[place] = (int)~(uint32_t)find.collected[j];
+      if (place == a.k - 1) find.least = (uint32_t)(find.collected[j] >> 32);
+    }
+    __syncthreads();
+    if (segments < a.k) {  // too few for a bound: the k-th of the threads' largest is one (fewer threads: none)
+      const bool some = (firstRun + warp < lastRun && (firstRun + warp) * (size_t)kPass + lane < in.nvec) || (int)threadIdx.x < odd;
+      find.tops[threadIdx.x] = some ? ascending(stream.s.l == stream.s.l ? stream.s.m : INFINITY) : 0;
+      __syncthreads();
+      if (before(find.tops, T, threadIdx.x) == a.k - 1) find.least = find.tops[threadIdx.x];
+      __syncthreads();
+    }
+    const uint32_t enough = max(1u, find.least);
+    // the k segments' vectors, to fn(a vector, whether it is one, its first element); warps stay together
+    const int number = min(segments, a.k) * a.span * 32;
+    auto forAll = [&](auto fn) {
+      for (int q0 = 0; q0 < number; q0 += U * T) {
+        uint4 v[U];
+        size_t i[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int q = q0 + u * T + threadIdx.x, load = q >> 5;
+          i[u] = in.nvec;
+          if (q < number) i[u] = ((size_t)firstRun * perRun * U + ((size_t)find.segment[load >> a.shift] << a.shift) + (load & (a.span - 1))) * 32 + lane;
+          v[u] = i[u] < in.nvec ? __ldcg(in.vec + i[u]) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) fn(v[u], i[u] < in.nvec, in.head + i[u] * V);
+      }
+    };
+    auto push = [&](uint32_t value, size_t index) {
+      const int to = atomicAdd(&find.entries, 1);
+      if (to < kCollected) find.collected[to] = keyOf(value, index);
+    };
+    forAll([&](const uint4& v, bool there, size_t first) {
+      if (!there || ascending(largestOf<DT>(v)) < enough) return;
+      float f[V];
+      Vec16<DT>::expand(v, f);
+#pragma unroll
+      for (int e = 0; e < V; ++e)
+        if (ascending(f[e]) >= enough) push(ascending(f[e]), first + e);
+    });
+    const bool single = (int)threadIdx.x < odd;
+    const size_t singleAt = single ? in.oddIndex(threadIdx.x) : 0;
+    const uint32_t singleValue = single ? ascending(in.at(singleAt)) : 0;
+    if (singleValue >= enough) push(singleValue, singleAt);
+    __syncthreads();
+    const int n = find.entries;
+    if (n <= kCollected) {
+      for (int j = threadIdx.x; j < n; j += T) {
+        const int place = above(find.collected, n, find.collected[j]);
+        if (place < a.k) find.best[place] = find.collected[j];
+      }
+    } else {
+      __syncthreads();  // (all have seen the number)
+      Key list = 0, bound = ((Key)enough << 32) - 1;
+      forAll([&](const uint4& v, bool there, size_t first) {
+        float f[V];
+        Vec16<DT>::expand(v, f);
+#pragma unroll
+        for (int e = 0; e < V; ++e) insert(list, bound, there ? keyOf(ascending(f[e]), first + e) : 0, a.k);
+      });
+      insert(list, bound, single ? keyOf(singleValue, singleAt) : 0, a.k);
+      list = mergedOverWarps<warps>(list, find.collected);
+      if (warp == 0) find.best[lane] = list;
+    }
+  }
   __syncthreads();
   if (parts > 1) {
-    if (threadIdx.x < 32) {
+    if (warp == 0) {
       r = warpJoin(lane < warps ? part[lane] : Sums{-INFINITY, 0.f, 0.f}, c);
       if (lane == 0) mine = r;
-      best[lane] = list;
     }
     cluster.sync();
-    if (rank == 0 && threadIdx.x < 32) {
-      Sums o = {-INFINITY, 0.f, 0.f};
-      if (lane < (int)parts) o = *cluster.map_shared_rank(&mine, lane);
-      part[lane] = o;
-      for (unsigned p = 1; a.k > 0 && p < parts; ++p) list = merged(list, cluster.map_shared_rank(best, p));
+    Key list = 0;
+    if (block == 0) {
+      if (warp == 0) part[lane] = lane < (int)parts ? *cluster.map_shared_rank(&mine, lane) : Sums{-INFINITY, 0.f, 0.f};
+      if constexpr (TOP)
+        if (warp < (int)parts) list = cluster.map_shared_rank(find.best, warp)[lane];
     }
     cluster.sync();
-    if (rank != 0) return;
+    if (block != 0) return;
+    if constexpr (TOP) {  // (a block has as many warps as the cluster has blocks, at least)
+      list = mergedOverWarps<warps>(list, find.collected);
+      if (warp == 0) find.best[lane] = list;
+    }
   }
-  if (threadIdx.x >= 32) return;
+  if (warp != 0) return;
+  __syncwarp();
   r = warpJoin(lane < (parts > 1 ? (int)parts : warps) ? part[lane] : Sums{-INFINITY, 0.f, 0.f}, c);
   const bool nothing = r.m == -INFINITY && r.l == 0.f;
   const float ll = nothing ? 0.f : logf(r.l);
   auto logOf = [&](float s) { return nothing ? -INFINITY : (s - r.m) * a.invT - ll; };
   if (lane == 0) {
-    if (a.logprob) a.logprob[row] = logOf(Ty<DT>::toF(logits[token]));
+    if (a.logprob) a.logprob[row] = logOf(given);
     if (a.entropy) a.entropy[row] = nothing ? 0.f : ll - r.w / r.l * kLn2;
     if (a.stats) a.stats[row] = make_float2(r.m, ll);
   }
-  if (lane < a.k) {
-    a.top[row * a.ldt + lane] = list ? logOf(fromAscending((uint32_t)(list >> 32))) : -INFINITY;
-    a.topIndex[row * a.ldi + lane] = list ? (int)~(uint32_t)list : -1;
+  if constexpr (TOP) {
+    if (lane < a.k) {
+      const Key entry = find.best[lane];
+      a.top[row * a.ldt + lane] = entry ? logOf(fromAscending((uint32_t)(entry >> 32))) : -INFINITY;
+      a.topIndex[row * a.ldi + lane] = entry ? (int)~(uint32_t)entry : -1;
+    }
   }
 }
 
@@ -439,18 +649,18 @@ __global__ void __launch_bounds__(T, 2 * kThreads / T) logProbBackward(const __g
 }
 
 // Threads of a block: with a row in 16 vectors a thread or fewer, so that several short rows share a multiprocessor and
-// one's reductions run under another's loads; more where blocks are few.
-int blockThreads(size_t bytes, size_t blocks) {
+// one's reductions run under another's loads; more where blocks are few. `most`: at most, where there are many.
+int blockThreads(size_t bytes, size_t blocks, int most) {
+  const bool few = blocks < (size_t)smCount() * 2;
   int t = 128;
-  const size_t most = blocks < (size_t)smCount() * 2 ? 64 : 256;  // bytes a thread
-  while (t < kThreads && bytes > t * most) t *= 2;
+  while (t < (few ? kThreads : most) && bytes > t * size_t(few ? 64 : 256)) t *= 2;
   return t;
 }
 
 using LogProbFn = void (*)(LogProbArgs);
-template <int DT>
+template <int DT, bool TOP>
 LogProbFn pickForward(int threads) {
-  return threads == 128 ? logProbForward<DT, 128> : threads == 256 ? logProbForward<DT, 256> : logProbForward<DT, 512>;
+  return threads == 128 ? logProbForward<DT, 128, TOP> : threads == 256 ? logProbForward<DT, 256, TOP> : logProbForward<DT, 512, TOP>;
 }
 template <int DT>
 LogProbFn pickBackward(int threads) {
@@ -508,10 +718,19 @@ extern "C" vrcclResult_t vrcclLogProbForward(const void* logits, size_t ldl, con
   unsigned parts = 1;
   const size_t bytes = vocab * E;
   while (parts < 8 && rows * parts * 2 <= (size_t)smCount() * 2 && bytes / (parts * 2) >= size_t(kThreads) * 32) parts *= 2;
-  const int threads = blockThreads(bytes / parts, rows * parts);
-  const LogProbFn fn = dtype == vrcclFloat32    ? pickForward<vrcclFloat32>(threads)
-                       : dtype == vrcclBfloat16 ? pickForward<vrcclBfloat16>(threads)
-                                                : pickForward<vrcclFloat16>(threads);
+  const int threads = std::max(blockThreads(bytes / parts, rows * parts, 256), (int)parts * 32);
+  // a segment: as few loads as make no more than kSegments of a block's part
+  const size_t passes = (bytes / 16 / kPass + 1 + parts - 1) / parts + 1;
+  a.span = 1;
+  while (a.span < kUnroll ? passes * (kUnroll / a.span) > kSegments : passes / (a.span / kUnroll) + 1 > kSegments) a.span *= 2;
+  while ((1 << a.shift) < a.span) ++a.shift;
+  auto pick = [&](auto dt) {
+    constexpr int DT = decltype(dt)::value;
+    return k ? pickForward<DT, true>(threads) : pickForward<DT, false>(threads);
+  };
+  const LogProbFn fn = dtype == vrcclFloat32    ? pick(std::integral_constant<int, vrcclFloat32>{})
+                       : dtype == vrcclBfloat16 ? pick(std::integral_constant<int, vrcclBfloat16>{})
+                                                : pick(std::integral_constant<int, vrcclFloat16>{});
   return launchShaped(fn, {dim3((unsigned)(rows * parts)), threads, 0, (int)parts, false}, (cudaStream_t)stream, a);
 }
 
@@ -555,7 +774,7 @@ extern "C" vrcclResult_t vrcclLogProbBackward(const void* logits, size_t ldl, co
   const size_t slices = (vocab + a.slice - 1) / a.slice;
   if (rows * slices >= (size_t(1) << 31)) return vrcclInvalidArgument;
   // as many blocks as four a multiprocessor are all at work at once with 256 threads each
-  const int threads = rows * slices <= (size_t)smCount() * 4 ? 256 : blockThreads(a.slice * E, rows * slices);
+  const int threads = rows * slices <= (size_t)smCount() * 4 ? 256 : blockThreads(a.slice * E, rows * slices, kThreads);
   const LogProbFn fn = dtype == vrcclFloat32    ? pickBackward<vrcclFloat32>(threads)
                        : dtype == vrcclBfloat16 ? pickBackward<vrcclBfloat16>(threads)
                                                 : pickBackward<vrcclFloat16>(threads);

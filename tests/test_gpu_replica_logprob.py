@@ -145,6 +145,18 @@ def test_logprob_masked(torch, v, dtype):  # noqa: F811
             _backward(torch, v, s, token, dev, entropy, stats, dtype, T)
 
 
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_logprob_of_huge_logits(torch, v, dtype):  # noqa: F811
+    """Logits whose differences are all there is: offsets at which a product with 1 / T keeps no fraction."""
+    for vocab, T in ((300, 1.0), (9000, 0.5)):
+        s, token, _ = _inputs(torch, 8, vocab, dtype, padding=0)
+        for r, big in enumerate((2e5, -3e7, 1e8, 5e9, -1e12, 1e30, -1e37, 0)):
+            s.view[r] = (s.view[r].double() * max(1.0, abs(big) * 2.0 ** -8) + big).to(s.view.dtype)
+        s.view[7, ::3] *= 1e20
+        dev, entropy, stats = _forward(torch, v, s, token, 6, dtype, T)
+        _backward(torch, v, s, token, dev, entropy, stats, dtype, T)
+
+
 def test_logprob_of_rows_that_are_not_finite(torch, v):  # noqa: F811
     """A NaN or +inf makes the row's values NaN; the alternatives keep their order, a NaN first."""
     for vocab in (500, 20001):
