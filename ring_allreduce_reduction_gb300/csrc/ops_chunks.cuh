@@ -60,8 +60,8 @@ struct Chunk {
   }
 };
 
-// out[i] = word i of the bytes that begin `skew` bytes into v (16 <= the bytes of v beyond out's). skew is the same for a
-// row, so that the switch does not diverge.
+// out[i] = word i of the bytes that begin `skew` bytes (at most 16) into v. skew is the same for a row, so that the switch
+// does not diverge where a warp has one (selections instead took as long or 3 % longer).
 template <int N, int M>
 __device__ __forceinline__ void shiftedWords(const uint32_t (&v)[M], unsigned skew, uint32_t (&out)[N]) {
   static_assert(M >= N + 4, "a block more");
@@ -85,13 +85,43 @@ __device__ __forceinline__ void shiftedWords(const uint32_t (&v)[M], unsigned sk
   }
 }
 
-// A warp loads 32 consecutive chunks of a row, this lane the one at p with
-// `left` elements to the row's end (none: left <= 0); [begin, end) are the
-// matrix's bytes. All lanes call it.
+// Whether 32 lanes whose first has chunk `chunk` hold whole chunks of a row, another one follows, and the row has others
+// before and after it: then every block that a chunk touches lies inside the matrix.
+__device__ __forceinline__ bool innerChunks(size_t row, size_t rows, int chunk, int cols) {
+  return row > 0 && row + 1 < rows && chunk <= cols / kChunk - 33;
+}
+
+// `lanes` lanes load consecutive chunks of a row, this one (its place among
+// them: lane) the one at p with `left` elements to the row's end (none: left <=
+// 0); [begin, end) are the matrix's bytes. All lanes of a warp call it.
 template <int DT>
-__device__ __forceinline__ Chunk<DT> loadChunk(const char* p, int left, uintptr_t begin, uintptr_t end) {
+__device__ __forceinline__ Chunk<DT> loadChunk(const char* p, int left, uintptr_t begin, uintptr_t end, int lane, int lanes, bool inner) {
   using C = Chunk<DT>;
   constexpr int E = C::E, NB = C::NB;
+  const bool last = lane == lanes - 1;
+  if (inner) {
+    C c;
+    const unsigned skew = (uintptr_t)p & 15;
+    const uint4* q = reinterpret_cast<const uint4*>(p - skew);
+    if (skew == 0) {
+#pragma unroll
+      for (int b = 0; b < NB; ++b) c.set(b, __ldcs(q + b));
+      return c;
+    }
+    uint32_t v[4 * NB + 4];
+    uint4 after = make_uint4(0, 0, 0, 0);
+    if (last) after = __ldcs(q + NB);
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const uint4 w = __ldcs(q + b);
+      v[4 * b] = w.x, v[4 * b + 1] = w.y, v[4 * b + 2] = w.z, v[4 * b + 3] = w.w;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[4 * NB + i] = __shfl_down_sync(0xffffffffu, v[i], 1);
+    if (last) v[4 * NB] = after.x, v[4 * NB + 1] = after.y, v[4 * NB + 2] = after.z, v[4 * NB + 3] = after.w;
+    shiftedWords(v, skew, c.w);
+    return c;
+  }
   C c;
   c.clear();
   const uintptr_t at = (uintptr_t)p, rowEnd = at + (intptr_t)left * E, first = at & ~(uintptr_t)15;
@@ -114,10 +144,10 @@ __device__ __forceinline__ Chunk<DT> loadChunk(const char* p, int left, uintptr_
       v[4 * b] = q.x, v[4 * b + 1] = q.y, v[4 * b + 2] = q.z, v[4 * b + 3] = q.w;
     }
     uint4 after = make_uint4(0, 0, 0, 0);
-    if ((threadIdx.x & 31) == 31) after = block(NB);
+    if (last) after = block(NB);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[4 * NB + i] = __shfl_down_sync(0xffffffffu, v[i], 1);
-    if ((threadIdx.x & 31) == 31) v[4 * NB] = after.x, v[4 * NB + 1] = after.y, v[4 * NB + 2] = after.z, v[4 * NB + 3] = after.w;
+    for (int i = 0; i < 4; ++i) v[4 * NB + i] = __shfl_down_sync(0xffffffffu, v[i], 1, lanes);
+    if (last) v[4 * NB] = after.x, v[4 * NB + 1] = after.y, v[4 * NB + 2] = after.z, v[4 * NB + 3] = after.w;
     if (whole) shiftedWords(v, skew, c.w);
   }
   if (left > 0 && !whole) {
@@ -133,43 +163,98 @@ __device__ __forceinline__ Chunk<DT> loadChunk(const char* p, int left, uintptr_
   return c;
 }
 
-// A warp stores 32 consecutive chunks of a row (p, left as above). All lanes call it.
+// A head of n bytes, the first of w, at p, and a rest of n bytes at a boundary p.
+__device__ __forceinline__ void storeHead(char* p, int n, uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3) {
+  const unsigned sh = (n & 2) * 8;
+  const uint32_t s0 = __funnelshift_r(w0, w1, sh), s1 = __funnelshift_r(w1, w2, sh), s2 = __funnelshift_r(w2, w3, sh);
+  if (n & 2) *reinterpret_cast<unsigned short*>(p) = (unsigned short)w0;
+  if (n & 4) *reinterpret_cast<uint32_t*>(p + headPiece(n, 4)) = s0;
+  if (n & 8) *reinterpret_cast<uint2*>(p + headPiece(n, 8)) = n & 4 ? make_uint2(s1, s2) : make_uint2(s0, s1);
+}
+__device__ __forceinline__ void storeRest(char* p, int n, uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3) {
+  if (n & 8) *reinterpret_cast<uint2*>(p) = make_uint2(w0, w1);
+  const uint32_t a = n & 8 ? w2 : w0, b = n & 8 ? w3 : w1;
+  if (n & 4) *reinterpret_cast<uint32_t*>(p + restPiece(n, 4)) = a;
+  if (n & 2) *reinterpret_cast<unsigned short*>(p + restPiece(n, 2)) = (unsigned short)(n & 4 ? b : a);
+}
+
+// Lanes store consecutive chunks of a row (p, left as above). All lanes of a warp call it.
 template <int DT>
-__device__ __forceinline__ void storeChunk(char* p, const Chunk<DT>& c, int left) {
+__device__ __forceinline__ void storeChunk(char* p, const Chunk<DT>& c, int left, const Place& at, bool inner) {
   using C = Chunk<DT>;
   constexpr int E = C::E, NB = C::NB;
   const unsigned skew = (uintptr_t)p & 15;
-  if (skew == 0) {
-    if (left >= kChunk) {
+  if (inner) {
+    if (skew == 0) {
+      if (at.lane < at.step)
 #pragma unroll
-      for (int b = 0; b < NB; ++b) __stcs(reinterpret_cast<uint4*>(p) + b, c.block(b));
-    } else {
+        for (int b = 0; b < NB; ++b) __stcs(reinterpret_cast<uint4*>(p) + b, c.block(b));
+      return;
+    }
+    uint32_t v[4 * NB + 4], out[4 * NB];
 #pragma unroll
-      for (int e = 0; e < kChunk; ++e)
-        if (e < left) c.storeOne(p, e);
+    for (int i = 0; i < 4 * NB; ++i) v[i] = c.w[i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[4 * NB + i] = __shfl_down_sync(0xffffffffu, c.w[i], 1);
+    const int head = headOf(skew);
+    shiftedWords(v, head, out);
+    if (at.lane >= at.step) return;
+    if (!headStored(skew, E, kChunk, at)) storeHead(p, head, c.w[0], c.w[1], c.w[2], c.w[3]);
+    p += head;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      if (b == NB - 1 && at.lane == 31)
+        storeRest(p + 16 * b, skew, out[4 * b], out[4 * b + 1], out[4 * b + 2], out[4 * b + 3]);
+      else
+        __stcs(reinterpret_cast<uint4*>(p) + b, make_uint4(out[4 * b], out[4 * b + 1], out[4 * b + 2], out[4 * b + 3]));
     }
     return;
   }
-  const int lane = threadIdx.x & 31;
   left = min(left, 64);  // (more says nothing more, and its bytes might pass 31 bits)
+  if (skew == 0 && left >= kChunk && at.lane < at.step) {
+#pragma unroll
+    for (int b = 0; b < NB; ++b) __stcs(reinterpret_cast<uint4*>(p) + b, c.block(b));
+  }
   uint32_t v[4 * NB + 4], out[4 * NB];
 #pragma unroll
   for (int i = 0; i < 4 * NB; ++i) v[i] = c.w[i];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) v[4 * NB + i] = __shfl_down_sync(0xffffffffu, c.w[i], 1);
-  if (left <= 0) return;
-  shiftedWords(v, 16 - skew, out);
-  bool all = headStored(skew, E, left, lane);
+  for (int i = 0; i < 4; ++i) v[4 * NB + i] = __shfl_down_sync(0xffffffffu, c.w[i], 1, at.lanes);
+  if (left <= 0 || at.lane >= at.step) return;
+  if (skew == 0) {
+    if (left < kChunk) {
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const int n = left * E - 16 * b;
+        if (n >= 16)
+          __stcs(reinterpret_cast<uint4*>(p) + b, c.block(b));
+        else if (n > 0)
+          storeRest(p + 16 * b, n, c.w[4 * b], c.w[4 * b + 1], c.w[4 * b + 2], c.w[4 * b + 3]);
+      }
+    }
+    return;
+  }
+  const int head = headOf(skew);
+  if (!headStored(skew, E, left, at)) {
+    if (left * E < head) {
+#pragma unroll
+      for (int e = 0; e < kChunk; ++e)
+        if (e < left) c.storeOne(p, e);
+      return;
+    }
+    storeHead(p, head, c.w[0], c.w[1], c.w[2], c.w[3]);
+  }
+  shiftedWords(v, head, out);
 #pragma unroll
   for (int b = 0; b < NB; ++b) {
-    const bool whole = wholeBlock(b, skew, E, left, lane);
-    if (whole) __stcs(reinterpret_cast<uint4*>(p + 16 - skew) + b, make_uint4(out[4 * b], out[4 * b + 1], out[4 * b + 2], out[4 * b + 3]));
-    all &= whole;
+    char* q = p + head + 16 * b;
+    if (wholeBlock(b, skew, E, left, at)) {
+      __stcs(reinterpret_cast<uint4*>(q), make_uint4(out[4 * b], out[4 * b + 1], out[4 * b + 2], out[4 * b + 3]));
+    } else {
+      const int n = restOf(b, skew, E, left);
+      if (n > 0) storeRest(q, n, out[4 * b], out[4 * b + 1], out[4 * b + 2], out[4 * b + 3]);
+    }
   }
-  if (all) return;
-#pragma unroll
-  for (int e = 0; e < kChunk; ++e)
-    if (storedSingly(e, skew, E, left, lane)) c.storeOne(p, e);
 }
 
 }  // namespace vrccl

@@ -9,24 +9,43 @@ namespace vrccl {
 
 constexpr int kChunk = 8;  // elements: 16 bytes of a 2-byte type, 32 of binary32
 
-// A warp's lanes hold consecutive chunks of a row that starts `skew` bytes
-// (a multiple of the element's size E) after a 16-byte boundary. With skew > 0
-// a chunk's memory is the end of one 16-byte block, and the beginnings of those
-// after it: block i of a chunk is the 16 bytes from its byte 16 (i + 1) - skew
-// on, the last one's end being the next lane's first bytes. A block is stored
-// at once if the row has all its elements (`left`: from the chunk's first to
-// the row's end) and the warp holds them; every other element by itself.
-VRCCL_HD bool wholeBlock(int i, unsigned skew, int E, int left, int lane) {
-  const int end = 16 * (i + 2) - (int)skew;  // in bytes from the chunk's first
-  return left * E >= end && (end <= kChunk * E || lane < 31);
+// Lanes of a warp hold consecutive chunks of a row: all 32, or 16 or 8 of them
+// the whole of a short one.
+struct Place {
+  int lane, lanes;  // this one among those of its row
+  int chunk, step;  // its chunk's number in the row; chunks that the lanes take at a time
+};
+// A row starts `skew` bytes (a multiple of the element's size E) after a
+// 16-byte boundary. With skew > 0 a chunk's memory is the end of one 16-byte
+// block, its head, and the beginnings of those after it: block i of a chunk is
+// the 16 bytes from its byte 16 (i + 1) - skew on, the last one's end being the
+// next lane's head. A block is stored at once if the row has all its elements
+// (`left`: from the chunk's first to the row's end) and the lanes hold them;
+// what lies in other blocks in pieces of 8, 4 and 2 bytes: a head ends, a rest
+// begins on a boundary. (A head that the row ends in goes by elements.)
+// The last lane's last block is never held. So a warp may take 31 chunks and
+// hold the next one's first (step = lanes - 1): its last lane stores nothing,
+// and pieces are left at the row's two ends alone. In place that is sound where
+// the row starts on the same skew as what it overwrites: no other lane stores
+// that head.
+VRCCL_HD int headOf(unsigned skew) { return 16 - (int)skew; }
+VRCCL_HD bool wholeBlock(int i, unsigned skew, int E, int left, const Place& at) {
+  const int end = headOf(skew) + 16 * (i + 1);  // in bytes from the chunk's first
+  return left * E >= end && (end <= kChunk * E || at.lane < at.lanes - 1);
 }
-// What a chunk has before its first block lies in the last block of the lane before: whether that one is stored whole.
-VRCCL_HD bool headStored(unsigned skew, int E, int left, int lane) { return lane > 0 && left * E >= 16 - (int)skew; }
-VRCCL_HD bool storedSingly(int e, unsigned skew, int E, int left, int lane) {
-  if (e >= left) return false;
-  return e * E < 16 - (int)skew ? !headStored(skew, E, left, lane)
-                                : !wholeBlock((e * E + (int)skew) / 16 - 1, skew, E, left, lane);
+// Whether the lane before stores this one's head.
+VRCCL_HD bool headStored(unsigned skew, int E, int left, const Place& at) {
+  return (at.step < at.lanes ? at.chunk : at.lane) > 0 && left * E >= headOf(skew);
 }
+// Bytes of the chunk in its block i, which is not whole.
+VRCCL_HD int restOf(int i, unsigned skew, int E, int left) {
+  return (left < kChunk ? left : kChunk) * E - headOf(skew) - 16 * i;
+}
+// Where the pieces of a head and of a rest of n bytes begin (of size 2, 4, 8: those whose bit n has).
+VRCCL_HD int headPiece(int n, int size) { return n & (size - 1); }
+VRCCL_HD int restPiece(int n, int size) { return n & (16 - 2 * size); }
+// Chunks that a warp takes at a time of rows of `per` > 32: the pieces of 32 cost it a seventh of its time.
+inline int stepOf(int per) { return (per + 30) / 31 * 7 <= (per + 31) / 32 * 8 ? 31 : 32; }
 // Loading, a lane asks for the blocks that its row touches and that lie inside the matrix's own bytes [begin, end) ...
 VRCCL_HD bool blockLoaded(uintptr_t block, uintptr_t rowEnd, uintptr_t begin, uintptr_t end) {
   return block < rowEnd && block >= begin && block + 16 <= end;
@@ -76,5 +95,17 @@ inline uint64_t magicOf(uint64_t d, uint64_t most) {
   if (d < 2 || most > ~(uint64_t)0 / d) return 0;
   return ~(uint64_t)0 / d + 1;
 }
+// The same for n below 2^31 by a 32-bit product: n / d is the upper half of n mul, shifted (d >= 2). mul is 2^(32 + shift) / d
+// rounded up, too large by less than d / 2^(32 + shift) of 1; shift is the least with 2^(shift + 1) >= d, so that n times that
+// stays below 1 / d, the least by which n / d misses the next integer.
+struct Division {
+  uint32_t mul, shift;
+};
+inline Division divisionOf(uint32_t d) {
+  uint32_t shift = 0;
+  while (((uint64_t)2 << shift) < d) ++shift;
+  return {(uint32_t)((((uint64_t)1 << (32 + shift)) + d - 1) / d), shift};
+}
+VRCCL_HD uint32_t quotient(uint32_t n, const Division& by) { return (uint32_t)(((uint64_t)n * by.mul) >> 32) >> by.shift; }
 
 }  // namespace vrccl

@@ -16,8 +16,9 @@
 //
 // Bound by memory. A thread takes chunks of its own. Where all rows start on
 // 16-byte boundaries and are whole chunks long, the matrix is one run of chunks
-// (the row by a multiplication); else a warp takes 32 chunks of one row, and
-// lanes put theirs together from 16-byte blocks and their neighbours'.
+// (the row by a multiplication); else a warp takes 32 chunks of one row, or
+// several short ones, and lanes put theirs together from 16-byte blocks and
+// their neighbours'.
 #include "ops_chunks.cuh"
 
 namespace vrccl {
@@ -27,13 +28,15 @@ struct DropoutArgs {
   const char* x;
   const char* r;  // NULL: none
   char* y;
+  uintptr_t xEnd, rEnd;  // behind the matrices' last elements
   const uint64_t* seed;
   uint64_t offset, firstChunk;  // the counter of chunk 0
-  uint64_t magic;               // of `per` (0: divide)
-  size_t ldx, ldr, ldy, rows, chunks;     // chunks: in all rows, or a warp's share of them (split rows)
-  size_t cols;
-  unsigned per;  // chunks a row
-  unsigned segments;  // runs of 32 chunks a row
+  Division division;            // by `per` or `segments`, for fewer than 2^31 chunks or shares
+  size_t ldx, ldr, ldy, rows, chunks;  // chunks: in all rows (one run), or warps' shares of them (split rows)
+  int cols;
+  unsigned per;       // chunks a row
+  unsigned segments;  // shares a row
+  int lanes, step;    // Place
   float scale;
   uint32_t last;  // what 32 bits with an element's in the upper half exceed if it is kept ...
   bool all;       // ... or all are
@@ -42,95 +45,129 @@ struct DropoutArgs {
 constexpr int kThreads = 256;
 
 template <int DT, bool RES>
-__device__ __forceinline__ void dropChunk(const DropoutArgs& a, uint64_t seed, uint64_t number, const Chunk<DT>& x,
-                                          const Chunk<DT>& r, Chunk<DT>& y) {
-  const Random128 bits = philox(seed, a.firstChunk + number, a.offset);
+__device__ __forceinline__ void dropChunk(const DropoutArgs& a, const Random128& bits, const Chunk<DT>& x, const Chunk<DT>& r,
+                                          Chunk<DT>& y) {
   float f[kChunk], g[kChunk];
   x.expand(f);
   if constexpr (RES) r.expand(g);
+  const F2 scale = pair(a.scale, a.scale);
 #pragma unroll
-  for (int e = 0; e < kChunk; ++e) {
-    // (chosen, not multiplied by zero: what is dropped may hold anything)
+  for (int e = 0; e < kChunk; e += 2) {
+    float2 v;
     if constexpr (RES)
-      f[e] = keeps(bits, e, a.last, a.all) ? fmaf(f[e], a.scale, g[e]) : g[e];
+      v = split(fma2(pair(f[e], f[e + 1]), scale, pair(g[e], g[e + 1])));
     else
-      f[e] = keeps(bits, e, a.last, a.all) ? f[e] * a.scale : 0.f;
+      v = split(mul2(pair(f[e], f[e + 1]), scale));
+    // (chosen, not multiplied by zero: what is dropped may hold anything)
+    f[e] = keeps(bits, e, a.last, a.all) ? v.x : RES ? g[e] : 0.f;
+    f[e + 1] = keeps(bits, e + 1, a.last, a.all) ? v.y : RES ? g[e + 1] : 0.f;
   }
   y.pack(f);
 }
 
-// One run of chunks; U a thread, asked for before the bits are drawn.
-template <int DT, bool RES, int U>
+// One run of chunks; U a thread, asked for before the bits are drawn. FLAT: no gaps between rows either.
+template <int DT, bool RES, int U, bool FLAT>
 __global__ void __launch_bounds__(kThreads) dropoutRun(const __grid_constant__ DropoutArgs a) {
   using C = Chunk<DT>;
   constexpr int E = C::E, NB = C::NB;
-  const size_t first = (size_t)blockIdx.x * (kThreads * U) + threadIdx.x;
+  const size_t block = (size_t)blockIdx.x * (kThreads * U);
   C x[U], r[U];
   size_t row[U];
   unsigned col[U];
+  auto place = [&](const char* p, size_t ld, int u) {
+    return FLAT ? reinterpret_cast<const uint4*>(p) + (block + threadIdx.x) * NB + u * (kThreads * NB)
+                : reinterpret_cast<const uint4*>(p + row[u] * ld * E) + (size_t)col[u] * NB;
+  };
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const size_t n = first + u * kThreads;
+    const size_t n = block + threadIdx.x + u * kThreads;
     if (n >= a.chunks) continue;
-    row[u] = a.magic ? __umul64hi(n, a.magic) : n / a.per;
-    col[u] = (unsigned)(n - row[u] * a.per);
-    const uint4* p = reinterpret_cast<const uint4*>(a.x + row[u] * a.ldx * E) + (size_t)col[u] * NB;
-    const uint4* q = reinterpret_cast<const uint4*>(a.r + row[u] * a.ldr * E) + (size_t)col[u] * NB;
+    if constexpr (!FLAT) {
+      row[u] = a.chunks >> 31 || a.per == 1 ? n / a.per : quotient((uint32_t)n, a.division);
+      col[u] = (unsigned)n - (unsigned)row[u] * a.per;
+    }
+    const uint4 *p = place(a.x, a.ldx, u), *q = place(a.r, a.ldr, u);
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       x[u].set(b, __ldcs(p + b));
       if constexpr (RES) r[u].set(b, __ldcs(q + b));
     }
   }
-  const uint64_t seed = *a.seed;
+  const uint64_t seed = *a.seed, counter = a.firstChunk + block;
+  // Where a block's counters share their upper half, a thread's chunks share the half of the first two rounds that comes of
+  // it and of the offset.
+  auto draw = [&](auto shared) {
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const size_t n = first + u * kThreads;
-    if (n >= a.chunks) continue;
-    C y;
-    dropChunk<DT, RES>(a, seed, n, x[u], r[u], y);
-    uint4* p = reinterpret_cast<uint4*>(a.y + row[u] * a.ldy * E) + (size_t)col[u] * NB;
+    for (int u = 0; u < U; ++u) {
+      if (block + threadIdx.x + u * kThreads >= a.chunks) continue;
+      const unsigned n = threadIdx.x + u * kThreads;
+      const uint64_t number = decltype(shared)::value ? (counter & ~(uint64_t)0xffffffffu) | ((uint32_t)counter + n) : counter + n;
+      C y;
+      dropChunk<DT, RES>(a, philox(seed, number, a.offset), x[u], r[u], y);
+      uint4* p = const_cast<uint4*>(place(a.y, a.ldy, u));
 #pragma unroll
-    for (int b = 0; b < NB; ++b) __stcs(p + b, y.block(b));
-  }
+      for (int b = 0; b < NB; ++b) __stcs(p + b, y.block(b));
+    }
+  };
+  if ((uint32_t)counter <= ~0u - kThreads * U)
+    draw(std::true_type{});
+  else
+    draw(std::false_type{});
 }
 
-// A warp a run of 32 chunks of one row, on any element.
+// Rows on any element: a warp takes `step` chunks of one, or short ones whole.
 template <int DT, bool RES>
 __global__ void __launch_bounds__(kThreads) dropoutRows(const __grid_constant__ DropoutArgs a) {
   using C = Chunk<DT>;
   constexpr int E = C::E;
-  const size_t warp = ((size_t)blockIdx.x * kThreads + threadIdx.x) / 32;
+  const size_t warp = (size_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
   if (warp >= a.chunks) return;
-  const size_t row = warp / a.segments;
-  const unsigned chunk = (unsigned)(warp - row * a.segments) * 32 + (threadIdx.x & 31);
-  const size_t col = (size_t)chunk * kChunk;
-  const int left = (int)min((long long)a.cols - (long long)col, (long long)(1 << 20));
-  auto span = [&](const char* p, size_t ld) { return (uintptr_t)p + ((a.rows - 1) * ld + a.cols) * E; };
-  const C x = loadChunk<DT>(a.x + (row * a.ldx + col) * E, left, (uintptr_t)a.x, span(a.x, a.ldx));
+  Place at = {(int)(threadIdx.x & 31), a.lanes, 0, a.step};
+  size_t row = warp;
+  int first = 0;  // the warp's first chunk
+  if (a.lanes < 32) {
+    row = warp * (32 / a.lanes) + at.lane / a.lanes;
+    at.lane &= a.lanes - 1;
+  } else if (a.segments > 1) {
+    row = a.chunks >> 31 ? warp / a.segments : quotient((uint32_t)warp, a.division);
+    first = (int)((unsigned)warp - (unsigned)row * a.segments) * a.step;
+  }
+  at.chunk = first + at.lane;
+  const int left = row < a.rows ? a.cols - at.chunk * kChunk : 0;
+  const bool inner = a.segments > 1 && innerChunks(row, a.rows, first, a.cols);
+  auto place = [&](const char* p, size_t ld) { return p + row * ld * E + (size_t)at.chunk * (kChunk * E); };
+  const C x = loadChunk<DT>(place(a.x, a.ldx), left, (uintptr_t)a.x, a.xEnd, at.lane, at.lanes, inner);
   C r, y;
-  if constexpr (RES) r = loadChunk<DT>(a.r + (row * a.ldr + col) * E, left, (uintptr_t)a.r, span(a.r, a.ldr));
-  dropChunk<DT, RES>(a, *a.seed, row * a.per + chunk, x, r, y);
-  storeChunk<DT>(a.y + (row * a.ldy + col) * E, y, left);
+  if constexpr (RES) r = loadChunk<DT>(place(a.r, a.ldr), left, (uintptr_t)a.r, a.rEnd, at.lane, at.lanes, inner);
+  dropChunk<DT, RES>(a, philox(*a.seed, a.firstChunk + row * a.per + at.chunk, a.offset), x, r, y);
+  storeChunk<DT>(const_cast<char*>(place(a.y, a.ldy)), y, left, at, inner);
 }
 
 template <int DT, bool RES>
 vrcclResult_t launchDropout(DropoutArgs& a, bool run, cudaStream_t st) {
+  const bool one = a.rows == 1;
   if (!run) {
-    a.segments = (a.per + 31) / 32;
-    a.chunks = a.rows * a.segments;
+    a.lanes = a.per <= 8 ? 8 : a.per <= 16 ? 16 : 32;
+    a.step = a.per > 32 ? stepOf((int)a.per) : a.lanes;
+    a.segments = (a.per + a.step - 1) / a.step;
+    a.chunks = a.lanes < 32 ? (a.rows + 32 / a.lanes - 1) / (32 / a.lanes) : a.rows * a.segments;
+    a.division = divisionOf(a.segments);
     const size_t blocks = (a.chunks + kThreads / 32 - 1) / (kThreads / 32);
     if (blocks >= (size_t(1) << 31)) return vrcclInvalidArgument;
     return launchShaped(dropoutRows<DT, RES>, {dim3((unsigned)blocks), kThreads, 0, 0, false}, st, a);
   }
   a.chunks = a.rows * a.per;
-  a.magic = magicOf(a.per, a.chunks);
+  a.division = divisionOf(a.per);
+  const size_t cols = a.cols;
+  const bool flat = one || (a.ldx == cols && a.ldy == cols && (!RES || a.ldr == cols));
   const bool many = a.chunks >= (size_t)smCount() * kThreads * 8;
-  const int u = many ? 4 : 1;
+  constexpr int U = DT == vrcclFloat32 ? 2 : 4;
+  const int u = many ? U : 1;
   const size_t blocks = (a.chunks + kThreads * u - 1) / (kThreads * u);
   if (blocks >= (size_t(1) << 31)) return vrcclInvalidArgument;
   const LaunchShape s = {dim3((unsigned)blocks), kThreads, 0, 0, false};
-  return many ? launchShaped(dropoutRun<DT, RES, 4>, s, st, a) : launchShaped(dropoutRun<DT, RES, 1>, s, st, a);
+  if (flat) return many ? launchShaped(dropoutRun<DT, RES, U, true>, s, st, a) : launchShaped(dropoutRun<DT, RES, 1, true>, s, st, a);
+  return many ? launchShaped(dropoutRun<DT, RES, U, false>, s, st, a) : launchShaped(dropoutRun<DT, RES, 1, false>, s, st, a);
 }
 
 vrcclResult_t dropout(const void* x, size_t ldx, const void* r, size_t ldr, void* y, size_t ldy, size_t rows, size_t cols,
@@ -157,6 +194,8 @@ vrcclResult_t dropout(const void* x, size_t ldx, const void* r, size_t ldr, void
   a.x = static_cast<const char*>(x);
   a.r = static_cast<const char*>(r);
   a.y = static_cast<char*>(y);
+  a.xEnd = (uintptr_t)x + ((rows - 1) * ldx + cols) * E;
+  a.rEnd = (uintptr_t)r + ((rows - 1) * ldr + cols) * E;
   a.seed = seed;
   a.offset = offset;
   a.firstChunk = firstRow * per;
@@ -164,7 +203,7 @@ vrcclResult_t dropout(const void* x, size_t ldx, const void* r, size_t ldr, void
   a.ldr = ldr;
   a.ldy = ldy;
   a.rows = rows;
-  a.cols = cols;
+  a.cols = (int)cols;
   a.per = (unsigned)per;
   a.scale = drop < 65536 ? 65536.f / (float)(65536 - drop) : 0.f;
   a.last = (uint32_t)drop * 65536u - 1;

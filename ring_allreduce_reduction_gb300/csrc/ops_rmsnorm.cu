@@ -13,9 +13,11 @@
 // several rows ahead, whatever element it starts on (the copy takes the
 // 16-byte blocks that it touches, and a thread shifts its chunk out of two
 // neighbouring blocks). The barrier inside a row's reduction is also the point
-// where every thread has taken its chunks, and the row's stage is filled anew.
+// where every thread has taken its chunks, and the row's stage is filled anew
+// (or, where registers do not hold the row, the stage of the one before it).
 // Teams of warps walk rows of their own, so that one team's reduction runs
-// under the others' loads and stores.
+// under the others' loads and stores. On rows that do not start on 16-byte
+// boundaries a warp takes 31 chunks and looks at the next one (ops_chunks.h).
 //
 // The weight's gradient is summed down the columns in the registers of the
 // threads that own them, over all the rows that a team walks; a block joins its
@@ -23,7 +25,8 @@
 // order. No atomics: the same call gives the same bits.
 //
 // Short rows that start on boundaries go several to a warp (narrow); rows beyond
-// 8192 columns are read twice, the second time through L2 (long).
+// a block's threads or shared memory are read twice, the second time through L2
+// (long): 2048 x 16384 fp32 backward 142 us.
 #include <cfloat>
 
 #include "ops_chunks.cuh"
@@ -52,12 +55,22 @@ struct RmsArgs {
   bool wideParams;  // gamma starts on a 16-byte boundary
   bool aligned;     // every source's rows are whole 16-byte blocks
   int stages, teams, threads, slot;
-  int quant, group;  // group: columns of a scale, 0 for the row
+  int step;  // chunks of its own that a warp takes
+  int quant, group;  // group: columns of a scale (then step is 32), 0 for the row
   float eps;
 };
 
 constexpr int kHeld = 2;  // chunks a thread holds
-constexpr int kRingThreads = 512, kRingCols = kRingThreads * kHeld * kChunk;
+// Warps of a block (one an SM), and so the registers of a thread: what is left of 65536, in steps of four warps. Measured
+// with 32768 x 4096 bf16 and residual: 16 warps 175 us, 20: 179, 24: 170, 28: 175, 32: 182; 16384 x 5120 to e4m3 20: 118.5,
+// 24: 120, 28: 140, 32: 117; 16384 x 4097 (three teams of nine from 27 on) 20: 136, 24: 142, 28: 118, 32: 132. Rows that
+// need more warps have 32 (wide).
+constexpr int forwardWarps(bool vec, bool q, bool wide) { return wide || q ? 32 : vec ? 24 : 28; }
+// Backward keeps a row's chunks in registers (hold) where 16 warps do: 16384 x 8192 bf16 159 us (20 warps: 205). Else it reads
+// them from the stage once more: 16384 x 4097 20 warps 178 us (16 and held: 246, 24: 222, 28: 201), 4096 x 16384 with 32: 110;
+// 3001 x 2003 fp32 16 warps 28.3 us (20: 29.7, 24: 35).
+constexpr int backwardWarps(bool vec, bool hold, int elem) { return hold ? 16 : vec ? 32 : elem == 4 ? 16 : 20; }
+constexpr int kMaxTeams = 15;  // (as many named barriers, and the block's)
 constexpr int kRingSmem = 208 * 1024;  // of the 227 KB a block may have
 
 template <int DT>
@@ -125,15 +138,39 @@ __device__ __forceinline__ float sumOfLanes(float x) {
   return x;
 }
 
+// VEC: every operand's rows are whole chunks and start on 16-byte boundaries.
+// Chunk j of a team's thread t (of `warps`); what the last lane of a warp holds beyond `step` is another warp's.
+template <bool VEC>
+__device__ __forceinline__ int chunkOf(const RmsArgs& a, int j, int warps, int t) {
+  return VEC ? (j * warps * 32 + t) : (j * warps + (t >> 5)) * a.step + (t & 31);
+}
+template <bool VEC>
+__device__ __forceinline__ bool ownChunk(const RmsArgs& a, int t) {
+  return VEC || (t & 31) < a.step;
+}
+template <int DT, bool VEC>
+__device__ __forceinline__ void putChunk(const RmsArgs& a, char* rows, size_t ld, size_t row, const Chunk<DT>& c, int ci) {
+  char* p = rows + row * ld * Chunk<DT>::E + (size_t)ci * (kChunk * Chunk<DT>::E);
+  if constexpr (VEC) {
+    if (ci < a.chunks)
+#pragma unroll
+      for (int b = 0; b < Chunk<DT>::NB; ++b) __stcs(reinterpret_cast<uint4*>(p) + b, c.block(b));
+  } else {
+    const Place at = {(int)(threadIdx.x & 31), 32, ci, a.step};
+    storeChunk<DT>(p, c, a.cols - ci * kChunk, at, innerChunks(row, a.rows, ci - at.lane, a.cols));
+  }
+}
+
 // ------------------------------------------------------------ 8 bits
 // The scale of a group whose largest |y| is given: no smaller than the least normal number, so that its reciprocal is
 // finite (a group of zeros has that one); not finite where a y is not, so that it shows in whatever the codes stand for.
 __device__ __forceinline__ float scaleOf(float most, int quant) {
-  return maxOrNan(most / (quant == vrcclQuantInt8 ? 127.f : 448.f), FLT_MIN);
+  return maxOrNan(most * (quant == vrcclQuantInt8 ? 1.f / 127.f : 1.f / 448.f), FLT_MIN);
 }
 // Eight codes at p, `left` of them to the row's end.
 __device__ __forceinline__ void storeCodes(unsigned char* p, const F2 (&y)[kChunk / 2], float scale, int quant, int left) {
-  const float inv = 1.f / scale;
+  float inv;  // (a unit or two off, which moves a code where y lies that near the middle of two; normal, as the scale is below 2^122)
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(scale));
   uint32_t w[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -164,7 +201,7 @@ __device__ __forceinline__ void storeCodes(unsigned char* p, const F2 (&y)[kChun
 }
 // The codes of chunk ci and, by its first lane, the group's scale; `rowMost`: the row's largest |y|. Groups lie within a
 // warp, one chunk a lane. All lanes call it.
-__device__ __forceinline__ void storeGroup(const RmsArgs& a, size_t row, int ci, const F2 (&y)[kChunk / 2], float rowMost) {
+__device__ __forceinline__ void storeGroup(const RmsArgs& a, size_t row, int ci, const F2 (&y)[kChunk / 2], float rowMost, bool own) {
   const int left = a.cols - ci * kChunk;
   float most = rowMost;
   if (a.group) {
@@ -174,7 +211,7 @@ __device__ __forceinline__ void storeGroup(const RmsArgs& a, size_t row, int ci,
     if (a.group > 32) most = maxOrNan(most, __shfl_xor_sync(0xffffffffu, most, 4));
     if (a.group > 64) most = maxOrNan(most, __shfl_xor_sync(0xffffffffu, most, 8));
   }
-  if (left <= 0) return;
+  if (left <= 0 || !own) return;
   const float scale = scaleOf(most, a.quant);
   const int lanes = a.group / kChunk;
   if (a.group ? ci % lanes == 0 : ci == 0) a.scales[row * a.ldsc + (a.group ? ci / lanes : 0)] = scale;
@@ -217,7 +254,7 @@ __device__ __forceinline__ void fillStage(const RmsArgs& a, unsigned char* stage
       bulkLoadOnce(stage + n * a.slot + (w[n].lo - (w[n].row & ~(uintptr_t)15)), (const void*)w[n].lo, w[n].hi - w[n].lo, bar, policy);
 }
 // Chunk ci of source n's row in a stage; elements past the row's end zero.
-template <int DT>
+template <int DT, bool VEC>
 __device__ __forceinline__ Chunk<DT> taken(const RmsArgs& a, const unsigned char* stage, int n, size_t row, int ci) {
   using C = Chunk<DT>;
   constexpr int NB = C::NB;
@@ -228,7 +265,7 @@ __device__ __forceinline__ Chunk<DT> taken(const RmsArgs& a, const unsigned char
     return c;
   }
   const uint4* b = reinterpret_cast<const uint4*>(stage + n * a.slot) + ci * NB;
-  const unsigned skew = a.aligned ? 0 : ((unsigned)(uintptr_t)a.src[n].p + (unsigned)row * (unsigned)a.src[n].ld * C::E) & 15;
+  const unsigned skew = VEC ? 0 : ((unsigned)(uintptr_t)a.src[n].p + (unsigned)row * (unsigned)a.src[n].ld * C::E) & 15;
   if (skew == 0) {
 #pragma unroll
     for (int i = 0; i < NB; ++i) c.set(i, b[i]);
@@ -241,7 +278,7 @@ __device__ __forceinline__ Chunk<DT> taken(const RmsArgs& a, const unsigned char
     }
     shiftedWords(v, skew, c.w);
   }
-  c.cut(left);
+  if (!VEC) c.cut(left);
   return c;
 }
 __device__ __forceinline__ void teamSync(int team, int threads) {
@@ -251,8 +288,9 @@ __device__ __forceinline__ void teamSync(int team, int threads) {
     asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(threads) : "memory");
 }
 
-// What forward and backward share: a team's place, its stages and their barriers.
-template <int E, int N>
+// What forward and backward share: a team's place, its stages and their barriers. LATE: a row stays in its stage until the
+// next one's barrier, which every thread reaches with the row's work done, and is then replaced.
+template <int E, int N, bool LATE>
 struct Ring {
   const RmsArgs& a;
   unsigned char* mine;
@@ -289,11 +327,13 @@ struct Ring {
   // The team's barrier of a turn, after which the stage takes a later row. true: a wait was given up, and the team leaves.
   __device__ __forceinline__ bool sync(size_t row) {
     teamSync(team, a.threads);
+    // (before giving up is asked for, so that then every stage has been filled again)
+    if (LATE && t == 0 && row >= first + stride) fill(stage ? stage - 1 : a.stages - 1, row - stride + a.stages * stride);
     if (givenUp(*reinterpret_cast<volatile int*>(dead), turn)) {
       abandon(bar, a.stages, stage, round, t == 0, dead, turn);
       return true;
     }
-    if (t == 0) fill(stage, row + a.stages * stride);
+    if (!LATE && t == 0) fill(stage, row + a.stages * stride);
     return false;
   }
   __device__ __forceinline__ void next() {
@@ -305,19 +345,19 @@ struct Ring {
   }
 };
 
-template <int DT, bool RES, bool Q>
-__global__ void __launch_bounds__(kRingThreads) rmsForward(const __grid_constant__ RmsArgs a) {
+template <int DT, bool RES, bool Q, bool VEC, bool WIDE>
+__global__ void __launch_bounds__(32 * forwardWarps(VEC, Q, WIDE)) rmsForward(const __grid_constant__ RmsArgs a) {
   using C = Chunk<DT>;
   constexpr int E = C::E, NP = kChunk / 2;
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ unsigned long long full[16 * kMaxStages];
-  __shared__ float2 red[16][2][16];  // team, turn, warp: (sum of squares, largest)
-  __shared__ int deadWord[16];
-  Ring<E, RES ? 2 : 1> ring(a, smem, full, deadWord);
+  __shared__ unsigned long long full[kMaxTeams * kMaxStages];
+  __shared__ float2 red[2][32];  // turn, warp: (sum of squares, largest)
+  __shared__ int deadWord[kMaxTeams];
+  Ring<E, RES ? 2 : 1, false> ring(a, smem, full, deadWord);
   const int t = ring.t, T = a.threads, lane = t & 31, warps = T / 32;
   F2 g[kHeld][NP];
 #pragma unroll
-  for (int j = 0; j < kHeld; ++j) gammaOf<DT>(a, j * T + t, g[j]);
+  for (int j = 0; j < kHeld; ++j) gammaOf<DT>(a, chunkOf<VEC>(a, j, warps, t), g[j]);
   const float inv = 1.f / (float)a.cols;
   teamSync(ring.team, T);
   for (size_t row = ring.first; row < a.rows; row += ring.stride, ring.next()) {
@@ -327,42 +367,46 @@ __global__ void __launch_bounds__(kRingThreads) rmsForward(const __grid_constant
     float most = 0.f;
 #pragma unroll
     for (int j = 0; j < kHeld; ++j) {
-      s[j] = taken<DT>(a, stage, 0, row, j * T + t);
-      if constexpr (RES) addTo(s[j], taken<DT>(a, stage, 1, row, j * T + t));
+      const int ci = chunkOf<VEC>(a, j, warps, t);
+      s[j] = taken<DT, VEC>(a, stage, 0, row, ci);
+      if constexpr (RES) addTo(s[j], taken<DT, VEC>(a, stage, 1, row, ci));
       F2 x[NP];
       pairsOf(s[j], x);
+      if (ownChunk<VEC>(a, t))
 #pragma unroll
-      for (int i = 0; i < NP; ++i) squares = fma2(x[i], x[i], squares);
+        for (int i = 0; i < NP; ++i) squares = fma2(x[i], x[i], squares);
       if constexpr (Q) {
 #pragma unroll
         for (int i = 0; i < NP; ++i) x[i] = mul2(x[i], g[j][i]);
         if (a.group == 0) most = maxOrNan(most, largest(x));
       }
+      // (in place: the row is in shared memory)
+      if (RES && a.sum) putChunk<DT, VEC>(a, a.sum, a.lds, row, s[j], ci);
     }
     float2 w = make_float2(warpSum(sumOf(squares)), most);
     if constexpr (Q)
       if (a.group == 0) w.y = largestOfLanes<32>(most);
-    if (lane == 0) red[ring.team][ring.turn][t >> 5] = w;
+    if (lane == 0) red[ring.turn][threadIdx.x >> 5] = w;
     if (ring.sync(row)) break;
     if (warps > 1) {
-      w = (lane & 15) < warps ? red[ring.team][ring.turn][lane & 15] : make_float2(0.f, 0.f);
-      w.x = sumOfLanes<16>(w.x);
+      w = lane < warps ? red[ring.turn][ring.team * warps + lane] : make_float2(0.f, 0.f);
+      w.x = sumOfLanes<32>(w.x);
       if constexpr (Q)
-        if (a.group == 0) w.y = largestOfLanes<16>(w.y);
+        if (a.group == 0) w.y = largestOfLanes<32>(w.y);
     }
     const float rstd = rsqrtf(w.x * inv + a.eps);
     if (t == 0 && a.rstd) a.rstd[row] = rstd;
     const F2 scale = pair(rstd, rstd);
 #pragma unroll
     for (int j = 0; j < kHeld; ++j) {
-      const int ci = j * T + t, left = a.cols - ci * kChunk;
-      if (a.sum) storeChunk<DT>(a.sum + (row * a.lds + (size_t)ci * kChunk) * E, s[j], left);
+      const int ci = chunkOf<VEC>(a, j, warps, t);
       F2 x[NP];
       pairsOf(s[j], x);
 #pragma unroll
       for (int i = 0; i < NP; ++i) x[i] = mul2(mul2(x[i], scale), g[j][i]);
-      if (!Q || a.y) storeChunk<DT>(a.y + (row * a.ldy + (size_t)ci * kChunk) * E, packed<DT>(x), left);
-      if constexpr (Q) storeGroup(a, row, ci, x, w.y * rstd);
+      if (!RES && a.sum) putChunk<DT, VEC>(a, a.sum, a.lds, row, s[j], ci);
+      if (!Q || a.y) putChunk<DT, VEC>(a, a.y, a.ldy, row, packed<DT>(x), ci);
+      if constexpr (Q) storeGroup(a, row, ci, x, w.y * rstd, ownChunk<VEC>(a, t));
     }
   }
 }
@@ -378,20 +422,20 @@ __device__ __forceinline__ void layOut(float* p, const F2 (&dg)[kChunk / 2], int
   }
 }
 
-template <int DT, bool DSUM>
-__global__ void __launch_bounds__(kRingThreads) rmsBackward(const __grid_constant__ RmsArgs a) {
+template <int DT, bool DSUM, bool VEC, bool HOLD>
+__global__ void __launch_bounds__(32 * backwardWarps(VEC, HOLD, floatTypeSize(DT))) rmsBackward(const __grid_constant__ RmsArgs a) {
   using C = Chunk<DT>;
   constexpr int E = C::E, NP = kChunk / 2;
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ unsigned long long full[16 * kMaxStages];
-  __shared__ float red[16][2][16];
-  __shared__ int deadWord[16];
-  Ring<E, DSUM ? 3 : 2> ring(a, smem, full, deadWord);
+  __shared__ unsigned long long full[kMaxTeams * kMaxStages];
+  __shared__ float red[2][32];
+  __shared__ int deadWord[kMaxTeams];
+  Ring<E, DSUM ? 3 : 2, !HOLD> ring(a, smem, full, deadWord);
   const int t = ring.t, T = a.threads, lane = t & 31, warps = T / 32;
   F2 g[kHeld][NP], dg[kHeld][NP];
 #pragma unroll
   for (int j = 0; j < kHeld; ++j) {
-    gammaOf<DT>(a, j * T + t, g[j]);
+    gammaOf<DT>(a, chunkOf<VEC>(a, j, warps, t), g[j]);
 #pragma unroll
     for (int i = 0; i < NP; ++i) dg[j][i] = 0;
   }
@@ -402,17 +446,21 @@ __global__ void __launch_bounds__(kRingThreads) rmsBackward(const __grid_constan
   for (size_t row = ring.first; row < a.rows; row += ring.stride, ring.next()) {
     const float rstd = nextRstd;
     const unsigned char* stage = ring.wait();
-    C s[kHeld], d[kHeld], r[kHeld];
+    C s[kHeld], d[kHeld], r[kHeld];  // (HOLD)
     const F2 scale = pair(rstd, rstd);
     F2 dot = 0;
 #pragma unroll
     for (int j = 0; j < kHeld; ++j) {
-      s[j] = taken<DT>(a, stage, 0, row, j * T + t);
-      d[j] = taken<DT>(a, stage, 1, row, j * T + t);
-      if constexpr (DSUM) r[j] = taken<DT>(a, stage, 2, row, j * T + t);
+      const int ci = chunkOf<VEC>(a, j, warps, t);
+      C sj = taken<DT, VEC>(a, stage, 0, row, ci), dj = taken<DT, VEC>(a, stage, 1, row, ci);
+      if constexpr (HOLD) {
+        s[j] = sj, d[j] = dj;
+        if constexpr (DSUM) r[j] = taken<DT, VEC>(a, stage, 2, row, ci);
+      }
+      if (!ownChunk<VEC>(a, t)) continue;
       F2 xh[NP], dy[NP];
-      pairsOf(s[j], xh);
-      pairsOf(d[j], dy);
+      pairsOf(sj, xh);
+      pairsOf(dj, dy);
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
         xh[i] = mul2(xh[i], scale);
@@ -421,24 +469,24 @@ __global__ void __launch_bounds__(kRingThreads) rmsBackward(const __grid_constan
       }
     }
     float w = warpSum(sumOf(dot));
-    if (lane == 0) red[ring.team][ring.turn][t >> 5] = w;
+    if (lane == 0) red[ring.turn][threadIdx.x >> 5] = w;
     if (ring.sync(row)) break;
     if (row + ring.stride < a.rows) nextRstd = a.rstd[row + ring.stride];
-    if (warps > 1) w = sumOfLanes<16>((lane & 15) < warps ? red[ring.team][ring.turn][lane & 15] : 0.f);
+    if (warps > 1) w = sumOfLanes<32>(lane < warps ? red[ring.turn][ring.team * warps + lane] : 0.f);
     const F2 minus = pair(-w * inv, -w * inv);
 #pragma unroll
     for (int j = 0; j < kHeld; ++j) {
-      const int ci = j * T + t;
+      const int ci = chunkOf<VEC>(a, j, warps, t);
       F2 xh[NP], dy[NP], add[NP];
-      pairsOf(s[j], xh);
-      pairsOf(d[j], dy);
-      if constexpr (DSUM) pairsOf(r[j], add);
+      pairsOf(HOLD ? s[j] : taken<DT, VEC>(a, stage, 0, row, ci), xh);
+      pairsOf(HOLD ? d[j] : taken<DT, VEC>(a, stage, 1, row, ci), dy);
+      if constexpr (DSUM) pairsOf(HOLD ? r[j] : taken<DT, VEC>(a, stage, 2, row, ci), add);
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
         const F2 v = fma2(mul2(xh[i], scale), minus, mul2(dy[i], g[j][i]));
         dy[i] = DSUM ? fma2(v, scale, add[i]) : mul2(v, scale);
       }
-      storeChunk<DT>(a.y + (row * a.ldy + (size_t)ci * kChunk) * E, packed<DT>(dy), a.cols - ci * kChunk);
+      putChunk<DT, VEC>(a, a.y, a.ldy, row, packed<DT>(dy), ci);
     }
   }
   if (!a.partial) return;
@@ -446,7 +494,8 @@ __global__ void __launch_bounds__(kRingThreads) rmsBackward(const __grid_constan
   float* sum = reinterpret_cast<float*>(smem);
   __syncthreads();  // no team reads its ring any more
 #pragma unroll
-  for (int j = 0; j < kHeld; ++j) layOut(sum + (size_t)ring.team * a.cols, dg[j], j * T + t, a.cols);
+  for (int j = 0; j < kHeld; ++j)
+    if (ownChunk<VEC>(a, t)) layOut(sum + (size_t)ring.team * a.cols, dg[j], chunkOf<VEC>(a, j, warps, t), a.cols);
   __syncthreads();
   float* p = a.partial + (size_t)blockIdx.x * a.cols;
   for (int c = threadIdx.x; c < a.cols; c += blockDim.x) {
@@ -615,7 +664,7 @@ __device__ __forceinline__ Chunk<DT> longChunk(const RmsArgs& a, int n, size_t r
   constexpr int E = Chunk<DT>::E;
   const Source& s = a.src[n];
   return loadChunk<DT>(s.p + (row * s.ld + (size_t)ci * kChunk) * E, a.cols - ci * kChunk, (uintptr_t)s.p,
-                       (uintptr_t)s.p + ((a.rows - 1) * s.ld + a.cols) * E);
+                       (uintptr_t)s.p + ((a.rows - 1) * s.ld + a.cols) * E, threadIdx.x & 31, 32, innerChunks(row, a.rows, ci - (threadIdx.x & 31), a.cols));
 }
 
 template <int DT, bool RES, bool Q>
@@ -659,7 +708,6 @@ __global__ void __launch_bounds__(kLongThreads) rmsForwardLong(const __grid_cons
     if (threadIdx.x == 0 && a.rstd) a.rstd[row] = rstd;
     const F2 scale = pair(rstd, rstd);
     for (int ci = threadIdx.x; ci - lane < a.chunks; ci += kLongThreads) {
-      const int left = a.cols - ci * kChunk;
       const C s = sumAt(ci);
       F2 x[NP], g[NP];
       pairsOf(s, x);
@@ -667,9 +715,9 @@ __global__ void __launch_bounds__(kLongThreads) rmsForwardLong(const __grid_cons
 #pragma unroll
       for (int i = 0; i < NP; ++i) x[i] = mul2(mul2(x[i], scale), g[i]);
       // (in place: a chunk's elements are read by its own lane alone, before this)
-      if (a.sum) storeChunk<DT>(a.sum + (row * a.lds + (size_t)ci * kChunk) * E, s, left);
-      if (!Q || a.y) storeChunk<DT>(a.y + (row * a.ldy + (size_t)ci * kChunk) * E, packed<DT>(x), left);
-      if constexpr (Q) storeGroup(a, row, ci, x, w.y * rstd);
+      if (a.sum) putChunk<DT, false>(a, a.sum, a.lds, row, s, ci);
+      if (!Q || a.y) putChunk<DT, false>(a, a.y, a.ldy, row, packed<DT>(x), ci);
+      if constexpr (Q) storeGroup(a, row, ci, x, w.y * rstd, true);
     }
   }
 }
@@ -731,7 +779,7 @@ __global__ void __launch_bounds__(kLongThreads) rmsBackwardLong(const __grid_con
         const F2 v = fma2(mul2(xh[i], scale), minus, mul2(dy[i], g[i]));
         dy[i] = DSUM ? fma2(v, scale, add[i]) : mul2(v, scale);
       }
-      storeChunk<DT>(a.y + (row * a.ldy + (size_t)ci * kChunk) * E, packed<DT>(dy), a.cols - ci * kChunk);
+      putChunk<DT, false>(a, a.y, a.ldy, row, packed<DT>(dy), ci);
     }
   }
   if constexpr (HOLD) {
@@ -774,33 +822,46 @@ __global__ void __launch_bounds__(1024) rmsJoin(const float* partial, int blocks
 enum Walk { kNarrow, kRing, kLong };
 struct Shape {
   Walk walk;
+  bool vec;
   int lanes;    // narrow: of a row
   int threads;  // of a team (narrow, long: of a block)
   int teams;    // of a block; narrow: the rows it takes at a time
+  int step;     // chunks of its own that a warp takes
+  bool wide, hold;  // ring: variants
   int stages, smem, resident;
 };
-// `sources`: matrices a row is read from; `aligned`: all rows of all operands start on 16-byte boundaries.
-Shape rmsShape(size_t rows, int cols, int elem, int sources, bool aligned, bool forward) {
+// `sources`: matrices a row is read from; `aligned`: all rows of all operands start on 16-byte boundaries; `grouped`: scales
+// of groups of columns, which lie in a warp as they do in the row.
+Shape rmsShape(size_t rows, int cols, int elem, int sources, bool aligned, bool forward, bool quantized, bool grouped) {
   Shape s = {};
   const int chunks = (cols + kChunk - 1) / kChunk;
-  if (aligned && cols % kChunk == 0 && cols <= kNarrowCols) {
+  s.vec = aligned && cols % kChunk == 0;
+  s.step = s.vec || grouped ? 32 : 31;
+  const int warps = (chunks + kHeld * s.step - 1) / (kHeld * s.step);
+  s.wide = forward && !quantized && warps > forwardWarps(s.vec, false, false);
+  s.hold = s.vec && warps <= backwardWarps(true, true, elem);
+  const int most = forward ? forwardWarps(s.vec, quantized, s.wide) : backwardWarps(s.vec, s.hold, elem);
+  const int row = (chunks * (kChunk * elem / 16) + 1) * 16 * sources;
+  const int least = forward || s.hold ? 1 : 2;  // stages
+  if (s.vec && cols <= kNarrowCols) {
     s.walk = kNarrow;
     s.lanes = chunks <= 4 ? 4 : chunks <= 8 ? 8 : 16;
     s.threads = kNarrowThreads;
     s.teams = kNarrowThreads / s.lanes * kNarrowTurn;
     s.resident = 4;
-  } else if (cols <= kRingCols) {
+  } else if (warps <= most && row * least <= kRingSmem) {
     s.walk = kRing;
-    s.threads = (chunks + kHeld * 32 - 1) / (kHeld * 32) * 32;
-    const int row = (chunks * (kChunk * elem / 16) + 1) * 16 * sources;
-    s.teams = (int)std::min<size_t>(kRingThreads / s.threads, std::max<size_t>(1, (rows + smCount() - 1) / smCount()));
-    // no more stages than a team has rows
-    const size_t turns = (rows + (size_t)smCount() * s.teams - 1) / ((size_t)smCount() * s.teams);
-    s.stages = (int)std::min<size_t>(std::min(kMaxStages, kRingSmem / (s.teams * row)), std::max<size_t>(1, turns));
-    s.smem = std::max(s.teams * s.stages * row, forward ? 0 : s.teams * cols * 4);
+    s.threads = warps * 32;
+    // a block an SM: as many teams as its warps make and as have a row, with no more stages than a team has rows
     s.resident = 1;
+    s.teams = std::min(std::min(kMaxTeams, most / warps), kRingSmem / (row * least));
+    s.teams = (int)std::min<size_t>(s.teams, (rows + smCount() - 1) / smCount());
+    const size_t all = (size_t)smCount() * s.teams, turns = (rows + all - 1) / all;
+    s.stages = (int)std::min<size_t>(std::min(kMaxStages, kRingSmem / (s.teams * row)), std::max<size_t>(turns, least));
+    s.smem = std::max(s.teams * s.stages * row, forward ? 0 : s.teams * cols * 4);
   } else {
     s.walk = kLong;
+    s.step = 32;
     s.threads = kLongThreads;
     s.teams = 1;
     s.resident = 2;
@@ -815,20 +876,25 @@ int mostBlocks(size_t rows, int cols) {
   int most = 0;
   for (int elem : {2, 4})
     for (int sources : {2, 3})
-      for (bool aligned : {false, true}) most = std::max(most, rmsBlocks(rows, rmsShape(rows, cols, elem, sources, aligned, false)));
+      for (bool aligned : {false, true}) most = std::max(most, rmsBlocks(rows, rmsShape(rows, cols, elem, sources, aligned, false, false, false)));
   return most;
 }
 
 using RmsFn = void (*)(RmsArgs);
 template <int DT, bool RES, bool Q>
 RmsFn pickForward(const Shape& s) {
-  if (s.walk == kRing) return rmsForward<DT, RES, Q>;
+  if (s.walk == kRing) {
+    if constexpr (!Q)
+      if (s.wide) return s.vec ? rmsForward<DT, RES, Q, true, true> : rmsForward<DT, RES, Q, false, true>;
+    return s.vec ? rmsForward<DT, RES, Q, true, false> : rmsForward<DT, RES, Q, false, false>;
+  }
   if (s.walk == kLong) return rmsForwardLong<DT, RES, Q>;
   return s.lanes == 4 ? rmsForwardNarrow<DT, 4, RES, Q> : s.lanes == 8 ? rmsForwardNarrow<DT, 8, RES, Q> : rmsForwardNarrow<DT, 16, RES, Q>;
 }
 template <int DT, bool DSUM>
 RmsFn pickBackward(const Shape& s, int cols) {
-  if (s.walk == kRing) return rmsBackward<DT, DSUM>;
+  if (s.walk == kRing)
+    return s.hold ? rmsBackward<DT, DSUM, true, true> : s.vec ? rmsBackward<DT, DSUM, true, false> : rmsBackward<DT, DSUM, false, false>;
   if (s.walk == kLong) return cols <= kLongHeld ? rmsBackwardLong<DT, DSUM, true> : rmsBackwardLong<DT, DSUM, false>;
   return s.lanes == 4 ? rmsBackwardNarrow<DT, 4, DSUM> : s.lanes == 8 ? rmsBackwardNarrow<DT, 8, DSUM> : rmsBackwardNarrow<DT, 16, DSUM>;
 }
@@ -846,6 +912,7 @@ vrcclResult_t launchRms(RmsFn fn, const Shape& s, unsigned blocks, RmsArgs& a, i
   a.stages = s.stages;
   a.teams = s.teams;
   a.threads = s.threads;
+  a.step = s.step;
   a.slot = (a.chunks * (kChunk * elem / 16) + 1) * 16;
   const int threads = s.walk == kRing ? s.threads * s.teams : s.threads;
   return launchShaped(fn, {dim3(blocks), threads, s.smem, 0, false}, st, a);
@@ -898,7 +965,7 @@ extern "C" vrcclResult_t vrcclRmsNormForward(const void* x, size_t ldx, const vo
     return vrcclInvalidArgument;
   const bool aligned = rowsAligned(x, ldx, E) && (!residual || rowsAligned(residual, ldr, E)) && (!sum || rowsAligned(sum, lds, E)) &&
                        (!y || rowsAligned(y, ldy, E));
-  const Shape s = rmsShape(rows, (int)cols, E, residual ? 2 : 1, aligned, true);
+  const Shape s = rmsShape(rows, (int)cols, E, residual ? 2 : 1, aligned, true, codes, codes && group);
   RmsArgs a = {};
   a.src[0] = sourceOf(x, ldx, E);
   a.src[1] = sourceOf(residual, ldr, E);
@@ -966,7 +1033,7 @@ extern "C" vrcclResult_t vrcclRmsNormBackward(const void* dy, size_t lddy, const
   const Span matrices[] = {spanDy, spanS, spanDsum};
   if (!apart(all, in) || !apart(other, matrices)) return vrcclInvalidArgument;
   const bool sources = rowsAligned(dy, lddy, E) && rowsAligned(s, lds, E) && (!dsum || rowsAligned(dsum, ldds, E));
-  const Shape shape = rmsShape(rows, (int)cols, E, dsum ? 3 : 2, sources && rowsAligned(dx, lddx, E), false);
+  const Shape shape = rmsShape(rows, (int)cols, E, dsum ? 3 : 2, sources && rowsAligned(dx, lddx, E), false, false, false);
   const int blocks = rmsBlocks(rows, shape);
   RmsArgs a = {};
   a.src[0] = sourceOf(s, lds, E);

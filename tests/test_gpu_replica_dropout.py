@@ -50,6 +50,23 @@ def test_dropout(torch, v, rows, cols, pad, offset, dtype):  # noqa: F811
     _check(torch, v, rows, cols, dtype, 0.1, pad, offset, residual=False, number=1 << 40, first=(1 << 33) + 5)
 
 
+@pytest.mark.parametrize("rows,cols,pad,offset", [(70, 3, 0, 0), (33, 65, 0, 0), (17, 127, 0, 2), (5, 250, 3, 0), (6, 1001, 0, 0), (5, 4097, 0, 1),
+                                                  (4, 2048, 3, 0)])
+def test_dropout_of_odd_rows(torch, v, rows, cols, pad, offset):  # noqa: F811
+    """Several rows a warp, and warps inside a row that look at the next one's beginning."""
+    for dtype in ("float32", "float16"):
+        _check(torch, v, rows, cols, dtype, 0.3, pad, offset)
+        _check(torch, v, rows, cols, dtype, 0.3, pad, offset, residual=False, yskew=(offset + 3) % 8)
+
+
+def test_dropout_counters_past_32_bits(torch, v):  # noqa: F811
+    """Row numbers at which a block's counters, and a warp's, pass a multiple of 2^32."""
+    for rows, cols, pad in ((100, 64, 0), (100, 64, 8), (9, 1001, 0)):
+        per = -(-cols // 8)
+        for upper in (1, 5):
+            _check(torch, v, rows, cols, "bfloat16", 0.5, pad, first=(upper << 32) // per - 5)
+
+
 @pytest.mark.parametrize("skew", range(8))
 def test_dropout_output_on_every_skew(torch, v, skew):  # noqa: F811
     _check(torch, v, 3, 300, "bfloat16", 0.5, 3, 2, yskew=skew)
@@ -72,6 +89,9 @@ def test_dropout_of_many_rows_matches_its_parts(torch, v):  # noqa: F811
     v.vrcclDropoutForward(x, None, y, rows, cols, "bfloat16", 0.3, seed, 9)
     v.vrcclDropoutForward(x, None, odd, rows, cols, "bfloat16", 0.3, seed, 9)
     assert torch.equal(y, odd)
+    gaps = torch.empty(rows, cols + 8, device="cuda", dtype=torch.bfloat16)[:, :cols]
+    v.vrcclDropoutForward(x, None, gaps, rows, cols, "bfloat16", 0.3, seed, 9)
+    assert torch.equal(y, gaps)
     part = torch.empty(13, cols, device="cuda", dtype=torch.bfloat16)
     for at in (0, 1, 2500, rows - 13):
         v.vrcclDropoutForward(x[at:at + 13], None, part, 13, cols, "bfloat16", 0.3, seed, 9, at)
@@ -94,7 +114,7 @@ def test_dropped_elements_may_hold_anything(torch, v):  # noqa: F811
             assert np.array_equal(y.cpu().numpy(), want.astype(np.float32))
 
 
-@pytest.mark.parametrize("cols,pad", [(128, 0), (131, 0), (131, 5)])
+@pytest.mark.parametrize("cols,pad", [(128, 0), (131, 0), (131, 5), (1001, 0), (4001, 6)])
 def test_dropout_in_place(torch, v, cols, pad):  # noqa: F811
     g = _rng(3)
     a, b = g.standard_normal((40, cols)), g.standard_normal((40, cols))

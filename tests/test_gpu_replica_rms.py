@@ -117,6 +117,17 @@ def test_rms_backward(torch, v, rows, cols, pad, offset, dtype):  # noqa: F811
     _backward(torch, v, rows, cols, dtype, "bfloat16", pad, offset, affine=False, dgamma=False)
 
 
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("rows,cols,pad,offset", [(3001, 2003, 3, 0), (2500, 1001, 0, 1), (2000, 520, 8, 0), (700, 9000, 0, 0), (900, 4097, 0, 0),
+                                                  (500, 9001, 0, 0), (310, 15001, 0, 0), (5000, 264, 1, 0)])
+def test_rms_of_more_rows_than_stages(torch, v, rows, cols, pad, offset, dtype):  # noqa: F811
+    """Every stage is filled again and again."""
+    _forward(torch, v, rows, cols, dtype, "float32", pad, offset)
+    _backward(torch, v, rows, cols, dtype, "float32", pad, offset)
+    _forward(torch, v, rows, cols, dtype, "float32", pad, offset, residual=False, quant="e4m3", group=64 if cols % 2 else 0, with_y=False)
+    _backward(torch, v, rows, cols, dtype, "float32", pad, offset, dsum=False)
+
+
 @pytest.mark.parametrize("quant", ["int8", "e4m3"])
 @pytest.mark.parametrize("group", [0, 32, 64, 128])
 @pytest.mark.parametrize("rows,cols,pad,offset", [(1, 1, 0, 0), (3, 30, 0, 0), (50, 64, 0, 0), (9, 96, 0, 0), (30, 128, 16, 0), (5, 129, 0, 0),
@@ -225,15 +236,17 @@ def test_rms_rows_beyond_32_bits(torch, v):  # noqa: F811
     for shift in (0, 1):
         x = buf.as_strided((3, cols), (ld, 1), shift)
         x.copy_(torch.as_tensor(_rng(7).standard_normal((3, cols))))
-        flat = x.clone()
-        y, want = torch.empty_like(flat), torch.empty_like(flat)
+        # the same rows close together, and on the same skew (on another one sums go in another order)
+        flat = torch.empty(3 * 528 + 1, device="cuda", dtype=torch.bfloat16).as_strided((3, cols), (528, 1), shift)
+        flat.copy_(x)
+        y, want = torch.empty(3, cols, device="cuda", dtype=torch.bfloat16), torch.empty(3, cols, device="cuda", dtype=torch.bfloat16)
         r1, r2 = torch.empty(3, device="cuda"), torch.empty(3, device="cuda")
         v.vrcclRmsNormForward(x, None, None, None, y, r1, 3, cols, "bfloat16", "float32")
         v.vrcclRmsNormForward(flat, None, None, None, want, r2, 3, cols, "bfloat16", "float32")
         assert torch.equal(y, want) and torch.equal(r1, r2)
         v.vrcclRmsNormBackward(flat, None, flat, None, r1, want, None, 3, cols, "bfloat16", "float32")
         v.vrcclRmsNormBackward(x, x, x, None, r1, y, None, 3, cols, "bfloat16", "float32")
-        both = torch.empty_like(flat)
+        both = torch.empty_like(y)
         v.vrcclRmsNormBackward(flat, flat, flat, None, r1, both, None, 3, cols, "bfloat16", "float32")
         assert torch.equal(y, both)
         v.vrcclRmsNormBackward(x, None, x, None, r1, x, None, 3, cols, "bfloat16", "float32")

@@ -14,26 +14,51 @@ from oracle import replica as o
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "ring_allreduce_reduction_gb300", "csrc")
 
 SOURCE = r"""
+#include <initializer_list>
 #include "ops_chunks.h"
 using namespace vrccl;
-// The bytes that a warp's store of a row writes, and which lane writes each: as storeChunk, lane by lane.
-extern "C" void storeOf(unsigned skew, int E, int cols, int firstChunk, int* writer, int* times) {
+// The bytes that the store of a row by lanes writes, and which lane writes each: as storeChunk, lane by lane.
+extern "C" void storeOf(unsigned skew, int E, int cols, int firstChunk, int lanes, int step, int* writer, int* times) {
   const int NB = kChunk * E / 16;
-  for (int lane = 0; lane < 32; ++lane) {
+  for (int lane = 0; lane < lanes; ++lane) {
+    const Place place = {lane, lanes, firstChunk + lane, step};
+    if (lane >= step) continue;
     const int at = (firstChunk + lane) * kChunk * E, left = cols - (firstChunk + lane) * kChunk;
     if (left <= 0) continue;
     auto mark = [&](int byte, int n) {
-      for (int i = 0; i < n; ++i) writer[byte + i] = lane, ++times[byte + i];
+      if ((byte + (int)skew) % n) writer[byte] = 1000;  // not aligned
+      for (int i = 0; i < n; ++i) writer[byte + i] += lane, ++times[byte + i];
+    };
+    auto rest = [&](int from, int n) {
+      for (int size : {8, 4, 2})
+        if (n & size) mark(from + restPiece(n, size), size);
     };
     if (skew == 0) {
-      for (int e = 0; e < kChunk; ++e)
-        if (e < left) mark(at + e * E, E);
+      for (int b = 0; b < NB; ++b) {
+        const int n = left * E - 16 * b;
+        if (n >= 16)
+          mark(at + 16 * b, 16);
+        else if (n > 0)
+          rest(at + 16 * b, n);
+      }
       continue;
     }
-    for (int b = 0; b < NB; ++b)
-      if (wholeBlock(b, skew, E, left, lane)) mark(at + 16 * (b + 1) - (int)skew, 16);
-    for (int e = 0; e < kChunk; ++e)
-      if (storedSingly(e, skew, E, left, lane)) mark(at + e * E, E);
+    const int head = headOf(skew);
+    if (!headStored(skew, E, left, place)) {
+      if (left * E < head) {
+        for (int e = 0; e < left; ++e) mark(at + e * E, E);
+        continue;
+      }
+      for (int size : {2, 4, 8})
+        if (head & size) mark(at + headPiece(head, size), size);
+    }
+    for (int b = 0; b < NB; ++b) {
+      const int from = at + head + 16 * b, n = restOf(b, skew, E, left);
+      if (wholeBlock(b, skew, E, left, place))
+        mark(from, 16);
+      else if (n > 0)
+        rest(from, n);
+    }
   }
 }
 extern "C" int loaded(uintptr_t block, uintptr_t rowEnd, uintptr_t begin, uintptr_t end) { return blockLoaded(block, rowEnd, begin, end); }
@@ -47,6 +72,7 @@ extern "C" int keepsOf(uint32_t word, int odd, int drop) {
   Random128 r = {{word, word, word, word}};
   return keeps(r, 4 + odd, (uint32_t)drop * 65536u - 1, drop == 0);
 }
+extern "C" uint32_t divided(uint32_t n, uint32_t d) { return quotient(n, divisionOf(d)); }
 extern "C" uint64_t magic(uint64_t d, uint64_t most) { return magicOf(d, most); }
 """
 
@@ -72,17 +98,20 @@ def lib(tmp_path_factory):
 
 @pytest.mark.parametrize("E", [2, 4])
 def test_every_byte_of_a_row_is_stored_once(lib, E):
-    """And none beside them; whole blocks lie on 16-byte boundaries by construction."""
+    """And none beside them, every piece on a boundary of its size."""
     for skew in range(0, 16, E):
         for cols in list(range(1, 40)) + [255, 256, 257, 300, 511, 512, 513]:
-            for first in range(0, (cols + 7) // 8, 32):
+            for lanes, step in ((8, 8), (16, 16), (32, 32), (32, 31)):
+                if lanes < 32 and cols > 8 * lanes:
+                    continue
                 writer, times = (ctypes.c_int * 8192)(), (ctypes.c_int * 8192)()
-                lib.storeOf(skew, E, cols, first, writer, times)
-                lo, hi = first * 8 * E, min(cols, (first + 32) * 8) * E
-                t = np.array(times)
-                assert (t[lo:hi] == 1).all() and t[:lo].sum() == 0 and t[hi:].sum() == 0, (skew, cols, first)
-                w = np.array(writer)[lo:hi] - (np.arange(lo, hi) // (8 * E) - first)
-                assert set(w) <= {0, -1}  # a lane writes its own chunk and what it took from the next one
+                for first in range(0, (cols + 7) // 8, step):
+                    lib.storeOf(skew, E, cols, first, lanes, step, writer, times)
+                t, end = np.array(times), cols * E
+                assert (t[:end] == 1).all() and t[end:].sum() == 0, (skew, cols, step)
+                # a lane writes its own chunk and what it took from the next one
+                lane = np.arange(end) // (8 * E) % step
+                assert all(w in (at, at - 1, step - 1 if at == 0 and step < lanes else at) for w, at in zip(writer[:end], lane))
 
 
 @pytest.mark.parametrize("E", [2, 4])
@@ -151,3 +180,12 @@ def test_division_by_a_product(lib):
                     [q * d - 1 for q in map(int, g.integers(1, most // d + 2, 50))]:
                 if 0 <= n <= most:
                     assert n * m >> 64 == n // d, (d, n)
+
+
+def test_division_by_a_32_bit_product(lib):
+    g = np.random.default_rng(2)
+    for d in [2, 3, 5, 7, 17, 31, 32, 33, 126, 512, 513, 1000, 12345, (1 << 23) - 1, 1 << 23, (1 << 23) + 1, (1 << 26) - 1]:
+        top = (1 << 31) - 1
+        for n in [0, 1, d - 1, d, d + 1, top - 1, top, top // d * d, top // d * d - 1] + [int(x) for x in g.integers(0, top, 200)] + \
+                [q * d - 1 for q in map(int, g.integers(1, top // d + 1, 200))]:
+            assert lib.divided(n, d) == n // d, (d, n)
