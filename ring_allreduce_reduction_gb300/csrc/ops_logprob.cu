@@ -30,7 +30,8 @@
 // one's largest (k entries do) is collected; places, of segments and of
 // entries, are counts of what is above. Of ties there may be too many to
 // collect (a row of one value): each warp then keeps its best in order, one a
-// lane, and the warps' lists are merged two and two.
+// lane, and the warps' lists are merged two and two. Many short rows go a warp
+// each, whose steps need no barrier.
 //
 // Backward reads the logits and writes the gradient; the statistics are saved,
 // so that a row may be cut into independent slices.
@@ -68,7 +69,7 @@ struct LogProbArgs {
   const float* dlogprob;
   const float* dentropy;
   void* dlogits;
-  size_t ldl, ldt, ldi, ldd, lstride, hstride, vocab;
+  size_t ldl, ldt, ldi, ldd, lstride, hstride, vocab, rows;
   size_t slice;  // backward: elements of a row one block takes
   int k, span, shift;  // span: loads of a segment, 2^shift
   bool wide;  // 64-bit tokens
@@ -313,13 +314,14 @@ struct Row {
 };
 
 // A thread's pass (vectors i, i + 32, ... of a row, i - lane a multiple of kPass) into its sums; own: the largest of each vector.
-template <int DT>
+// AGAIN: they will soon be read once more.
+template <int DT, bool AGAIN = false>
 __device__ __forceinline__ void runPass(Stream& stream, const Row<DT>& in, size_t i, float (&own)[kUnroll], float c) {
   constexpr int U = kUnroll;
   if (i - (threadIdx.x & 31) + kPass <= in.nvec) {
     uint4 v[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) v[u] = __ldcs(in.vec + i + u * 32);
+    for (int u = 0; u < U; ++u) v[u] = (AGAIN ? __ldca(in.vec + i + u * 32) : __ldcs(in.vec + i + u * 32));
 #pragma unroll
     for (int u = 0; u < U; ++u) own[u] = largestOf<DT>(v[u]);
     runOver<DT, U>(stream, v, maxOrNan(maxOrNan(own[0], own[1]), maxOrNan(own[2], own[3])), c);
@@ -328,7 +330,7 @@ __device__ __forceinline__ void runPass(Stream& stream, const Row<DT>& in, size_
     for (int u = 0; u < U; ++u) {
       own[u] = -INFINITY;
       if (i + u * 32 < in.nvec) {
-        const uint4 v[1] = {__ldcs(in.vec + i + u * 32)};
+        const uint4 v[1] = {(AGAIN ? __ldca(in.vec + i + u * 32) : __ldcs(in.vec + i + u * 32))};
         own[u] = largestOf<DT>(v[0]);
         runOver<DT, 1>(stream, v, own[u], c);
       }
@@ -345,6 +347,26 @@ __device__ __forceinline__ void sayPadding(const LogProbArgs& a, size_t row) {  
   if (lane < a.k) {
     a.top[row * a.ldt + lane] = -INFINITY;
     a.topIndex[row * a.ldi + lane] = -1;
+  }
+}
+// A row's results from its sums, the token's logit and the likeliest entries' keys: a warp.
+template <bool TOP>
+__device__ __forceinline__ void sayRow(const LogProbArgs& a, size_t row, const Sums& r, float given, const Key* best) {
+  const int lane = threadIdx.x & 31;
+  const bool nothing = r.m == -INFINITY && r.l == 0.f;
+  const float ll = nothing ? 0.f : logf(r.l);
+  auto logOf = [&](float s) { return nothing ? -INFINITY : (s - r.m) * a.invT - ll; };
+  if (lane == 0) {
+    if (a.logprob) a.logprob[row] = logOf(given);
+    if (a.entropy) a.entropy[row] = nothing ? 0.f : ll - r.w / r.l * kLn2;
+    if (a.stats) a.stats[row] = make_float2(r.m, ll);
+  }
+  if constexpr (TOP) {
+    if (lane < a.k) {
+      const Key entry = best[lane];
+      a.top[row * a.ldt + lane] = entry ? logOf(fromAscending((uint32_t)(entry >> 32))) : -INFINITY;
+      a.topIndex[row * a.ldi + lane] = entry ? (int)~(uint32_t)entry : -1;
+    }
   }
 }
 template <int DT>
@@ -376,6 +398,140 @@ struct Finder {
   int entries, candidates;
 };
 struct NoFinder {};
+
+// ------------------------------------------------------------ short rows
+// A warp a row: nothing but shuffles between its lanes. Each lane has the largest of either half of its vectors, and the k-th
+// of those 64 bounds the k-th entry from below; what reaches it (64 log 2 = 44 entries are to be expected for k = 32, however
+// long the row) is collected in a second reading.
+constexpr int kShortThreads = 128, kShortCollected = 128, kShortVectors = 1024;  // (a lane has the largest logit of 32 vectors)
+struct ShortFinder {
+  Key collected[kShortCollected];
+  Key best[32];
+  int entries;
+};
+// The lanes' values in order, the largest in lane 0 ; of two values a lane, the 32 largest.
+__device__ __forceinline__ uint32_t sortedOverLanes(uint32_t x) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int size = 2; size <= 32; size *= 2)
+#pragma unroll
+    for (int o = size / 2; o; o /= 2) {
+      const uint32_t y = __shfl_xor_sync(0xffffffffu, x, o);
+      x = ((lane & o) == 0) == ((lane & size) == 0 || size == 32) ? max(x, y) : min(x, y);
+    }
+  return x;
+}
+__device__ __forceinline__ uint32_t sortedOverLanes(uint32_t x, uint32_t y) {
+  const int lane = threadIdx.x & 31;
+  x = max(sortedOverLanes(x), __shfl_sync(0xffffffffu, sortedOverLanes(y), 31 - lane));
+#pragma unroll
+  for (int o = 16; o; o /= 2) {
+    const uint32_t b = __shfl_xor_sync(0xffffffffu, x, o);
+    x = (lane & o) == 0 ? max(x, b) : min(x, b);
+  }
+  return x;
+}
+template <int DT, bool TOP>
+__global__ void __launch_bounds__(kShortThreads, 8) logProbForwardShort(const __grid_constant__ LogProbArgs a) {
+  constexpr int V = Vec16<DT>::N, U = kUnroll;
+  __shared__ __align__(16) std::conditional_t<TOP, ShortFinder, NoFinder> finders[kShortThreads / 32];
+  const int lane = threadIdx.x & 31;
+  const size_t row = (size_t)blockIdx.x * (kShortThreads / 32) + threadIdx.x / 32;
+  if (row >= a.rows) return;
+  const Row<DT> in(a, row);
+  const float c = a.invT * kLog2e;
+  const long long token = tokenOf(a, row);
+  if (token == -2) {
+    sayPadding(a, row);
+    return;
+  }
+  const float given = token >= 0 ? in.at(token) : 0.f;
+  const bool single = lane < in.odd();
+  const size_t singleAt = single ? in.oddIndex(lane) : 0;
+  const float singleLogit = single ? in.at(singleAt) : 0.f;
+  Stream stream = {{-INFINITY, 0.f, 0.f}, -INFINITY, false};
+  float half[2] = {-INFINITY, -INFINITY}, top = -INFINITY;  // the lane's, and of vectors 32 lane ..
+  for (size_t i = lane; i < in.nvec + lane; i += kPass) {  // (the warp's lanes together)
+    float own[U];
+    runPass<DT, TOP>(stream, in, i, own, c);
+    if constexpr (TOP) {
+      half[0] = maxOrNan(half[0], maxOrNan(own[0], own[1]));
+      half[1] = maxOrNan(half[1], maxOrNan(own[2], own[3]));
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const float x = largestOfWarp(own[u]);
+        if (lane == (int)(i / 32) + u) top = x;
+      }
+    }
+  }
+  Sums r = settled(stream, c);
+  if (single) {
+    const float f[1] = {singleLogit};
+    runOver<1>(r, f, c);
+  }
+  r = warpJoin(r, c);
+  if constexpr (TOP) {
+    ShortFinder& find = finders[threadIdx.x / 32];
+    const uint32_t first = (size_t)lane < in.nvec ? ascending(half[0]) : 0, second = (size_t)lane + 64 < in.nvec ? ascending(half[1]) : 0;
+    const uint32_t enough = __shfl_sync(0xffffffffu, sortedOverLanes(first, second), a.k - 1);
+    const float bound = enough ? fromAscending(enough) : -INFINITY;  // (an infinity where that is a NaN's)
+    find.best[lane] = 0;
+    if (lane == 0) find.entries = 0;
+    __syncwarp();
+    auto push = [&](float f, size_t index) {
+      const int to = atomicAdd(&find.entries, 1);
+      if (to < kShortCollected) find.collected[to] = keyOf(ascending(f), index);
+    };
+    // the warp's loads with such entries, U at a time, to fn(a vector, whether it is one, its first element)
+    const unsigned loads = __ballot_sync(0xffffffffu, !(top < bound));
+    auto forAll = [&](auto fn) {
+      for (unsigned rest = loads; rest;) {
+        uint4 v[U];
+        int i[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          i[u] = rest ? (__ffs(rest) - 1) * 32 + lane : kShortVectors;
+          rest &= rest - 1;
+          v[u] = i[u] < (int)in.nvec ? __ldca(in.vec + i[u]) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) fn(v[u], i[u] < (int)in.nvec, in.head + i[u] * V);
+      }
+    };
+    forAll([&](const uint4& v, bool there, size_t first) {
+      if (!there || largestOf<DT>(v) < bound) return;  // (a NaN is the largest, and not below)
+      float f[V];
+      Vec16<DT>::expand(v, f);
+      unsigned who = 0;
+#pragma unroll
+      for (int e = 0; e < V; ++e) who |= f[e] < bound ? 0 : 1u << e;
+      for (; who; who &= who - 1) push(in.at(first + __ffs(who) - 1), first + __ffs(who) - 1);
+    });
+    if (single && !(singleLogit < bound)) push(singleLogit, singleAt);
+    __syncwarp();
+    const int n = find.entries;
+    if (n <= kShortCollected) {
+      for (int j = lane; j < n; j += 32) {
+        const int place = above(find.collected, n, find.collected[j]);
+        if (place < a.k) find.best[place] = find.collected[j];
+      }
+    } else {
+      Key list = 0, last = 0;
+      forAll([&](const uint4& v, bool there, size_t first) {
+        float f[V];
+        Vec16<DT>::expand(v, f);
+#pragma unroll
+        for (int e = 0; e < V; ++e) insert(list, last, there ? keyOf(ascending(f[e]), first + e) : 0, a.k);
+      });
+      insert(list, last, single ? keyOf(ascending(singleLogit), singleAt) : 0, a.k);
+      find.best[lane] = list;
+    }
+    __syncwarp();
+    sayRow<TOP>(a, row, r, given, find.best);
+  } else {
+    sayRow<TOP>(a, row, r, given, nullptr);
+  }
+}
 
 // A row over the blocks of a cluster, T threads each. TOP: with the likeliest entries.
 template <int DT, int T, bool TOP>
@@ -542,21 +698,10 @@ __global__ void __launch_bounds__(T, T == 128 ? 8 : 3 * kThreads / T) logProbFor
   if (warp != 0) return;
   __syncwarp();
   r = warpJoin(lane < (parts > 1 ? (int)parts : warps) ? part[lane] : Sums{-INFINITY, 0.f, 0.f}, c);
-  const bool nothing = r.m == -INFINITY && r.l == 0.f;
-  const float ll = nothing ? 0.f : logf(r.l);
-  auto logOf = [&](float s) { return nothing ? -INFINITY : (s - r.m) * a.invT - ll; };
-  if (lane == 0) {
-    if (a.logprob) a.logprob[row] = logOf(given);
-    if (a.entropy) a.entropy[row] = nothing ? 0.f : ll - r.w / r.l * kLn2;
-    if (a.stats) a.stats[row] = make_float2(r.m, ll);
-  }
-  if constexpr (TOP) {
-    if (lane < a.k) {
-      const Key entry = find.best[lane];
-      a.top[row * a.ldt + lane] = entry ? logOf(fromAscending((uint32_t)(entry >> 32))) : -INFINITY;
-      a.topIndex[row * a.ldi + lane] = entry ? (int)~(uint32_t)entry : -1;
-    }
-  }
+  if constexpr (TOP)
+    sayRow<TOP>(a, row, r, given, find.best);
+  else
+    sayRow<TOP>(a, row, r, given, nullptr);
 }
 
 template <int DT, int T>
@@ -714,6 +859,7 @@ extern "C" vrcclResult_t vrcclLogProbForward(const void* logits, size_t ldl, con
   a.ldt = ldt;
   a.ldi = ldi;
   a.k = (int)k;
+  a.rows = rows;
   // split a row over a cluster until the grid fills the GPU or a block has less than two vectors a thread
   unsigned parts = 1;
   const size_t bytes = vocab * E;
@@ -724,13 +870,20 @@ extern "C" vrcclResult_t vrcclLogProbForward(const void* logits, size_t ldl, con
   a.span = 1;
   while (a.span < kUnroll ? passes * (kUnroll / a.span) > kSegments : passes / (a.span / kUnroll) + 1 > kSegments) a.span *= 2;
   while ((1 << a.shift) < a.span) ++a.shift;
-  auto pick = [&](auto dt) {
+  // a warp a row, where rows are short and many. bf16, k = 8, a warp against a block a row: 1024 columns 400 rows 4.6 / 7.7 us,
+  // 20000: 28 / 152; 4096 columns 400 rows 8.7 / 6.5, 2000: 9.2 / 14.8, 20000: 52 / 122; 8192 columns 1000 rows 12.0 / 10.2, 5000:
+  // 29 / 40; 20000: 78 / 144; 16384 columns 10000 rows (with longer segments) 118 / 98. Without a list 20000 x 4096 31 / 48.
+  const bool brief = bytes <= kShortVectors * 16 && rows >= bytes / 8;
+  auto pick = [&](auto dt) -> LogProbFn {
     constexpr int DT = decltype(dt)::value;
+    if (brief) return k ? logProbForwardShort<DT, true> : logProbForwardShort<DT, false>;
     return k ? pickForward<DT, true>(threads) : pickForward<DT, false>(threads);
   };
+
   const LogProbFn fn = dtype == vrcclFloat32    ? pick(std::integral_constant<int, vrcclFloat32>{})
                        : dtype == vrcclBfloat16 ? pick(std::integral_constant<int, vrcclBfloat16>{})
                                                 : pick(std::integral_constant<int, vrcclFloat16>{});
+  if (brief) return launchShaped(fn, {dim3((unsigned)((rows + kShortThreads / 32 - 1) / (kShortThreads / 32))), kShortThreads, 0, 0, false}, (cudaStream_t)stream, a);
   return launchShaped(fn, {dim3((unsigned)(rows * parts)), threads, 0, (int)parts, false}, (cudaStream_t)stream, a);
 }
 

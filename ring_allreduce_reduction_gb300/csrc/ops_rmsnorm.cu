@@ -67,9 +67,8 @@ constexpr int kHeld = 2;  // chunks a thread holds
 // need more warps have 32 (wide).
 constexpr int forwardWarps(bool vec, bool q, bool wide) { return wide || q ? 32 : vec ? 24 : 28; }
 // Backward keeps a row's chunks in registers (hold) where 16 warps do: 16384 x 8192 bf16 159 us (20 warps: 205). Else it reads
-// them from the stage once more: 16384 x 4097 20 warps 178 us (16 and held: 246, 24: 222, 28: 201), 4096 x 16384 with 32: 110;
-// 3001 x 2003 fp32 16 warps 28.3 us (20: 29.7, 24: 35).
-constexpr int backwardWarps(bool vec, bool hold, int elem) { return hold ? 16 : vec ? 32 : elem == 4 ? 16 : 20; }
+// them from the stage once more: 16384 x 4097 20 warps 178 us (16 and held: 246, 24: 222, 28: 201), 4096 x 16384 with 32: 110.
+constexpr int backwardWarps(bool vec, bool hold) { return hold ? 16 : vec ? 32 : 20; }
 constexpr int kMaxTeams = 15;  // (as many named barriers, and the block's)
 constexpr int kRingSmem = 208 * 1024;  // of the 227 KB a block may have
 
@@ -423,7 +422,7 @@ __device__ __forceinline__ void layOut(float* p, const F2 (&dg)[kChunk / 2], int
 }
 
 template <int DT, bool DSUM, bool VEC, bool HOLD>
-__global__ void __launch_bounds__(32 * backwardWarps(VEC, HOLD, floatTypeSize(DT))) rmsBackward(const __grid_constant__ RmsArgs a) {
+__global__ void __launch_bounds__(32 * backwardWarps(VEC, HOLD)) rmsBackward(const __grid_constant__ RmsArgs a) {
   using C = Chunk<DT>;
   constexpr int E = C::E, NP = kChunk / 2;
   extern __shared__ __align__(128) unsigned char smem[];
@@ -839,8 +838,8 @@ Shape rmsShape(size_t rows, int cols, int elem, int sources, bool aligned, bool 
   s.step = s.vec || grouped ? 32 : 31;
   const int warps = (chunks + kHeld * s.step - 1) / (kHeld * s.step);
   s.wide = forward && !quantized && warps > forwardWarps(s.vec, false, false);
-  s.hold = s.vec && warps <= backwardWarps(true, true, elem);
-  const int most = forward ? forwardWarps(s.vec, quantized, s.wide) : backwardWarps(s.vec, s.hold, elem);
+  s.hold = s.vec && warps <= backwardWarps(true, true);
+  const int most = forward ? forwardWarps(s.vec, quantized, s.wide) : backwardWarps(s.vec, s.hold);
   const int row = (chunks * (kChunk * elem / 16) + 1) * 16 * sources;
   const int least = forward || s.hold ? 1 : 2;  // stages
   if (s.vec && cols <= kNarrowCols) {

@@ -283,3 +283,50 @@ def test_logprob_rows_beyond_32_bits(torch, v):  # noqa: F811
         v.vrcclLogProbBackward(t, dev, outs[2], outs[1], one, one, t, 3, vocab, "bfloat16", "int64")
         res.append(outs + [t.clone()])
     assert all(torch.equal(a, b) for a, b in zip(*res))
+
+
+@pytest.mark.parametrize("dtype", FLOATS)
+@pytest.mark.parametrize("vocab,pad,offset", [(40, 0, 0), (257, 1, 0), (1003, 0, 3), (1891, 8, 1), (2048, 0, 0), (4090, 3, 0)])
+def test_logprob_of_many_short_rows(torch, v, vocab, pad, offset, dtype):  # noqa: F811
+    """A warp a row: masks, ties (too many to collect, too), padding, every length of the list."""
+    E = 4 if dtype == "float32" else 2
+    rows = max(80, vocab * E // 8 + 5)
+    s, token, _ = _inputs(torch, rows, vocab, dtype, pad, offset)
+    low, a = float(torch.finfo(getattr(torch, dtype)).min), s.view
+    a[1] = 1.5
+    a[2] = (a[2] * 0.5).round()
+    a[3, ::2] = -float("inf")
+    a[4] = -float("inf")
+    a[5] = low
+    a[6, 1:] = -float("inf")
+    a[7, : vocab // 2] = 0.0
+    a[7, vocab // 3: vocab // 2] = -0.0
+    a[7, vocab // 2:] = -1.0
+    a[8] = -3.0
+    a[8, vocab - 1] = a[8, 0] = a[8, vocab // 2] = 2.0
+    a[9, : vocab - 5] = -float("inf")
+    token[[1, 4, 8]] = 0, vocab - 1, vocab // 2
+    for k, T in ((1, 1.0), (5, 0.7), (32, 2.0), (0, 1.0), (17, 1.0)):
+        _forward(torch, v, s, token, k, dtype, T)
+
+
+def test_short_rows_that_are_not_finite(torch, v):  # noqa: F811
+    """Rows of a NaN or infinity among many give what they give among few, which go another way."""
+    rows, vocab, k = 600, 1001, 6
+    x = torch.as_tensor(_rng(8).standard_normal((rows, vocab))).float().cuda()
+    x[1, 77] = x[2, 5] = x[2, 999] = float("inf")
+    x[3, 9] = float("inf")
+    x[3, 300] = x[3, 200] = x[4, 1000] = x[0, 0] = float("nan")
+    token = torch.arange(rows, device="cuda")
+
+    def call(n):
+        f = [torch.empty(n, device="cuda") for _ in range(2)]
+        stats, top, index = torch.empty(n, 2, device="cuda"), torch.empty(n, k, device="cuda"), torch.empty(n, k, device="cuda", dtype=torch.int32)
+        v.vrcclLogProbForward(x[:n], token[:n], f[0], f[1], stats, top, index, n, vocab, k, "float32", "int64")
+        return f, top, index
+
+    (few, ft, fi), (many, mt, mi) = call(5), call(rows)
+    assert torch.equal(mi[:5], fi)
+    for p, q in zip([*many, mt], [*few, ft]):
+        assert torch.isnan(p[:5]).equal(torch.isnan(q)) and torch.isfinite(p[5:]).all()
+    assert torch.isnan(many[0][:5]).all() and fi[4, 0] == 1000 and fi[3, :3].tolist() == [200, 300, 9] and fi[2, :2].tolist() == [5, 999]
