@@ -744,7 +744,8 @@ typedef enum {
  *                sum and y may each be x or residual (same stride), not both
  *                the same one.
  *   codes        out, [rows, cols] bytes, or NULL: y in 8 bits, code = y /
- *                scale rounded to the nearest (even) int8 or e4m3.
+ *                scale (to binary32's precision) rounded to the nearest (even)
+ *                int8 or e4m3.
  *   scales       out, binary32 [rows, ceil(cols / group)], what a code is
  *                multiplied by: the largest |y| of the group (unrounded) over
  *                the largest code, at least 2^-126. Not finite where a y of the

@@ -474,7 +474,7 @@ __global__ void __launch_bounds__(kShortThreads, 8) logProbForwardShort(const __
     ShortFinder& find = finders[threadIdx.x / 32];
     const uint32_t first = (size_t)lane < in.nvec ? ascending(half[0]) : 0, second = (size_t)lane + 64 < in.nvec ? ascending(half[1]) : 0;
     const uint32_t enough = __shfl_sync(0xffffffffu, sortedOverLanes(first, second), a.k - 1);
-    const float bound = enough ? fromAscending(enough) : -INFINITY;  // (an infinity where that is a NaN's)
+    const float bound = enough ? fromAscending(enough) : -INFINITY;  // (a NaN: all are taken)
     find.best[lane] = 0;
     if (lane == 0) find.entries = 0;
     __syncwarp();
