@@ -25,8 +25,8 @@ FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", f"-I{INCLUDE}"
 SOURCES = ["kernels_simple.cu", "kernels_simple_x.cu", "kernels_ll.cu", "kernels_ll128.cu", "kernels_ll128w.cu",
            "kernels_ll128w_x.cu", "kernels_oneshot.cu", "kernels_group_simple.cu",
            "kernels_group_ll.cu", "kernels_group_ll128.cu", "vrccl.cu", "vrccl_noalloc.cu", "tuner.cc", "parse.cc",
-           "model.cc", "ops_norm.cu", "ops_linear.cu", "ops_distill.cu", "ops_rmsnorm.cu", "ops_dropout.cu",
-           "ops_logprob.cu"]
+           "model.cc", "ops_norm.cu", "ops_linear.cu", "ops_distill.cu", "ops_rmsnorm.cu",
+           "ops_rmsnorm_backward.cu", "ops_dropout.cu", "ops_logprob.cu"]
 
 
 def _nvcc() -> str:

@@ -51,6 +51,16 @@ struct Chunk {
         w[i] = 2 * i + 1 < left ? w[i] : 2 * i < left ? w[i] & 0xffffu : 0;
     }
   }
+  // Elements before number n become zero (n < 8).
+  __device__ __forceinline__ void cutHead(int n) {
+#pragma unroll
+    for (int i = 0; i < NW; ++i) {
+      if constexpr (E == 4)
+        w[i] = i < n ? 0 : w[i];
+      else
+        w[i] = 2 * i + 1 < n ? 0 : 2 * i < n ? w[i] & 0xffff0000u : w[i];
+    }
+  }
   __device__ __forceinline__ uint32_t bits(int e) const { return E == 4 ? w[E == 4 ? e : 0] : (w[e / 2] >> (e % 2 * 16)) & 0xffffu; }
   __device__ __forceinline__ void storeOne(char* p, int e) const {
     if constexpr (E == 4)

@@ -53,6 +53,7 @@ inline Span unlessInPlace(const Span& in, size_t ldin, const void* out, size_t l
 // A failed wait of the layer norm's and the RMS norm's kernels (each translation unit holds its own device-side word).
 int normStatus(int* code);
 int rmsStatus(int* code);
+int rmsBackwardStatus(int* code);
 // Multiprocessors of the current device (asked for once a device).
 int smCount();
 // Lets a kernel's blocks ask for all the dynamic shared memory there is on the current device; once a kernel and device.

@@ -1669,14 +1669,14 @@ extern "C" vrcclResult_t vrcclLinearBackward(const void* dy, size_t lddy, const 
 
 extern "C" vrcclResult_t vrcclReplicaGetAsyncError(vrcclResult_t* asyncErr) {
   if (!asyncErr) return vrcclInvalidArgument;
-  int code = 0, norm = 0, rms = 0;
+  int code = 0, norm = 0, rms = 0, rmsBackward = 0;
   // (the copies alone run on the legacy default stream, which does not wait for non-blocking ones)
   if (cudaDeviceSynchronize() != cudaSuccess ||
       cudaMemcpyFromSymbol(&code, gLinearStatus, sizeof(code)) != cudaSuccess || normStatus(&norm) != cudaSuccess ||
-      rmsStatus(&rms) != cudaSuccess) {
+      rmsStatus(&rms) != cudaSuccess || rmsBackwardStatus(&rmsBackward) != cudaSuccess) {
     cudaGetLastError();
     return vrcclCudaError;
   }
-  *asyncErr = (vrcclResult_t)(code ? code : norm ? norm : rms);
+  *asyncErr = (vrcclResult_t)(code ? code : norm ? norm : rms ? rms : rmsBackward);
   return vrcclSuccess;
 }

@@ -128,6 +128,31 @@ def test_rms_of_more_rows_than_stages(torch, v, rows, cols, pad, offset, dtype):
     _backward(torch, v, rows, cols, dtype, "float32", pad, offset, dsum=False)
 
 
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("rows,cols,opad,oskew", [(1500, 1001, 2, 3), (700, 4096, 1, 0), (320, 9001, 0, 1), (310, 13001, 4, 2), (2000, 130, 3, 1)])
+def test_rms_of_many_rows_on_other_skews(torch, v, rows, cols, opad, oskew, dtype):  # noqa: F811
+    """The outputs' rows on other skews than the inputs'."""
+    _forward(torch, v, rows, cols, dtype, "float32", opad=opad, oskew=oskew)
+    _backward(torch, v, rows, cols, dtype, "float32", opad=opad, oskew=oskew)
+    _forward(torch, v, rows, cols, dtype, "float32", residual=False, quant="int8", opad=opad, oskew=oskew)
+    _backward(torch, v, rows, cols, dtype, "float32", dsum=False, dgamma=False, opad=opad, oskew=oskew)
+
+
+@pytest.mark.parametrize("cols", [1001, 9001, 20001])
+def test_rms_in_place_beside_another_skew(torch, v, cols):  # noqa: F811
+    """The sum in the place of x, y elsewhere on another skew."""
+    g, rows = _rng(9), 330
+    a, b = (g.standard_normal((rows, cols)) for _ in range(2))
+    for offset, pad in ((3, 2), (5, 0), (0, 7)):
+        x, r, s = Mat(torch, rows, cols, "float16", a, 0, 1), Mat(torch, rows, cols, "float16", b, 1, 2), Mat(torch, rows, cols, "float16", None, 0, 1)
+        y, y2 = (Mat(torch, rows, cols, "float16", None, pad, offset) for _ in range(2))
+        call = lambda s, y: v.vrcclRmsNormForward(x.ptr, r.ptr, None, s.ptr, y.ptr, None, rows, cols, "float16", "float32", ldx=x.ld,  # noqa: E731
+                                                  ldr=r.ld, lds=s.ld, ldy=y.ld)
+        call(s, y)
+        call(x, y2)
+        assert torch.equal(x.view, s.view) and torch.equal(y.view, y2.view) and x.intact() and y2.intact()
+
+
 @pytest.mark.parametrize("quant", ["int8", "e4m3"])
 @pytest.mark.parametrize("group", [0, 32, 64, 128])
 @pytest.mark.parametrize("rows,cols,pad,offset", [(1, 1, 0, 0), (3, 30, 0, 0), (50, 64, 0, 0), (9, 96, 0, 0), (30, 128, 16, 0), (5, 129, 0, 0),
@@ -244,13 +269,13 @@ def test_rms_rows_beyond_32_bits(torch, v):  # noqa: F811
         v.vrcclRmsNormForward(x, None, None, None, y, r1, 3, cols, "bfloat16", "float32")
         v.vrcclRmsNormForward(flat, None, None, None, want, r2, 3, cols, "bfloat16", "float32")
         assert torch.equal(y, want) and torch.equal(r1, r2)
-        v.vrcclRmsNormBackward(flat, None, flat, None, r1, want, None, 3, cols, "bfloat16", "float32")
         v.vrcclRmsNormBackward(x, x, x, None, r1, y, None, 3, cols, "bfloat16", "float32")
         both = torch.empty_like(y)
         v.vrcclRmsNormBackward(flat, flat, flat, None, r1, both, None, 3, cols, "bfloat16", "float32")
         assert torch.equal(y, both)
-        v.vrcclRmsNormBackward(x, None, x, None, r1, x, None, 3, cols, "bfloat16", "float32")
-        assert torch.equal(x, want)
+        for rows in (x, flat):
+            v.vrcclRmsNormBackward(rows, None, rows, None, r1, rows, None, 3, cols, "bfloat16", "float32")
+        assert torch.equal(x, flat)
 
 
 def test_rms_same_bits_in_graphs_and_on_streams(torch, v):  # noqa: F811
