@@ -7,6 +7,11 @@
 
 namespace vrccl {
 
+// Whether rows of the same number lie on the same skew in two matrices.
+inline bool sameSkew(const void* p, size_t ldp, const void* q, size_t ldq, int elem) {
+  return ((uintptr_t)p - (uintptr_t)q) % 16 == 0 && (ldp - ldq) * elem % 16 == 0;
+}
+
 template <int DT>
 struct Chunk {
   static constexpr int E = floatTypeSize(DT), NB = kChunk * E / 16, NW = 4 * NB;
@@ -186,6 +191,77 @@ __device__ __forceinline__ void storeRest(char* p, int n, uint32_t w0, uint32_t 
   const uint32_t a = n & 8 ? w2 : w0, b = n & 8 ? w3 : w1;
   if (n & 4) *reinterpret_cast<uint32_t*>(p + restPiece(n, 4)) = a;
   if (n & 2) *reinterpret_cast<unsigned short*>(p + restPiece(n, 2)) = (unsigned short)(n & 4 ? b : a);
+}
+
+// Bytes [from, to) of the 16-byte block at p.
+template <int E>
+__device__ __forceinline__ void storePart(char* p, int from, int to, const uint4& v) {
+  if (from == 0 && to == 16) {
+    __stcs(reinterpret_cast<uint4*>(p), v);
+  } else if (from == 0) {
+    storeRest(p, to, v.x, v.y, v.z, v.w);
+  } else if (to == 16) {
+    const int n = 16 - from;
+    if (n & 8) *reinterpret_cast<uint2*>(p + 8) = make_uint2(v.z, v.w);
+    const uint32_t a = n & 8 ? v.y : v.w, b = n & 8 ? v.x : v.z;
+    if (n & 4) *reinterpret_cast<uint32_t*>(p + 12 - (n & 8)) = a;
+    if (n & 2) *reinterpret_cast<unsigned short*>(p + from) = (unsigned short)((n & 4 ? b : a) >> 16);
+  } else {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int at = 0; at < 16; at += E) {
+      if (at < from || at >= to) continue;
+      if constexpr (E == 4)
+        *reinterpret_cast<uint32_t*>(p + at) = w[at / 4];
+      else
+        *reinterpret_cast<unsigned short*>(p + at) = (unsigned short)(w[at / 4] >> (at % 4 * 8));
+    }
+  }
+}
+// Of a chunk at a boundary p its elements from number `from` on and before number `to`.
+template <int DT>
+__device__ __forceinline__ void storeElements(char* p, const Chunk<DT>& c, int from, int to) {
+  constexpr int E = Chunk<DT>::E, NB = Chunk<DT>::NB;
+  from = max(0, from) * E;
+  to = min(kChunk, to) * E;
+  if (from == 0 && to == kChunk * E) {
+#pragma unroll
+    for (int b = 0; b < NB; ++b) __stcs(reinterpret_cast<uint4*>(p) + b, c.block(b));
+  } else {
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+      if (max(from - 16 * b, 0) < min(to - 16 * b, 16)) storePart<E>(p + 16 * b, max(from - 16 * b, 0), min(to - 16 * b, 16), c.block(b));
+  }
+}
+// And the same loaded, from a matrix of bytes [begin, end): what lies beside them is anything.
+template <int DT>
+__device__ __forceinline__ Chunk<DT> loadElements(const char* p, int from, int to, uintptr_t begin, uintptr_t end) {
+  constexpr int E = Chunk<DT>::E, NB = Chunk<DT>::NB;
+  Chunk<DT> c;
+  if (from <= 0 && to >= kChunk) {
+#pragma unroll
+    for (int b = 0; b < NB; ++b) c.set(b, __ldcs(reinterpret_cast<const uint4*>(p) + b));
+    return c;
+  }
+  c.clear();
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    const int first = max(from, 16 / E * b), last = min(to, 16 / E * (b + 1));
+    if (first >= last) continue;
+    if ((uintptr_t)p + 16 * b >= begin && (uintptr_t)p + 16 * (b + 1) <= end) {
+      c.set(b, __ldcs(reinterpret_cast<const uint4*>(p) + b));
+      continue;
+    }
+#pragma unroll
+    for (int e = 16 / E * b; e < 16 / E * (b + 1); ++e) {
+      if (e < first || e >= last) continue;
+      if constexpr (E == 4)
+        c.w[e] = reinterpret_cast<const uint32_t*>(p)[e];
+      else
+        c.w[e / 2] |= (uint32_t) reinterpret_cast<const unsigned short*>(p)[e] << (e % 2 * 16);
+    }
+  }
+  return c;
 }
 
 // Lanes store consecutive chunks of a row (p, left as above). All lanes of a warp call it.

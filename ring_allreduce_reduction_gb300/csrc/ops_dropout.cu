@@ -16,9 +16,9 @@
 //
 // Bound by memory. A thread takes chunks of its own. Where all rows start on
 // 16-byte boundaries and are whole chunks long, the matrix is one run of chunks
-// (the row by a multiplication); else a warp takes 32 chunks of one row, or
-// several short ones, and lanes put theirs together from 16-byte blocks and
-// their neighbours'.
+// (the row by a multiplication); else a warp takes chunks of one row, or
+// several short ones: whole blocks where rows lie on the same skew in every
+// matrix, else put together from blocks and the neighbouring lanes'.
 #include "ops_chunks.cuh"
 
 namespace vrccl {
@@ -115,6 +115,44 @@ __global__ void __launch_bounds__(kThreads) dropoutRun(const __grid_constant__ D
     draw(std::false_type{});
 }
 
+// Rows each on the same skew in every matrix. Chunks are counted from the boundary before the row's first element, column
+// -shift, and are whole blocks in every matrix (parts of them at the row's ends); a lane draws the bits of the columns' chunk
+// of that number and takes the other part of its own from the lane before. In rows of more than 32 chunks a warp takes 31,
+// its first lane drawing for the second alone.
+template <int DT, bool RES>
+__global__ void __launch_bounds__(kThreads) dropoutSame(const __grid_constant__ DropoutArgs a) {
+  using C = Chunk<DT>;
+  constexpr int E = C::E;
+  const size_t warp = (size_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
+  if (warp >= a.chunks) return;
+  int lane = threadIdx.x & 31, ci;
+  size_t row = warp;
+  if (a.segments > 1) {
+    row = a.chunks >> 31 ? warp / a.segments : quotient((uint32_t)warp, a.division);
+    ci = (int)((unsigned)warp - (unsigned)row * a.segments) * 31 + lane - 1;
+  } else {
+    row = warp * (32 / a.lanes) + lane / a.lanes;
+    ci = lane &= a.lanes - 1;
+  }
+  const char* px = a.x + row * a.ldx * E;
+  const int shift = (int)((uintptr_t)px & 15) / E, from = shift - ci * kChunk, to = a.cols + from;
+  const bool own = row < a.rows && to > 0 && ci >= 0 && (a.segments == 1 || lane > 0);
+  const ptrdiff_t at = ((ptrdiff_t)ci * kChunk - shift) * E;
+  C x, r, y;
+  if (own) {
+    x = loadElements<DT>(px + at, from, to, (uintptr_t)a.x, a.xEnd);
+    if constexpr (RES) r = loadElements<DT>(a.r + row * a.ldr * E + at, from, to, (uintptr_t)a.r, a.rEnd);
+  }
+  Random128 bits = philox(*a.seed, a.firstChunk + row * a.per + ci, a.offset);
+  uint32_t v[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = __shfl_up_sync(0xffffffffu, bits.w[i], 1, a.lanes), v[4 + i] = bits.w[i];
+  if (!own) return;
+  if (shift) shiftedWords(v, 16 - 2 * shift, bits.w);  // two bytes an element
+  dropChunk<DT, RES>(a, bits, x, r, y);
+  storeElements<DT>(a.y + row * a.ldy * E + at, y, from, to);
+}
+
 // Rows on any element: a warp takes `step` chunks of one, or short ones whole.
 template <int DT, bool RES>
 __global__ void __launch_bounds__(kThreads) dropoutRows(const __grid_constant__ DropoutArgs a) {
@@ -144,17 +182,26 @@ __global__ void __launch_bounds__(kThreads) dropoutRows(const __grid_constant__ 
 }
 
 template <int DT, bool RES>
-vrcclResult_t launchDropout(DropoutArgs& a, bool run, cudaStream_t st) {
+vrcclResult_t launchDropout(DropoutArgs& a, bool run, bool same, cudaStream_t st) {
   const bool one = a.rows == 1;
   if (!run) {
-    a.lanes = a.per <= 8 ? 8 : a.per <= 16 ? 16 : 32;
-    a.step = a.per > 32 ? stepOf((int)a.per) : a.lanes;
-    a.segments = (a.per + a.step - 1) / a.step;
-    a.chunks = a.lanes < 32 ? (a.rows + 32 / a.lanes - 1) / (32 / a.lanes) : a.rows * a.segments;
+    // Lanes of a row, shares of longer ones, and the warps that are made of them, on any skew of the rows.
+    auto deal = [&](unsigned most, int step) {
+      a.lanes = most <= 8 ? 8 : most <= 16 ? 16 : 32;
+      a.step = a.lanes < 32 ? a.lanes : step;
+      a.segments = (most + a.step - 1) / a.step;
+      return a.segments > 1 ? a.rows * a.segments : (a.rows + 32 / a.lanes - 1) / (32 / a.lanes);
+    };
+    const unsigned most = (unsigned)(((size_t)a.cols + 16 / Chunk<DT>::E - 1 + kChunk - 1) / kChunk);
+    const size_t sameWarps = deal(most, most > 32 ? 31 : 32), warps = deal(a.per, a.per > 32 ? stepOf((int)a.per) : 32);
+    // A warp of rows on the same skew takes nine tenths of the other's time, three quarters with a residual (16384 x 4097 bf16 with
+    // it 114 -> 82 us, 16384 x 4096 without 86 -> 77, 262144 x 65 77 -> 49), but there may be more of them (262144 x 255: 98, 157).
+    same = same && (RES ? sameWarps * 3 <= warps * 4 : sameWarps * 9 <= warps * 10);
+    a.chunks = same ? deal(most, most > 32 ? 31 : 32) : warps;
     a.division = divisionOf(a.segments);
     const size_t blocks = (a.chunks + kThreads / 32 - 1) / (kThreads / 32);
     if (blocks >= (size_t(1) << 31)) return vrcclInvalidArgument;
-    return launchShaped(dropoutRows<DT, RES>, {dim3((unsigned)blocks), kThreads, 0, 0, false}, st, a);
+    return launchShaped(same ? dropoutSame<DT, RES> : dropoutRows<DT, RES>, {dim3((unsigned)blocks), kThreads, 0, 0, false}, st, a);
   }
   a.chunks = a.rows * a.per;
   a.division = divisionOf(a.per);
@@ -209,9 +256,10 @@ vrcclResult_t dropout(const void* x, size_t ldx, const void* r, size_t ldr, void
   a.last = (uint32_t)drop * 65536u - 1;
   a.all = drop == 0;
   const bool run = cols % kChunk == 0 && rowsAligned(x, ldx, E) && rowsAligned(y, ldy, E) && (!r || rowsAligned(r, ldr, E));
+  const bool same = sameSkew(x, ldx, y, ldy, E) && (!r || sameSkew(r, ldr, y, ldy, E));
   auto go = [&](auto dt) {
     constexpr int DT = decltype(dt)::value;
-    return r ? launchDropout<DT, true>(a, run, st) : launchDropout<DT, false>(a, run, st);
+    return r ? launchDropout<DT, true>(a, run, same, st) : launchDropout<DT, false>(a, run, same, st);
   };
   return dtype == vrcclFloat32    ? go(std::integral_constant<int, vrcclFloat32>{})
          : dtype == vrcclBfloat16 ? go(std::integral_constant<int, vrcclBfloat16>{})

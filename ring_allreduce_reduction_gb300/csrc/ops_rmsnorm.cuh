@@ -131,31 +131,6 @@ template <Lie LIE>
 __device__ __forceinline__ bool ownChunk(const RmsArgs& a, int t) {
   return LIE != kAny || (t & 31) < a.step;
 }
-// Bytes [from, to) of the 16-byte block at p.
-template <int E>
-__device__ __forceinline__ void storePart(char* p, int from, int to, const uint4& v) {
-  if (from == 0 && to == 16) {
-    __stcs(reinterpret_cast<uint4*>(p), v);
-  } else if (from == 0) {
-    storeRest(p, to, v.x, v.y, v.z, v.w);
-  } else if (to == 16) {
-    const int n = 16 - from;
-    if (n & 8) *reinterpret_cast<uint2*>(p + 8) = make_uint2(v.z, v.w);
-    const uint32_t a = n & 8 ? v.y : v.w, b = n & 8 ? v.x : v.z;
-    if (n & 4) *reinterpret_cast<uint32_t*>(p + 12 - (n & 8)) = a;
-    if (n & 2) *reinterpret_cast<unsigned short*>(p + from) = (unsigned short)((n & 4 ? b : a) >> 16);
-  } else {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int at = 0; at < 16; at += E) {
-      if (at < from || at >= to) continue;
-      if constexpr (E == 4)
-        *reinterpret_cast<uint32_t*>(p + at) = w[at / 4];
-      else
-        *reinterpret_cast<unsigned short*>(p + at) = (unsigned short)(w[at / 4] >> (at % 4 * 8));
-    }
-  }
-}
 // kSame: a row begins `shift` columns into its first chunk, which starts on a 16-byte boundary in every matrix.
 template <int DT, Lie LIE>
 __device__ __forceinline__ void putChunk(const RmsArgs& a, char* rows, size_t ld, size_t row, const Chunk<DT>& c, int ci, int shift) {
@@ -169,15 +144,7 @@ __device__ __forceinline__ void putChunk(const RmsArgs& a, char* rows, size_t ld
 #pragma unroll
       for (int b = 0; b < NB; ++b) __stcs(reinterpret_cast<uint4*>(p) + b, c.block(b));
   } else {
-    const int from = max(0, shift - ci * kChunk) * E, to = min(kChunk, a.cols + shift - ci * kChunk) * E;
-    if (from == 0 && to == kChunk * E) {
-#pragma unroll
-      for (int b = 0; b < NB; ++b) __stcs(reinterpret_cast<uint4*>(p) + b, c.block(b));
-    } else {
-#pragma unroll
-      for (int b = 0; b < NB; ++b)
-        if (max(from - 16 * b, 0) < min(to - 16 * b, 16)) storePart<E>(p + 16 * b, max(from - 16 * b, 0), min(to - 16 * b, 16), c.block(b));
-    }
+    storeElements<DT>(p, c, shift - ci * kChunk, a.cols + shift - ci * kChunk);
   }
 }
 
@@ -526,7 +493,7 @@ inline Lie lieOf(std::initializer_list<Matrix> all, size_t cols, int elem) {
   for (const Matrix& m : all) {
     if (!m.p) continue;
     whole &= rowsAligned(m.p, m.ld, elem);
-    same &= ((uintptr_t)m.p - (uintptr_t)first.p) % 16 == 0 && (m.ld - first.ld) * elem % 16 == 0;
+    same &= sameSkew(m.p, m.ld, first.p, first.ld, elem);
   }
   return whole ? kWhole : same ? kSame : kAny;
 }
