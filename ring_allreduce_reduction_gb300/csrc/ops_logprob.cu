@@ -613,7 +613,9 @@ __global__ void __launch_bounds__(T, T == 128 ? 8 : 3 * kThreads / T) logProbFor
       if (place == a.k - 1) find.least = (uint32_t)(find.collected[j] >> 32);
     }
     __syncthreads();
-    if (segments < a.k) {  // too few for a bound: the k-th of the threads' largest is one (fewer threads: none)
+    const size_t firstVector = (size_t)firstRun * perRun * kPass, lastVector = min((size_t)lastRun * perRun * kPass, in.nvec);
+    if (firstVector + (size_t)(a.k - 1) * a.span * 32 >= lastVector) {
+      // too few segments hold anything for a bound: the k-th of the threads' largest is one (fewer threads: none)
       const bool some = (firstRun + warp < lastRun && (firstRun + warp) * (size_t)kPass + lane < in.nvec) || (int)threadIdx.x < odd;
       find.tops[threadIdx.x] = some ? ascending(stream.s.l == stream.s.l ? stream.s.m : INFINITY) : 0;
       __syncthreads();
@@ -704,12 +706,15 @@ __global__ void __launch_bounds__(T, T == 128 ? 8 : 3 * kThreads / T) logProbFor
     sayRow<TOP>(a, row, r, given, nullptr);
 }
 
+// T threads a slice of a row: a block, or a warp (T = 32) a short row.
 template <int DT, int T>
-__global__ void __launch_bounds__(T, 2 * kThreads / T) logProbBackward(const __grid_constant__ LogProbArgs a) {
+__global__ void __launch_bounds__(T == 32 ? kShortThreads : T, T == 32 ? 8 : 2 * kThreads / T) logProbBackward(const __grid_constant__ LogProbArgs a) {
   using S = typename Ty<DT>::S;
   constexpr int E = floatTypeSize(DT), V = 16 / E, U = kUnroll;
   const size_t slices = (a.vocab + a.slice - 1) / a.slice;
-  const size_t row = blockIdx.x / slices, part = blockIdx.x % slices;
+  const size_t row = T == 32 ? (size_t)blockIdx.x * (kShortThreads / 32) + threadIdx.x / 32 : blockIdx.x / slices, part = T == 32 ? 0 : blockIdx.x % slices;
+  const unsigned thread = T == 32 ? threadIdx.x & 31 : threadIdx.x;
+  if (T == 32 && row >= a.rows) return;
   const S* logits = reinterpret_cast<const S*>(a.logits) + row * a.ldl;
   S* out = reinterpret_cast<S*>(a.dlogits) + row * a.ldd;
   // A block's elements: slices are whole vectors of the output counted from its row's first boundary, and the first one
@@ -722,7 +727,7 @@ __global__ void __launch_bounds__(T, 2 * kThreads / T) logProbBackward(const __g
   const size_t nvec = end > first ? (end - first) / V : 0, tail = first + nvec * V, edge = part == 0 ? min(head, end) : 0;
   const uint4* src = reinterpret_cast<const uint4*>(logits + first);
   uint4* dst = reinterpret_cast<uint4*>(out + first);
-  size_t i = threadIdx.x;
+  size_t i = thread;
   uint4 v[U];
   if (together)
 #pragma unroll
@@ -732,8 +737,8 @@ __global__ void __launch_bounds__(T, 2 * kThreads / T) logProbBackward(const __g
   const long long token = tokenOf(a, row);
   if (token == -2 || (st.x == -INFINITY && st.y == 0.f)) {
     for (; i < nvec; i += T) __stcs(dst + i, make_uint4(0, 0, 0, 0));
-    if (threadIdx.x < edge) out[threadIdx.x] = S(0);
-    if (tail + threadIdx.x < end) out[tail + threadIdx.x] = S(0);
+    if (thread < edge) out[thread] = S(0);
+    if (tail + thread < end) out[tail + thread] = S(0);
     return;
   }
   // With x = log2 q: gradient = 2^x (A + B x), and dlogprob / T more at the token.
@@ -789,8 +794,8 @@ __global__ void __launch_bounds__(T, 2 * kThreads / T) logProbBackward(const __g
     }
   }
   auto single = [&](size_t j) { out[j] = Ty<DT>::fromF(at(Ty<DT>::toF(logits[j])) + ((long long)j == token ? dl : 0.f)); };
-  if (threadIdx.x < edge) single(threadIdx.x);
-  if (tail + threadIdx.x < end) single(tail + threadIdx.x);
+  if (thread < edge) single(thread);
+  if (tail + thread < end) single(tail + thread);
 }
 
 // Threads of a block: with a row in 16 vectors a thread or fewer, so that several short rows share a multiprocessor and
@@ -809,7 +814,7 @@ LogProbFn pickForward(int threads) {
 }
 template <int DT>
 LogProbFn pickBackward(int threads) {
-  return threads == 128 ? logProbBackward<DT, 128> : threads == 256 ? logProbBackward<DT, 256> : logProbBackward<DT, 512>;
+  return threads == 32 ? logProbBackward<DT, 32> : threads == 128 ? logProbBackward<DT, 128> : threads == 256 ? logProbBackward<DT, 256> : logProbBackward<DT, 512>;
 }
 
 bool goodTypes(size_t rows, size_t vocab, int dtype, int ttype, float temperature) {
@@ -870,10 +875,10 @@ extern "C" vrcclResult_t vrcclLogProbForward(const void* logits, size_t ldl, con
   a.span = 1;
   while (a.span < kUnroll ? passes * (kUnroll / a.span) > kSegments : passes / (a.span / kUnroll) + 1 > kSegments) a.span *= 2;
   while ((1 << a.shift) < a.span) ++a.shift;
-  // a warp a row, where rows are short and many. bf16, k = 8, a warp against a block a row: 1024 columns 400 rows 4.6 / 7.7 us,
-  // 20000: 28 / 152; 4096 columns 400 rows 8.7 / 6.5, 2000: 9.2 / 14.8, 20000: 52 / 122; 8192 columns 1000 rows 12.0 / 10.2, 5000:
+  // a warp a row, where rows are short and many, or very short. bf16, k = 8, a warp against a block a row: 1024 columns 4 rows 3.8 / 5.3 us,
+  // 400: 4.6 / 7.7, 20000: 28 / 152; 4096 columns 400 rows 8.7 / 6.5, 2000: 9.2 / 14.8, 20000: 52 / 122; 8192 columns 1000 rows 12.0 / 10.2, 5000:
   // 29 / 40; 20000: 78 / 144; 16384 columns 10000 rows (with longer segments) 118 / 98. Without a list 20000 x 4096 31 / 48.
-  const bool brief = bytes <= kShortVectors * 16 && rows >= bytes / 8;
+  const bool brief = bytes <= kShortVectors * 16 && (bytes <= 4096 || rows >= bytes / 8);
   auto pick = [&](auto dt) -> LogProbFn {
     constexpr int DT = decltype(dt)::value;
     if (brief) return k ? logProbForwardShort<DT, true> : logProbForwardShort<DT, false>;
@@ -918,6 +923,7 @@ extern "C" vrcclResult_t vrcclLogProbBackward(const void* logits, size_t ldl, co
   a.lstride = dlogprobStride;
   a.hstride = dentropyStride;
   a.dlogits = dlogits;
+  a.rows = rows;
   a.ldd = ldd;
   // even pieces, until there are four blocks a multiprocessor or a piece has 32 KB. (In place too: an element is read by the
   // thread that writes it, and by no other.)
@@ -927,9 +933,12 @@ extern "C" vrcclResult_t vrcclLogProbBackward(const void* logits, size_t ldl, co
   const size_t slices = (vocab + a.slice - 1) / a.slice;
   if (rows * slices >= (size_t(1) << 31)) return vrcclInvalidArgument;
   // as many blocks as four a multiprocessor are all at work at once with 256 threads each
-  const int threads = rows * slices <= (size_t)smCount() * 4 ? 256 : blockThreads(a.slice * E, rows * slices, kThreads);
+  // a warp a row: 1467 x 1269 bf16 4.0 us for 4.9, 20000 x 1024 17 for 38, 20000 x 4096 52 for 54 (8192 columns 104 for 95)
+  const bool brief = vocab * E <= 8192 && rows >= (size_t)smCount() * 8;
+  const int threads = brief ? 32 : rows * slices <= (size_t)smCount() * 4 ? 256 : blockThreads(a.slice * E, rows * slices, kThreads);
   const LogProbFn fn = dtype == vrcclFloat32    ? pickBackward<vrcclFloat32>(threads)
                        : dtype == vrcclBfloat16 ? pickBackward<vrcclBfloat16>(threads)
                                                 : pickBackward<vrcclFloat16>(threads);
-  return launchShaped(fn, {dim3((unsigned)(rows * slices)), threads, 0, 0, false}, (cudaStream_t)stream, a);
+  const size_t blocks = brief ? (rows + kShortThreads / 32 - 1) / (kShortThreads / 32) : rows * slices;
+  return launchShaped(fn, {dim3((unsigned)blocks), brief ? kShortThreads : threads, 0, 0, false}, (cudaStream_t)stream, a);
 }

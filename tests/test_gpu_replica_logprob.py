@@ -310,6 +310,27 @@ def test_logprob_of_many_short_rows(torch, v, vocab, pad, offset, dtype):  # noq
         _forward(torch, v, s, token, k, dtype, T)
 
 
+@pytest.mark.parametrize("dtype,vocab", [("bfloat16", 2419), ("float16", 4000), ("float32", 3585), ("bfloat16", 8191)])
+def test_lists_as_long_as_a_row_has_segments(torch, v, dtype, vocab):  # noqa: F811
+    """Around the number of a row's 512-byte pieces, which are counted in fours."""
+    s, token, _ = _inputs(torch, 15, vocab, dtype, padding=0.1)
+    for k in range(vocab * (4 if dtype == "float32" else 2) // 512 - 2, vocab * (4 if dtype == "float32" else 2) // 512 + 5):
+        if 0 < k <= 32:
+            _forward(torch, v, s, token, k, dtype)
+
+
+@pytest.mark.parametrize("dtype", FLOATS)
+@pytest.mark.parametrize("vocab,pad,opad,oskew", [(5, 0, 0, 0), (257, 1, 1, 0), (1003, 0, 3, 3), (1347, 3, 3, 0), (2048, 0, 8, 0)])
+def test_logprob_gradient_of_many_short_rows(torch, v, vocab, pad, opad, oskew, dtype):  # noqa: F811
+    s, token, _ = _inputs(torch, 1300, vocab, dtype, pad)
+    s.view[7] = -float("inf")
+    s.view[8, ::2] = -float("inf")
+    token[8] = vocab - 1 if vocab % 2 == 0 else 1
+    dev, entropy, stats = _forward(torch, v, s, token, 0, dtype, 0.9)
+    _backward(torch, v, s, token, dev, entropy, stats, dtype, 0.9, opad, oskew)
+    _backward(torch, v, s, token, dev, entropy, stats, dtype, 0.9, in_place=True)
+
+
 def test_short_rows_that_are_not_finite(torch, v):  # noqa: F811
     """Rows of a NaN or infinity among many give what they give among few, which go another way."""
     rows, vocab, k = 600, 1001, 6
