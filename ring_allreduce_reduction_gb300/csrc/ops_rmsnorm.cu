@@ -41,7 +41,7 @@ namespace vrccl {
 namespace {
 
 template <int DT, bool RES, bool Q, Lie LIE, bool WIDE>
-__global__ void __launch_bounds__(32 * forwardWarps(LIE, Q, WIDE)) rmsForward(const __grid_constant__ RmsArgs a) {
+__global__ void __launch_bounds__(32 * forwardWarps(LIE, WIDE)) rmsForward(const __grid_constant__ RmsArgs a) {
   using C = Chunk<DT>;
   constexpr int E = C::E, NP = kChunk / 2;
   extern __shared__ __align__(128) unsigned char smem[];
@@ -71,11 +71,12 @@ __global__ void __launch_bounds__(32 * forwardWarps(LIE, Q, WIDE)) rmsForward(co
       if (ownChunk<LIE>(a, t))
 #pragma unroll
         for (int i = 0; i < NP; ++i) squares = fma2(x[i], x[i], squares);
-      if constexpr (Q) {
+      if constexpr (Q)
+        if (a.group == 0) {
 #pragma unroll
-        for (int i = 0; i < NP; ++i) x[i] = mul2(x[i], g[j][i]);
-        if (a.group == 0) most = maxOrNan(most, largest(x));
-      }
+          for (int i = 0; i < NP; ++i) x[i] = mul2(x[i], g[j][i]);
+          most = maxOrNan(most, largest(x));
+        }
       // (in place: the row is in shared memory)
       if (RES && a.sum) putChunk<DT, LIE>(a, a.sum, a.lds, row, s[j], ci, shift);
     }
@@ -108,7 +109,7 @@ __global__ void __launch_bounds__(32 * forwardWarps(LIE, Q, WIDE)) rmsForward(co
 }
 
 template <int DT, int G, bool RES, bool Q>
-__global__ void __launch_bounds__(kNarrowThreads) rmsForwardNarrow(const __grid_constant__ RmsArgs a) {
+__global__ void __launch_bounds__(kNarrowThreads, RES || DT == vrcclFloat32 ? 2 : 4) rmsForwardNarrow(const __grid_constant__ RmsArgs a) {
   using C = Chunk<DT>;
   constexpr int NP = kChunk / 2, R = 32 / G, U = kNarrowTurn;
   const int lane = threadIdx.x & 31, own = lane % G;
@@ -219,9 +220,8 @@ __global__ void __launch_bounds__(kLongThreads) rmsForwardLong(const __grid_cons
 template <int DT, bool RES, bool Q>
 RmsFn pickForward(const Shape& s) {
   if (s.walk == kRing) {
-    if constexpr (!Q)
-      if (s.wide)
-        return s.lie == kWhole ? rmsForward<DT, RES, Q, kWhole, true> : s.lie == kSame ? rmsForward<DT, RES, Q, kSame, true> : rmsForward<DT, RES, Q, kAny, true>;
+    if (s.wide)
+      return s.lie == kWhole ? rmsForward<DT, RES, Q, kWhole, true> : s.lie == kSame ? rmsForward<DT, RES, Q, kSame, true> : rmsForward<DT, RES, Q, kAny, true>;
     return s.lie == kWhole ? rmsForward<DT, RES, Q, kWhole, false> : s.lie == kSame ? rmsForward<DT, RES, Q, kSame, false> : rmsForward<DT, RES, Q, kAny, false>;
   }
   if (s.walk == kLong) return rmsForwardLong<DT, RES, Q>;
@@ -267,7 +267,7 @@ extern "C" vrcclResult_t vrcclRmsNormForward(const void* x, size_t ldx, const vo
   if (!apart(rest, in) || !apart(rest, matrices) || !apart({spanSum}, besideSum) || !apart({spanY}, besideY))
     return vrcclInvalidArgument;
   const Lie lie = lieOf({{x, ldx}, {residual, ldr}, {sum, lds}, {y, ldy}}, cols, E);
-  const Shape s = rmsShape(rows, (int)cols, E, residual ? 2 : 1, lie, true, codes, codes && group);
+  const Shape s = rmsShape(rows, (int)cols, E, residual ? 2 : 1, lie, true, codes && group);
   RmsArgs a = {};
   a.src[0] = sourceOf(x, ldx, E);
   a.src[1] = sourceOf(residual, ldr, E);

@@ -43,8 +43,8 @@ enum Lie { kWhole, kSame, kAny };
 // Warps of a block (one an SM), and so the registers of a thread: what is left of 65536, in steps of four warps. Forward:
 // 32768 x 4096 bf16 with residual 16 warps 175 us, 20: 179, 24: 170, 28: 175, 32: 182; 16384 x 4097 20: 88, 24: 93, 28: 97, 32:
 // 104, and 65536 x 1025 83, 74, 92, 94; anyhow (three teams of nine from 27 on) 20: 136, 24: 142, 28: 118, 32: 132; 16384 x 5120
-// to e4m3 20: 118.5, 24: 120, 28: 140, 32: 117. Rows that need more warps have 32 (wide).
-constexpr int forwardWarps(Lie lie, bool q, bool wide) { return wide || q ? 32 : lie == kAny ? 28 : 24; }
+// to e4m3 20: 95, 24: 96, 28: 133, 32: 106, and x 4096 87, 79, 92, 86. Rows that need more warps have 32 (wide).
+constexpr int forwardWarps(Lie lie, bool wide) { return wide ? 32 : lie == kAny ? 28 : 24; }
 // Backward keeps a row's chunks in registers (hold) where 16 warps do and teams of them leave few idle: 16384 x 8192 bf16
 // 159 us (20 warps: 205), 20000 x 2500 fp32 141 (not held 169). Else it reads them from the stage once more: 16384 x 5120 20
 // warps 104 us (held 118), 16384 x 4097 20: 133, 24: 147, 28: 132, held 192; 8192 x 9001 20: 135, 24: 147, 28: 170. Rows that need
@@ -158,23 +158,25 @@ __device__ __forceinline__ float scaleOf(float most, int quant) {
 __device__ __forceinline__ void storeCodes(unsigned char* p, const F2 (&y)[kChunk / 2], float scale, int quant, int from, int to) {
   float inv;  // (a unit or two off, which moves a code where y lies that near the middle of two; normal, as the scale is below 2^122)
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(scale));
+  const F2 inv2 = pair(inv, inv);
   uint32_t w[2];
+  if (quant == vrcclQuantInt8) {
+    // 1.5 2^23 + q has q, rounded to the nearest (even), in its lowest bits; codes of a scale that is not finite are 0
+    const F2 round = pair(12582912.f, 12582912.f);
+    const bool finite = scale < INFINITY;
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const float2 a = split(y[2 * h]), b = split(y[2 * h + 1]);
-    const float f[4] = {a.x * inv, a.y * inv, b.x * inv, b.y * inv};
-    if (quant == vrcclQuantInt8) {
-      w[h] = 0;
+    for (int h = 0; h < 2; ++h) {
+      const float2 a = split(fma2(y[2 * h], inv2, round)), b = split(fma2(y[2 * h + 1], inv2, round));
+      const uint32_t lo = __byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x0040), hi = __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040);
+      w[h] = finite ? __byte_perm(lo, hi, 0x5410) : 0;
+    }
+  } else {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        int q;
-        asm("cvt.rni.sat.s8.f32 %0, %1;" : "=r"(q) : "f"(f[e]));
-        w[h] |= (uint32_t)(q & 0xff) << (8 * e);
-      }
-    } else {
+    for (int h = 0; h < 2; ++h) {
+      const float2 a = split(mul2(y[2 * h], inv2)), b = split(mul2(y[2 * h + 1], inv2));
       unsigned short lo, hi;
-      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(f[1]), "f"(f[0]));
-      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(f[3]), "f"(f[2]));
+      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(a.y), "f"(a.x));
+      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(b.y), "f"(b.x));
       w[h] = lo | (uint32_t)hi << 16;
     }
   }
@@ -200,8 +202,8 @@ __device__ __forceinline__ void storeGroup(const RmsArgs& a, size_t row, int ci,
   }
   if (left <= 0 || !own) return;
   const float scale = scaleOf(most, a.quant);
-  const int lanes = a.group / kChunk;
-  if (a.group ? ci % lanes == 0 : ci == 0) a.scales[row * a.ldsc + (a.group ? ci / lanes : 0)] = scale;
+  const int shares = a.group == 32 ? 2 : a.group == 64 ? 3 : a.group == 128 ? 4 : 31;  // 2^that lanes have one scale
+  if ((ci & ((1u << shares) - 1)) == 0) a.scales[row * a.ldsc + (ci >> shares)] = scale;
   storeCodes(a.codes + row * a.ldc + (ptrdiff_t)ci * kChunk - shift, y, scale, a.quant, shift - ci * kChunk, left);
 }
 
@@ -403,7 +405,7 @@ struct Shape {
   int stages, smem, resident;
 };
 // `sources`: matrices a row is read from; `grouped`: scales of groups of columns, which lie in a warp as they do in the row.
-inline Shape rmsShape(size_t rows, int cols, int elem, int sources, Lie lie, bool forward, bool quantized, bool grouped) {
+inline Shape rmsShape(size_t rows, int cols, int elem, int sources, Lie lie, bool forward, bool grouped) {
   Shape s = {};
   const int E16 = 16 / elem;
   // a row's skew comes again E16 rows on, if not before: a team's step is a multiple of that, or it takes one row
@@ -413,8 +415,8 @@ inline Shape rmsShape(size_t rows, int cols, int elem, int sources, Lie lie, boo
   const int chunks = (cols + kChunk - 1) / kChunk, most = (cols + (lie == kSame ? E16 - 1 : 0) + kChunk - 1) / kChunk;
   const int warps = (most + kHeld * s.step - 1) / (kHeld * s.step);
   s.hold = !forward && lie != kAny && warps <= 16 && 16 / warps * warps >= 12;
-  s.wide = forward ? !quantized && warps > forwardWarps(lie, false, false) : !s.hold && lie != kAny && warps > backwardWarps(false, false);
-  const int room = forward ? forwardWarps(lie, quantized, s.wide) : backwardWarps(s.hold, s.wide);
+  s.wide = forward ? warps > forwardWarps(lie, false) : !s.hold && lie != kAny && warps > backwardWarps(false, false);
+  const int room = forward ? forwardWarps(lie, s.wide) : backwardWarps(s.hold, s.wide);
   const int row = slotOf(lie, chunks, elem) * sources;
   const int least = forward || s.hold ? 1 : 2;  // stages
   if (lie == kWhole && cols <= kNarrowCols) {
@@ -450,7 +452,7 @@ inline int mostBlocks(size_t rows, int cols) {
   int most = 0;
   for (int elem : {2, 4})
     for (int sources : {2, 3})
-      for (Lie lie : {kWhole, kSame, kAny}) most = std::max(most, rmsBlocks(rows, rmsShape(rows, cols, elem, sources, lie, false, false, false)));
+      for (Lie lie : {kWhole, kSame, kAny}) most = std::max(most, rmsBlocks(rows, rmsShape(rows, cols, elem, sources, lie, false, false)));
   return most;
 }
 

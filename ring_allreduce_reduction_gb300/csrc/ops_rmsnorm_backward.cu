@@ -311,7 +311,7 @@ extern "C" vrcclResult_t vrcclRmsNormBackward(const void* dy, size_t lddy, const
   if (!apart(all, in) || !apart(other, matrices)) return vrcclInvalidArgument;
   const bool sources = rowsAligned(dy, lddy, E) && rowsAligned(s, lds, E) && (!dsum || rowsAligned(dsum, ldds, E));
   const Lie lie = lieOf({{s, lds}, {dy, lddy}, {dsum, ldds}, {dx, lddx}}, cols, E);
-  const Shape shape = rmsShape(rows, (int)cols, E, dsum ? 3 : 2, lie, false, false, false);
+  const Shape shape = rmsShape(rows, (int)cols, E, dsum ? 3 : 2, lie, false, false);
   const int blocks = rmsBlocks(rows, shape);
   RmsArgs a = {};
   a.src[0] = sourceOf(s, lds, E);
