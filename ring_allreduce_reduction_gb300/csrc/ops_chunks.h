@@ -89,15 +89,9 @@ VRCCL_HD bool keeps(const Random128& r, int e, uint32_t last, bool all) {
 }
 inline int dropThreshold(float p) { return (int)((double)p * 65536 + 0.5); }
 
-// n / d for n below 2^64 / d by the high half of one product: magicOf(d) is the least integer not below 2^64 / d (0 where
-// the quotients need not be exact or fit: the caller then divides).
-inline uint64_t magicOf(uint64_t d, uint64_t most) {
-  if (d < 2 || most > ~(uint64_t)0 / d) return 0;
-  return ~(uint64_t)0 / d + 1;
-}
-// The same for n below 2^31 by a 32-bit product: n / d is the upper half of n mul, shifted (d >= 2). mul is 2^(32 + shift) / d
-// rounded up, too large by less than d / 2^(32 + shift) of 1; shift is the least with 2^(shift + 1) >= d, so that n times that
-// stays below 1 / d, the least by which n / d misses the next integer.
+// n / d for n below 2^31 by a 32-bit product: the upper half of n mul, shifted (d >= 2). mul is 2^(32 + shift) / d rounded up, too
+// large by less than d / 2^(32 + shift) of 1; shift is the least with 2^(shift + 1) >= d, so that n times that stays below 1 / d,
+// the least by which n / d misses the next integer.
 struct Division {
   uint32_t mul, shift;
 };

@@ -73,7 +73,6 @@ extern "C" int keepsOf(uint32_t word, int odd, int drop) {
   return keeps(r, 4 + odd, (uint32_t)drop * 65536u - 1, drop == 0);
 }
 extern "C" uint32_t divided(uint32_t n, uint32_t d) { return quotient(n, divisionOf(d)); }
-extern "C" uint64_t magic(uint64_t d, uint64_t most) { return magicOf(d, most); }
 """
 
 
@@ -86,8 +85,6 @@ def lib(tmp_path_factory):
     subprocess.run([cxx, "-std=c++17", "-O1", "-shared", "-fPIC", f"-I{CSRC}", str(d / "chunks.cc"), "-o", str(d / "chunks.so")],
                    check=True)
     lib = ctypes.CDLL(str(d / "chunks.so"))
-    lib.magic.restype = ctypes.c_uint64
-    lib.magic.argtypes = [ctypes.c_uint64, ctypes.c_uint64]
     lib.threshold.argtypes = [ctypes.c_float]
     lib.philoxOf.argtypes = [ctypes.c_uint64] * 3 + [ctypes.POINTER(ctypes.c_uint32)]
     lib.keepsOf.argtypes = [ctypes.c_uint32, ctypes.c_int, ctypes.c_int]
@@ -168,21 +165,6 @@ def test_threshold_and_keeping(lib):
 
 
 def test_division_by_a_product(lib):
-    """floor(n * magic / 2^64) is n / d wherever a magic is given."""
-    g = np.random.default_rng(1)
-    for d in [1, 2, 3, 5, 7, 8, 126, 512, 1000, 12345, (1 << 28) - 1]:
-        for most in (d, 1 << 20, 1 << 35, (1 << 43) - 1):
-            m = lib.magic(d, most)
-            if not m:
-                assert d == 1 or most > ((1 << 64) - 1) // d
-                continue
-            for n in [0, 1, d - 1, d, d + 1, most - 1, most] + [int(x) for x in g.integers(0, most, 50)] + \
-                    [q * d - 1 for q in map(int, g.integers(1, most // d + 2, 50))]:
-                if 0 <= n <= most:
-                    assert n * m >> 64 == n // d, (d, n)
-
-
-def test_division_by_a_32_bit_product(lib):
     g = np.random.default_rng(2)
     for d in [2, 3, 5, 7, 17, 31, 32, 33, 126, 512, 513, 1000, 12345, (1 << 23) - 1, 1 << 23, (1 << 23) + 1, (1 << 26) - 1]:
         top = (1 << 31) - 1
