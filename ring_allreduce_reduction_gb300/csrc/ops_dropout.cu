@@ -65,24 +65,31 @@ __device__ __forceinline__ void dropChunk(const DropoutArgs& a, const Random128&
   y.pack(f);
 }
 
-// One run of chunks; U a thread, asked for before the bits are drawn. FLAT: no gaps between rows either.
-template <int DT, bool RES, int U, bool FLAT>
+// How rows of whole chunks on 16-byte boundaries lie: with no gaps between them; with the same stride in every matrix, which
+// ends less than 4 GB from its beginning (16384 x 4096 + 8 bf16 52 us, by 64-bit addresses 58); anyhow.
+enum Gaps { kNone, kAlike, kAny };
+// One run of chunks; U a thread, asked for before the bits are drawn.
+template <int DT, bool RES, int U, Gaps GAPS>
 __global__ void __launch_bounds__(kThreads) dropoutRun(const __grid_constant__ DropoutArgs a) {
   using C = Chunk<DT>;
   constexpr int E = C::E, NB = C::NB;
   const size_t block = (size_t)blockIdx.x * (kThreads * U);
   C x[U], r[U];
   size_t row[U];
-  unsigned col[U];
+  unsigned col[U];  // kAlike: the chunk's place in bytes
   auto place = [&](const char* p, size_t ld, int u) {
-    return FLAT ? reinterpret_cast<const uint4*>(p) + (block + threadIdx.x) * NB + u * (kThreads * NB)
-                : reinterpret_cast<const uint4*>(p + row[u] * ld * E) + (size_t)col[u] * NB;
+    return GAPS == kNone    ? reinterpret_cast<const uint4*>(p) + (block + threadIdx.x) * NB + u * (kThreads * NB)
+           : GAPS == kAlike ? reinterpret_cast<const uint4*>(p + col[u])
+                            : reinterpret_cast<const uint4*>(p + row[u] * ld * E) + (size_t)col[u] * NB;
   };
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const size_t n = block + threadIdx.x + u * kThreads;
     if (n >= a.chunks) continue;
-    if constexpr (!FLAT) {
+    if constexpr (GAPS == kAlike) {
+      const uint32_t r = a.per == 1 ? (uint32_t)n : quotient((uint32_t)n, a.division);
+      col[u] = r * (uint32_t)(a.ldx * E) + ((uint32_t)n - r * a.per) * (16 * NB);
+    } else if constexpr (GAPS == kAny) {
       row[u] = a.chunks >> 31 || a.per == 1 ? n / a.per : quotient((uint32_t)n, a.division);
       col[u] = (unsigned)n - (unsigned)row[u] * a.per;
     }
@@ -206,15 +213,21 @@ vrcclResult_t launchDropout(DropoutArgs& a, bool run, bool same, cudaStream_t st
   a.chunks = a.rows * a.per;
   a.division = divisionOf(a.per);
   const size_t cols = a.cols;
-  const bool flat = one || (a.ldx == cols && a.ldy == cols && (!RES || a.ldr == cols));
+  const bool alike = a.ldx == a.ldy && (!RES || a.ldr == a.ldy), none = one || (alike && a.ldx == cols);
+  const bool near = alike && a.chunks >> 31 == 0 && ((a.rows - 1) * a.ldx + cols) * Chunk<DT>::E < (size_t(1) << 32);
   const bool many = a.chunks >= (size_t)smCount() * kThreads * 8;
   constexpr int U = DT == vrcclFloat32 ? 2 : 4;
   const int u = many ? U : 1;
   const size_t blocks = (a.chunks + kThreads * u - 1) / (kThreads * u);
   if (blocks >= (size_t(1) << 31)) return vrcclInvalidArgument;
   const LaunchShape s = {dim3((unsigned)blocks), kThreads, 0, 0, false};
-  if (flat) return many ? launchShaped(dropoutRun<DT, RES, U, true>, s, st, a) : launchShaped(dropoutRun<DT, RES, 1, true>, s, st, a);
-  return many ? launchShaped(dropoutRun<DT, RES, U, false>, s, st, a) : launchShaped(dropoutRun<DT, RES, 1, false>, s, st, a);
+  auto launch = [&](auto gaps) {
+    constexpr Gaps G = decltype(gaps)::value;
+    return many ? launchShaped(dropoutRun<DT, RES, U, G>, s, st, a) : launchShaped(dropoutRun<DT, RES, 1, G>, s, st, a);
+  };
+  return none   ? launch(std::integral_constant<Gaps, kNone>{})
+         : near ? launch(std::integral_constant<Gaps, kAlike>{})
+                : launch(std::integral_constant<Gaps, kAny>{});
 }
 
 vrcclResult_t dropout(const void* x, size_t ldx, const void* r, size_t ldr, void* y, size_t ldy, size_t rows, size_t cols,

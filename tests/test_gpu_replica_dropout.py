@@ -92,6 +92,10 @@ def test_dropout_of_many_rows_matches_its_parts(torch, v):  # noqa: F811
     gaps = torch.empty(rows, cols + 8, device="cuda", dtype=torch.bfloat16)[:, :cols]
     v.vrcclDropoutForward(x, None, gaps, rows, cols, "bfloat16", 0.3, seed, 9)
     assert torch.equal(y, gaps)
+    wide = torch.ones(rows, cols + 8, device="cuda", dtype=torch.bfloat16)[:, :cols]
+    gaps.zero_()
+    v.vrcclDropoutForward(wide, None, gaps, rows, cols, "bfloat16", 0.3, seed, 9)
+    assert torch.equal(y, gaps)
     part = torch.empty(13, cols, device="cuda", dtype=torch.bfloat16)
     for at in (0, 1, 2500, rows - 13):
         v.vrcclDropoutForward(x[at:at + 13], None, part, 13, cols, "bfloat16", 0.3, seed, 9, at)
