@@ -764,7 +764,7 @@ vrcclResult_t vrcclRmsNormForward(const void* x, size_t ldx, const void* residua
                                   vrcclStream_t stream);
 
 /* vrcclRmsNormWorkspace -- bytes of workspace the backward pass of this size
- * needs (the partial sums of the weight's gradient). */
+ * needs (the partial sums of the weight's gradient); 0 for 0 rows or columns. */
 vrcclResult_t vrcclRmsNormWorkspace(size_t rows, size_t cols, size_t* bytes);
 
 /*

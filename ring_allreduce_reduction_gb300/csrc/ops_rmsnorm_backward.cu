@@ -275,7 +275,7 @@ using namespace vrccl;
 
 extern "C" vrcclResult_t vrcclRmsNormWorkspace(size_t rows, size_t cols, size_t* bytes) {
   if (!bytes || !goodSizes(rows, cols, vrcclFloat32, vrcclFloat32)) return vrcclInvalidArgument;
-  *bytes = size_t(mostBlocks(rows, (int)cols)) * cols * sizeof(float);
+  *bytes = rows && cols ? size_t(mostBlocks(rows, (int)cols)) * cols * sizeof(float) : 0;  // (rmsShape divides by what fits)
   return vrcclSuccess;
 }
 
