@@ -113,7 +113,7 @@ __device__ __forceinline__ Sums warpJoin(Sums r, float c) {
 // The largest of a warp's lanes, NaN if one is.
 __device__ __forceinline__ float largestOfWarp(float x) {
   float r;
-  asm("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+  asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));  // (not to be moved under a lane's condition)
   return r;
 }
 template <int DT>
