@@ -73,7 +73,7 @@ struct LogProbArgs {
   size_t slice;  // backward: elements of a row one block takes
   int k, span, shift;  // span: loads of a segment, 2^shift
   bool wide;  // 64-bit tokens
-  float temperature, invT;
+  float invT;
 };
 
 // The row's token; -1: none given (no list), -2: one outside the vocabulary.
@@ -828,7 +828,6 @@ LogProbArgs logProbArgs(const void* logits, size_t ldl, const void* token, int t
   a.ldl = ldl;
   a.vocab = vocab;
   a.wide = ttype == vrcclInt64;
-  a.temperature = temperature;
   a.invT = 1.f / temperature;
   return a;
 }
