@@ -754,7 +754,9 @@ typedef enum {
  *                share a scale: 32, 64, 128, or 0 for the whole row.
  *   rstd         out, [rows] binary32, what the backward pass takes; or NULL.
  *   rows, cols   0 of either -> success, nothing launched.
- *   eps          >= 0.
+ *   eps          >= 0. A row's squares are summed in binary32: where the sum
+ *                passes its range (|s| beyond some 1e19) rstd is 0; where it is
+ *                0 and eps too, infinite.
  * vrcclAllGather carries codes as vrcclInt8 or vrcclUint8.
  */
 vrcclResult_t vrcclRmsNormForward(const void* x, size_t ldx, const void* residual, size_t ldr, const void* gamma,

@@ -12,7 +12,7 @@
 //
 // Sixteen bits an element, not 32: the probability is then a multiple of 2^-16
 // (and the scale that of the rounded one, so that the expectation is exact),
-// and the generator takes 5 products an element instead of 10.
+// and the generator takes 2.5 products an element instead of 5.
 //
 // Bound by memory. A thread takes chunks of its own. Where all rows start on
 // 16-byte boundaries and are whole chunks long, the matrix is one run of chunks

@@ -14,7 +14,8 @@
 // own rounding is taken back exactly at the end (M - m c is one more). When m
 // grows by d (in units of x), w' = (w + l d) 2^d and l' = l 2^d. The passes are
 // bound by issue slots nearly as much as by memory, so that the loop looks at
-// nothing else: a product of 0 and -inf (a masked entry), an M beyond binary32
+// nothing else: a product of 0 and -inf (a masked entry, of -inf or the type's lowest
+// value), an M beyond binary32
 // or a NaN leave w not finite, and the thread then takes the step back and goes
 // on with care: x = (s - m) c, held above -1000, where 2^x and 2^x x are 0. A
 // NaN stays NaN through that bound. So do rows whose M is no longer small

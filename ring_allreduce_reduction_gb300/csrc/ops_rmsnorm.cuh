@@ -43,7 +43,7 @@ enum Lie { kWhole, kSame, kAny };
 // Warps of a block (one an SM), and so the registers of a thread: what is left of 65536, in steps of four warps. Forward:
 // 32768 x 4096 bf16 with residual 16 warps 175 us, 20: 179, 24: 170, 28: 175, 32: 182; 16384 x 4097 20: 88, 24: 93, 28: 97, 32:
 // 104, and 65536 x 1025 83, 74, 92, 94; anyhow (three teams of nine from 27 on) 20: 136, 24: 142, 28: 118, 32: 132; 16384 x 5120
-// to e4m3 20: 95, 24: 96, 28: 133, 32: 106, and x 4096 87, 79, 92, 86. Rows that need more warps have 32 (wide).
+// to e4m3 20: 100, 24: 100, 28: 135, 32: 110, and x 4096 91, 76, 94, 86. Rows that need more warps have 32 (wide).
 constexpr int forwardWarps(Lie lie, bool wide) { return wide ? 32 : lie == kAny ? 28 : 24; }
 // Backward keeps a row's chunks in registers (hold) where 16 warps do and teams of them leave few idle: 16384 x 8192 bf16
 // 159 us (20 warps: 205), 20000 x 2500 fp32 141 (not held 169). Else it reads them from the stage once more: 16384 x 5120 20

@@ -61,3 +61,12 @@ def test_rms_of_more_narrow_rows_than_are_at_work(torch, v, rows, cols, dtype): 
     _forward(torch, v, rows, cols, dtype, "float32")
     _forward(torch, v, rows, cols, dtype, dtype, residual=False, quant="int8", group=32, with_y=False)
     _backward(torch, v, rows, cols, dtype, "float32")
+
+
+def test_rms_of_rows_whose_squares_leave_the_range(torch, v):  # noqa: F811
+    """As the header says: an inverse root of 0 where the sum of squares passes binary32, infinite where it is 0 and eps too."""
+    for rows, cols in ((5, 64), (5, 1001), (3, 20001)):
+        x, y, rstd = torch.ones(rows, cols, device="cuda"), torch.empty(rows, cols, device="cuda"), torch.empty(rows, device="cuda")
+        x[0], x[1] = 1e20, 0
+        v.vrcclRmsNormForward(x, None, None, None, y, rstd, rows, cols, "float32", "float32", 0.0)
+        assert rstd[0] == 0 and (y[0] == 0).all() and rstd[1] == float("inf") and (rstd[2:] == 1).all() and (y[2:] == 1).all()
